@@ -18,10 +18,11 @@ import ctypes
 import torch
 
 from ._abi import (EXPORTS, LIB_PATH, MSA_FLAG_REUSE_REGROUP, MSA_FLAG_TEST_STALL_SELECT, MSA_OK,
-                   MsaError, MsaParams, STATUS_NAMES, load)
+                   MsaDenseParams, MsaError, MsaParams, STATUS_NAMES, load)
 
 __all__ = [
-    "MsaError", "MsaParams", "MSA_FLAG_REUSE_REGROUP", "MSA_FLAG_TEST_STALL_SELECT", "make_params", "msa_select_workspace_size", "msa_fwd_workspace_size",
+    "MsaError", "MsaParams", "MsaDenseParams", "make_dense_params", "msa_dense_fwd", "msa_dense_bwd",
+    "msa_dense_bwd_workspace_size", "MSA_FLAG_REUSE_REGROUP", "MSA_FLAG_TEST_STALL_SELECT", "make_params", "msa_select_workspace_size", "msa_fwd_workspace_size",
     "msa_bwd_workspace_size", "msa_proxy_select", "msa_proxy_select_noalloc", "msa_fwd", "msa_bwd", "msa_get_device_status",
     "msa_last_status_word", "msa_launch_count", "msa_set_profile_events", "msa_status_string", "allocate_outputs", "workspace", "EXPORTS", "LIB_PATH", "load",
 ]
@@ -37,6 +38,18 @@ def make_params(total_tokens, num_docs, max_seqlen, hq, hkv, d, dp, top_k, block
                      dilation=int(dilation), softmax_scale=float(softmax_scale),
                      proxy_scale=float(proxy_scale), kl_weight=float(kl_weight),
                      flags=int(flags))
+
+
+def make_dense_params(total_tokens, num_docs, hq, hkv, d, softmax_scale=1.0, bucket_starts=(),
+                      q_stride=0, k_stride=0, v_stride=0, do_stride=0, flags=0) -> MsaDenseParams:
+    """msa_dense_params; bucket_starts: first distance of each bias bucket (empty: no bias)."""
+    n = len(bucket_starts)
+    starts = (ctypes.c_int32 * n)(*bucket_starts) if n else None
+    return MsaDenseParams(total_tokens=int(total_tokens), num_docs=int(num_docs), hq=int(hq),
+                          hkv=int(hkv), d=int(d), num_buckets=n, bucket_starts=starts,
+                          q_stride=int(q_stride), k_stride=int(k_stride), v_stride=int(v_stride),
+                          do_stride=int(do_stride), softmax_scale=float(softmax_scale),
+                          flags=int(flags))
 
 
 def _ptr(t) -> ctypes.c_void_p:
@@ -109,6 +122,32 @@ def msa_bwd(params, cu_seqlens, q, k, v, q_p, k_p, o, o_res, lse, mass, dO, sel_
                           ws.numel() * ws.element_size(), _stream(stream)), "msa_bwd")
 
 
+def _rows(t) -> ctypes.c_void_p:
+    """A [tokens, heads, d] tensor whose token stride the params carry."""
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError("the heads of one token must be contiguous")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def msa_dense_fwd(params, cu_seqlens, q, k, v, bias, o, lse, stream=None) -> None:
+    """Dense attention forward; q, k, v may have the token strides given in `params`."""
+    _check(load().msa_dense_fwd(ctypes.byref(params), _ptr(cu_seqlens), _rows(q), _rows(k),
+                                _rows(v), _ptr(bias), _ptr(o), _ptr(lse), _stream(stream)),
+           "msa_dense_fwd")
+
+
+def msa_dense_bwd_workspace_size(params: MsaDenseParams) -> int:
+    return int(load().msa_dense_bwd_workspace_size(ctypes.byref(params)))
+
+
+def msa_dense_bwd(params, cu_seqlens, q, k, v, bias, o, lse, dO, dq, dk, dv, dbias, ws,
+                  stream=None) -> None:
+    _check(load().msa_dense_bwd(ctypes.byref(params), _ptr(cu_seqlens), _rows(q), _rows(k),
+                                _rows(v), _ptr(bias), _ptr(o), _ptr(lse), _rows(dO), _ptr(dq),
+                                _ptr(dk), _ptr(dv), _ptr(dbias), _ptr(ws),
+                                ws.numel() * ws.element_size(), _stream(stream)), "msa_dense_bwd")
+
+
 def msa_get_device_status(stream=None) -> int:
     return int(load().msa_get_device_status(_stream(stream)))
 
@@ -159,6 +198,8 @@ def allocate_outputs(params: MsaParams, device="cuda") -> dict:
 
 
 # autograd front end (imported last: it builds on the calls above)
+from .dense import DenseFunction, dense_attention, log_buckets  # noqa: E402
 from .function import MSAFunction, last_kl_loss, msa_attention  # noqa: E402
 
-__all__ += ["MSAFunction", "msa_attention", "last_kl_loss"]
+__all__ += ["MSAFunction", "msa_attention", "last_kl_loss", "DenseFunction", "dense_attention",
+            "log_buckets"]

@@ -29,6 +29,9 @@ EXPORTS = (
     "msa_proxy_select_noalloc",
     "msa_fwd",
     "msa_bwd",
+    "msa_dense_fwd",
+    "msa_dense_bwd_workspace_size",
+    "msa_dense_bwd",
     "msa_get_device_status",
     "msa_last_status_word",
     "msa_launch_count",
@@ -53,6 +56,24 @@ class MsaParams(ctypes.Structure):
         ("softmax_scale", ctypes.c_float),
         ("proxy_scale", ctypes.c_float),
         ("kl_weight", ctypes.c_float),
+        ("flags", ctypes.c_uint32),
+    ]
+
+
+class MsaDenseParams(ctypes.Structure):
+    _fields_ = [
+        ("total_tokens", ctypes.c_int32),
+        ("num_docs", ctypes.c_int32),
+        ("hq", ctypes.c_int32),
+        ("hkv", ctypes.c_int32),
+        ("d", ctypes.c_int32),
+        ("num_buckets", ctypes.c_int32),
+        ("bucket_starts", ctypes.POINTER(ctypes.c_int32)),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("do_stride", ctypes.c_int64),
+        ("softmax_scale", ctypes.c_float),
         ("flags", ctypes.c_uint32),
     ]
 
@@ -90,6 +111,13 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.msa_fwd.restype = i32
     lib.msa_bwd.argtypes = [P] + [vp] * 21 + [vp, sz, vp]
     lib.msa_bwd.restype = i32
+    DP = ctypes.POINTER(MsaDenseParams)
+    lib.msa_dense_fwd.argtypes = [DP] + [vp] * 8
+    lib.msa_dense_fwd.restype = i32
+    lib.msa_dense_bwd_workspace_size.argtypes = [DP]
+    lib.msa_dense_bwd_workspace_size.restype = sz
+    lib.msa_dense_bwd.argtypes = [DP] + [vp] * 12 + [vp, sz, vp]
+    lib.msa_dense_bwd.restype = i32
     lib.msa_get_device_status.argtypes = [vp]
     lib.msa_get_device_status.restype = i32
     lib.msa_last_status_word.argtypes = []

@@ -6,7 +6,7 @@
 
 #include <cstdlib>
 
-#include "msa_internal.cuh"
+#include "dense_common.cuh"
 
 namespace msa {
 
@@ -165,9 +165,8 @@ Workspace workspace_layout(const Shape& s, WsKind kind) {
   return w;
 }
 
-cudaError_t make_tmap_3d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t mid,
-                         uint64_t outer, uint32_t box_inner, uint32_t box_mid, uint32_t box_outer,
-                         int swizzle_bytes) {
+namespace {
+EncodeTiledFn encode_fn() {
   std::call_once(g_encode_once, [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -176,7 +175,28 @@ cudaError_t make_tmap_3d(CUtensorMap* map, const void* base, uint64_t inner, uin
         q == cudaDriverEntryPointSuccess)
       g_encode = reinterpret_cast<EncodeTiledFn>(fn);
   });
-  if (!g_encode) return cudaErrorNotSupported;
+  return g_encode;
+}
+}  // namespace
+
+cudaError_t make_tmap_rows(CUtensorMap* map, const void* base, int d, int heads, int T,
+                           long long stride, int box_heads, int box_tokens) {
+  if (!encode_fn()) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)T};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+  const cuuint32_t es[3] = {1, 1, 1};
+  const CUresult r =
+      g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+               box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t make_tmap_3d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t mid,
+                         uint64_t outer, uint32_t box_inner, uint32_t box_mid, uint32_t box_outer,
+                         int swizzle_bytes) {
+  if (!encode_fn()) return cudaErrorNotSupported;
   const cuuint64_t dims[3] = {inner, mid, outer > 0 ? outer : 1};
   const cuuint64_t strides[2] = {inner * 2, inner * mid * 2};
   const cuuint32_t box[3] = {box_inner, box_mid, box_outer};

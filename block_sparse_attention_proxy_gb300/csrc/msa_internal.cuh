@@ -22,7 +22,8 @@ constexpr long long kWaitCycles = 1000000000ll;
 
 // Where a bounded wait gave up, stored above the status code in the status
 // word: kernel id (4 bits), barrier index (8 bits), tile or block index (12 bits).
-enum : uint32_t { kKerSelect = 1, kKerFwd = 2, kKerBwd = 3, kKerSelArg = 4 };
+enum : uint32_t { kKerSelect = 1, kKerFwd = 2, kKerBwd = 3, kKerSelArg = 4,
+                kKerDenseFwd = 5, kKerDenseDq = 6, kKerDenseDkv = 7 };
 __host__ __device__ constexpr uint32_t wait_site(uint32_t kernel, uint32_t bar, int n) {
   return kernel | (bar << 4) | ((uint32_t)(n < 0 ? 0 : (n > 4095 ? 4095 : n)) << 12);
 }

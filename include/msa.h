@@ -239,6 +239,64 @@ msa_status msa_proxy_select_noalloc(const msa_params* params, const int32_t* cu_
                                     msa_stream_t stream);
 
 /*
+ * Dense causal attention over the same packed batches, for the layers of a
+ * model that attend to every earlier key: grouped heads, optionally a learned
+ * relative position bias, forward and backward.
+ *   S_ij = softmax_scale q_i . k_j + bias[h][bucket(i - j)],   j <= i in i's document,
+ *   P = softmax over j,  o_i = sum_j P_ij v_j,  lse_i = ln sum_j exp(S_ij).
+ * bucket(x) is the last b with bucket_starts[b] <= x.
+ *
+ * Layouts as above: q, dO, o, dq [T, hq, d]; k, v, dk, dv [T, hkv, d]; lse
+ * [T, hq] fp32; bias, dbias [hq, num_buckets]; all but lse bf16.  The outputs
+ * are contiguous; q, k, v and dO may have a token stride (a slice of a fused
+ * projection), their heads are d elements apart.  Gradients are summed in fp32
+ * and rounded once.
+ *
+ *   - Any hq / hkv from 1 to 64, hq <= 1024, d in {64, 128}, T < 2^27.
+ *   - cu_seqlens may end before T (a padded batch): the rows behind the last
+ *     document get zero o, dq, dk and dv and lse = -inf.
+ *   - Documents do not affect one another, whatever values they hold.
+ *   - A bias of -inf masks its distances.  A row without a key left has o = 0,
+ *     lse = -inf and no gradient.
+ *   - Every sum has a fixed order: results repeat bit for bit.
+ *   - The conventions above on ownership, alignment, streams, graph capture and
+ *     errors hold; only the backward has a workspace, and calls that share none
+ *     may run at the same time.
+ */
+typedef struct msa_dense_params {
+  int32_t total_tokens; /* T */
+  int32_t num_docs;
+  int32_t hq, hkv; /* query heads, KV heads; hq % hkv == 0 */
+  int32_t d;
+  int32_t num_buckets; /* entries of the bias table per head, at most 64; 0: no bias */
+  /* host pointer, read during the call: first distance of each bucket, starting
+     with 0 and strictly increasing; null without a bias */
+  const int32_t* bucket_starts;
+  /* token strides in elements, multiples of 8 and at least heads * d; 0: contiguous */
+  int64_t q_stride, k_stride, v_stride, do_stride;
+  float softmax_scale; /* finite and positive */
+  uint32_t flags;      /* must be 0 */
+} msa_dense_params;
+
+/* Inputs: cu_seqlens, q, k, v, bias (null without one).  Outputs: o, and lse,
+   which msa_dense_bwd needs (null: not stored). */
+msa_status msa_dense_fwd(const msa_dense_params* params, const int32_t* cu_seqlens,
+                         const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                         const uint16_t* bias, uint16_t* o, float* lse, msa_stream_t stream);
+
+/* Workspace bytes of msa_dense_bwd (0 if params are invalid). */
+size_t msa_dense_bwd_workspace_size(const msa_dense_params* params);
+
+/* Gradients of sum(o * dO).  Inputs: the forward's inputs and outputs and dO.
+   Outputs (overwritten): dq, dk, dv and, with a bias, dbias. */
+msa_status msa_dense_bwd(const msa_dense_params* params, const int32_t* cu_seqlens,
+                         const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                         const uint16_t* bias, const uint16_t* o, const float* lse,
+                         const uint16_t* dO, uint16_t* dq, uint16_t* dk, uint16_t* dv,
+                         uint16_t* dbias, void* workspace, size_t workspace_bytes,
+                         msa_stream_t stream);
+
+/*
  * Synchronises `stream`, returns the device status word of the current device
  * (MSA_OK, MSA_ERR_TIMEOUT or MSA_ERR_DEVICE_CHECK; the first error recorded
  * wins) and resets it to MSA_OK.  Returns MSA_ERR_CUDA if the stream itself
@@ -250,7 +308,8 @@ msa_status msa_get_device_status(msa_stream_t stream);
  * Full device status word seen by the last msa_get_device_status call on the
  * calling host thread.  Bits 0-7 hold the status code.  For MSA_ERR_TIMEOUT,
  * bits 8-11 name the kernel whose wait ran out (1 proxy select, 2 forward,
- * 3 backward), bits 12-19 the barrier index inside it and bits 20-31 the tile
+ * 3 backward, 4 selection argmax, 5 dense forward, 6 dense dQ, 7 dense dK and
+ * dV), bits 12-19 the barrier index inside it and bits 20-31 the tile
  * (or key block) it was working on, saturated at 4095.
  */
 uint32_t msa_last_status_word(void);
