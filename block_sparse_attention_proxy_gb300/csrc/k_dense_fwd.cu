@@ -47,13 +47,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sQ = smem;  // [2]; after the last S also the staging of O
   uint8_t* sKV = sQ + 2 * C::kTile;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + NR * C::kTile);
-  constexpr int B_Q = 0, B_F = 1, B_E = 1 + NR, B_S = 1 + 2 * NR, B_P = B_S + 2, B_PV = B_S + 4,
-                B_END = B_S + 6;
+  constexpr int B_Q = 0, B_F = 1, B_E = 1 + NR, B_S = 1 + 2 * NR, B_P = B_S + 2, B_P2 = B_S + 4,
+                B_PV = B_S + 6, B_END = B_S + 8;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + B_END + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   static_assert((B_END + 1) * 8 + 8 <= 256, "barrier block");
   auto bar = [&](int i) { return smem_u32(bars + i); };
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (blockIdx.x == 0 && warp == 11) dense_check_docs(a);
   // heaviest tiles of a document first: they end last otherwise
@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(B_S + t), 1);
       mbar_init(bar(B_P + t), 4);
+      mbar_init(bar(B_P2 + t), 4);
       mbar_init(bar(B_PV + t), 1);
     }
     mbar_init(bar(B_END), 1);
@@ -139,67 +140,61 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------ MMA issue ----------------------------------
       constexpr uint32_t idS = make_idesc_bf16(128, 128, false, false);
       constexpr uint32_t idO = make_idesc_bf16(128, D, false, true);
+      const uint32_t el = elect_one(), tm = uniform(tbase);
+      const int len = uniform(it.len), nt0 = uniform(nt[0]), nt1 = uniform(nt[1]);
+      const int nm = max(nt0, nt1);
+      const uint32_t q_lo = desc_lo(smem_u32(sQ), 16), k_lo = desc_lo(smem_u32(sKV), 16),
+                     v_lo = desc_lo(smem_u32(sKV), 16384);
       auto wait = [&](int b, uint32_t par, int n) {
         return wait_bar_warp(bar(b), par, abort_flag, a.status, wait_site(kKerDenseFwd, b, n));
       };
       auto wait_full = [&](int x) { return wait(B_F + x % NR, (x / NR) & 1, x >> 1); };
       auto issue_s = [&](int t, int n) {
-        const uint32_t q = smem_u32(sQ + t * C::kTile);
-        const uint32_t k = smem_u32(sKV + (2 * n % NR) * C::kTile);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-          umma_bf16(tbase + 128 * t, make_sdesc(q + off, 16, 1024, kLayoutSW128),
-                    make_sdesc(k + off, 16, 1024, kLayoutSW128), idS, kk > 0);
-        }
-        umma_commit(bar(B_S + t));
+        mma_tile_ss<D>(el, tm + 128 * t, q_lo + t * (C::kTile >> 4),
+                       k_lo + (2 * n % NR) * (C::kTile >> 4), idS);
+        mma_commit(el, bar(B_S + t));
       };
       bool ok = wait(B_Q, 0, 0) && wait_full(0);
       if (ok) {
         tc_fence_after();
-        if (lane == 0) {
-          for (int t = 0; t < 2; ++t)
-            if (nt[t] > 0) issue_s(t, 0);
-          umma_commit(bar(B_E + 0));
-        }
-        __syncwarp();
+        if (nt0 > 0) issue_s(0, 0);
+        if (nt1 > 0) issue_s(1, 0);
+        mma_commit(el, bar(B_E + 0));
       }
-      for (int n = 0; ok && n < nmax; ++n) {
+      for (int n = 0; ok && n < nm; ++n) {
         const int xv = 2 * n + 1, sv = xv % NR;
         if (!(ok = wait_full(xv))) break;
         // keys behind the document's end: P is zero there, V must be finite
-        if ((n + 1) * 128 > it.len)
-          dense_zero_rows<D>(sKV + sv * C::kTile, it.len - n * 128);
-        for (int t = 0; ok && t < 2; ++t) {
-          if (n >= nt[t]) continue;
+        if ((n + 1) * 128 > len) dense_zero_rows<D>(sKV + sv * C::kTile, len - n * 128);
+        const uint32_t v = v_lo + sv * (C::kTile >> 4);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int ntt = t ? nt1 : nt0;
+          if (!ok || n >= ntt) continue;
+          const uint32_t po = tm + 256 + D * t, pa = tm + 128 * t;
           if (!(ok = wait(B_P + t, n & 1, n))) break;
           tc_fence_after();
-          if (lane == 0) {
-            const uint32_t v = smem_u32(sKV + sv * C::kTile);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              umma_bf16_ts(tbase + 256 + D * t, tbase + 128 * t + 8 * kk,
-                           make_sdesc(v + kk * 2048, 16384, 1024, kLayoutSW128), idO,
-                           n > 0 || kk > 0);
-            umma_commit(bar(B_PV + t));
-          }
-          __syncwarp();
-          if (n + 1 < nt[t]) {
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ts(el, po, pa + 8 * kk, v + kk * (2048 >> 4), idO, n > 0 || kk > 0);
+          if (!(ok = wait(B_P2 + t, n & 1, n))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 4; kk < 8; ++kk)
+            mma_ts(el, po, pa + 8 * kk, v + kk * (2048 >> 4), idO, 1);
+          mma_commit(el, bar(B_PV + t));
+          if (n + 1 < ntt) {
             if (!(ok = wait_full(xv + 1))) break;
             tc_fence_after();
-            if (lane == 0) issue_s(t, n + 1);
-            __syncwarp();
+            issue_s(t, n + 1);
           }
         }
         if (!ok) break;
-        if (lane == 0) {
-          umma_commit(bar(B_E + sv));
-          if (n + 1 < nmax) umma_commit(bar(B_E + (xv + 1) % NR));
-        }
-        __syncwarp();
+        mma_commit(el, bar(B_E + sv));
+        if (n + 1 < nm) mma_commit(el, bar(B_E + (xv + 1) % NR));
       }
-      if (!ok && lane == 0) {  // products in flight end before TMEM is freed
-        umma_commit(bar(B_END));
+      if (!ok) {  // products in flight end before TMEM is freed
+        mma_commit(el, bar(B_END));
         drain_bar(bar(B_END), 0);
       }
     }
@@ -225,14 +220,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     wait_site(kKerDenseFwd, B_S + t, n));
       tc_fence_after();
       if (!dead) {
-        uint32_t x[4][32];
-        tmem_ld32x2(ts, ts + 32, x[0], x[1]);
-        tmem_ld32x2(ts + 64, ts + 96, x[2], x[3]);
+        uint32_t x[128];
+        tmem_ld128(ts, x);
         const int rel = qi - n * 128;  // keys 0..rel of the tile are visible
         if (__any_sync(0xffffffffu, rel < 127)) {
 #pragma unroll
           for (int i = 0; i < 128; ++i)
-            if (i > rel) x[i >> 5][i & 31] = __float_as_uint(-INFINITY);
+            if (i > rel) x[i] = __float_as_uint(-INFINITY);
         }
         // P = 2^(x mul + add - m)
         float mul = c, add = 0.f;
@@ -252,8 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 st = b > 0 ? a.starts[b] : INT_MIN;
                 bv = dense_bias_log2(__ldg(tab + b));
               }
-              x[i >> 5][i & 31] =
-                  __float_as_uint(fmaf(__uint_as_float(x[i >> 5][i & 31]), c, bv));
+              x[i] =
+                  __float_as_uint(fmaf(__uint_as_float(x[i]), c, bv));
             }
             __syncwarp();
             mul = 1.f;
@@ -262,11 +256,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         float m4[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          m4[u] = __uint_as_float(x[u][0]);
+          m4[u] = __uint_as_float(x[32 * u]);
 #pragma unroll
           for (int i = 1; i < 31; i += 2)
-            m4[u] = fmax3(m4[u], __uint_as_float(x[u][i]), __uint_as_float(x[u][i + 1]));
-          m4[u] = fmaxf(m4[u], __uint_as_float(x[u][31]));
+            m4[u] = fmax3(m4[u], __uint_as_float(x[32 * u + i]), __uint_as_float(x[32 * u + i + 1]));
+          m4[u] = fmaxf(m4[u], __uint_as_float(x[32 * u + 31]));
         }
         const float mx = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), mul, add);
         const bool grow = mx > m + kRescale || (m == -INFINITY && mx > m);
@@ -294,26 +288,40 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float sub = add - (m == -INFINITY ? 0.f : m);
-        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+        const f32x2 mul2_ = pack2(mul, mul), sub2 = pack2(sub, sub);
+        f32x2 ls[2] = {0ull, 0ull};
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           uint32_t w[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const int e = 64 * u + 2 * i;
-            const float p0 = ex2_approx(fmaf(__uint_as_float(x[e >> 5][e & 31]), mul, sub));
-            const float p1 =
-                ex2_approx(fmaf(__uint_as_float(x[e >> 5][(e & 31) + 1]), mul, sub));
-            l4[i & 3] += p0 + p1;
+            float p0, p1;
+            unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), mul2_, sub2), p0,
+                    p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            ls[i & 1] = add2(ls[i & 1], pack2(p0, p1));
             w[i] = pack_bf16(p0, p1);
           }
-          tmem_st32(ts + 32 * u, w);
+          tmem_st32_async(ts + 32 * u, w);
+          tmem_wait_st();
+          // the product over the first 64 keys starts while the rest is computed
+          if (u == 0) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_P + t));
+          }
         }
-        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        float l0, l1;
+        unpack2(add2(ls[0], ls[1]), l0, l1);
+        l += l0 + l1;
+      } else if (lane == 0) {
+        mbar_arrive(bar(B_P + t));
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_P + t));
+      if (lane == 0) mbar_arrive(bar(B_P2 + t));
     }
     if (nt[t] > 0) {
       const int last = nt[t] - 1;
