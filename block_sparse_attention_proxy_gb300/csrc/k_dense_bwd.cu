@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   static_assert((B_END + 1) * 8 + 8 <= 256, "barrier block");
   auto bar = [&](int i) { return smem_u32(bars + i); };
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (blockIdx.x == 0 && warp == 11) dense_check_docs(a);
   const int g = blockIdx.x % a.hkv;
@@ -152,65 +152,49 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------ MMA issue ----------------------------------
       constexpr uint32_t idS = make_idesc_bf16(128, 128, false, false);
       constexpr uint32_t idQ = make_idesc_bf16(128, D, false, true);
+      const uint32_t el = elect_one(), tm = uniform(tbase);
+      const int len = uniform(it.len), NT = uniform(N);
+      constexpr uint32_t T16 = C::kTile >> 4;
+      const uint32_t q_lo = desc_lo(smem_u32(sQ), 16), o_lo = desc_lo(smem_u32(sO), 16),
+                     k_lo = desc_lo(smem_u32(sK), 16), v_lo = desc_lo(smem_u32(sV), 16),
+                     kt_lo = desc_lo(smem_u32(sK), 16384);
       auto wait = [&](int b, uint32_t par, int n) {
         return wait_bar_warp(bar(b), par, abort_flag, a.status, wait_site(kKerDenseDq, b, n));
       };
-      auto product = [&](uint32_t d, uint32_t pa, uint32_t pb) {  // 128 x 128, both K-major
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-          umma_bf16(d, make_sdesc(pa + off, 16, 1024, kLayoutSW128),
-                    make_sdesc(pb + off, 16, 1024, kLayoutSW128), idS, kk > 0);
-        }
-      };
-      const uint32_t aq = smem_u32(sQ), ao = smem_u32(sO);
       auto s_of = [&](int n) -> bool {
         if (!wait(B_KF + n % NK, (n / NK) & 1, n)) return false;
         // keys behind the document's end: dS is zero there, K must be finite
-        if ((n + 1) * 128 > it.len) dense_zero_rows<D>(sK + (n % NK) * C::kTile, it.len - n * 128);
+        if ((n + 1) * 128 > len) dense_zero_rows<D>(sK + (n % NK) * C::kTile, len - n * 128);
         tc_fence_after();
-        if (lane == 0) {
-          product(tbase + 128 * (n & 1), aq, smem_u32(sK + (n % NK) * C::kTile));
-          umma_commit(bar(B_S + (n & 1)));
-        }
-        __syncwarp();
+        mma_tile_ss<D>(el, tm + 128 * (n & 1), q_lo, k_lo + (n % NK) * T16, idS);
+        mma_commit(el, bar(B_S + (n & 1)));
         return true;
       };
       auto dp_of = [&](int n) -> bool {
         if (!wait(B_VF + n % NV, (n / NV) & 1, n)) return false;
         if (n > 0 && !wait(B_DPE, (n - 1) & 1, n)) return false;
         tc_fence_after();
-        if (lane == 0) {
-          product(tbase + 256, ao, smem_u32(sV + (n % NV) * C::kTile));
-          umma_commit(bar(B_DP));
-          umma_commit(bar(B_VE + n % NV));
-        }
-        __syncwarp();
+        mma_tile_ss<D>(el, tm + 256, o_lo, v_lo + (n % NV) * T16, idS);
+        mma_commit(el, bar(B_DP));
+        mma_commit(el, bar(B_VE + n % NV));
         return true;
       };
       bool ok = wait(B_Q, 0, 0) && s_of(0) && dp_of(0);
-      for (int n = 0; ok && n < N; ++n) {
-        if (n + 1 < N && !(ok = s_of(n + 1) && dp_of(n + 1))) break;
+      for (int n = 0; ok && n < NT; ++n) {
+        if (n + 1 < NT && !(ok = s_of(n + 1) && dp_of(n + 1))) break;
         if (!(ok = wait(B_DS + (n & 1), (n >> 1) & 1, n))) break;
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t k = smem_u32(sK + (n % NK) * C::kTile);
-          const uint32_t ds = tbase + 128 * (n & 1);
+        const uint32_t k = kt_lo + (n % NK) * T16, ds = tm + 128 * (n & 1);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_bf16_ts(tbase + 384, ds + 64 * (kk >> 2) + 8 * (kk & 3),
-                         make_sdesc(k + kk * 2048, 16384, 1024, kLayoutSW128), idQ,
-                         n > 0 || kk > 0);
-          umma_commit(bar(B_KE + n % NK));
-        }
-        __syncwarp();
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(el, tm + 384, ds + 64 * (kk >> 2) + 8 * (kk & 3), k + kk * (2048 >> 4), idQ,
+                 n > 0 || kk > 0);
+        mma_commit(el, bar(B_KE + n % NK));
       }
-      if (lane == 0) {
-        umma_commit(bar(B_DQ));
-        if (!ok) {  // products in flight end before TMEM is freed
-          umma_commit(bar(B_END));
-          drain_bar(bar(B_END), 0);
-        }
+      mma_commit(el, bar(B_DQ));
+      if (!ok) {  // products in flight end before TMEM is freed
+        mma_commit(el, bar(B_END));
+        drain_bar(bar(B_END), 0);
       }
     }
   } else {
@@ -433,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   static_assert((B_END + 1) * 8 + 8 <= 256, "barrier block");
   auto bar = [&](int i) { return smem_u32(bars + i); };
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   const int g = blockIdx.x % a.hkv;
   DenseItem it;
@@ -518,6 +502,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------ MMA issue ----------------------------------
       constexpr uint32_t idS = make_idesc_bf16(128, 128, false, false);
       constexpr uint32_t idG = make_idesc_bf16(128, D, false, true);
+      const uint32_t el = elect_one(), tm = uniform(tbase);
+      const int left = uniform(it.len - j0), nqt = uniform(nq), NT = uniform(N);
+      constexpr uint32_t T16 = C::kTile >> 4;
+      const uint32_t k_lo = desc_lo(smem_u32(sK), 16), v_lo = desc_lo(smem_u32(sV), 16),
+                     q_lo = desc_lo(smem_u32(sQ), 16), o_lo = desc_lo(smem_u32(sO), 16),
+                     qt_lo = desc_lo(smem_u32(sQ), 16384), ot_lo = desc_lo(smem_u32(sO), 16384);
       auto wait = [&](int b, uint32_t par, int n) {
         return wait_bar_warp(bar(b), par, abort_flag, a.status, wait_site(kKerDenseDkv, b, n));
       };
@@ -525,67 +515,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       // probabilities are zero, but the products sum over them
       auto arrived = [&](int bf, int depth, uint8_t* ring, int n) -> bool {
         if (!wait(bf + n % depth, (n / depth) & 1, n)) return false;
-        const int i0 = j0 + (n % nq) * 128;
-        if (i0 + 128 > it.len) dense_zero_rows<D>(ring + (n % depth) * C::kTile, it.len - i0);
+        const int i0 = (n % nqt) * 128;
+        if (i0 + 128 > left) dense_zero_rows<D>(ring + (n % depth) * C::kTile, left - i0);
         tc_fence_after();
         return true;
       };
-      auto product = [&](uint32_t d, uint32_t pa, uint32_t pb) {  // 128 x 128, both K-major
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-          umma_bf16(d, make_sdesc(pa + off, 16, 1024, kLayoutSW128),
-                    make_sdesc(pb + off, 16, 1024, kLayoutSW128), idS, kk > 0);
-        }
-      };
-      auto gradient = [&](uint32_t d, uint32_t ta, uint32_t pb, int n) {
+      auto gradient = [&](uint32_t d, uint32_t ta, uint32_t b_lo, int n) {
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          umma_bf16_ts(d, ta + 64 * (kk >> 2) + 8 * (kk & 3),
-                       make_sdesc(pb + kk * 2048, 16384, 1024, kLayoutSW128), idG, n > 0 || kk > 0);
+          mma_ts(el, d, ta + 64 * (kk >> 2) + 8 * (kk & 3), b_lo + kk * (2048 >> 4), idG,
+                 n > 0 || kk > 0);
       };
-      const uint32_t ak = smem_u32(sK), av = smem_u32(sV);
       auto s_of = [&](int n) -> bool {
         if (!arrived(B_QF, NQ, sQ, n)) return false;
-        if (lane == 0) {
-          product(tbase, ak, smem_u32(sQ + (n % NQ) * C::kTile));
-          umma_commit(bar(B_S));
-        }
-        __syncwarp();
+        mma_tile_ss<D>(el, tm, k_lo, q_lo + (n % NQ) * T16, idS);
+        mma_commit(el, bar(B_S));
         return true;
       };
       auto dp_of = [&](int n) -> bool {
         if (!arrived(B_OF, NO, sO, n)) return false;
-        if (lane == 0) {
-          product(tbase + 128, av, smem_u32(sO + (n % NO) * C::kTile));
-          umma_commit(bar(B_DP));
-        }
-        __syncwarp();
+        mma_tile_ss<D>(el, tm + 128, v_lo, o_lo + (n % NO) * T16, idS);
+        mma_commit(el, bar(B_DP));
         return true;
       };
       bool ok = wait(B_KV, 0, 0) && s_of(0) && dp_of(0);
-      for (int n = 0; ok && n < N; ++n) {
+      for (int n = 0; ok && n < NT; ++n) {
         if (!(ok = wait(B_P, n & 1, n))) break;
         tc_fence_after();
-        if (lane == 0) {
-          gradient(tbase + 256, tbase, smem_u32(sO + (n % NO) * C::kTile), n);
-          umma_commit(bar(B_OE + n % NO));
-        }
-        __syncwarp();
-        if (n + 1 < N && !(ok = s_of(n + 1))) break;
+        gradient(tm + 256, tm, ot_lo + (n % NO) * T16, n);
+        mma_commit(el, bar(B_OE + n % NO));
+        if (n + 1 < NT && !(ok = s_of(n + 1))) break;
         if (!(ok = wait(B_DS, n & 1, n))) break;
         tc_fence_after();
-        if (lane == 0) {
-          gradient(tbase + 384, tbase + 128, smem_u32(sQ + (n % NQ) * C::kTile), n);
-          umma_commit(bar(B_QE + n % NQ));
-        }
-        __syncwarp();
-        if (n + 1 < N && !(ok = dp_of(n + 1))) break;
+        gradient(tm + 384, tm + 128, qt_lo + (n % NQ) * T16, n);
+        mma_commit(el, bar(B_QE + n % NQ));
+        if (n + 1 < NT && !(ok = dp_of(n + 1))) break;
       }
-      if (lane == 0) {
-        umma_commit(bar(B_END));
-        if (!ok) drain_bar(bar(B_END), 0);  // products in flight end before TMEM is freed
-      }
+      mma_commit(el, bar(B_END));
+      if (!ok) drain_bar(bar(B_END), 0);  // products in flight end before TMEM is freed
     } else if (warp == 10) {
       // ------------------------------ statistics ---------------------------------
       int h = g * a.G, qt = 0;
