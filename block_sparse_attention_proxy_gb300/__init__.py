@@ -122,29 +122,29 @@ def msa_bwd(params, cu_seqlens, q, k, v, q_p, k_p, o, o_res, lse, mass, dO, sel_
                           ws.numel() * ws.element_size(), _stream(stream)), "msa_bwd")
 
 
-def _rows(t) -> ctypes.c_void_p:
+def _rows(t) -> int:
     """A [tokens, heads, d] tensor whose token stride the params carry."""
     if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
         raise ValueError("the heads of one token must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-def msa_dense_fwd(params, cu_seqlens, q, k, v, bias, o, lse, stream=None) -> None:
+def msa_dense_fwd(params, cu_seqlens, q, k, v, bias, o, o_res, lse, stream=None) -> None:
     """Dense attention forward; q, k, v may have the token strides given in `params`."""
     _check(load().msa_dense_fwd(ctypes.byref(params), _ptr(cu_seqlens), _rows(q), _rows(k),
-                                _rows(v), _ptr(bias), _ptr(o), _ptr(lse), _stream(stream)),
-           "msa_dense_fwd")
+                                _rows(v), _ptr(bias), _ptr(o), _ptr(o_res), _ptr(lse),
+                                _stream(stream)), "msa_dense_fwd")
 
 
 def msa_dense_bwd_workspace_size(params: MsaDenseParams) -> int:
     return int(load().msa_dense_bwd_workspace_size(ctypes.byref(params)))
 
 
-def msa_dense_bwd(params, cu_seqlens, q, k, v, bias, o, lse, dO, dq, dk, dv, dbias, ws,
+def msa_dense_bwd(params, cu_seqlens, q, k, v, bias, o, o_res, lse, dO, dq, dk, dv, dbias, ws,
                   stream=None) -> None:
     _check(load().msa_dense_bwd(ctypes.byref(params), _ptr(cu_seqlens), _rows(q), _rows(k),
-                                _rows(v), _ptr(bias), _ptr(o), _ptr(lse), _rows(dO), _ptr(dq),
-                                _ptr(dk), _ptr(dv), _ptr(dbias), _ptr(ws),
+                                _rows(v), _ptr(bias), _ptr(o), _ptr(o_res), _ptr(lse), _rows(dO),
+                                _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dbias), _ptr(ws),
                                 ws.numel() * ws.element_size(), _stream(stream)), "msa_dense_bwd")
 
 

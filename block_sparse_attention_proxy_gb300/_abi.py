@@ -112,11 +112,11 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.msa_bwd.argtypes = [P] + [vp] * 21 + [vp, sz, vp]
     lib.msa_bwd.restype = i32
     DP = ctypes.POINTER(MsaDenseParams)
-    lib.msa_dense_fwd.argtypes = [DP] + [vp] * 8
+    lib.msa_dense_fwd.argtypes = [DP] + [vp] * 9
     lib.msa_dense_fwd.restype = i32
     lib.msa_dense_bwd_workspace_size.argtypes = [DP]
     lib.msa_dense_bwd_workspace_size.restype = sz
-    lib.msa_dense_bwd.argtypes = [DP] + [vp] * 12 + [vp, sz, vp]
+    lib.msa_dense_bwd.argtypes = [DP] + [vp] * 13 + [vp, sz, vp]
     lib.msa_dense_bwd.restype = i32
     lib.msa_get_device_status.argtypes = [vp]
     lib.msa_get_device_status.restype = i32

@@ -40,8 +40,9 @@ struct DenseArgs {
   const uint16_t* bias;
   int nb;
   int starts[kDenseMaxBuckets];
-  // forward outputs; in the backward o and lse are inputs
+  // forward outputs; in the backward o, o_res and lse are inputs
   uint16_t* o;
+  uint16_t* o_res;  // bf16(O - o); null: not stored
   float* lse;
   // backward
   const uint16_t* d_o;
@@ -283,7 +284,9 @@ __device__ __forceinline__ void dense_zero_rows(uint8_t* tile, int first) {
 // A warp's 32 rows x 64 columns of fp32 values (one row per lane), scaled and
 // rounded to bf16, through a private swizzled 32-row x 128-byte staging tile to
 // global memory, four rows x 128 contiguous bytes per warp store.  `row` is
-// the lane's destination (its first element; null: not stored).
+// the lane's destination (its first element; null: not stored).  RES: what the
+// rounding drops, itself as bf16, instead of the values.
+template <bool RES = false>
 __device__ __forceinline__ void dense_store_rows(const uint32_t (&va)[32], const uint32_t (&vb)[32],
                                                  float f, uint8_t* stg, uint16_t* row) {
   const int lane = threadIdx.x & 31;
@@ -292,10 +295,16 @@ __device__ __forceinline__ void dense_store_rows(const uint32_t (&va)[32], const
     uint32_t w[4], x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      w[i] = pack_bf16(__uint_as_float(va[8 * q + 2 * i]) * f,
-                       __uint_as_float(va[8 * q + 2 * i + 1]) * f);
-      x[i] = pack_bf16(__uint_as_float(vb[8 * q + 2 * i]) * f,
-                       __uint_as_float(vb[8 * q + 2 * i + 1]) * f);
+      const float a0 = __uint_as_float(va[8 * q + 2 * i]) * f;
+      const float a1 = __uint_as_float(va[8 * q + 2 * i + 1]) * f;
+      const float b0 = __uint_as_float(vb[8 * q + 2 * i]) * f;
+      const float b1 = __uint_as_float(vb[8 * q + 2 * i + 1]) * f;
+      w[i] = pack_bf16(a0, a1);
+      x[i] = pack_bf16(b0, b1);
+      if (RES) {
+        w[i] = pack_bf16(a0 - bf16_lo(w[i]), a1 - bf16_hi(w[i]));
+        x[i] = pack_bf16(b0 - bf16_lo(x[i]), b1 - bf16_hi(x[i]));
+      }
     }
     *reinterpret_cast<uint4*>(stg + sw128_offset(lane, q)) = make_uint4(w[0], w[1], w[2], w[3]);
     *reinterpret_cast<uint4*>(stg + sw128_offset(lane, q + 4)) = make_uint4(x[0], x[1], x[2], x[3]);

@@ -214,14 +214,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint4* po = reinterpret_cast<const uint4*>(a.o + row * D);
       const uint4* pd = reinterpret_cast<const uint4*>(
           a.d_o + (size_t)(it.start + qi) * a.do_stride + (size_t)(g * a.G + hl) * D);
+      const uint4* pr = reinterpret_cast<const uint4*>(a.o_res + row * D);
       float s4[4] = {0.f, 0.f, 0.f, 0.f};
+      auto dot = [](uint32_t o, uint32_t res, uint32_t d_o) {
+        return (bf16_lo(o) + bf16_lo(res)) * bf16_lo(d_o) +
+               (bf16_hi(o) + bf16_hi(res)) * bf16_hi(d_o);
+      };
 #pragma unroll 4
       for (int u = 0; u < D / 8; ++u) {
-        const uint4 x = __ldg(po + u), y = __ldg(pd + u);
-        s4[0] += bf16_lo(x.x) * bf16_lo(y.x) + bf16_hi(x.x) * bf16_hi(y.x);
-        s4[1] += bf16_lo(x.y) * bf16_lo(y.y) + bf16_hi(x.y) * bf16_hi(y.y);
-        s4[2] += bf16_lo(x.z) * bf16_lo(y.z) + bf16_hi(x.z) * bf16_hi(y.z);
-        s4[3] += bf16_lo(x.w) * bf16_lo(y.w) + bf16_hi(x.w) * bf16_hi(y.w);
+        const uint4 x = __ldg(po + u), z = __ldg(pr + u), y = __ldg(pd + u);
+        s4[0] += dot(x.x, z.x, y.x);
+        s4[1] += dot(x.y, z.y, y.y);
+        s4[2] += dot(x.z, z.z, y.z);
+        s4[3] += dot(x.w, z.w, y.w);
       }
       dsum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
       const float lse = __ldg(a.lse + row);

@@ -68,6 +68,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int r = threadIdx.x; r < n; r += kThreads) {
       const size_t row = (size_t)(it.start + q0 + r / a.G) * a.hq + g * a.G + r % a.G;
       dense_zero_row(a.o + row * D, D);
+      if (a.o_res) dense_zero_row(a.o_res + row * D, D);
       if (a.lse) a.lse[row] = -INFINITY;
     }
     return;
@@ -341,6 +342,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 32; ++i) va[i] = vb[i] = 0;
           }
           dense_store_rows(va, vb, inv, stg, valid ? a.o + row * D + 64 * u : nullptr);
+          if (a.o_res)
+            dense_store_rows<true>(va, vb, inv, stg,
+                                   valid ? a.o_res + row * D + 64 * u : nullptr);
         }
         if (valid && a.lse) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
       }

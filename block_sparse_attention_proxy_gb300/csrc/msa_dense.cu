@@ -59,9 +59,10 @@ msa_status check_dense(const msa_dense_params* p, DenseShape* s, DenseArgs* a) {
 // thread's first CUDA call may be this one (autograd runs backwards on threads of its own),
 // and encoding a tensor map does not do that by itself.
 cudaError_t bind_device(unsigned** status) {
+  static thread_local int bound = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaSetDevice(dev);
+  if (e == cudaSuccess && dev != bound && (e = cudaSetDevice(dev)) == cudaSuccess) bound = dev;
   return e == cudaSuccess ? status_ptr(status) : e;
 }
 
@@ -101,7 +102,7 @@ size_t msa_dense_bwd_workspace_size(const msa_dense_params* p) {
 
 msa_status msa_dense_fwd(const msa_dense_params* p, const int32_t* cu_seqlens, const uint16_t* q,
                          const uint16_t* k, const uint16_t* v, const uint16_t* bias, uint16_t* o,
-                         float* lse, msa_stream_t stream) {
+                         uint16_t* o_res, float* lse, msa_stream_t stream) {
   DenseShape s;
   DenseArgs a;
   const msa_status st = check_dense(p, &s, &a);
@@ -110,12 +111,13 @@ msa_status msa_dense_fwd(const msa_dense_params* p, const int32_t* cu_seqlens, c
   if (!cu_seqlens || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3)) return MSA_ERR_INVALID_ARG;
   for (const void* ptr : {(const void*)q, (const void*)k, (const void*)v, (const void*)o})
     if (!ptr || !aligned16(ptr)) return MSA_ERR_INVALID_ARG;
-  if (!aligned16(lse)) return MSA_ERR_INVALID_ARG;
+  if (!aligned16(lse) || !aligned16(o_res)) return MSA_ERR_INVALID_ARG;
   if (a.nb > 0 && (!bias || !aligned2(bias))) return MSA_ERR_INVALID_ARG;
   if (bind_device(&a.status) != cudaSuccess) return MSA_ERR_CUDA;
   a.cu = cu_seqlens;
   a.bias = a.nb > 0 ? bias : nullptr;
   a.o = o;
+  a.o_res = o_res;
   a.lse = lse;
   if (launch_dense_fwd(s, q, k, v, a, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
     return MSA_ERR_CUDA;
@@ -125,9 +127,9 @@ msa_status msa_dense_fwd(const msa_dense_params* p, const int32_t* cu_seqlens, c
 
 msa_status msa_dense_bwd(const msa_dense_params* p, const int32_t* cu_seqlens, const uint16_t* q,
                          const uint16_t* k, const uint16_t* v, const uint16_t* bias,
-                         const uint16_t* o, const float* lse, const uint16_t* dO, uint16_t* dq,
-                         uint16_t* dk, uint16_t* dv, uint16_t* dbias, void* ws, size_t ws_bytes,
-                         msa_stream_t stream) {
+                         const uint16_t* o, const uint16_t* o_res, const float* lse,
+                         const uint16_t* dO, uint16_t* dq, uint16_t* dk, uint16_t* dv,
+                         uint16_t* dbias, void* ws, size_t ws_bytes, msa_stream_t stream) {
   DenseShape s;
   DenseArgs a;
   const msa_status st = check_dense(p, &s, &a);
@@ -142,7 +144,7 @@ msa_status msa_dense_bwd(const msa_dense_params* p, const int32_t* cu_seqlens, c
   if (a.T == 0) return MSA_OK;
   if (!cu_seqlens || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3)) return MSA_ERR_INVALID_ARG;
   for (const void* ptr : {(const void*)q, (const void*)k, (const void*)v, (const void*)o,
-                          (const void*)lse, (const void*)dO, (const void*)dq, (const void*)dk,
+                          (const void*)o_res, (const void*)lse, (const void*)dO, (const void*)dq, (const void*)dk,
                           (const void*)dv})
     if (!ptr || !aligned16(ptr)) return MSA_ERR_INVALID_ARG;
   const DenseWorkspace w = dense_workspace(a);
@@ -153,6 +155,7 @@ msa_status msa_dense_bwd(const msa_dense_params* p, const int32_t* cu_seqlens, c
   a.cu = cu_seqlens;
   a.bias = a.nb > 0 ? bias : nullptr;
   a.o = const_cast<uint16_t*>(o);
+  a.o_res = const_cast<uint16_t*>(o_res);
   a.lse = const_cast<float*>(lse);
   a.d_o = dO;
   a.do_stride = s.do_stride;

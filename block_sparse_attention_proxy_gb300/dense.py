@@ -17,12 +17,13 @@ and v may be slices of a fused projection (any token stride that keeps rows on
 """
 from __future__ import annotations
 
+import ctypes
 import functools
 
 import torch
 
-from . import (make_dense_params, msa_dense_bwd, msa_dense_bwd_workspace_size, msa_dense_fwd,
-               workspace)
+from . import _check as _raise_on
+from . import load, make_dense_params, msa_dense_bwd_workspace_size
 
 
 def log_buckets(num_buckets: int, max_distance: int) -> tuple[int, ...]:
@@ -39,23 +40,101 @@ def log_buckets(num_buckets: int, max_distance: int) -> tuple[int, ...]:
     return tuple(starts)
 
 
-@functools.lru_cache(maxsize=256)
-def _params(*args):
-    """The call's parameters and the backward's workspace bytes."""
-    prm = make_dense_params(*args)
-    return prm, msa_dense_bwd_workspace_size(prm)
+class _Plan:
+    """What a call's shapes decide: the library's parameters and buffer sizes."""
+
+    def __init__(self, T, num_docs, hq, hkv, d, scale, starts, strides, do_stride):
+        self.params = make_dense_params(T, num_docs, hq, hkv, d, scale, starts, *strides, do_stride)
+        self.ref = ctypes.byref(self.params)
+        self.workspace = max(msa_dense_bwd_workspace_size(self.params), 256)
+        self.o_res_at = (T * hq * 4 + 255) // 256 * 256  # saved for the backward: lse, then o_res
+        self.saved = max(self.o_res_at + T * hq * d * 2, 256)
+        lib = load()
+        self.fwd, self.bwd = lib.msa_dense_fwd, lib.msa_dense_bwd
 
 
-def _rows(t: torch.Tensor) -> torch.Tensor:
-    """`t` [tokens, heads, d] as the library takes it: heads packed, a token stride that
-    is a multiple of 8 elements and rows that do not overlap, on 16 bytes."""
-    heads, d = t.shape[1], t.shape[2]
-    s = t.stride()
-    if (s[2] == 1 and (s[1] == d or heads == 1) and s[0] >= heads * d and s[0] % 8 == 0
-            and t.data_ptr() % 16 == 0):
-        return t
-    # contiguous tensors off a 16-byte boundary are copied too
-    return t.clone(memory_format=torch.contiguous_format)
+def _stride_of(shape, stride):
+    """Token stride the library takes for a [tokens, heads, d] tensor (0: packed), or None
+    where the layout has to be copied: heads not packed, rows that overlap, off 16 bytes."""
+    tokens, heads, d = shape
+    if tokens <= 1 and stride[2] == 1 and (heads == 1 or stride[1] == d):
+        return 0
+    if (stride[2] != 1 or (heads > 1 and stride[1] != d) or stride[0] < heads * d
+            or stride[0] % 8):
+        return None
+    return stride[0]
+
+
+# The checks and the plan depend on shapes, strides, types and devices alone, so they
+# are made once for each combination and not once per call.
+@functools.lru_cache(maxsize=512)
+def _plan(qs, ks, vs, q_st, k_st, v_st, types, devices, cus, biass, scale, starts):
+    if types[:3] != (torch.bfloat16,) * 3 or devices[0].type != "cuda":
+        raise TypeError("q, k, v must be bf16 CUDA tensors")
+    if len(qs) != 3 or len(ks) != 3 or len(vs) != 3 or any(x != devices[0] for x in devices):
+        raise ValueError("q, k, v must be [tokens, heads, d], all tensors on one device")
+    if ks != vs or ks[0] != qs[0] or ks[2] != qs[2]:
+        raise ValueError("q [T, Hq, d] and k, v [T, Hkv, d] expected")
+    if len(cus) != 1 or cus[0] < 2:
+        raise ValueError("cu_seqlens must be [num_docs + 1]")
+    if types[3] not in (torch.int32, torch.int64):
+        raise TypeError("cu_seqlens must be integers")
+    if (biass is None) != (not starts):
+        raise ValueError("bias and bucket_starts go together")
+    if biass is not None:
+        if types[4] != torch.bfloat16:
+            raise TypeError("bias must be bf16")
+        if biass != (qs[1], len(starts)):
+            raise ValueError("bias must be [Hq, number of buckets]")
+    strides = [_stride_of(s, st) for s, st in ((qs, q_st), (ks, k_st), (vs, v_st))]
+    copy = tuple(s is None for s in strides)
+    args = (qs[0], cus[0] - 1, qs[1], ks[1], qs[2], scale, starts,
+            tuple(s or 0 for s in strides))
+    return _Plan(*args, 0), copy, args
+
+
+@functools.lru_cache(maxsize=512)
+def _bwd_plan(args, do_stride):
+    return _Plan(*args, do_stride)
+
+
+def _take(t, copy):
+    # tensors off a 16-byte boundary are copied too
+    if copy or t.data_ptr() % 16:
+        return t.clone(memory_format=torch.contiguous_format)
+    return t
+
+
+def _stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _forward(q, k, v, cu, bias, scale, starts, keep):
+    devices = (q.device, k.device, v.device, cu.device)
+    types = (q.dtype, k.dtype, v.dtype, cu.dtype)
+    if bias is not None:
+        devices, types = devices + (bias.device,), types + (bias.dtype,)
+    plan, copy, args = _plan(q.shape, k.shape, v.shape, q.stride(), k.stride(), v.stride(), types,
+                             devices, cu.shape, None if bias is None else bias.shape, scale, starts)
+    with torch.cuda.device(devices[0]):
+        q, k, v = _take(q, copy[0]), _take(k, copy[1]), _take(v, copy[2])
+        if any(copy):  # copies are packed
+            args = args[:7] + (tuple(0 if c else s for c, s in zip(copy, args[7])),)
+        if cu.dtype != torch.int32:
+            cu = cu.to(torch.int32)
+        cu = cu.contiguous()
+        if bias is not None:
+            bias = bias.contiguous()
+        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        lse = o_res = saved = None
+        if keep:
+            saved = torch.empty(plan.saved, dtype=torch.uint8, device=q.device)
+            lse = saved.data_ptr()
+            o_res = lse + plan.o_res_at
+        _raise_on(plan.fwd(plan.ref, cu.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                           None if bias is None else bias.data_ptr(), o.data_ptr(), o_res, lse,
+                           _stream(devices[0])), "msa_dense_fwd")
+    return o, saved, (q, k, v, cu, bias), args
 
 
 class DenseFunction(torch.autograd.Function):
@@ -63,67 +142,34 @@ class DenseFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, cu_seqlens, bias, softmax_scale: float, starts: tuple):
-        o, lse, saved, args = _forward(q, k, v, cu_seqlens, bias, softmax_scale, starts,
-                                       any(ctx.needs_input_grad))
-        ctx.args = args
-        ctx.save_for_backward(*saved, o, lse)
+        o, saved, tensors, ctx.args = _forward(q, k, v, cu_seqlens, bias, softmax_scale, starts,
+                                               True)
+        ctx.save_for_backward(*tensors, o, saved)
         return o
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, d_o):
-        q, k, v, cu, bias, o, lse = ctx.saved_tensors
-        with torch.cuda.device(q.device):
+        q, k, v, cu, bias, o, saved = ctx.saved_tensors
+        device = q.device
+        with torch.cuda.device(device):
             if d_o.dtype != torch.bfloat16:
                 d_o = d_o.to(torch.bfloat16)
-            d_o = _rows(d_o)
-            prm, nbytes = _params(*ctx.args, d_o.stride(0) if d_o.shape[0] > 1 else 0)
-            dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device)
-                          for t in (q, k, v))
+            stride = _stride_of(d_o.shape, d_o.stride())
+            d_o = _take(d_o, stride is None)
+            plan = _bwd_plan(ctx.args, stride or 0)
+            dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=device) for t in (q, k, v))
             dbias = torch.empty_like(bias) if bias is not None else None
             # its own workspace per call: calls on other streams, and other graphs, share none
-            msa_dense_bwd(prm, cu, q, k, v, bias, o, lse, d_o, dq, dk, dv, dbias,
-                          workspace(nbytes, q.device))
+            ws = torch.empty(plan.workspace, dtype=torch.uint8, device=device)
+            lse = saved.data_ptr()
+            _raise_on(plan.bwd(plan.ref, cu.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                               None if bias is None else bias.data_ptr(), o.data_ptr(),
+                               lse + plan.o_res_at, lse, d_o.data_ptr(), dq.data_ptr(),
+                               dk.data_ptr(), dv.data_ptr(),
+                               None if bias is None else dbias.data_ptr(), ws.data_ptr(),
+                               plan.workspace, _stream(device)), "msa_dense_bwd")
         return dq, dk, dv, None, dbias, None, None
-
-
-def _forward(q, k, v, cu_seqlens, bias, softmax_scale, starts, keep):
-    T, hq, d = q.shape
-    with torch.cuda.device(q.device):
-        q, k, v = _rows(q), _rows(k), _rows(v)
-        cu = cu_seqlens
-        if cu.dtype != torch.int32 or not cu.is_contiguous():
-            cu = cu.to(torch.int32).contiguous()
-        if bias is not None:
-            bias = bias.contiguous()
-        strides = [t.stride(0) if T > 1 else 0 for t in (q, k, v)]  # one token: no stride
-        args = (T, cu.numel() - 1, hq, k.shape[1], d, softmax_scale, starts, *strides)
-        prm, _ = _params(*args)
-        o = torch.empty((T, hq, d), dtype=q.dtype, device=q.device)
-        lse = torch.empty((T, hq), dtype=torch.float32, device=q.device) if keep else None
-        msa_dense_fwd(prm, cu, q, k, v, bias, o, lse)
-    return o, lse, (q, k, v, cu, bias), args
-
-
-def _check(q, k, v, cu_seqlens, bias, starts):
-    for t in (q, k, v):
-        if t.dtype != torch.bfloat16 or not t.is_cuda:
-            raise TypeError("q, k, v must be bf16 CUDA tensors")
-        if t.dim() != 3 or t.device != q.device:
-            raise ValueError("q, k, v must be [tokens, heads, d] on one device")
-    if k.shape != v.shape or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
-        raise ValueError("q [T, Hq, d] and k, v [T, Hkv, d] expected")
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 or cu_seqlens.device != q.device:
-        raise ValueError("cu_seqlens must be [num_docs + 1] on the device of q")
-    if cu_seqlens.dtype not in (torch.int32, torch.int64):
-        raise TypeError("cu_seqlens must be integers")
-    if (bias is None) != (not starts):
-        raise ValueError("bias and bucket_starts go together")
-    if bias is not None:
-        if bias.dtype != torch.bfloat16 or bias.device != q.device:
-            raise TypeError("bias must be a bf16 tensor on the device of q")
-        if tuple(bias.shape) != (q.shape[1], len(starts)):
-            raise ValueError("bias must be [Hq, number of buckets]")
 
 
 def dense_attention(q, k, v, cu_seqlens, softmax_scale: float = 1.0, bias=None,
@@ -134,8 +180,7 @@ def dense_attention(q, k, v, cu_seqlens, softmax_scale: float = 1.0, bias=None,
     the last bucket whose first distance, `bucket_starts[b]`, is at most i - j.
     bucket_starts begins with 0 and increases strictly (`log_buckets` makes one).
     Malformed cu_seqlens are found on the device (`msa_get_device_status`)."""
-    starts = tuple(bucket_starts) if bucket_starts is not None else ()
-    _check(q, k, v, cu_seqlens, bias, starts)
+    starts = () if bucket_starts is None else tuple(bucket_starts)
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad
                                     or (bias is not None and bias.requires_grad)):
         return DenseFunction.apply(q, k, v, cu_seqlens, bias, float(softmax_scale), starts)

@@ -278,11 +278,13 @@ typedef struct msa_dense_params {
   uint32_t flags;      /* must be 0 */
 } msa_dense_params;
 
-/* Inputs: cu_seqlens, q, k, v, bias (null without one).  Outputs: o, and lse,
-   which msa_dense_bwd needs (null: not stored). */
+/* Inputs: cu_seqlens, q, k, v, bias (null without one).  Outputs: o, and what
+   msa_dense_bwd needs: o_res [T, hq, d], the bf16 rounding residual of o (as
+   msa_fwd's), and lse (each null: not stored). */
 msa_status msa_dense_fwd(const msa_dense_params* params, const int32_t* cu_seqlens,
                          const uint16_t* q, const uint16_t* k, const uint16_t* v,
-                         const uint16_t* bias, uint16_t* o, float* lse, msa_stream_t stream);
+                         const uint16_t* bias, uint16_t* o, uint16_t* o_res, float* lse,
+                         msa_stream_t stream);
 
 /* Workspace bytes of msa_dense_bwd (0 if params are invalid). */
 size_t msa_dense_bwd_workspace_size(const msa_dense_params* params);
@@ -291,10 +293,10 @@ size_t msa_dense_bwd_workspace_size(const msa_dense_params* params);
    Outputs (overwritten): dq, dk, dv and, with a bias, dbias. */
 msa_status msa_dense_bwd(const msa_dense_params* params, const int32_t* cu_seqlens,
                          const uint16_t* q, const uint16_t* k, const uint16_t* v,
-                         const uint16_t* bias, const uint16_t* o, const float* lse,
-                         const uint16_t* dO, uint16_t* dq, uint16_t* dk, uint16_t* dv,
-                         uint16_t* dbias, void* workspace, size_t workspace_bytes,
-                         msa_stream_t stream);
+                         const uint16_t* bias, const uint16_t* o, const uint16_t* o_res,
+                         const float* lse, const uint16_t* dO, uint16_t* dq, uint16_t* dk,
+                         uint16_t* dv, uint16_t* dbias, void* workspace,
+                         size_t workspace_bytes, msa_stream_t stream);
 
 /*
  * Synchronises `stream`, returns the device status word of the current device

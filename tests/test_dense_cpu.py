@@ -112,7 +112,7 @@ def test_parameters_refused_on_the_host(m, change):
     assert m.msa_dense_bwd_workspace_size(good) > 0
     assert m.msa_dense_bwd_workspace_size(bad) == 0
     p = [ctypes.c_void_p(0x1000)] * 8
-    assert m.load().msa_dense_fwd(ctypes.byref(bad), *p[:7], None) in (1, 2)
+    assert m.load().msa_dense_fwd(ctypes.byref(bad), *p, None) in (1, 2)
 
 
 def test_pointers_and_workspace_refused_on_the_host(m):
@@ -122,26 +122,26 @@ def test_pointers_and_workspace_refused_on_the_host(m):
     need = m.msa_dense_bwd_workspace_size(good)
 
     def fwd(prm, i=None, to=0):
-        p = [0x1000] * 7
+        p = [0x1000] * 8
         if i is not None:
             p[i] = to
         return lib.msa_dense_fwd(ctypes.byref(prm), *map(at, p), None)
 
     def bwd(prm, i=None, to=0, size=need):
-        p = [0x1000] * 13
+        p = [0x1000] * 14
         if i is not None:
             p[i] = to
         return lib.msa_dense_bwd(ctypes.byref(prm), *map(at, p), size, None)
 
     for i in (0, 1, 2, 3, 5):  # cu, q, k, v, o
         assert fwd(good, i) == 1
-    for i in (1, 2, 3, 5, 6):  # lse too: misaligned
+    for i in (1, 2, 3, 5, 6, 7):  # o_res and lse too: misaligned
         assert fwd(good, i, 0x1008) == 1
     assert fwd(table, 4) == 1 and fwd(table, 4, 0x1001) == 1
-    for i in (0, 1, 2, 3, 5, 6, 7, 8, 9, 10, 12):
+    for i in (0, 1, 2, 3, 5, 6, 7, 8, 9, 10, 11, 13):
         assert bwd(good, i) == 1
-    assert bwd(table, 4) == 1 and bwd(table, 11) == 1
-    assert bwd(good, 12, 0x1010) == 1
+    assert bwd(table, 4) == 1 and bwd(table, 12) == 1
+    assert bwd(good, 13, 0x1010) == 1
     assert bwd(good, size=need - 1) == 3
     empty = m.make_dense_params(**{**OK, "total_tokens": 0})
     assert fwd(empty) == 0 and bwd(empty) == 0

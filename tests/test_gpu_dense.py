@@ -112,7 +112,7 @@ def test_masking_bias(masked):
     t = sum(lens)
     o, lse = torch.empty_like(x["q"]), torch.empty(t, 4, device="cuda")
     msa_dense_fwd(make_dense_params(t, 3, 4, 2, 64, 1.0, starts), x["cu"], x["q"], x["k"], x["v"],
-                  x["bias"], o, lse)
+                  x["bias"], o, None, lse)
     assert torch.isneginf(lse[firsts][:, heads]).all()
     ref, err = dense_reference(x["q"], x["k"], x["v"], lens, 1.0, x["bias"], starts)
     check({"lse": lse}, ref, err, ["lse"])
