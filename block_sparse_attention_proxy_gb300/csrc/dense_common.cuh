@@ -39,6 +39,7 @@ struct DenseArgs {
   // starts[b] <= i - j < starts[b + 1]
   const uint16_t* bias;
   int nb;
+  int lut_w, lut_stride;  // bias by distance in shared memory (DenseBias): distances, row length
   int starts[kDenseMaxBuckets];
   // forward outputs; in the backward o, o_res and lse are inputs
   uint16_t* o;
@@ -263,6 +264,57 @@ __device__ __forceinline__ void mma_tile_ss(uint32_t el, uint32_t d, uint32_t a_
 __device__ __forceinline__ float dense_bias_log2(uint16_t raw) {
   const float b = __uint_as_float((uint32_t)raw << 16);
   return b < -FLT_MAX ? b : fmaxf(b * kLog2E, -FLT_MAX);
+}
+
+// What a CTA keeps of the bias table in shared memory.  Tiles whose rows each lie in
+// one bucket (most tiles far from the diagonal) take it as one constant per row.  Near
+// the diagonal a row crosses many buckets: there the bias is read by distance
+// from `lut` (one conflict-free load per score, no search and no branch), which
+// holds the distances below lut_w for every head of the group, preceded by zeros
+// for the negative distances of masked scores.  Rows that cross a bucket farther
+// out walk the bucket starts, 16 scores at a time where none begins.
+constexpr int kDenseLut = 4096;       // entries over all heads of the group
+constexpr int kDenseBits = 8192;      // distances whose bucket starts are kept as bits
+constexpr int kDenseBitsPad = 256;    // bits before distance 0
+struct DenseBias {
+  float lut[kDenseLut];
+  uint32_t bits[(kDenseBits + kDenseBitsPad) / 32 + 2];
+  int starts[kDenseMaxBuckets];
+};
+// Row length of the table (heads end on different banks: a warp reads 32/G tokens of G
+// heads at once) and the distances that fit.
+__host__ inline void dense_lut_shape(DenseArgs* a) {
+  const int per = kDenseLut / a->G;
+  a->lut_stride = a->G <= 32 ? (per - 32) / 32 * 32 + 32 / a->G : per;
+  const int w = a->lut_stride - (127 + a->tpt), last = a->nb > 0 ? a->starts[a->nb - 1] : 0;
+  a->lut_w = w < 0 ? 0 : w;
+  if (a->lut_w > last + 1) a->lut_w = last + 1;  // one bucket from there on
+}
+__device__ __forceinline__ int dense_lut_pad(const DenseArgs& a) { return 127 + a.tpt; }
+
+// Fills it (all threads of the CTA; the caller synchronises behind it): distances up to
+// `most` can occur.  BITS: the bucket starts as bits too (with a barrier inside).
+template <bool BITS>
+__device__ __forceinline__ void dense_bias_fill(const DenseArgs& a, DenseBias* s, int g, int most) {
+  const int tid = threadIdx.x, nt = blockDim.x, pad = dense_lut_pad(a);
+  const uint16_t* tab = a.bias + (size_t)g * a.G * a.nb;
+  if (a.lut_w > 0) {
+    for (int x = tid; x < pad; x += nt)
+      for (int h = 0; h < a.G; ++h) s->lut[h * a.lut_stride + x] = 0.f;
+    int b = 0;
+    for (int x = tid; x < min(a.lut_w, most + 1); x += nt) {
+      while (b + 1 < a.nb && a.starts[b + 1] <= x) ++b;
+      for (int h = 0; h < a.G; ++h)
+        s->lut[h * a.lut_stride + pad + x] = dense_bias_log2(__ldg(tab + h * a.nb + b));
+    }
+  }
+  if (tid < a.nb) s->starts[tid] = a.starts[tid];
+  if (BITS) {
+    for (int x = tid; x < (kDenseBits + kDenseBitsPad) / 32 + 2; x += nt) s->bits[x] = 0;
+    __syncthreads();
+    if (tid > 0 && tid < a.nb && a.starts[tid] < kDenseBits)
+      atomicOr(&s->bits[(a.starts[tid] + kDenseBitsPad) >> 5], 1u << (a.starts[tid] & 31));
+  }
 }
 
 // Zeroes rows [first, 128) of a 128-row bf16 tile of D columns in shared memory

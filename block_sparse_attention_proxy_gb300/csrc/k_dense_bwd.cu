@@ -36,11 +36,13 @@ __device__ __forceinline__ void store_tmem_rows(uint32_t taddr, float f, uint8_t
 // while the softmax warps turn S(n), dP(n) into dS(n) (bf16, over S(n)'s
 // columns), S(n + 1) is computed, and dP(n + 1) as soon as dP(n) has been read.
 // ---------------------------------------------------------------------------
-template <int D>
+template <int D, bool BIAS>
 struct DqCfg {
   static constexpr int kTile = 128 * D * 2;
-  static constexpr int kNK = D == 128 ? 3 : 5, kNV = D == 128 ? 2 : 4;  // K and V rings
-  static constexpr int kSmem = (2 + kNK + kNV) * kTile + 256;
+  // K and V rings; with a bias its tables take the place of a tile
+  static constexpr int kNK = D == 128 ? 3 : 5, kNV = D == 128 ? (BIAS ? 1 : 2) : 4;
+  static constexpr int kSmem =
+      (2 + kNK + kNV) * kTile + 256 + 512 + (BIAS ? (int)sizeof(DenseBias) : 0);
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 
@@ -49,7 +51,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_dense_dq(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                const __grid_constant__ DenseArgs a) {
-  using C = DqCfg<D>;
+  using C = DqCfg<D, BIAS>;
   constexpr int NCH = D / 64, NK = C::kNK, NV = C::kNV;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;  // after the last S also the staging of dQ
@@ -63,6 +65,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + B_END + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   static_assert((B_END + 1) * 8 + 8 <= 256, "barrier block");
+  float* sD = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 256);  // [128] D
+  DenseBias* sB = reinterpret_cast<DenseBias*>(sD + 128);
   auto bar = [&](int i) { return smem_u32(bars + i); };
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
@@ -105,6 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(tslot), 512);
     tmem_relinquish();
   }
+  if (BIAS) dense_bias_fill<true>(a, sB, g, min(q0 + a.tpt, it.len) - 1);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -208,27 +213,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int qi = q0 + ti;
     const bool valid = ti < a.tpt && qi < it.len;
     const size_t row = (size_t)(it.start + qi) * a.hq + g * a.G + hl;
-    // D and -lse of the row (both warpgroups; the first also leaves them for dK, dV)
+    // D of 16 rows per warp: D/8 lanes read a row's o, o_res and dO, 16 bytes each
+    {
+      constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes per row, rows per step
+      const int r0 = (warp & 3) * 32 + 16 * w, part_ = lane % LPR;
+      float s[16 / RPI];
+#pragma unroll
+      for (int u = 0; u < 16 / RPI; ++u) {
+        const int rr = r0 + u * RPI + lane / LPR, tok = rr / a.G, hh = g * a.G + rr % a.G;
+        s[u] = 0.f;
+        if (tok < a.tpt && q0 + tok < it.len) {
+          const size_t t = (size_t)(it.start + q0 + tok);
+          const size_t at = (t * a.hq + hh) * D + part_ * 8;
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.o + at));
+          const uint4 z = __ldg(reinterpret_cast<const uint4*>(a.o_res + at));
+          const uint4 y = __ldg(reinterpret_cast<const uint4*>(
+              a.d_o + t * a.do_stride + (size_t)hh * D + part_ * 8));
+          auto dot = [](uint32_t o, uint32_t res, uint32_t d_o) {
+            return (bf16_lo(o) + bf16_lo(res)) * bf16_lo(d_o) +
+                   (bf16_hi(o) + bf16_hi(res)) * bf16_hi(d_o);
+          };
+          s[u] = (dot(x.x, z.x, y.x) + dot(x.y, z.y, y.y)) +
+                 (dot(x.z, z.z, y.z) + dot(x.w, z.w, y.w));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 16 / RPI; ++u) {
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
+        if (part_ == 0) sD[r0 + u * RPI + lane / LPR] = s[u];
+      }
+      named_bar_sync(1, 256);
+    }
+    // -lse and D of the row (both warpgroups; the first also leaves them for dK, dV)
     float nl = -INFINITY, dsum = 0.f;
     if (valid) {
-      const uint4* po = reinterpret_cast<const uint4*>(a.o + row * D);
-      const uint4* pd = reinterpret_cast<const uint4*>(
-          a.d_o + (size_t)(it.start + qi) * a.do_stride + (size_t)(g * a.G + hl) * D);
-      const uint4* pr = reinterpret_cast<const uint4*>(a.o_res + row * D);
-      float s4[4] = {0.f, 0.f, 0.f, 0.f};
-      auto dot = [](uint32_t o, uint32_t res, uint32_t d_o) {
-        return (bf16_lo(o) + bf16_lo(res)) * bf16_lo(d_o) +
-               (bf16_hi(o) + bf16_hi(res)) * bf16_hi(d_o);
-      };
-#pragma unroll 4
-      for (int u = 0; u < D / 8; ++u) {
-        const uint4 x = __ldg(po + u), z = __ldg(pr + u), y = __ldg(pd + u);
-        s4[0] += dot(x.x, z.x, y.x);
-        s4[1] += dot(x.y, z.y, y.y);
-        s4[2] += dot(x.z, z.z, y.z);
-        s4[3] += dot(x.w, z.w, y.w);
-      }
-      dsum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+      dsum = sD[r];
       const float lse = __ldg(a.lse + row);
       nl = lse == -INFINITY ? -INFINITY : -lse * kLog2E;
       if (w == 0)
@@ -260,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32x2(tl + 128 * b + 64 * w, tl + 128 * b + 64 * w + 32, x[0], x[1]);
         if (BIAS) {
           int nb_ = bk;
-          while (nb_ > 0 && a.starts[nb_] > rel) --nb_;
+          while (nb_ > 0 && sB->starts[nb_] > rel) --nb_;
           if (nb_ != bk) {
             my[bk * 256] = acc;
             acc = 0.f;
@@ -269,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // P = 2^(S scale log2(e) + bias - lse)
         bool one = true;
-        if (BIAS) one = __all_sync(0xffffffffu, bk == 0 || a.starts[bk] <= rel - 63);
+        if (BIAS) one = __all_sync(0xffffffffu, bk == 0 || sB->starts[bk] <= rel - 63);
         if (one) {
           const float sub = nl + (BIAS ? dense_bias_log2(__ldg(tab + bk)) : 0.f);
 #pragma unroll
@@ -277,18 +297,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             x[i >> 5][i & 31] = __float_as_uint(
                 ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), a.scale_log2, sub)));
         } else {
-          int q = bk;
-          int st = q > 0 ? a.starts[q] : INT_MIN;
-          float sub = nl + dense_bias_log2(__ldg(tab + q));
+          if (__all_sync(0xffffffffu, rel < a.lut_w)) {
+            const float* lut = sB->lut + hl * a.lut_stride + dense_lut_pad(a) + rel;
 #pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            if (rel - i < st) {
-              --q;
-              st = q > 0 ? a.starts[q] : INT_MIN;
-              sub = nl + dense_bias_log2(__ldg(tab + q));
+            for (int i = 0; i < 64; ++i)
+              x[i >> 5][i & 31] = __float_as_uint(ex2_approx(
+                  fmaf(__uint_as_float(x[i >> 5][i & 31]), a.scale_log2, nl + lut[-i])));
+          } else {
+            int q = bk;
+            int st = q > 0 ? sB->starts[q] : INT_MIN;
+            float sub = nl + dense_bias_log2(__ldg(tab + q));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const bool cross = __any_sync(0xffffffffu, rel - 16 * u - 15 < st);
+#pragma unroll
+              for (int i = 16 * u; i < 16 * u + 16; ++i) {
+                if (cross && rel - i < st) {
+                  --q;
+                  st = q > 0 ? sB->starts[q] : INT_MIN;
+                  sub = nl + dense_bias_log2(__ldg(tab + q));
+                }
+                x[i >> 5][i & 31] = __float_as_uint(
+                    ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), a.scale_log2, sub)));
+              }
             }
-            x[i >> 5][i & 31] = __float_as_uint(
-                ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), a.scale_log2, sub)));
           }
           __syncwarp();
         }
@@ -316,17 +348,42 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < 64; ++i) s4[i & 3] += __uint_as_float(x[i >> 5][i & 31]);
               acc += (s4[0] + s4[1]) + (s4[2] + s4[3]);
             } else {
-              int st = bk > 0 ? a.starts[bk] : INT_MIN;
-#pragma unroll
-              for (int i = 0; i < 64; ++i) {
-                if (rel - i < st) {
-                  my[bk * 256] = acc;
-                  acc = 0.f;
-                  --bk;
-                  st = bk > 0 ? a.starts[bk] : INT_MIN;
+              // bit i of `last`: score i is the last of its bucket in this row
+              uint32_t last[2];
+              if (rel < kDenseBits) {
+                const int p = rel - 63 + kDenseBitsPad;
+                const uint32_t* b = sB->bits + (p >> 5);
+                last[1] = __brev(__funnelshift_r(b[0], b[1], p & 31));
+                last[0] = __brev(__funnelshift_r(b[1], b[2], p & 31));
+              } else {
+                last[0] = last[1] = 0;
+                for (int q = bk; q > 0 && sB->starts[q] >= rel - 63; --q) {
+                  const int i = rel - sB->starts[q];
+                  last[i >> 5] |= 1u << (i & 31);
                 }
-                acc += __uint_as_float(x[i >> 5][i & 31]);
               }
+              float* to = my + bk * 256;
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                if (__any_sync(0xffffffffu, (last[u >> 1] >> (16 * (u & 1))) & 0xffffu)) {
+#pragma unroll
+                  for (int i = 16 * u; i < 16 * u + 16; ++i) {
+                    acc += __uint_as_float(x[i >> 5][i & 31]);
+                    if (last[u >> 1] & (1u << (i & 31))) {
+                      *to = acc;
+                      to -= 256;
+                      acc = 0.f;
+                    }
+                  }
+                } else {
+                  float s2[2] = {0.f, 0.f};
+#pragma unroll
+                  for (int i = 16 * u; i < 16 * u + 16; ++i)
+                    s2[i & 1] += __uint_as_float(x[i >> 5][i & 31]);
+                  acc += s2[0] + s2[1];
+                }
+              }
+              bk -= __popc(last[0]) + __popc(last[1]);
               __syncwarp();  // the TMEM store below is warp-collective
             }
           }
@@ -391,12 +448,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Warps 0-3 and 4-7 take 64 of a tile's 128 queries each; warp 8 loads, warp 9
 // issues the MMAs, warp 10 brings the rows' {-lse, D}.
 // ---------------------------------------------------------------------------
-template <int D>
+template <int D, bool BIAS>
 struct DkvCfg {
   static constexpr int kTile = 128 * D * 2;
-  static constexpr int kNQ = D == 128 ? 3 : 4, kNO = D == 128 ? 2 : 4;  // Q and dO rings
+  // with a bias its tables take the place of a tile
+  static constexpr int kNQ = D == 128 ? (BIAS ? 2 : 3) : 4, kNO = D == 128 ? 2 : 4;  // Q and dO rings
   static constexpr int kNS = 2;                                           // statistics ring
-  static constexpr int kSmem = (2 + kNQ + kNO) * kTile + kNS * 1024 + 256;
+  static constexpr int kSmem =
+      (2 + kNQ + kNO) * kTile + kNS * 1024 + 256 + (BIAS ? (int)sizeof(DenseBias) : 0);
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 
@@ -406,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const __grid_constant__ CUtensorMap tm_do,
                 const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                 const __grid_constant__ DenseArgs a) {
-  using C = DkvCfg<D>;
+  using C = DkvCfg<D, BIAS>;
   constexpr int NCH = D / 64, NQ = C::kNQ, NO = C::kNO, NS = C::kNS;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sK = smem;
@@ -421,6 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + B_END + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   static_assert((B_END + 1) * 8 + 8 <= 256, "barrier block");
+  DenseBias* sB = reinterpret_cast<DenseBias*>(reinterpret_cast<uint8_t*>(bars) + 256);
   auto bar = [&](int i) { return smem_u32(bars + i); };
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
@@ -458,6 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(tslot), 512);
     tmem_relinquish();
   }
+  if (BIAS) dense_bias_fill<false>(a, sB, g, nq * 128 - 1);  // the padded last tile included
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -607,8 +668,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint16_t* tab = a.bias + (size_t)(g * a.G + hl) * a.nb;
         if (BIAS) {
           if (qt == 0) bk = 0;
-          while (bk + 1 < a.nb && a.starts[bk + 1] <= rel) ++bk;
-          one = __all_sync(0xffffffffu, bk + 1 == a.nb || a.starts[bk + 1] > rel + 63);
+          while (bk + 1 < a.nb && sB->starts[bk + 1] <= rel) ++bk;
+          one = __all_sync(0xffffffffu, bk + 1 == a.nb || sB->starts[bk + 1] > rel + 63);
         }
         if (one) {
           const float bv = BIAS ? dense_bias_log2(__ldg(tab + bk)) : 0.f;
@@ -622,19 +683,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fmaf(__uint_as_float(x[e >> 5][(e & 31) + 1]), c, BIAS ? v.z + bv : v.z)));
           }
         } else {
-          int q = bk;
-          int nx = q + 1 < a.nb ? a.starts[q + 1] : INT_MAX;
-          float bv = dense_bias_log2(__ldg(tab + q));
+          const float2* sl = sSt + s * 128 + 64 * w;
+          if (__all_sync(0xffffffffu, rel + 63 < a.lut_w)) {
+            const float* lut = sB->lut + hl * a.lut_stride + dense_lut_pad(a) + rel;
 #pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            if (rel + i >= nx) {
-              ++q;
-              nx = q + 1 < a.nb ? a.starts[q + 1] : INT_MAX;
-              bv = dense_bias_log2(__ldg(tab + q));
+            for (int i = 0; i < 64; ++i)
+              x[i >> 5][i & 31] = __float_as_uint(
+                  ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), c, sl[i].x + lut[i])));
+          } else {
+            int q = bk;
+            int nx = q + 1 < a.nb ? sB->starts[q + 1] : INT_MAX;
+            float bv = dense_bias_log2(__ldg(tab + q));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const bool cross = __any_sync(0xffffffffu, rel + 16 * u + 15 >= nx);
+#pragma unroll
+              for (int i = 16 * u; i < 16 * u + 16; ++i) {
+                if (cross && rel + i >= nx) {
+                  ++q;
+                  nx = q + 1 < a.nb ? sB->starts[q + 1] : INT_MAX;
+                  bv = dense_bias_log2(__ldg(tab + q));
+                }
+                x[i >> 5][i & 31] = __float_as_uint(
+                    ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), c, sl[i].x + bv)));
+              }
             }
-            const float nl = sSt[s * 128 + 64 * w + i].x;
-            x[i >> 5][i & 31] = __float_as_uint(
-                ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), c, nl + bv)));
           }
           __syncwarp();  // the TMEM store below is warp-collective
         }
@@ -730,16 +803,16 @@ template <int D, bool BIAS>
 cudaError_t launch_t(const CUtensorMap& mqp, const CUtensorMap& mop, const CUtensorMap& mk,
                      const CUtensorMap& mv, const CUtensorMap& mq, const CUtensorMap& mo,
                      DenseArgs a, cudaStream_t st) {
-  cudaError_t e = dense_prepare<k_dense_dq<D, BIAS>>(kThreads, kBudget, DqCfg<D>::kSmem);
+  cudaError_t e = dense_prepare<k_dense_dq<D, BIAS>>(kThreads, kBudget, DqCfg<D, BIAS>::kSmem);
   if (e != cudaSuccess) return e;
-  e = dense_prepare<k_dense_dkv<D, BIAS>>(kThreads, kBudget, DkvCfg<D>::kSmem);
+  e = dense_prepare<k_dense_dkv<D, BIAS>>(kThreads, kBudget, DkvCfg<D, BIAS>::kSmem);
   if (e != cudaSuccess) return e;
   a.nslots = dense_slots(a.T, a.ndoc, a.tpt);
-  k_dense_dq<D, BIAS><<<(unsigned)a.nslots * a.hkv, kThreads, DqCfg<D>::kSmem, st>>>(mqp, mop, mk,
+  k_dense_dq<D, BIAS><<<(unsigned)a.nslots * a.hkv, kThreads, DqCfg<D, BIAS>::kSmem, st>>>(mqp, mop, mk,
                                                                                      mv, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   a.nslots = dense_slots(a.T, a.ndoc, 128);
-  k_dense_dkv<D, BIAS><<<(unsigned)a.nslots * a.hkv, kThreads, DkvCfg<D>::kSmem, st>>>(mq, mo, mk, mv, a);
+  k_dense_dkv<D, BIAS><<<(unsigned)a.nslots * a.hkv, kThreads, DkvCfg<D, BIAS>::kSmem, st>>>(mq, mo, mk, mv, a);
   return cudaGetLastError();
 }
 

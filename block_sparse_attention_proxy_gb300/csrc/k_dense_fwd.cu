@@ -29,11 +29,12 @@ constexpr int kThreads = 384;
 constexpr uint32_t kRegsSoftmax = 200, kRegsCtl = 104;
 constexpr float kRescale = 8.f;  // log2 growth of a row's maximum that moves m
 
-template <int D>
+template <int D, bool BIAS>
 struct FwdCfg {
   static constexpr int kTile = 128 * D * 2;
-  static constexpr int kRing = D == 128 ? 5 : 8;  // K and V tiles in flight
-  static constexpr int kSmem = (2 + kRing) * kTile + 256;
+  // K and V tiles in flight; with a bias its tables take the place of one
+  static constexpr int kRing = D == 128 ? (BIAS ? 4 : 5) : 8;
+  static constexpr int kSmem = (2 + kRing) * kTile + 256 + (BIAS ? (int)sizeof(DenseBias) : 0);
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 
@@ -41,7 +42,7 @@ template <int D, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
     k_dense_fwd(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ DenseArgs a) {
-  using C = FwdCfg<D>;
+  using C = FwdCfg<D, BIAS>;
   constexpr int NCH = D / 64, NR = C::kRing;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;  // [2]; after the last S also the staging of O
@@ -52,6 +53,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + B_END + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   static_assert((B_END + 1) * 8 + 8 <= 256, "barrier block");
+  DenseBias* sB = reinterpret_cast<DenseBias*>(reinterpret_cast<uint8_t*>(bars) + 256);
   auto bar = [&](int i) { return smem_u32(bars + i); };
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
@@ -102,6 +104,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(tslot), 512);
     tmem_relinquish();
   }
+  if (BIAS) dense_bias_fill<false>(a, sB, g, min(q0 + tpc, it.len) - 1);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -232,26 +235,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         // P = 2^(x mul + add - m)
         float mul = c, add = 0.f;
         if (BIAS) {
-          while (bk > 0 && a.starts[bk] > rel) --bk;
-          const bool one = bk == 0 || a.starts[bk] <= rel - 127;
+          while (bk > 0 && sB->starts[bk] > rel) --bk;
+          const bool one = bk == 0 || sB->starts[bk] <= rel - 127;
           if (__all_sync(0xffffffffu, one)) {
             add = dense_bias_log2(__ldg(tab + bk));  // one bucket over the row's part of the tile
           } else {
-            int b = bk;
-            int st = b > 0 ? a.starts[b] : INT_MIN;
-            float bv = dense_bias_log2(__ldg(tab + b));
+            mul = 1.f;
+            if (__all_sync(0xffffffffu, rel < a.lut_w)) {
+              const float* lut = sB->lut + hl * a.lut_stride + dense_lut_pad(a) + rel;
 #pragma unroll
-            for (int i = 0; i < 128; ++i) {
-              if (rel - i < st) {
-                --b;
-                st = b > 0 ? a.starts[b] : INT_MIN;
-                bv = dense_bias_log2(__ldg(tab + b));
+              for (int i = 0; i < 128; ++i)
+                x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, lut[-i]));
+            } else {
+              int b = bk;
+              int st = b > 0 ? sB->starts[b] : INT_MIN;
+              float bv = dense_bias_log2(__ldg(tab + b));
+#pragma unroll
+              for (int u = 0; u < 8; ++u) {
+                if (__any_sync(0xffffffffu, rel - 16 * u - 15 < st)) {
+#pragma unroll
+                  for (int i = 16 * u; i < 16 * u + 16; ++i) {
+                    if (rel - i < st) {
+                      --b;
+                      st = b > 0 ? sB->starts[b] : INT_MIN;
+                      bv = dense_bias_log2(__ldg(tab + b));
+                    }
+                    x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, bv));
+                  }
+                } else {
+#pragma unroll
+                  for (int i = 16 * u; i < 16 * u + 16; ++i)
+                    x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, bv));
+                }
               }
-              x[i] =
-                  __float_as_uint(fmaf(__uint_as_float(x[i]), c, bv));
             }
             __syncwarp();
-            mul = 1.f;
           }
         }
         float m4[4];
@@ -364,9 +382,9 @@ cudaError_t launch_t(const DenseArgs& a, const CUtensorMap& mq, const CUtensorMa
                      const CUtensorMap& mv, cudaStream_t st) {
   constexpr int kBudget = 2 * 128 * kRegsSoftmax + 128 * kRegsCtl;
   static_assert(kBudget <= 65536, "register budgets exceed the register file");
-  cudaError_t e = dense_prepare<k_dense_fwd<D, BIAS>>(kThreads, kBudget, FwdCfg<D>::kSmem);
+  cudaError_t e = dense_prepare<k_dense_fwd<D, BIAS>>(kThreads, kBudget, FwdCfg<D, BIAS>::kSmem);
   if (e != cudaSuccess) return e;
-  k_dense_fwd<D, BIAS><<<(unsigned)a.nslots * a.hkv, kThreads, FwdCfg<D>::kSmem, st>>>(mq, mk, mv,
+  k_dense_fwd<D, BIAS><<<(unsigned)a.nslots * a.hkv, kThreads, FwdCfg<D, BIAS>::kSmem, st>>>(mq, mk, mv,
                                                                                        a);
   return cudaGetLastError();
 }

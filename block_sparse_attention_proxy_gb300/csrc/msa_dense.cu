@@ -47,6 +47,7 @@ msa_status check_dense(const msa_dense_params* p, DenseShape* s, DenseArgs* a) {
   a->G = p->hq / p->hkv;
   a->tpt = 128 / a->G;
   a->nb = p->num_buckets;
+  dense_lut_shape(a);
   a->scale = p->softmax_scale;
   a->scale_log2 = p->softmax_scale * kLog2E;
   // CTAs of the largest grid (one per slot and KV head)
