@@ -317,6 +317,17 @@ __device__ __forceinline__ void dense_bias_fill(const DenseArgs& a, DenseBias* s
   }
 }
 
+// The bucket of distance x among 0..hi (0 for a negative one): the last one that begins
+// at or before x.
+__device__ __forceinline__ int dense_bucket(const DenseBias* s, int hi, int x) {
+  int lo = 0;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s->starts[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
 // Zeroes rows [first, 128) of a 128-row bf16 tile of D columns in shared memory
 // (64-column chunks of 16 KB) and makes that visible to the tensor core.  One
 // warp.  The rows behind a document's end belong to the next one; as rows of

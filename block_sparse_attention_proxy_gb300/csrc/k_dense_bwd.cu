@@ -274,52 +274,70 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       wait_site(kKerDenseDq, bb, n));
         tc_fence_after();
       };
+      bool one = true, near = false;  // see DenseBias
+      float bias0 = 0.f;
+      if (BIAS) {
+        const int first = dense_bucket(sB, bk, rel);
+        if (first != bk) {
+          my[bk * 256] = acc;
+          acc = 0.f;
+          bk = first;
+        }
+        one = __all_sync(0xffffffffu, bk == 0 || sB->starts[bk] <= rel - 63);
+        near = __all_sync(0xffffffffu, rel < a.lut_w);
+        bias0 = dense_bias_log2(__ldg(tab + bk));
+      }
       uint32_t x[2][32];
       wait(B_S + b, (n >> 1) & 1);
       if (!dead) {
         tmem_ld32x2(tl + 128 * b + 64 * w, tl + 128 * b + 64 * w + 32, x[0], x[1]);
-        if (BIAS) {
-          int nb_ = bk;
-          while (nb_ > 0 && sB->starts[nb_] > rel) --nb_;
-          if (nb_ != bk) {
-            my[bk * 256] = acc;
-            acc = 0.f;
-            bk = nb_;
-          }
-        }
         // P = 2^(S scale log2(e) + bias - lse)
-        bool one = true;
-        if (BIAS) one = __all_sync(0xffffffffu, bk == 0 || sB->starts[bk] <= rel - 63);
         if (one) {
-          const float sub = nl + (BIAS ? dense_bias_log2(__ldg(tab + bk)) : 0.f);
+          const float sub = nl + bias0;
 #pragma unroll
           for (int i = 0; i < 64; ++i)
             x[i >> 5][i & 31] = __float_as_uint(
                 ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), a.scale_log2, sub)));
         } else {
-          if (__all_sync(0xffffffffu, rel < a.lut_w)) {
+          if (near) {
             const float* lut = sB->lut + hl * a.lut_stride + dense_lut_pad(a) + rel;
 #pragma unroll
             for (int i = 0; i < 64; ++i)
               x[i >> 5][i & 31] = __float_as_uint(ex2_approx(
                   fmaf(__uint_as_float(x[i >> 5][i & 31]), a.scale_log2, nl + lut[-i])));
+          } else if (__all_sync(0xffffffffu, bk < 2 || sB->starts[bk - 1] <= rel - 63)) {
+            // at most one start inside: scores before `cut` take v0, the others v1
+            const int cut = bk > 0 ? rel - sB->starts[bk] + 1 : 64;
+            const float v0 = nl + bias0;
+            const float v1 = nl + dense_bias_log2(__ldg(tab + max(bk - 1, 0)));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              if (__any_sync(0xffffffffu, cut > 16 * u && cut < 16 * u + 16)) {
+#pragma unroll
+                for (int i = 16 * u; i < 16 * u + 16; ++i)
+                  x[i >> 5][i & 31] = __float_as_uint(ex2_approx(fmaf(
+                      __uint_as_float(x[i >> 5][i & 31]), a.scale_log2, i < cut ? v0 : v1)));
+              } else {
+                const float sub = 16 * u < cut ? v0 : v1;
+#pragma unroll
+                for (int i = 16 * u; i < 16 * u + 16; ++i)
+                  x[i >> 5][i & 31] = __float_as_uint(
+                      ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), a.scale_log2, sub)));
+              }
+            }
           } else {
             int q = bk;
             int st = q > 0 ? sB->starts[q] : INT_MIN;
-            float sub = nl + dense_bias_log2(__ldg(tab + q));
+            float sub = nl + bias0;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const bool cross = __any_sync(0xffffffffu, rel - 16 * u - 15 < st);
-#pragma unroll
-              for (int i = 16 * u; i < 16 * u + 16; ++i) {
-                if (cross && rel - i < st) {
-                  --q;
-                  st = q > 0 ? sB->starts[q] : INT_MIN;
-                  sub = nl + dense_bias_log2(__ldg(tab + q));
-                }
-                x[i >> 5][i & 31] = __float_as_uint(
-                    ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), a.scale_log2, sub)));
+            for (int i = 0; i < 64; ++i) {
+              if (rel - i < st) {
+                --q;
+                st = q > 0 ? sB->starts[q] : INT_MIN;
+                sub = nl + dense_bias_log2(__ldg(tab + q));
               }
+              x[i >> 5][i & 31] = __float_as_uint(
+                  ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), a.scale_log2, sub)));
             }
           }
           __syncwarp();
@@ -647,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = (warp & 3) * 32 + lane;  // key of the tile
     const uint32_t tl = tbase + ((uint32_t)((warp & 3) * 32) << 16);
     bool dead = false;
-    int qt = 0, hl = 0, bk = 0;
+    int qt = 0, hl = 0, bk = 0;  // bk: bucket of the first distance (bias)
     for (int n = 0; n < N; ++n) {
       const int s = n % NS;
       const int rel = qt * 128 + 64 * w - r;  // distance of the first of this warpgroup's queries
@@ -659,20 +677,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       uint32_t x[2][32];
       const float4* st = reinterpret_cast<const float4*>(sSt + s * 128 + 64 * w);
+      bool one = true, near = false;  // see DenseBias
+      float bias0 = 0.f;
+      const uint16_t* tab = a.bias + (size_t)(g * a.G + hl) * a.nb;
+      if (BIAS) {
+        bk = dense_bucket(sB, a.nb - 1, rel);
+        one = __all_sync(0xffffffffu, bk + 1 == a.nb || sB->starts[bk + 1] > rel + 63);
+        near = __all_sync(0xffffffffu, rel + 63 < a.lut_w);
+        bias0 = dense_bias_log2(__ldg(tab + bk));
+      }
       wait(B_TF + s, (n / NS) & 1);
       wait(B_S, n & 1);
       if (!dead) {
         tmem_ld32x2(tl + 64 * w, tl + 64 * w + 32, x[0], x[1]);
         const float c = a.scale_log2;
-        bool one = true;
-        const uint16_t* tab = a.bias + (size_t)(g * a.G + hl) * a.nb;
-        if (BIAS) {
-          if (qt == 0) bk = 0;
-          while (bk + 1 < a.nb && sB->starts[bk + 1] <= rel) ++bk;
-          one = __all_sync(0xffffffffu, bk + 1 == a.nb || sB->starts[bk + 1] > rel + 63);
-        }
         if (one) {
-          const float bv = BIAS ? dense_bias_log2(__ldg(tab + bk)) : 0.f;
+          const float bv = bias0;
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const float4 v = st[i];
@@ -684,29 +704,47 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
           const float2* sl = sSt + s * 128 + 64 * w;
-          if (__all_sync(0xffffffffu, rel + 63 < a.lut_w)) {
+          if (near) {
             const float* lut = sB->lut + hl * a.lut_stride + dense_lut_pad(a) + rel;
 #pragma unroll
             for (int i = 0; i < 64; ++i)
               x[i >> 5][i & 31] = __float_as_uint(
                   ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), c, sl[i].x + lut[i])));
+          } else if (__all_sync(0xffffffffu,
+                                bk + 2 >= a.nb || sB->starts[bk + 2] > rel + 63)) {
+            // at most one start inside: queries before `cut` take v0, the others v1
+            const int nx = min(bk + 1, a.nb - 1);
+            const int cut = bk + 1 < a.nb ? sB->starts[nx] - rel : 64;
+            const float v0 = bias0;
+            const float v1 = dense_bias_log2(__ldg(tab + nx));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              if (__any_sync(0xffffffffu, cut > 16 * u && cut < 16 * u + 16)) {
+#pragma unroll
+                for (int i = 16 * u; i < 16 * u + 16; ++i)
+                  x[i >> 5][i & 31] = __float_as_uint(ex2_approx(fmaf(
+                      __uint_as_float(x[i >> 5][i & 31]), c, sl[i].x + (i < cut ? v0 : v1))));
+              } else {
+                const float bv = 16 * u < cut ? v0 : v1;
+#pragma unroll
+                for (int i = 16 * u; i < 16 * u + 16; ++i)
+                  x[i >> 5][i & 31] = __float_as_uint(
+                      ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), c, sl[i].x + bv)));
+              }
+            }
           } else {
             int q = bk;
             int nx = q + 1 < a.nb ? sB->starts[q + 1] : INT_MAX;
-            float bv = dense_bias_log2(__ldg(tab + q));
+            float bv = bias0;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const bool cross = __any_sync(0xffffffffu, rel + 16 * u + 15 >= nx);
-#pragma unroll
-              for (int i = 16 * u; i < 16 * u + 16; ++i) {
-                if (cross && rel + i >= nx) {
-                  ++q;
-                  nx = q + 1 < a.nb ? sB->starts[q + 1] : INT_MAX;
-                  bv = dense_bias_log2(__ldg(tab + q));
-                }
-                x[i >> 5][i & 31] = __float_as_uint(
-                    ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), c, sl[i].x + bv)));
+            for (int i = 0; i < 64; ++i) {
+              if (rel + i >= nx) {
+                ++q;
+                nx = q + 1 < a.nb ? sB->starts[q + 1] : INT_MAX;
+                bv = dense_bias_log2(__ldg(tab + q));
               }
+              x[i >> 5][i & 31] = __float_as_uint(
+                  ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), c, sl[i].x + bv)));
             }
           }
           __syncwarp();  // the TMEM store below is warp-collective

@@ -220,13 +220,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     int bk = a.nb - 1;
     const uint16_t* tab = a.bias + (size_t)(g * a.G + hl) * a.nb;
     for (int n = 0; n < nt[t]; ++n) {
+      const int rel = qi - n * 128;  // keys 0..rel of the tile are visible
+      bool one = true, near = false;  // see DenseBias
+      float v0 = 0.f;
+      if (BIAS) {
+        bk = dense_bucket(sB, bk, rel);
+        one = __all_sync(0xffffffffu, bk == 0 || sB->starts[bk] <= rel - 127);
+        near = __all_sync(0xffffffffu, rel < a.lut_w);
+        v0 = dense_bias_log2(__ldg(tab + bk));
+      }
       dead = dead || !wait_bar_warp(bar(B_S + t), n & 1, abort_flag, a.status,
                                     wait_site(kKerDenseFwd, B_S + t, n));
       tc_fence_after();
       if (!dead) {
         uint32_t x[128];
         tmem_ld128(ts, x);
-        const int rel = qi - n * 128;  // keys 0..rel of the tile are visible
         if (__any_sync(0xffffffffu, rel < 127)) {
 #pragma unroll
           for (int i = 0; i < 128; ++i)
@@ -235,38 +243,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         // P = 2^(x mul + add - m)
         float mul = c, add = 0.f;
         if (BIAS) {
-          while (bk > 0 && sB->starts[bk] > rel) --bk;
-          const bool one = bk == 0 || sB->starts[bk] <= rel - 127;
-          if (__all_sync(0xffffffffu, one)) {
-            add = dense_bias_log2(__ldg(tab + bk));  // one bucket over the row's part of the tile
+          if (one) {
+            add = v0;  // one bucket over the row's part of the tile
           } else {
             mul = 1.f;
-            if (__all_sync(0xffffffffu, rel < a.lut_w)) {
+            if (near) {
               const float* lut = sB->lut + hl * a.lut_stride + dense_lut_pad(a) + rel;
 #pragma unroll
               for (int i = 0; i < 128; ++i)
                 x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, lut[-i]));
-            } else {
-              int b = bk;
-              int st = b > 0 ? sB->starts[b] : INT_MIN;
-              float bv = dense_bias_log2(__ldg(tab + b));
+            } else if (__all_sync(0xffffffffu, bk < 2 || sB->starts[bk - 1] <= rel - 127)) {
+              // at most one start inside: scores before `cut` take v0, the others v1
+              const int cut = bk > 0 ? rel - sB->starts[bk] + 1 : 128;
+              const float v1 = dense_bias_log2(__ldg(tab + max(bk - 1, 0)));
 #pragma unroll
               for (int u = 0; u < 8; ++u) {
-                if (__any_sync(0xffffffffu, rel - 16 * u - 15 < st)) {
+                if (__any_sync(0xffffffffu, cut > 16 * u && cut < 16 * u + 16)) {
 #pragma unroll
-                  for (int i = 16 * u; i < 16 * u + 16; ++i) {
-                    if (rel - i < st) {
-                      --b;
-                      st = b > 0 ? sB->starts[b] : INT_MIN;
-                      bv = dense_bias_log2(__ldg(tab + b));
-                    }
-                    x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, bv));
-                  }
+                  for (int i = 16 * u; i < 16 * u + 16; ++i)
+                    x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, i < cut ? v0 : v1));
                 } else {
+                  const float bv = 16 * u < cut ? v0 : v1;
 #pragma unroll
                   for (int i = 16 * u; i < 16 * u + 16; ++i)
                     x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, bv));
                 }
+              }
+            } else {
+              int b = bk;
+              int st = b > 0 ? sB->starts[b] : INT_MIN;
+              float bv = v0;
+#pragma unroll
+              for (int i = 0; i < 128; ++i) {
+                if (rel - i < st) {
+                  --b;
+                  st = b > 0 ? sB->starts[b] : INT_MIN;
+                  bv = dense_bias_log2(__ldg(tab + b));
+                }
+                x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, bv));
               }
             }
             __syncwarp();

@@ -17,6 +17,7 @@ and v may be slices of a fused projection (any token stride that keeps rows on
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 
@@ -105,8 +106,17 @@ def _take(t, copy):
     return t
 
 
-def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+# The current stream's handle; torch.cuda.current_stream would build an object around it,
+# which costs as much host time as a kernel launch.
+_stream = torch._C._cuda_getCurrentRawStream
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device):
+    """Makes `device` current; nothing to do (and no host time) where it is already."""
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def _forward(q, k, v, cu, bias, scale, starts, keep):
@@ -116,7 +126,7 @@ def _forward(q, k, v, cu, bias, scale, starts, keep):
         devices, types = devices + (bias.device,), types + (bias.dtype,)
     plan, copy, args = _plan(q.shape, k.shape, v.shape, q.stride(), k.stride(), v.stride(), types,
                              devices, cu.shape, None if bias is None else bias.shape, scale, starts)
-    with torch.cuda.device(devices[0]):
+    with _on(devices[0]):
         q, k, v = _take(q, copy[0]), _take(k, copy[1]), _take(v, copy[2])
         if any(copy):  # copies are packed
             args = args[:7] + (tuple(0 if c else s for c, s in zip(copy, args[7])),)
@@ -133,7 +143,7 @@ def _forward(q, k, v, cu, bias, scale, starts, keep):
             o_res = lse + plan.o_res_at
         _raise_on(plan.fwd(plan.ref, cu.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
                            None if bias is None else bias.data_ptr(), o.data_ptr(), o_res, lse,
-                           _stream(devices[0])), "msa_dense_fwd")
+                           _stream(devices[0].index)), "msa_dense_fwd")
     return o, saved, (q, k, v, cu, bias), args
 
 
@@ -152,7 +162,7 @@ class DenseFunction(torch.autograd.Function):
     def backward(ctx, d_o):
         q, k, v, cu, bias, o, saved = ctx.saved_tensors
         device = q.device
-        with torch.cuda.device(device):
+        with _on(device):
             if d_o.dtype != torch.bfloat16:
                 d_o = d_o.to(torch.bfloat16)
             stride = _stride_of(d_o.shape, d_o.stride())
@@ -168,7 +178,7 @@ class DenseFunction(torch.autograd.Function):
                                lse + plan.o_res_at, lse, d_o.data_ptr(), dq.data_ptr(),
                                dk.data_ptr(), dv.data_ptr(),
                                None if bias is None else dbias.data_ptr(), ws.data_ptr(),
-                               plan.workspace, _stream(device)), "msa_dense_bwd")
+                               plan.workspace, _stream(device.index)), "msa_dense_bwd")
         return dq, dk, dv, None, dbias, None, None
 
 
