@@ -69,23 +69,25 @@ struct DenseItem {
 // every token index derived from the item is inside the batch.
 __device__ __forceinline__ bool dense_item(const DenseArgs& a, int s, int bt, DenseItem& it) {
   const int lane = threadIdx.x & 31;
-  // last b in [0, ndoc] with cu[b] / bt + b <= s, 32 candidates at a time
-  int lo = 0, n = a.ndoc + 1;
-  while (n > 1) {
+  // last b in [0, ndoc] with cu[b] / bt + b <= s, 32 candidates at a time; the last
+  // round's lanes hold the document's first token and the next one's
+  int lo = 0, n = a.ndoc + 1, b0 = 0, b1 = 0;
+  for (bool found = false; !found;) {
     const int step = (n + 31) >> 5;
-    const int off = lane * step;
-    bool le = false;
-    if (off < n) {
-      const int c = min(max(__ldg(a.cu + lo + off), 0), a.T);
-      le = c / bt + lo + off <= s;
+    const int b = lo + lane * step;
+    const bool in = lane * step < n;
+    const int c = in ? __ldg(a.cu + b) : 0;
+    const int next = step == 1 && in ? (b < a.ndoc ? __ldg(a.cu + b + 1) : a.T) : 0;
+    const bool le = in && min(max(c, 0), a.T) / bt + b <= s;
+    const int last = max(__popc(__ballot_sync(0xffffffffu, le)) - 1, 0);
+    found = step == 1;
+    if (found) {
+      b0 = __shfl_sync(0xffffffffu, c, last);
+      b1 = __shfl_sync(0xffffffffu, next, last);
     }
-    const int last = __popc(__ballot_sync(0xffffffffu, le)) - 1;
-    const int skip = max(last, 0) * step;
-    lo += skip;
-    n = min(step, n - skip);
+    lo += last * step;
+    n = min(step, n - last * step);
   }
-  const int b0 = __ldg(a.cu + lo);
-  const int b1 = lo < a.ndoc ? __ldg(a.cu + lo + 1) : a.T;
   if (b0 < 0 || b1 < b0 || b1 > a.T) {
     if (threadIdx.x == 0) set_status(a.status, MSA_ERR_DEVICE_CHECK);
     return false;
@@ -110,8 +112,31 @@ __device__ __forceinline__ void dense_check_docs(const DenseArgs& a) {
   if (bad) set_status(a.status, MSA_ERR_DEVICE_CHECK);
 }
 
-// TMEM -> registers: 128 columns of this thread's lane, one wait for all of them.
-__device__ __forceinline__ void tmem_ld128(uint32_t ta, uint32_t (&r)[128]) {
+// TMEM -> registers: 64 or 128 columns of this thread's lane, one wait for all of them.
+__device__ __forceinline__ void tmem_ld_row(uint32_t ta, uint32_t (&r)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]),
+        "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]),
+        "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]),
+        "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]),
+        "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(ta), "r"(ta + 32)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_row(uint32_t ta, uint32_t (&r)[128]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -288,34 +313,10 @@ __host__ inline void dense_lut_shape(DenseArgs* a) {
   a->lut_stride = a->G <= 32 ? (per - 32) / 32 * 32 + 32 / a->G : per;
   const int w = a->lut_stride - (127 + a->tpt), last = a->nb > 0 ? a->starts[a->nb - 1] : 0;
   a->lut_w = w < 0 ? 0 : w;
-  if (a->lut_w > last + 1) a->lut_w = last + 1;  // one bucket from there on
+  // a warp's part of a tile spans fewer than 256 distances: beyond this it lies in one bucket
+  if (a->lut_w > last + 256) a->lut_w = last + 256;
 }
 __device__ __forceinline__ int dense_lut_pad(const DenseArgs& a) { return 127 + a.tpt; }
-
-// Fills it (all threads of the CTA; the caller synchronises behind it): distances up to
-// `most` can occur.  BITS: the bucket starts as bits too (with a barrier inside).
-template <bool BITS>
-__device__ __forceinline__ void dense_bias_fill(const DenseArgs& a, DenseBias* s, int g, int most) {
-  const int tid = threadIdx.x, nt = blockDim.x, pad = dense_lut_pad(a);
-  const uint16_t* tab = a.bias + (size_t)g * a.G * a.nb;
-  if (a.lut_w > 0) {
-    for (int x = tid; x < pad; x += nt)
-      for (int h = 0; h < a.G; ++h) s->lut[h * a.lut_stride + x] = 0.f;
-    int b = 0;
-    for (int x = tid; x < min(a.lut_w, most + 1); x += nt) {
-      while (b + 1 < a.nb && a.starts[b + 1] <= x) ++b;
-      for (int h = 0; h < a.G; ++h)
-        s->lut[h * a.lut_stride + pad + x] = dense_bias_log2(__ldg(tab + h * a.nb + b));
-    }
-  }
-  if (tid < a.nb) s->starts[tid] = a.starts[tid];
-  if (BITS) {
-    for (int x = tid; x < (kDenseBits + kDenseBitsPad) / 32 + 2; x += nt) s->bits[x] = 0;
-    __syncthreads();
-    if (tid > 0 && tid < a.nb && a.starts[tid] < kDenseBits)
-      atomicOr(&s->bits[(a.starts[tid] + kDenseBitsPad) >> 5], 1u << (a.starts[tid] & 31));
-  }
-}
 
 // The bucket of distance x among 0..hi (0 for a negative one): the last one that begins
 // at or before x.
@@ -326,6 +327,38 @@ __device__ __forceinline__ int dense_bucket(const DenseBias* s, int hi, int x) {
     if (s->starts[mid] <= x) lo = mid; else hi = mid - 1;
   }
   return lo;
+}
+
+// Fills it in two steps with a barrier between them and one behind: the starts (and the
+// words of the bits, cleared) by any warp, the rest by threads 0..255.  Distances up to
+// `most` can occur.
+__device__ __forceinline__ void dense_bias_starts(const DenseArgs& a, DenseBias* s) {
+  for (int x = threadIdx.x & 31; x < a.nb; x += 32) s->starts[x] = a.starts[x];
+}
+template <bool BITS>
+__device__ __forceinline__ void dense_bias_fill(const DenseArgs& a, DenseBias* s, int g, int most) {
+  const int tid = threadIdx.x, pad = dense_lut_pad(a);
+  const uint16_t* tab = a.bias + (size_t)g * a.G * a.nb;
+  if (a.lut_w > 0) {
+    for (int x = tid; x < pad; x += 256)
+      for (int h = 0; h < a.G; ++h) s->lut[h * a.lut_stride + x] = 0.f;
+    for (int x = tid; x < min(a.lut_w, most + 1); x += 256) {
+      const int b = dense_bucket(s, a.nb - 1, x);
+      for (int h = 0; h < a.G; ++h)
+        s->lut[h * a.lut_stride + pad + x] = dense_bias_log2(__ldg(tab + h * a.nb + b));
+    }
+  }
+  if (BITS) {
+    constexpr int kWords = (kDenseBits + kDenseBitsPad) / 32 + 2;
+    for (int x = tid; x < kWords; x += 256) {
+      // word x holds distances 32 x - pad .. + 31
+      const int first = 32 * x - kDenseBitsPad;
+      uint32_t v = 0;
+      for (int b = dense_bucket(s, a.nb - 1, first + 31); b > 0 && s->starts[b] >= first; --b)
+        v |= 1u << (s->starts[b] - first);
+      s->bits[x] = v;
+    }
+  }
 }
 
 // Zeroes rows [first, 128) of a 128-row bf16 tile of D columns in shared memory

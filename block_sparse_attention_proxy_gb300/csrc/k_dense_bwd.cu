@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(tslot), 512);
     tmem_relinquish();
   }
-  if (BIAS) dense_bias_fill<true>(a, sB, g, min(q0 + a.tpt, it.len) - 1);
+  if (BIAS && warp == 10) dense_bias_starts(a, sB);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -204,6 +204,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     setmaxnreg_inc<kRegsSoftmax>();
+    if (BIAS) {
+      dense_bias_fill<true>(a, sB, g, min(q0 + a.tpt, it.len) - 1);
+      named_bar_sync(2, 256);
+    }
     // ------------------------------ dS ---------------------------------------------
     const int w = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
@@ -536,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(tslot), 512);
     tmem_relinquish();
   }
-  if (BIAS) dense_bias_fill<false>(a, sB, g, nq * 128 - 1);  // the padded last tile included
+  if (BIAS && warp == 10) dense_bias_starts(a, sB);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -660,6 +664,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     setmaxnreg_inc<kRegsSoftmax>();
+    if (BIAS) {  // the padded last tile included
+      dense_bias_fill<false>(a, sB, g, nq * 128 - 1);
+      named_bar_sync(2, 256);
+    }
     // ------------------------------ P^T and dS^T ------------------------------------
     const int w = warp >> 2;
     const int r = (warp & 3) * 32 + lane;  // key of the tile

@@ -15,6 +15,11 @@
 // O is rescaled in TMEM a few times per row instead of once per key tile.
 // P is rounded to bf16 for the product (as o itself is); l sums the fp32 values.
 //
+// At d = 64 a product over 128 keys takes half as long while the exponentials take the
+// same time, so the wait for the next S would show: there the softmax works on 64 keys
+// at a time (S, P and their barriers in halves), and one half's products run under the
+// other half's exponentials.
+//
 // Roles (384 threads): warps 0-3 and 4-7 are the softmax warpgroups of tile 0
 // and 1, so one tile's softmax overlaps the other's products; warp 8 loads;
 // warp 9 issues the MMAs: P V of a tile, then its next S, tile after tile.
@@ -32,6 +37,7 @@ constexpr float kRescale = 8.f;  // log2 growth of a row's maximum that moves m
 template <int D, bool BIAS>
 struct FwdCfg {
   static constexpr int kTile = 128 * D * 2;
+  static constexpr int kHalves = D == 128 ? 1 : 2;  // softmax steps per key tile
   // K and V tiles in flight; with a bias its tables take the place of one
   static constexpr int kRing = D == 128 ? (BIAS ? 4 : 5) : 8;
   static constexpr int kSmem = (2 + kRing) * kTile + 256 + (BIAS ? (int)sizeof(DenseBias) : 0);
@@ -43,13 +49,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_dense_fwd(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ DenseArgs a) {
   using C = FwdCfg<D, BIAS>;
-  constexpr int NCH = D / 64, NR = C::kRing;
+  constexpr int NCH = D / 64, NR = C::kRing, NH = C::kHalves, W = 128 / NH;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;  // [2]; after the last S also the staging of O
   uint8_t* sKV = sQ + 2 * C::kTile;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + NR * C::kTile);
-  constexpr int B_Q = 0, B_F = 1, B_E = 1 + NR, B_S = 1 + 2 * NR, B_P = B_S + 2, B_P2 = B_S + 4,
-                B_PV = B_S + 6, B_END = B_S + 8;
+  // [t][h]: S of tile t, half h complete; P's first / second 64 keys stored; the P V of
+  // tile t's even / odd steps complete (the softmax may be a step ahead of a product)
+  constexpr int B_Q = 0, B_F = 1, B_E = 1 + NR, B_S = 1 + 2 * NR, B_P = B_S + 4, B_PV = B_P + 4,
+                B_END = B_PV + 4;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + B_END + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   static_assert((B_END + 1) * 8 + 8 <= 256, "barrier block");
@@ -75,14 +83,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return;
   }
-  // key tiles of each row tile: up to its last valid token
-  int nt[2];
+  // steps of W keys of each row tile: up to its last valid token
+  int nu[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int first = q0 + t * a.tpt;
-    nt[t] = first < it.len ? (min(first + a.tpt, it.len) + 127) >> 7 : 0;
+    nu[t] = first < it.len ? (min(first + a.tpt, it.len) + W - 1) / W : 0;
   }
-  const int nmax = max(nt[0], nt[1]);
+  const int ntile = (max(nu[0], nu[1]) + NH - 1) / NH;  // key tiles
 
   if (threadIdx.x == 0) {
     mbar_init(bar(B_Q), 1);
@@ -91,10 +99,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(B_E + s), 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(bar(B_S + t), 1);
-      mbar_init(bar(B_P + t), 4);
-      mbar_init(bar(B_P2 + t), 4);
-      mbar_init(bar(B_PV + t), 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(bar(B_S + 2 * t + h), 1);
+        mbar_init(bar(B_P + 2 * t + h), 4);
+        mbar_init(bar(B_PV + 2 * t + h), 1);
+      }
     }
     mbar_init(bar(B_END), 1);
     *abort_flag = 0;
@@ -104,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(tslot), 512);
     tmem_relinquish();
   }
-  if (BIAS) dense_bias_fill<false>(a, sB, g, min(q0 + tpc, it.len) - 1);
+  if (BIAS && warp == 10) dense_bias_starts(a, sB);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -117,13 +126,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------ loads --------------------------------------
       if (lane == 0) {
         const uint32_t rows = (uint32_t)a.tpt * a.G * 128;  // bytes of one 64-column box
-        mbar_arrive_expect_tx(bar(B_Q), (nt[1] ? 2 : 1) * NCH * rows);
-        for (int t = 0; t < (nt[1] ? 2 : 1); ++t)
+        mbar_arrive_expect_tx(bar(B_Q), (nu[1] ? 2 : 1) * NCH * rows);
+        for (int t = 0; t < (nu[1] ? 2 : 1); ++t)
           for (int c = 0; c < NCH; ++c)
             tma_load_3d(smem_u32(sQ + t * C::kTile + c * 16384), &tm_q, bar(B_Q), 64 * c, g * a.G,
                         it.start + q0 + t * a.tpt);
         int x = 0;  // ring position: K0, V0, K1, V1, ...
-        for (; x < 2 * nmax; ++x) {
+        for (; x < 2 * ntile; ++x) {
           const int s = x % NR;
           if (x >= NR && !wait_bar(bar(B_E + s), ((x / NR) & 1) ^ 1, abort_flag, a.status,
                                    wait_site(kKerDenseFwd, B_E + s, x >> 1)))
@@ -142,60 +151,66 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 9) {
       // ------------------------------ MMA issue ----------------------------------
-      constexpr uint32_t idS = make_idesc_bf16(128, 128, false, false);
+      constexpr uint32_t idS = make_idesc_bf16(128, W, false, false);
       constexpr uint32_t idO = make_idesc_bf16(128, D, false, true);
       const uint32_t el = elect_one(), tm = uniform(tbase);
-      const int len = uniform(it.len), nt0 = uniform(nt[0]), nt1 = uniform(nt[1]);
-      const int nm = max(nt0, nt1);
+      const int len = uniform(it.len), nu0 = uniform(nu[0]), nu1 = uniform(nu[1]);
+      const int nk = uniform(ntile);
       const uint32_t q_lo = desc_lo(smem_u32(sQ), 16), k_lo = desc_lo(smem_u32(sKV), 16),
                      v_lo = desc_lo(smem_u32(sKV), 16384);
       auto wait = [&](int b, uint32_t par, int n) {
         return wait_bar_warp(bar(b), par, abort_flag, a.status, wait_site(kKerDenseFwd, b, n));
       };
       auto wait_full = [&](int x) { return wait(B_F + x % NR, (x / NR) & 1, x >> 1); };
-      auto issue_s = [&](int t, int n) {
-        mma_tile_ss<D>(el, tm + 128 * t, q_lo + t * (C::kTile >> 4),
-                       k_lo + (2 * n % NR) * (C::kTile >> 4), idS);
-        mma_commit(el, bar(B_S + t));
+      auto issue_s = [&](int t, int n, int h) {
+        mma_tile_ss<D>(el, tm + 128 * t + W * h, q_lo + t * (C::kTile >> 4),
+                       k_lo + (2 * n % NR) * (C::kTile >> 4) + h * (W * 128 >> 4), idS);
+        mma_commit(el, bar(B_S + 2 * t + h));
       };
       bool ok = wait(B_Q, 0, 0) && wait_full(0);
       if (ok) {
         tc_fence_after();
-        if (nt0 > 0) issue_s(0, 0);
-        if (nt1 > 0) issue_s(1, 0);
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          if (h < nu0) issue_s(0, 0, h);
+          if (h < nu1) issue_s(1, 0, h);
+        }
         mma_commit(el, bar(B_E + 0));
       }
-      for (int n = 0; ok && n < nm; ++n) {
+      for (int n = 0; ok && n < nk; ++n) {
         const int xv = 2 * n + 1, sv = xv % NR;
         if (!(ok = wait_full(xv))) break;
         // keys behind the document's end: P is zero there, V must be finite
         if ((n + 1) * 128 > len) dense_zero_rows<D>(sKV + sv * C::kTile, len - n * 128);
         const uint32_t v = v_lo + sv * (C::kTile >> 4);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int ntt = t ? nt1 : nt0;
-          if (!ok || n >= ntt) continue;
+        for (int ht = 0; ht < 2 * NH; ++ht) {
+          const int h = ht >> 1, t = ht & 1, u = n * NH + h, nut = t ? nu1 : nu0;
+          if (!ok || u >= nut) continue;
           const uint32_t po = tm + 256 + D * t, pa = tm + 128 * t;
-          if (!(ok = wait(B_P + t, n & 1, n))) break;
-          tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_ts(el, po, pa + 8 * kk, v + kk * (2048 >> 4), idO, n > 0 || kk > 0);
-          if (!(ok = wait(B_P2 + t, n & 1, n))) break;
-          tc_fence_after();
+          for (int q = 0; ok && q < 2 / NH; ++q) {  // 64 keys of O += P V
+            const int pb = NH == 1 ? q : h;
+            ok = wait(B_P + 2 * t + pb, n & 1, n);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t p = NH == 1 ? pa + 32 * q : pa + W * h;
 #pragma unroll
-          for (int kk = 4; kk < 8; ++kk)
-            mma_ts(el, po, pa + 8 * kk, v + kk * (2048 >> 4), idO, 1);
-          mma_commit(el, bar(B_PV + t));
-          if (n + 1 < ntt) {
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ts(el, po, p + 8 * kk, v + (4 * pb + kk) * (2048 >> 4), idO,
+                     u > 0 || q > 0 || kk > 0);
+          }
+          if (!ok) break;
+          mma_commit(el, bar(B_PV + 2 * t + (u & 1)));
+          if (u + NH < nut) {
             if (!(ok = wait_full(xv + 1))) break;
             tc_fence_after();
-            issue_s(t, n + 1);
+            issue_s(t, n + 1, h);
           }
         }
         if (!ok) break;
         mma_commit(el, bar(B_E + sv));
-        if (n + 1 < nm) mma_commit(el, bar(B_E + (xv + 1) % NR));
+        if (n + 1 < nk) mma_commit(el, bar(B_E + (xv + 1) % NR));
       }
       if (!ok) {  // products in flight end before TMEM is freed
         mma_commit(el, bar(B_END));
@@ -204,6 +219,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     setmaxnreg_inc<kRegsSoftmax>();
+    if (BIAS) {
+      dense_bias_fill<false>(a, sB, g, min(q0 + tpc, it.len) - 1);
+      named_bar_sync(2, 256);
+    }
     // ------------------------------ softmax ---------------------------------------
     // A failed wait marks the warp dead: it keeps arriving on its barriers
     // without touching TMEM.
@@ -219,25 +238,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool dead = false;
     int bk = a.nb - 1;
     const uint16_t* tab = a.bias + (size_t)(g * a.G + hl) * a.nb;
-    for (int n = 0; n < nt[t]; ++n) {
-      const int rel = qi - n * 128;  // keys 0..rel of the tile are visible
+    const int nut = t ? nu[1] : nu[0];
+    for (int u = 0; u < nut; ++u) {
+      const int h = u % NH, n = u / NH;
+      const int rel = qi - u * W;  // keys 0..rel of this step are visible
       bool one = true, near = false;  // see DenseBias
       float v0 = 0.f;
       if (BIAS) {
         bk = dense_bucket(sB, bk, rel);
-        one = __all_sync(0xffffffffu, bk == 0 || sB->starts[bk] <= rel - 127);
+        one = __all_sync(0xffffffffu, bk == 0 || sB->starts[bk] <= rel - (W - 1));
         near = __all_sync(0xffffffffu, rel < a.lut_w);
         v0 = dense_bias_log2(__ldg(tab + bk));
       }
-      dead = dead || !wait_bar_warp(bar(B_S + t), n & 1, abort_flag, a.status,
-                                    wait_site(kKerDenseFwd, B_S + t, n));
+      dead = dead || !wait_bar_warp(bar(B_S + 2 * t + h), n & 1, abort_flag, a.status,
+                                    wait_site(kKerDenseFwd, B_S + 2 * t + h, n));
       tc_fence_after();
       if (!dead) {
-        uint32_t x[128];
-        tmem_ld128(ts, x);
-        if (__any_sync(0xffffffffu, rel < 127)) {
+        uint32_t x[W];
+        tmem_ld_row(ts + W * h, x);
+        if (__any_sync(0xffffffffu, rel < W - 1)) {
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
+          for (int i = 0; i < W; ++i)
             if (i > rel) x[i] = __float_as_uint(-INFINITY);
         }
         // P = 2^(x mul + add - m)
@@ -247,40 +268,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             add = v0;  // one bucket over the row's part of the tile
           } else {
             mul = 1.f;
-            if (near) {
-              const float* lut = sB->lut + hl * a.lut_stride + dense_lut_pad(a) + rel;
+            const float* lut = sB->lut + hl * a.lut_stride + dense_lut_pad(a) + rel;
+            int b = bk;  // the bucket of the next scores
+            float bv = v0;
 #pragma unroll
-              for (int i = 0; i < 128; ++i)
-                x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, lut[-i]));
-            } else if (__all_sync(0xffffffffu, bk < 2 || sB->starts[bk - 1] <= rel - 127)) {
-              // at most one start inside: scores before `cut` take v0, the others v1
-              const int cut = bk > 0 ? rel - sB->starts[bk] + 1 : 128;
-              const float v1 = dense_bias_log2(__ldg(tab + max(bk - 1, 0)));
+            for (int y = 0; y < W / 16; ++y) {
+              const int lowest = rel - 16 * y - 15;  // distance of the last of these 16 scores
+              const int st = b > 0 ? sB->starts[b] : INT_MIN;
+              if (near) {
 #pragma unroll
-              for (int u = 0; u < 8; ++u) {
-                if (__any_sync(0xffffffffu, cut > 16 * u && cut < 16 * u + 16)) {
+                for (int i = 16 * y; i < 16 * y + 16; ++i)
+                  x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, lut[-i]));
+              } else if (!__any_sync(0xffffffffu, lowest < st)) {
 #pragma unroll
-                  for (int i = 16 * u; i < 16 * u + 16; ++i)
-                    x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, i < cut ? v0 : v1));
-                } else {
-                  const float bv = 16 * u < cut ? v0 : v1;
+                for (int i = 16 * y; i < 16 * y + 16; ++i)
+                  x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, bv));
+              } else if (__all_sync(0xffffffffu, b < 2 || sB->starts[b - 1] <= lowest)) {
+                // one start inside: scores before `cut` take bv, the others v1
+                const int cut = b > 0 ? rel - st + 1 : W;
+                const float v1 = dense_bias_log2(__ldg(tab + max(b - 1, 0)));
 #pragma unroll
-                  for (int i = 16 * u; i < 16 * u + 16; ++i)
-                    x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, bv));
-                }
-              }
-            } else {
-              int b = bk;
-              int st = b > 0 ? sB->starts[b] : INT_MIN;
-              float bv = v0;
-#pragma unroll
-              for (int i = 0; i < 128; ++i) {
-                if (rel - i < st) {
+                for (int i = 16 * y; i < 16 * y + 16; ++i)
+                  x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, i < cut ? bv : v1));
+                if (lowest < st) {
                   --b;
-                  st = b > 0 ? sB->starts[b] : INT_MIN;
-                  bv = dense_bias_log2(__ldg(tab + b));
+                  bv = v1;
                 }
-                x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, bv));
+              } else {
+#pragma unroll
+                for (int i = 16 * y; i < 16 * y + 16; ++i) {
+                  while (b > 0 && sB->starts[b] > rel - i) {
+                    --b;
+                    bv = dense_bias_log2(__ldg(tab + b));
+                  }
+                  x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, bv));
+                }
               }
             }
             __syncwarp();
@@ -288,12 +310,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float m4[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          m4[u] = __uint_as_float(x[32 * u]);
+        for (int y = 0; y < 4; ++y) {
+          m4[y] = __uint_as_float(x[W / 4 * y]);
 #pragma unroll
-          for (int i = 1; i < 31; i += 2)
-            m4[u] = fmax3(m4[u], __uint_as_float(x[32 * u + i]), __uint_as_float(x[32 * u + i + 1]));
-          m4[u] = fmaxf(m4[u], __uint_as_float(x[32 * u + 31]));
+          for (int i = W / 4 * y + 1; i + 1 < W / 4 * (y + 1); i += 2)
+            m4[y] = fmax3(m4[y], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+          m4[y] = fmaxf(m4[y], __uint_as_float(x[W / 4 * (y + 1) - 1]));
         }
         const float mx = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), mul, add);
         const bool grow = mx > m + kRescale || (m == -INFINITY && mx > m);
@@ -302,20 +324,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float f = m_new == m ? 1.f : ex2_approx(m - m_new);
           l *= f;
           m = m_new;
-          if (n > 0) {
-            // O is complete up to tile n - 1 once its P V product has been read
-            dead = dead || !wait_bar_warp(bar(B_PV + t), (n - 1) & 1, abort_flag, a.status,
-                                          wait_site(kKerDenseFwd, B_PV + t, n));
+          if (u > 0) {
+            // O is complete up to the last step once that step's P V product is
+            const int b = B_PV + 2 * t + ((u - 1) & 1);
+            dead = dead || !wait_bar_warp(bar(b), ((u - 1) >> 1) & 1, abort_flag, a.status,
+                                          wait_site(kKerDenseFwd, b, n));
             tc_fence_after();
             if (!dead) {
 #pragma unroll 1
-              for (int u = 0; u < D / 32; ++u) {
+              for (int q = 0; q < D / 32; ++q) {
                 uint32_t y[32];
-                tmem_ld32(to + 32 * u, y);
+                tmem_ld32(to + 32 * q, y);
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                   y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
-                tmem_st32(to + 32 * u, y);
+                tmem_st32(to + 32 * q, y);
               }
             }
           }
@@ -324,11 +347,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const f32x2 mul2_ = pack2(mul, mul), sub2 = pack2(sub, sub);
         f32x2 ls[2] = {0ull, 0ull};
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int q = 0; q < W / 64; ++q) {
           uint32_t w[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const int e = 64 * u + 2 * i;
+            const int e = 64 * q + 2 * i;
             float p0, p1;
             unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), mul2_, sub2), p0,
                     p1);
@@ -337,29 +360,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             ls[i & 1] = add2(ls[i & 1], pack2(p0, p1));
             w[i] = pack_bf16(p0, p1);
           }
-          tmem_st32_async(ts + 32 * u, w);
+          tmem_st32_async(ts + W * h + 32 * q, w);
           tmem_wait_st();
           // the product over the first 64 keys starts while the rest is computed
-          if (u == 0) {
+          if (q + 1 < W / 64) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_P + t));
+            if (lane == 0) mbar_arrive(bar(B_P + 2 * t));
           }
         }
         float l0, l1;
         unpack2(add2(ls[0], ls[1]), l0, l1);
         l += l0 + l1;
-      } else if (lane == 0) {
-        mbar_arrive(bar(B_P + t));
+      } else if (NH == 1 && lane == 0) {
+        mbar_arrive(bar(B_P + 2 * t));
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_P2 + t));
+      if (lane == 0) mbar_arrive(bar(B_P + 2 * t + (NH == 1 ? 1 : h)));
     }
-    if (nt[t] > 0) {
-      const int last = nt[t] - 1;
-      dead = dead || !wait_bar_warp(bar(B_PV + t), last & 1, abort_flag, a.status,
-                                    wait_site(kKerDenseFwd, B_PV + t, last));
+    if (nut > 0) {
+      const int last = nut - 1;
+      const int b = B_PV + 2 * t + (last & 1);
+      dead = dead || !wait_bar_warp(bar(b), (last >> 1) & 1, abort_flag, a.status,
+                                    wait_site(kKerDenseFwd, b, last));
       tc_fence_after();
       if (!dead) {
         const size_t row = (size_t)(it.start + qi) * a.hq + g * a.G + hl;
