@@ -64,39 +64,96 @@ struct DenseItem {
   int doc, start, len, tile;  // document, its first token and length, tile inside it
 };
 
-// The tile of slot `s` (all lanes of a warp; the same in every warp).  A
-// document outside [0, T] or of negative length is flagged and skipped, so
-// every token index derived from the item is inside the batch.
-__device__ __forceinline__ bool dense_item(const DenseArgs& a, int s, int bt, DenseItem& it) {
+// Work item number `x` of dense_slots(): a tile of a document (all lanes of a warp; the
+// same in every warp).  A document outside [0, T] or of negative length is flagged
+// and skipped, so every token index derived from the item is inside the batch.
+//
+// Up to 64 documents, items come by falling work: the hardware starts CTAs in order, and
+// a long one started last would run alone.  Work grows with the tile's index i (LAST: with
+// its distance from the document's end), so item x has the largest i for which
+// N(i) = sum over documents of max(0, tiles - i) exceeds x; a lane keeps two documents'
+// tile counts and N(i) is a warp sum.  More documents (many short ones) go document by
+// document through the slots above, found 32 documents at a time.
+template <bool LAST>
+__device__ __forceinline__ bool dense_item(const DenseArgs& a, int x, int bt, DenseItem& it) {
   const int lane = threadIdx.x & 31;
-  // last b in [0, ndoc] with cu[b] / bt + b <= s, 32 candidates at a time; the last
-  // round's lanes hold the document's first token and the next one's
-  int lo = 0, n = a.ndoc + 1, b0 = 0, b1 = 0;
-  for (bool found = false; !found;) {
-    const int step = (n + 31) >> 5;
-    const int b = lo + lane * step;
-    const bool in = lane * step < n;
-    const int c = in ? __ldg(a.cu + b) : 0;
-    const int next = step == 1 && in ? (b < a.ndoc ? __ldg(a.cu + b + 1) : a.T) : 0;
-    const bool le = in && min(max(c, 0), a.T) / bt + b <= s;
-    const int last = max(__popc(__ballot_sync(0xffffffffu, le)) - 1, 0);
-    found = step == 1;
-    if (found) {
-      b0 = __shfl_sync(0xffffffffu, c, last);
-      b1 = __shfl_sync(0xffffffffu, next, last);
+  constexpr uint32_t kAll = 0xffffffffu;
+  int doc, b0, b1, tile;
+  if (a.ndoc <= 64) {
+    int first[2], len[2], n[2];
+    bool bad = false;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int b = lane + 32 * u;
+      first[u] = b <= a.ndoc ? __ldg(a.cu + b) : 0;
+      const int next = b < a.ndoc ? __ldg(a.cu + b + 1) : first[u];
+      len[u] = next - first[u];
+      bad |= first[u] < 0 || len[u] < 0 || next > a.T || (b == 0 && first[u] != 0);
+      n[u] = (len[u] + bt - 1) / bt;
     }
-    lo += last * step;
-    n = min(step, n - last * step);
+    if (__any_sync(kAll, bad)) {
+      if (threadIdx.x == 0) set_status(a.status, MSA_ERR_DEVICE_CHECK);
+      return false;
+    }
+    const int total = __reduce_add_sync(kAll, n[0] + n[1]);
+    if (x >= total) {  // behind the documents: the padding
+      doc = a.ndoc;
+      b0 = __ldg(a.cu + a.ndoc);
+      b1 = a.T;
+      tile = x - total;
+    } else {
+      int lo = 0, hi = __reduce_max_sync(kAll, max(n[0], n[1])) - 1;
+      int above = 0;  // N(lo + 1)
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((int)__reduce_add_sync(kAll, max(0, n[0] - mid) + max(0, n[1] - mid)) > x) lo = mid;
+        else hi = mid - 1;
+      }
+      above = __reduce_add_sync(kAll, max(0, n[0] - lo - 1) + max(0, n[1] - lo - 1));
+      // the (x - above)-th document with more than lo tiles
+      const uint32_t m0 = __ballot_sync(kAll, n[0] > lo), m1 = __ballot_sync(kAll, n[1] > lo);
+      int r = x - above;
+      const bool second = r >= __popc(m0);
+      if (second) r -= __popc(m0);
+      const int l = __fns(second ? m1 : m0, 0, r + 1);
+      doc = l + (second ? 32 : 0);
+      b0 = __shfl_sync(kAll, second ? first[1] : first[0], l);
+      b1 = b0 + __shfl_sync(kAll, second ? len[1] : len[0], l);
+      tile = LAST ? (b1 - b0 + bt - 1) / bt - 1 - lo : lo;
+    }
+  } else {
+    const int s = LAST ? x : a.nslots - 1 - x;  // longest tiles of a document first
+    // last b in [0, ndoc] with cu[b] / bt + b <= s; the last round's lanes hold the
+    // document's first token and the next one's
+    int n = a.ndoc + 1;
+    doc = b0 = b1 = 0;
+    for (bool found = false; !found;) {
+      const int step = (n + 31) >> 5;
+      const int b = doc + lane * step;
+      const bool in = lane * step < n;
+      const int c = in ? __ldg(a.cu + b) : 0;
+      const int next = step == 1 && in ? (b < a.ndoc ? __ldg(a.cu + b + 1) : a.T) : 0;
+      const bool le = in && min(max(c, 0), a.T) / bt + b <= s;
+      const int last = max(__popc(__ballot_sync(kAll, le)) - 1, 0);
+      found = step == 1;
+      if (found) {
+        b0 = __shfl_sync(kAll, c, last);
+        b1 = __shfl_sync(kAll, next, last);
+      }
+      doc += last * step;
+      n = min(step, n - last * step);
+    }
+    if (b0 < 0 || b1 < b0 || b1 > a.T) {
+      if (threadIdx.x == 0) set_status(a.status, MSA_ERR_DEVICE_CHECK);
+      return false;
+    }
+    tile = s - (b0 / bt + doc);
   }
-  if (b0 < 0 || b1 < b0 || b1 > a.T) {
-    if (threadIdx.x == 0) set_status(a.status, MSA_ERR_DEVICE_CHECK);
-    return false;
-  }
-  it.doc = lo;
+  it.doc = doc;
   it.start = b0;
   it.len = b1 - b0;
-  it.tile = s - (b0 / bt + lo);
-  return it.tile >= 0 && (long long)it.tile * bt < it.len;
+  it.tile = tile;
+  return tile >= 0 && (long long)tile * bt < it.len;
 }
 
 // Whole check of cu_seqlens (one warp of one CTA of a launch): first entry 0,

@@ -72,9 +72,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (blockIdx.x == 0 && warp == 11) dense_check_docs(a);
   const int g = blockIdx.x % a.hkv;
-  const int slot = a.nslots - 1 - (int)(blockIdx.x / a.hkv);  // long rows first
+  const int slot = (int)(blockIdx.x / a.hkv);
   DenseItem it;
-  const bool have = dense_item(a, slot, a.tpt, it);
+  const bool have = dense_item<false>(a, slot, a.tpt, it);
   float* part = BIAS ? a.parts + ((size_t)slot * a.hq + g * a.G) * a.nb : nullptr;
   if (!have || it.doc == a.ndoc) {
     if (BIAS)
@@ -508,8 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int g = blockIdx.x % a.hkv;
   DenseItem it;
-  // the first keys of a document meet the most queries: ascending order
-  if (!dense_item(a, (int)(blockIdx.x / a.hkv), 128, it)) return;
+  if (!dense_item<true>(a, (int)(blockIdx.x / a.hkv), 128, it)) return;  // a tile of keys
   const int j0 = it.tile * 128;
   if (it.doc == a.ndoc) {
     const int n = min(128, it.len - j0);

@@ -66,11 +66,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (blockIdx.x == 0 && warp == 11) dense_check_docs(a);
-  // heaviest tiles of a document first: they end last otherwise
   const int g = blockIdx.x % a.hkv;
   DenseItem it;
   const int tpc = 2 * a.tpt;  // tokens per CTA
-  if (!dense_item(a, a.nslots - 1 - (int)(blockIdx.x / a.hkv), tpc, it)) return;
+  if (!dense_item<false>(a, (int)(blockIdx.x / a.hkv), tpc, it)) return;
   const int q0 = it.tile * tpc;  // first token of the CTA inside the document
   if (it.doc == a.ndoc) {
     // padding behind the last document: zero rows
