@@ -397,12 +397,14 @@ __device__ __forceinline__ void dense_bias_fill(const DenseArgs& a, DenseBias* s
   const int tid = threadIdx.x, pad = dense_lut_pad(a);
   const uint16_t* tab = a.bias + (size_t)g * a.G * a.nb;
   if (a.lut_w > 0) {
-    for (int x = tid; x < pad; x += 256)
-      for (int h = 0; h < a.G; ++h) s->lut[h * a.lut_stride + x] = 0.f;
-    for (int x = tid; x < min(a.lut_w, most + 1); x += 256) {
-      const int b = dense_bucket(s, a.nb - 1, x);
-      for (int h = 0; h < a.G; ++h)
-        s->lut[h * a.lut_stride + pad + x] = dense_bias_log2(__ldg(tab + h * a.nb + b));
+    const int row = pad + min(a.lut_w, most + 1);  // entries of a head that can be read
+#pragma unroll 4
+    for (int x = tid; x < a.G * row; x += 256) {
+      const int h = x / row, at = x - h * row;
+      float v = 0.f;
+      if (at >= pad)
+        v = dense_bias_log2(__ldg(tab + h * a.nb + dense_bucket(s, a.nb - 1, at - pad)));
+      s->lut[h * a.lut_stride + at] = v;
     }
   }
   if (BITS) {

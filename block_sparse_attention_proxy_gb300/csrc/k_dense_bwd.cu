@@ -201,6 +201,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(el, bar(B_END));
         drain_bar(bar(B_END), 0);
       }
+    } else if (BIAS && warp == 11) {
+      // ------------------------------ bucket sums: clear --------------------------
+      float4* all = reinterpret_cast<float4*>(a.slots + ((size_t)slot * a.hkv + g) * a.nb * 256);
+      for (int x = lane; x < a.nb * 64; x += 32) all[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+      __threadfence_block();
+      named_bar_sync(1, 288);
     }
   } else {
     setmaxnreg_inc<kRegsSoftmax>();
@@ -221,25 +227,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     {
       constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes per row, rows per step
       const int r0 = (warp & 3) * 32 + 16 * w, part_ = lane % LPR;
+      const int rows = min(a.tpt, it.len - q0);  // tokens of the item
       float s[16 / RPI];
 #pragma unroll
       for (int u = 0; u < 16 / RPI; ++u) {
-        const int rr = r0 + u * RPI + lane / LPR, tok = rr / a.G, hh = g * a.G + rr % a.G;
-        s[u] = 0.f;
-        if (tok < a.tpt && q0 + tok < it.len) {
-          const size_t t = (size_t)(it.start + q0 + tok);
-          const size_t at = (t * a.hq + hh) * D + part_ * 8;
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.o + at));
-          const uint4 z = __ldg(reinterpret_cast<const uint4*>(a.o_res + at));
-          const uint4 y = __ldg(reinterpret_cast<const uint4*>(
-              a.d_o + t * a.do_stride + (size_t)hh * D + part_ * 8));
-          auto dot = [](uint32_t o, uint32_t res, uint32_t d_o) {
-            return (bf16_lo(o) + bf16_lo(res)) * bf16_lo(d_o) +
-                   (bf16_hi(o) + bf16_hi(res)) * bf16_hi(d_o);
-          };
-          s[u] = (dot(x.x, z.x, y.x) + dot(x.y, z.y, y.y)) +
-                 (dot(x.z, z.z, y.z) + dot(x.w, z.w, y.w));
-        }
+        // rows behind the last one read an earlier row, so that no load is conditional
+        const int rr = r0 + u * RPI + lane / LPR, tok = min(rr / a.G, rows - 1);
+        const int hh = g * a.G + rr % a.G;
+        const size_t t = (size_t)(it.start + q0 + tok);
+        const size_t at = (t * a.hq + hh) * D + part_ * 8;
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.o + at));
+        const uint4 z = __ldg(reinterpret_cast<const uint4*>(a.o_res + at));
+        const uint4 y = __ldg(reinterpret_cast<const uint4*>(
+            a.d_o + t * a.do_stride + (size_t)hh * D + part_ * 8));
+        auto dot = [](uint32_t o, uint32_t res, uint32_t d_o) {
+          return (bf16_lo(o) + bf16_lo(res)) * bf16_lo(d_o) +
+                 (bf16_hi(o) + bf16_hi(res)) * bf16_hi(d_o);
+        };
+        s[u] = (dot(x.x, z.x, y.x) + dot(x.y, z.y, y.y)) +
+               (dot(x.z, z.z, y.z) + dot(x.w, z.w, y.w));
       }
 #pragma unroll
       for (int u = 0; u < 16 / RPI; ++u) {
@@ -247,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int o = LPR / 2; o > 0; o >>= 1) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
         if (part_ == 0) sD[r0 + u * RPI + lane / LPR] = s[u];
       }
-      named_bar_sync(1, 256);
+      named_bar_sync(1, BIAS ? 288 : 256);  // with a bias warp 11 too: its sums are cleared
     }
     // -lse and D of the row (both warpgroups; the first also leaves them for dK, dV)
     float nl = -INFINITY, dsum = 0.f;
@@ -263,10 +269,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* my = nullptr;
     if (BIAS) {
       my = a.slots + ((size_t)slot * a.hkv + g) * a.nb * 256 + w * 128 + r;
-      for (int b = 0; b < a.nb; ++b) my[b * 256] = 0.f;
     }
     float acc = 0.f;
-    int bk = a.nb - 1;
+    int bk = a.nb - 1, stk = INT_MAX;  // bucket of the next scores and its first distance
+    float bias0 = 0.f;                 // its bias
     const uint16_t* tab = a.bias + (size_t)(g * a.G + hl) * a.nb;
     bool dead = false;
     for (int n = 0; n < N; ++n) {
@@ -279,17 +285,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       };
       bool one = true, near = false;  // see DenseBias
-      float bias0 = 0.f;
       if (BIAS) {
-        const int first = dense_bucket(sB, bk, rel);
-        if (first != bk) {
-          my[bk * 256] = acc;
-          acc = 0.f;
-          bk = first;
+        if (__any_sync(0xffffffffu, rel < stk)) {  // the row's first bucket here is another
+          const int first = dense_bucket(sB, bk, rel);
+          if (first != bk) {
+            my[bk * 256] = acc;
+            acc = 0.f;
+            bk = first;
+          }
+          stk = bk > 0 ? sB->starts[bk] : INT_MIN;
+          bias0 = dense_bias_log2(__ldg(tab + bk));
         }
-        one = __all_sync(0xffffffffu, bk == 0 || sB->starts[bk] <= rel - 63);
+        one = __all_sync(0xffffffffu, bk == 0 || stk <= rel - 63);
         near = __all_sync(0xffffffffu, rel < a.lut_w);
-        bias0 = dense_bias_log2(__ldg(tab + bk));
       }
       uint32_t x[2][32];
       wait(B_S + b, (n >> 1) & 1);
@@ -406,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
               bk -= __popc(last[0]) + __popc(last[1]);
+              stk = INT_MAX;  // looked up again for the next tile
               __syncwarp();  // the TMEM store below is warp-collective
             }
           }
@@ -427,19 +436,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (BIAS) {
       if (valid) my[bk * 256] = acc;
-      // sums over the item's rows, in row order; the barrier orders the stores
-      // above before the loads
+      // sums over the item's rows, in a fixed order: a warp takes every eighth bucket, brings
+      // its row sums (contiguous) to shared memory and adds them up head by head, 32/G lanes
+      // to a head.  The barrier orders the stores above before the loads, and the last
+      // use of the bias tables before their memory is reused.
       __threadfence_block();
-      named_bar_sync(1, 256);
-      const float* all = a.slots + ((size_t)slot * a.hkv + g) * a.nb * 256;
-      for (int x = threadIdx.x; x < a.G * a.nb; x += 256) {
-        const int h = x / a.nb, b = x % a.nb;
-        float s = 0.f;
-        for (int i = 0; i < a.tpt; ++i) {
-          const float* p = all + b * 256 + i * a.G + h;
-          s += __ldcg(p) + __ldcg(p + 128);
+      named_bar_sync(2, 256);
+      const float* all = a.slots + ((size_t)slot * a.hkv + g) * a.nb * 256 + lane;
+      float* scr = sB->lut + warp * 128;
+      const int P = max(32 / a.G, 1), hd = lane % a.G, pt = lane / a.G;
+      float v[8];
+      auto fetch = [&](int b) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = b < a.nb ? __ldcg(all + b * 256 + 32 * i) : 0.f;
+      };
+      fetch(warp);
+      for (int b = warp; b < a.nb; b += 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) scr[32 * i + lane] = v[i] + v[4 + i];
+        __syncwarp();
+        fetch(b + 8);
+        if (a.G <= 32) {
+          float x = 0.f;
+          if (pt < P)
+            for (int i = pt; i < a.tpt; i += P) x += scr[i * a.G + hd];
+          float sum = x;
+          for (int i = 1; i < P; ++i) sum += __shfl_sync(0xffffffffu, x, (hd + i * a.G) & 31);
+          if (lane < a.G) part[lane * a.nb + b] = sum;
+        } else {
+          for (int h = lane; h < a.G; h += 32) {
+            float sum = 0.f;
+            for (int i = 0; i < a.tpt; ++i) sum += scr[i * a.G + h];
+            part[h * a.nb + b] = sum;
+          }
         }
-        part[x] = s;
+        __syncwarp();
       }
     }
     if (w == 0) {
@@ -672,7 +703,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = (warp & 3) * 32 + lane;  // key of the tile
     const uint32_t tl = tbase + ((uint32_t)((warp & 3) * 32) << 16);
     bool dead = false;
-    int qt = 0, hl = 0, bk = 0;  // bk: bucket of the first distance (bias)
+    int qt = 0, hl = 0;
+    int bk = 0, stn = 0;  // bias: bucket of the next queries, first distance of the one behind
+    float bias0 = 0.f;    // its bias
     for (int n = 0; n < N; ++n) {
       const int s = n % NS;
       const int rel = qt * 128 + 64 * w - r;  // distance of the first of this warpgroup's queries
@@ -685,13 +718,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t x[2][32];
       const float4* st = reinterpret_cast<const float4*>(sSt + s * 128 + 64 * w);
       bool one = true, near = false;  // see DenseBias
-      float bias0 = 0.f;
       const uint16_t* tab = a.bias + (size_t)(g * a.G + hl) * a.nb;
       if (BIAS) {
-        bk = dense_bucket(sB, a.nb - 1, rel);
-        one = __all_sync(0xffffffffu, bk + 1 == a.nb || sB->starts[bk + 1] > rel + 63);
+        if (qt == 0 || __any_sync(0xffffffffu, rel >= stn)) {  // another head, or bucket
+          bk = dense_bucket(sB, a.nb - 1, rel);
+          stn = bk + 1 < a.nb ? sB->starts[bk + 1] : INT_MAX;
+          bias0 = dense_bias_log2(__ldg(tab + bk));
+        }
+        one = __all_sync(0xffffffffu, stn > rel + 63);
         near = __all_sync(0xffffffffu, rel + 63 < a.lut_w);
-        bias0 = dense_bias_log2(__ldg(tab + bk));
       }
       wait(B_TF + s, (n / NS) & 1);
       wait(B_S, n & 1);
@@ -824,17 +859,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// dtable[h][b] = sum over the work slots, in fp64 and in a fixed order.  One
-// CTA per head; thread (b, c) sums every (256 / nb2)-th slot, then thread b its
-// chunks.
-__global__ void __launch_bounds__(256) k_dense_dtable(const DenseArgs a, uint16_t* dtable) {
-  __shared__ double sum[256];
+// dtable[h][b] = sum over the work items, in fp64 and in a fixed order.  One CTA per head;
+// thread (b, c) sums every nc-th item, then the chunks are added in order.
+constexpr int kTableThreads = 1024;
+__global__ void __launch_bounds__(kTableThreads) k_dense_dtable(const DenseArgs a,
+                                                                uint16_t* dtable) {
+  __shared__ double sum[kTableThreads];
   int nb2 = 1;
   while (nb2 < a.nb) nb2 <<= 1;
-  const int h = blockIdx.x, b = threadIdx.x % nb2, c = threadIdx.x / nb2, nc = 256 / nb2;
+  const int h = blockIdx.x, b = threadIdx.x % nb2, c = threadIdx.x / nb2, nc = kTableThreads / nb2;
   double s = 0.0;
-  if (b < a.nb)
-    for (int x = c; x < a.nslots; x += nc) s += (double)a.parts[((size_t)x * a.hq + h) * a.nb + b];
+  if (b < a.nb) {
+#pragma unroll 8
+    for (int x = c; x < a.nslots; x += nc)
+      s += (double)__ldg(a.parts + ((size_t)x * a.hq + h) * a.nb + b);
+  }
   sum[threadIdx.x] = s;
   __syncthreads();
   if (c == 0 && b < a.nb) {
@@ -884,7 +923,7 @@ cudaError_t launch_dense_bwd(const DenseShape& s, const uint16_t* q, const uint1
   if (e != cudaSuccess || !a.bias) return e;
   DenseArgs b = a;
   b.nslots = dense_slots(a.T, a.ndoc, a.tpt);
-  k_dense_dtable<<<a.hq, 256, 0, st>>>(b, dtable);
+  k_dense_dtable<<<a.hq, kTableThreads, 0, st>>>(b, dtable);
   return cudaGetLastError();
 }
 

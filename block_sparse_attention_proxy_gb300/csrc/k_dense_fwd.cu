@@ -235,19 +235,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = a.scale_log2;
     float m = -INFINITY, l = 0.f;
     bool dead = false;
-    int bk = a.nb - 1;
+    int bk = a.nb - 1, stk = INT_MAX;  // bucket of the next scores and its first distance
+    float v0 = 0.f;                    // its bias
     const uint16_t* tab = a.bias + (size_t)(g * a.G + hl) * a.nb;
     const int nut = t ? nu[1] : nu[0];
     for (int u = 0; u < nut; ++u) {
       const int h = u % NH, n = u / NH;
       const int rel = qi - u * W;  // keys 0..rel of this step are visible
       bool one = true, near = false;  // see DenseBias
-      float v0 = 0.f;
       if (BIAS) {
-        bk = dense_bucket(sB, bk, rel);
-        one = __all_sync(0xffffffffu, bk == 0 || sB->starts[bk] <= rel - (W - 1));
+        if (__any_sync(0xffffffffu, rel < stk)) {  // the row's first bucket here is another
+          bk = dense_bucket(sB, bk, rel);
+          stk = bk > 0 ? sB->starts[bk] : INT_MIN;
+          v0 = dense_bias_log2(__ldg(tab + bk));
+        }
+        one = __all_sync(0xffffffffu, bk == 0 || stk <= rel - (W - 1));
         near = __all_sync(0xffffffffu, rel < a.lut_w);
-        v0 = dense_bias_log2(__ldg(tab + bk));
       }
       dead = dead || !wait_bar_warp(bar(B_S + 2 * t + h), n & 1, abort_flag, a.status,
                                     wait_site(kKerDenseFwd, B_S + 2 * t + h, n));
