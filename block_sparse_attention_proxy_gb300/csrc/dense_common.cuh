@@ -169,6 +169,15 @@ __device__ __forceinline__ void dense_check_docs(const DenseArgs& a) {
   if (bad) set_status(a.status, MSA_ERR_DEVICE_CHECK);
 }
 
+// 16 bytes of read-only global memory; not moved across other volatile instructions.
+__device__ __forceinline__ uint4 ld_nc_v4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 // TMEM -> registers: 64 or 128 columns of this thread's lane, one wait for all of them.
 __device__ __forceinline__ void tmem_ld_row(uint32_t ta, uint32_t (&r)[64]) {
   asm volatile(
@@ -358,10 +367,12 @@ __device__ __forceinline__ float dense_bias_log2(uint16_t raw) {
 constexpr int kDenseLut = 4096;       // entries over all heads of the group
 constexpr int kDenseBits = 8192;      // distances whose bucket starts are kept as bits
 constexpr int kDenseBitsPad = 256;    // bits before distance 0
+constexpr int kDenseTable = 512;      // staged table entries over all heads of the group
 struct DenseBias {
   float lut[kDenseLut];
   uint32_t bits[(kDenseBits + kDenseBitsPad) / 32 + 2];
-  int starts[kDenseMaxBuckets];
+  int starts[kDenseMaxBuckets];  // INT_MAX behind the last bucket
+  float table[kDenseTable];      // [G][nb] in log2 units, if it fits
 };
 // Row length of the table (heads end on different banks: a warp reads 32/G tokens of G
 // heads at once) and the distances that fit.
@@ -375,49 +386,54 @@ __host__ inline void dense_lut_shape(DenseArgs* a) {
 }
 __device__ __forceinline__ int dense_lut_pad(const DenseArgs& a) { return 127 + a.tpt; }
 
-// The bucket of distance x among 0..hi (0 for a negative one): the last one that begins
-// at or before x.
-__device__ __forceinline__ int dense_bucket(const DenseBias* s, int hi, int x) {
-  int lo = 0;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (s->starts[mid] <= x) lo = mid; else hi = mid - 1;
-  }
-  return lo;
+// The bucket of distance x (0 for a negative one): the last one that begins at or before x.
+__device__ __forceinline__ int dense_bucket(const DenseBias* s, int x) {
+  int b = 0;
+#pragma unroll
+  for (int step = kDenseMaxBuckets / 2; step > 0; step >>= 1)
+    if (s->starts[b + step] <= x) b += step;
+  return b;
 }
 
-// Fills it in two steps with a barrier between them and one behind: the starts (and the
-// words of the bits, cleared) by any warp, the rest by threads 0..255.  Distances up to
-// `most` can occur.
-__device__ __forceinline__ void dense_bias_starts(const DenseArgs& a, DenseBias* s) {
-  for (int x = threadIdx.x & 31; x < a.nb; x += 32) s->starts[x] = a.starts[x];
+// Fills it in two steps with a barrier between them and one behind: the starts, the
+// table and the cleared bits by warps 10 and 11, the rest by threads 0..255.  Distances
+// up to `most` can occur.
+template <bool BITS>
+__device__ __forceinline__ void dense_bias_starts(const DenseArgs& a, DenseBias* s, int g) {
+  const int tid = threadIdx.x & 63;
+  s->starts[tid] = tid < a.nb ? a.starts[tid] : INT_MAX;
+  if (a.G * a.nb <= kDenseTable)
+    for (int x = tid; x < a.G * a.nb; x += 64)
+      s->table[x] = dense_bias_log2(__ldg(a.bias + (size_t)g * a.G * a.nb + x));
+  if (BITS)
+    for (int x = tid; x < (kDenseBits + kDenseBitsPad) / 32 + 2; x += 64) s->bits[x] = 0;
 }
 template <bool BITS>
 __device__ __forceinline__ void dense_bias_fill(const DenseArgs& a, DenseBias* s, int g, int most) {
   const int tid = threadIdx.x, pad = dense_lut_pad(a);
+  const int W = min(a.lut_w, most + 1);
+  const bool staged = a.G * a.nb <= kDenseTable;
   const uint16_t* tab = a.bias + (size_t)g * a.G * a.nb;
   if (a.lut_w > 0) {
-    const int row = pad + min(a.lut_w, most + 1);  // entries of a head that can be read
-#pragma unroll 4
-    for (int x = tid; x < a.G * row; x += 256) {
-      const int h = x / row, at = x - h * row;
-      float v = 0.f;
-      if (at >= pad)
-        v = dense_bias_log2(__ldg(tab + h * a.nb + dense_bucket(s, a.nb - 1, at - pad)));
-      s->lut[h * a.lut_stride + at] = v;
+    for (int x = tid; x < pad; x += 256)
+      for (int h = 0; h < a.G; ++h) s->lut[h * a.lut_stride + x] = 0.f;
+    for (int x0 = tid; x0 < W; x0 += 1024) {
+      int b[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) b[u] = dense_bucket(s, x0 + 256 * u);
+      for (int h = 0; h < a.G; ++h) {
+        float* row = s->lut + h * a.lut_stride + pad + x0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int at = h * a.nb + b[u];
+          if (x0 + 256 * u < W)
+            row[256 * u] = staged ? s->table[at] : dense_bias_log2(__ldg(tab + at));
+        }
+      }
     }
   }
-  if (BITS) {
-    constexpr int kWords = (kDenseBits + kDenseBitsPad) / 32 + 2;
-    for (int x = tid; x < kWords; x += 256) {
-      // word x holds distances 32 x - pad .. + 31
-      const int first = 32 * x - kDenseBitsPad;
-      uint32_t v = 0;
-      for (int b = dense_bucket(s, a.nb - 1, first + 31); b > 0 && s->starts[b] >= first; --b)
-        v |= 1u << (s->starts[b] - first);
-      s->bits[x] = v;
-    }
-  }
+  if (BITS && tid > 0 && tid < a.nb && s->starts[tid] < kDenseBits)
+    atomicOr(&s->bits[(s->starts[tid] + kDenseBitsPad) >> 5], 1u << (s->starts[tid] & 31));
 }
 
 // Zeroes rows [first, 128) of a 128-row bf16 tile of D columns in shared memory

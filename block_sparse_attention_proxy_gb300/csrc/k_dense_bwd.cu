@@ -90,6 +90,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int q0 = it.tile * a.tpt;
   const int N = (min(q0 + a.tpt, it.len) + 127) >> 7;  // key tiles
 
+  // D = rowsum(dO o O), O = o + o_res, of 16 rows per warp of the first eight: D/8 lanes to
+  // a row, 16 bytes each.  Loaded here, so that the loads run under the set-up.
+  constexpr int kLanes = D / 8, kSteps = 16 * kLanes / 32;
+  const int dr0 = (warp & 3) * 32 + 16 * (warp >> 2);
+  uint4 xo[kSteps], xr[kSteps], xd[kSteps];
+  if (warp < 8) {
+    const int rows = min(a.tpt, it.len - q0);  // tokens of the item
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) {
+      // rows behind the last one read an earlier row, so that no load is conditional
+      const int rr = dr0 + u * (32 / kLanes) + lane / kLanes, tok = min(rr / a.G, rows - 1);
+      const int hh = g * a.G + rr % a.G;
+      const size_t t = (size_t)(it.start + q0 + tok);
+      const size_t at = (t * a.hq + hh) * D + lane % kLanes * 8;
+      xo[u] = ld_nc_v4(a.o + at);
+      xr[u] = ld_nc_v4(a.o_res + at);
+      xd[u] = ld_nc_v4(a.d_o + t * a.do_stride + (size_t)hh * D + lane % kLanes * 8);
+    }
+  }
+
   if (threadIdx.x == 0) {
     mbar_init(bar(B_Q), 1);
     for (int s = 0; s < NK; ++s) mbar_init(bar(B_KF + s), 1), mbar_init(bar(B_KE + s), 1);
@@ -109,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(tslot), 512);
     tmem_relinquish();
   }
-  if (BIAS && warp == 10) dense_bias_starts(a, sB);
+  if (BIAS && warp >= 10) dense_bias_starts<true>(a, sB, g);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -223,35 +243,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int qi = q0 + ti;
     const bool valid = ti < a.tpt && qi < it.len;
     const size_t row = (size_t)(it.start + qi) * a.hq + g * a.G + hl;
-    // D of 16 rows per warp: D/8 lanes read a row's o, o_res and dO, 16 bytes each
+    // D of 16 rows per warp
     {
-      constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes per row, rows per step
-      const int r0 = (warp & 3) * 32 + 16 * w, part_ = lane % LPR;
-      const int rows = min(a.tpt, it.len - q0);  // tokens of the item
-      float s[16 / RPI];
+      float s[kSteps];
 #pragma unroll
-      for (int u = 0; u < 16 / RPI; ++u) {
-        // rows behind the last one read an earlier row, so that no load is conditional
-        const int rr = r0 + u * RPI + lane / LPR, tok = min(rr / a.G, rows - 1);
-        const int hh = g * a.G + rr % a.G;
-        const size_t t = (size_t)(it.start + q0 + tok);
-        const size_t at = (t * a.hq + hh) * D + part_ * 8;
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.o + at));
-        const uint4 z = __ldg(reinterpret_cast<const uint4*>(a.o_res + at));
-        const uint4 y = __ldg(reinterpret_cast<const uint4*>(
-            a.d_o + t * a.do_stride + (size_t)hh * D + part_ * 8));
+      for (int u = 0; u < kSteps; ++u) {
         auto dot = [](uint32_t o, uint32_t res, uint32_t d_o) {
           return (bf16_lo(o) + bf16_lo(res)) * bf16_lo(d_o) +
                  (bf16_hi(o) + bf16_hi(res)) * bf16_hi(d_o);
         };
-        s[u] = (dot(x.x, z.x, y.x) + dot(x.y, z.y, y.y)) +
-               (dot(x.z, z.z, y.z) + dot(x.w, z.w, y.w));
+        s[u] = (dot(xo[u].x, xr[u].x, xd[u].x) + dot(xo[u].y, xr[u].y, xd[u].y)) +
+               (dot(xo[u].z, xr[u].z, xd[u].z) + dot(xo[u].w, xr[u].w, xd[u].w));
       }
 #pragma unroll
-      for (int u = 0; u < 16 / RPI; ++u) {
+      for (int u = 0; u < kSteps; ++u) {
 #pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
-        if (part_ == 0) sD[r0 + u * RPI + lane / LPR] = s[u];
+        for (int o = kLanes / 2; o > 0; o >>= 1) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
+        if (lane % kLanes == 0) sD[dr0 + u * (32 / kLanes) + lane / kLanes] = s[u];
       }
       named_bar_sync(1, BIAS ? 288 : 256);  // with a bias warp 11 too: its sums are cleared
     }
@@ -287,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool one = true, near = false;  // see DenseBias
       if (BIAS) {
         if (__any_sync(0xffffffffu, rel < stk)) {  // the row's first bucket here is another
-          const int first = dense_bucket(sB, bk, rel);
+          const int first = dense_bucket(sB, rel);
           if (first != bk) {
             my[bk * 256] = acc;
             acc = 0.f;
@@ -437,40 +445,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (BIAS) {
       if (valid) my[bk * 256] = acc;
       // sums over the item's rows, in a fixed order: a warp takes every eighth bucket, brings
-      // its row sums (contiguous) to shared memory and adds them up head by head, 32/G lanes
-      // to a head.  The barrier orders the stores above before the loads, and the last
+      // its row sums (contiguous) and adds them up head by head, through shared memory where G
+      // is no power of two.  The barrier orders the stores above before the loads, and the last
       // use of the bias tables before their memory is reused.
       __threadfence_block();
       named_bar_sync(2, 256);
       const float* all = a.slots + ((size_t)slot * a.hkv + g) * a.nb * 256 + lane;
       float* scr = sB->lut + warp * 128;
-      const int P = max(32 / a.G, 1), hd = lane % a.G, pt = lane / a.G;
-      float v[8];
-      auto fetch = [&](int b) {
+      float v[kDenseMaxBuckets / 8][4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = b < a.nb ? __ldcg(all + b * 256 + 32 * i) : 0.f;
-      };
-      fetch(warp);
-      for (int b = warp; b < a.nb; b += 8) {
+      for (int u = 0; u < kDenseMaxBuckets / 8; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) scr[32 * i + lane] = v[i] + v[4 + i];
-        __syncwarp();
-        fetch(b + 8);
-        if (a.G <= 32) {
-          float x = 0.f;
-          if (pt < P)
-            for (int i = pt; i < a.tpt; i += P) x += scr[i * a.G + hd];
-          float sum = x;
-          for (int i = 1; i < P; ++i) sum += __shfl_sync(0xffffffffu, x, (hd + i * a.G) & 31);
+        for (int i = 0; i < 4; ++i) {
+          const float* p = all + (warp + 8 * u) * 256 + 32 * i;
+          v[u][i] = warp + 8 * u < a.nb ? __ldcg(p) + __ldcg(p + 128) : 0.f;
+        }
+#pragma unroll
+      for (int u = 0; u < kDenseMaxBuckets / 8; ++u) {
+        const int b = warp + 8 * u;
+        if (b >= a.nb) break;
+        if (a.G <= 32 && (a.G & (a.G - 1)) == 0) {  // rows 32 apart belong to one head
+          float sum = (v[u][0] + v[u][1]) + (v[u][2] + v[u][3]);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1)
+            if (o >= a.G) sum += __shfl_xor_sync(0xffffffffu, sum, o);
           if (lane < a.G) part[lane * a.nb + b] = sum;
         } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) scr[32 * i + lane] = v[u][i];
+          __syncwarp();
           for (int h = lane; h < a.G; h += 32) {
-            float sum = 0.f;
-            for (int i = 0; i < a.tpt; ++i) sum += scr[i * a.G + h];
-            part[h * a.nb + b] = sum;
+            float sum[2] = {0.f, 0.f};
+#pragma unroll 8
+            for (int i = 0; i < a.tpt; ++i) sum[i & 1] += scr[i * a.G + h];
+            part[h * a.nb + b] = sum[0] + sum[1];
           }
+          __syncwarp();
         }
-        __syncwarp();
       }
     }
     if (w == 0) {
@@ -570,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(tslot), 512);
     tmem_relinquish();
   }
-  if (BIAS && warp == 10) dense_bias_starts(a, sB);
+  if (BIAS && warp >= 10) dense_bias_starts<false>(a, sB, g);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -721,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint16_t* tab = a.bias + (size_t)(g * a.G + hl) * a.nb;
       if (BIAS) {
         if (qt == 0 || __any_sync(0xffffffffu, rel >= stn)) {  // another head, or bucket
-          bk = dense_bucket(sB, a.nb - 1, rel);
+          bk = dense_bucket(sB, rel);
           stn = bk + 1 < a.nb ? sB->starts[bk + 1] : INT_MAX;
           bias0 = dense_bias_log2(__ldg(tab + bk));
         }

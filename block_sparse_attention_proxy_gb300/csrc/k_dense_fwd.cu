@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(tslot), 512);
     tmem_relinquish();
   }
-  if (BIAS && warp == 10) dense_bias_starts(a, sB);
+  if (BIAS && warp >= 10) dense_bias_starts<false>(a, sB, g);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool one = true, near = false;  // see DenseBias
       if (BIAS) {
         if (__any_sync(0xffffffffu, rel < stk)) {  // the row's first bucket here is another
-          bk = dense_bucket(sB, bk, rel);
+          bk = dense_bucket(sB, rel);
           stk = bk > 0 ? sB->starts[bk] : INT_MIN;
           v0 = dense_bias_log2(__ldg(tab + bk));
         }
