@@ -198,8 +198,7 @@ def allocate_outputs(params: MsaParams, device="cuda") -> dict:
 
 
 # autograd front end (imported last: it builds on the calls above)
-from .dense import DenseFunction, dense_attention, log_buckets  # noqa: E402
+from .dense import dense_attention, log_buckets  # noqa: E402
 from .function import MSAFunction, last_kl_loss, msa_attention  # noqa: E402
 
-__all__ += ["MSAFunction", "msa_attention", "last_kl_loss", "DenseFunction", "dense_attention",
-            "log_buckets"]
+__all__ += ["MSAFunction", "msa_attention", "last_kl_loss", "dense_attention", "log_buckets"]

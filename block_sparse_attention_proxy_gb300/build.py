@@ -1,4 +1,5 @@
-"""Builds libmsa.so in-tree with nvcc for sm_103a (GB300).
+"""Builds libmsa.so in-tree with nvcc for sm_103a (GB300), and the torch front end of the
+dense attention (_dense_torch.so, host C++) that calls it.
 
 Each CUDA source compiles to its own object in parallel under ``_build/``;
 objects newer than every source and header are reused.  The CUDA runtime is
@@ -18,6 +19,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmsa.so")
+TORCH_LIB = os.path.join(PKG, "_dense_torch.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 SOURCES = ["msa_api.cu", "k_regroup.cu", "k_select.cu", "k_selarg.cu", "k_fwd.cu", "k_bwd.cu",
@@ -50,12 +52,50 @@ def _compile(src: str, newest: float, extra: list[str]) -> str:
     return obj
 
 
+def _compile_torch(newest: float) -> str:
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    obj = os.path.join(BUILD, "dense_torch.o")
+    if os.path.exists(obj) and os.path.getmtime(obj) >= newest:
+        return obj
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    dirs = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"],
+            os.path.join(cuda, "include")]
+    cmd = ["g++", "-O1", "-std=c++17", "-fPIC", "-DTORCH_EXTENSION_NAME=_dense_torch",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           *(x for d in dirs for x in ("-isystem", d)), "-c",
+           os.path.join(CSRC, "dense_torch.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for dense_torch.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_torch(obj: str) -> None:
+    from torch.utils import cpp_extension
+
+    if os.path.exists(TORCH_LIB) and os.path.getmtime(TORCH_LIB) >= os.path.getmtime(obj):
+        return
+    libs = [x for d in cpp_extension.library_paths() for x in ("-L", d)]
+    tmp = TORCH_LIB + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, *libs, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch",
+           "-ltorch_python", "-L", PKG, "-l:libmsa.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TORCH_LIB)
+
+
 def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     """Compile (if needed) and return the path of libmsa.so."""
     os.makedirs(BUILD, exist_ok=True)
     newest = _deps()
     extra = list(extra_flags or [])
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        front = ex.submit(_compile_torch, newest)
         objs = list(ex.map(lambda s: _compile(s, newest, extra), SOURCES))
     if not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
         tmp = LIB + ".tmp"
@@ -64,6 +104,7 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    _link_torch(front.result())
     if verbose:
         print("built", LIB)
     return LIB
