@@ -17,6 +17,7 @@ namespace msa {
 
 constexpr int kDenseMaxBuckets = 64;
 constexpr int kDenseMaxGroup = 64;     // query heads per KV head
+constexpr int kDenseMaxGrid = 160;     // CTAs of a persistent kernel
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -50,7 +51,7 @@ struct DenseArgs {
   long long do_stride;
   float2* stats;  // [hq][T] {lse log2(e) (+inf: no key left), D = rowsum(dO o O)}
   uint16_t *dq, *dk, *dv;
-  float* slots;   // [work item][nb][2][128] per-row bucket sums of dS
+  float* slots;   // [CTA][nb][2][128] per-row bucket sums of dS
   float* parts;   // [nslots][hq][nb] their sums over the rows of an item
 };
 
@@ -64,61 +65,74 @@ struct DenseItem {
   int doc, start, len, tile;  // document, its first token and length, tile inside it
 };
 
+// The documents as a warp holds them: up to 64, two to a lane.
+struct DenseDocs {
+  int first[2], len[2], n[2];  // first token, length, tiles
+  int total, most;             // tiles of all documents, of the longest
+};
+// Loads them (all lanes; the same in every warp); false if cu_seqlens is malformed (flagged).
+__device__ __forceinline__ bool dense_docs(const DenseArgs& a, int bt, DenseDocs& d) {
+  if (a.ndoc > 64) return true;
+  const int lane = threadIdx.x & 31;
+  bool bad = false;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int b = lane + 32 * u;
+    d.first[u] = b <= a.ndoc ? __ldg(a.cu + b) : 0;
+    const int next = b < a.ndoc ? __ldg(a.cu + b + 1) : d.first[u];
+    d.len[u] = next - d.first[u];
+    bad |= d.first[u] < 0 || d.len[u] < 0 || next > a.T || (b == 0 && d.first[u] != 0);
+    d.n[u] = (d.len[u] + bt - 1) / bt;
+  }
+  if (__any_sync(0xffffffffu, bad)) {
+    if (threadIdx.x == 0) set_status(a.status, MSA_ERR_DEVICE_CHECK);
+    return false;
+  }
+  d.total = __reduce_add_sync(0xffffffffu, d.n[0] + d.n[1]);
+  d.most = __reduce_max_sync(0xffffffffu, max(d.n[0], d.n[1]));
+  return true;
+}
+
 // Work item number `x` of dense_slots(): a tile of a document (all lanes of a warp; the
 // same in every warp).  A document outside [0, T] or of negative length is flagged
 // and skipped, so every token index derived from the item is inside the batch.
 //
-// Up to 64 documents, items come by falling work: the hardware starts CTAs in order, and
-// a long one started last would run alone.  Work grows with the tile's index i (LAST: with
-// its distance from the document's end), so item x has the largest i for which
-// N(i) = sum over documents of max(0, tiles - i) exceeds x; a lane keeps two documents'
-// tile counts and N(i) is a warp sum.  More documents (many short ones) go document by
-// document through the slots above, found 32 documents at a time.
+// Up to 64 documents, items come by falling work, so that a long one does not start last
+// and run alone.  Work grows with the tile's index i (LAST: with its distance from the
+// document's end), so item x has the largest i for which
+// N(i) = sum over documents of max(0, tiles - i) exceeds x, a warp sum.  More documents (many
+// short ones) go document by document through the slots above, found 32 documents at a
+// time.
 template <bool LAST>
-__device__ __forceinline__ bool dense_item(const DenseArgs& a, int x, int bt, DenseItem& it) {
+__device__ __forceinline__ bool dense_item(const DenseArgs& a, const DenseDocs& d, int x, int bt,
+                                           DenseItem& it) {
   const int lane = threadIdx.x & 31;
   constexpr uint32_t kAll = 0xffffffffu;
   int doc, b0, b1, tile;
   if (a.ndoc <= 64) {
-    int first[2], len[2], n[2];
-    bool bad = false;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int b = lane + 32 * u;
-      first[u] = b <= a.ndoc ? __ldg(a.cu + b) : 0;
-      const int next = b < a.ndoc ? __ldg(a.cu + b + 1) : first[u];
-      len[u] = next - first[u];
-      bad |= first[u] < 0 || len[u] < 0 || next > a.T || (b == 0 && first[u] != 0);
-      n[u] = (len[u] + bt - 1) / bt;
-    }
-    if (__any_sync(kAll, bad)) {
-      if (threadIdx.x == 0) set_status(a.status, MSA_ERR_DEVICE_CHECK);
-      return false;
-    }
-    const int total = __reduce_add_sync(kAll, n[0] + n[1]);
-    if (x >= total) {  // behind the documents: the padding
+    if (x >= d.total) {  // behind the documents: the padding
       doc = a.ndoc;
       b0 = __ldg(a.cu + a.ndoc);
       b1 = a.T;
-      tile = x - total;
+      tile = x - d.total;
     } else {
-      int lo = 0, hi = __reduce_max_sync(kAll, max(n[0], n[1])) - 1;
-      int above = 0;  // N(lo + 1)
+      int lo = 0, hi = d.most - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if ((int)__reduce_add_sync(kAll, max(0, n[0] - mid) + max(0, n[1] - mid)) > x) lo = mid;
+        if ((int)__reduce_add_sync(kAll, max(0, d.n[0] - mid) + max(0, d.n[1] - mid)) > x) lo = mid;
         else hi = mid - 1;
       }
-      above = __reduce_add_sync(kAll, max(0, n[0] - lo - 1) + max(0, n[1] - lo - 1));
+      const int above =
+          __reduce_add_sync(kAll, max(0, d.n[0] - lo - 1) + max(0, d.n[1] - lo - 1));
       // the (x - above)-th document with more than lo tiles
-      const uint32_t m0 = __ballot_sync(kAll, n[0] > lo), m1 = __ballot_sync(kAll, n[1] > lo);
+      const uint32_t m0 = __ballot_sync(kAll, d.n[0] > lo), m1 = __ballot_sync(kAll, d.n[1] > lo);
       int r = x - above;
       const bool second = r >= __popc(m0);
       if (second) r -= __popc(m0);
       const int l = __fns(second ? m1 : m0, 0, r + 1);
       doc = l + (second ? 32 : 0);
-      b0 = __shfl_sync(kAll, second ? first[1] : first[0], l);
-      b1 = b0 + __shfl_sync(kAll, second ? len[1] : len[0], l);
+      b0 = __shfl_sync(kAll, second ? d.first[1] : d.first[0], l);
+      b1 = b0 + __shfl_sync(kAll, second ? d.len[1] : d.len[0], l);
       tile = LAST ? (b1 - b0 + bt - 1) / bt - 1 - lo : lo;
     }
   } else {
@@ -154,6 +168,22 @@ __device__ __forceinline__ bool dense_item(const DenseArgs& a, int x, int bt, De
   it.len = b1 - b0;
   it.tile = tile;
   return tile >= 0 && (long long)tile * bt < it.len;
+}
+
+// Round k of a persistent CTA over `total` = slots x KV heads items, sorted by falling work:
+// even rounds run through the CTAs forwards, odd ones backwards, which evens their sums out,
+// and a CTA keeps its KV head where the grid is a multiple of hkv.
+__device__ __forceinline__ bool dense_round(const DenseArgs& a, int k, int* slot, int* g) {
+  const long long grid = gridDim.x;
+  const long long x = (k & 1) ? (k + 1) * grid - 1 - blockIdx.x : k * grid + blockIdx.x;
+  if (x >= (long long)a.nslots * a.hkv) return false;
+  *slot = (int)(x / a.hkv);
+  const int h = (int)(x % a.hkv);
+  *g = (k & 1) ? a.hkv - 1 - h : h;
+  return true;
+}
+__device__ __forceinline__ int dense_rounds(const DenseArgs& a) {
+  return (int)(((long long)a.nslots * a.hkv + gridDim.x - 1) / gridDim.x);
 }
 
 // Whole check of cu_seqlens (one warp of one CTA of a launch): first entry 0,
@@ -395,25 +425,20 @@ __device__ __forceinline__ int dense_bucket(const DenseBias* s, int x) {
   return b;
 }
 
-// Fills it in two steps with a barrier between them and one behind: the starts, the
-// table and the cleared bits by warps 10 and 11, the rest by threads 0..255.  Distances
-// up to `most` can occur.
+// Fills it for KV head g (threads 0..255, all of them; none may still read the last one's).
 template <bool BITS>
-__device__ __forceinline__ void dense_bias_starts(const DenseArgs& a, DenseBias* s, int g) {
-  const int tid = threadIdx.x & 63;
-  s->starts[tid] = tid < a.nb ? a.starts[tid] : INT_MAX;
-  if (a.G * a.nb <= kDenseTable)
-    for (int x = tid; x < a.G * a.nb; x += 64)
-      s->table[x] = dense_bias_log2(__ldg(a.bias + (size_t)g * a.G * a.nb + x));
-  if (BITS)
-    for (int x = tid; x < (kDenseBits + kDenseBitsPad) / 32 + 2; x += 64) s->bits[x] = 0;
-}
-template <bool BITS>
-__device__ __forceinline__ void dense_bias_fill(const DenseArgs& a, DenseBias* s, int g, int most) {
+__device__ __forceinline__ void dense_bias_tables(const DenseArgs& a, DenseBias* s, int g) {
   const int tid = threadIdx.x, pad = dense_lut_pad(a);
-  const int W = min(a.lut_w, most + 1);
+  const int W = min(a.lut_w, (a.T + 127) / 128 * 128);  // distances that can occur
   const bool staged = a.G * a.nb <= kDenseTable;
   const uint16_t* tab = a.bias + (size_t)g * a.G * a.nb;
+  named_bar_sync(2, 256);
+  if (tid < kDenseMaxBuckets) s->starts[tid] = tid < a.nb ? a.starts[tid] : INT_MAX;
+  if (staged)
+    for (int x = tid; x < a.G * a.nb; x += 256) s->table[x] = dense_bias_log2(__ldg(tab + x));
+  if (BITS)
+    for (int x = tid; x < (kDenseBits + kDenseBitsPad) / 32 + 2; x += 256) s->bits[x] = 0;
+  named_bar_sync(2, 256);
   if (a.lut_w > 0) {
     for (int x = tid; x < pad; x += 256)
       for (int h = 0; h < a.G; ++h) s->lut[h * a.lut_stride + x] = 0.f;
@@ -434,6 +459,7 @@ __device__ __forceinline__ void dense_bias_fill(const DenseArgs& a, DenseBias* s
   }
   if (BITS && tid > 0 && tid < a.nb && s->starts[tid] < kDenseBits)
     atomicOr(&s->bits[(s->starts[tid] + kDenseBitsPad) >> 5], 1u << (s->starts[tid] & 31));
+  named_bar_sync(2, 256);
 }
 
 // Zeroes rows [first, 128) of a 128-row bf16 tile of D columns in shared memory
@@ -452,49 +478,32 @@ __device__ __forceinline__ void dense_zero_rows(uint8_t* tile, int first) {
   __syncwarp();
 }
 
-// A warp's 32 rows x 64 columns of fp32 values (one row per lane), scaled and
-// rounded to bf16, through a private swizzled 32-row x 128-byte staging tile to
-// global memory, four rows x 128 contiguous bytes per warp store.  `row` is
-// the lane's destination (its first element; null: not stored).  RES: what the
-// rounding drops, itself as bf16, instead of the values.
+// 64 fp32 columns of a row (one row per lane), times f, rounded to bf16, to `row` (its first
+// element; null: not stored): 32 bytes to a store, whole sectors, so that lanes need not
+// exchange rows through shared memory first.  RES: what the rounding drops, itself as
+// bf16, instead of the values.
+__device__ __forceinline__ void st_v8(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 template <bool RES = false>
-__device__ __forceinline__ void dense_store_rows(const uint32_t (&va)[32], const uint32_t (&vb)[32],
-                                                 float f, uint8_t* stg, uint16_t* row) {
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void dense_store_row(const uint32_t (&v)[64], float f, uint16_t* row) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    uint32_t w[4], x[4];
+    uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a0 = __uint_as_float(va[8 * q + 2 * i]) * f;
-      const float a1 = __uint_as_float(va[8 * q + 2 * i + 1]) * f;
-      const float b0 = __uint_as_float(vb[8 * q + 2 * i]) * f;
-      const float b1 = __uint_as_float(vb[8 * q + 2 * i + 1]) * f;
-      w[i] = pack_bf16(a0, a1);
-      x[i] = pack_bf16(b0, b1);
-      if (RES) {
-        w[i] = pack_bf16(a0 - bf16_lo(w[i]), a1 - bf16_hi(w[i]));
-        x[i] = pack_bf16(b0 - bf16_lo(x[i]), b1 - bf16_hi(x[i]));
-      }
+    for (int i = 0; i < 8; ++i) {
+      const float x = __uint_as_float(v[16 * q + 2 * i]) * f;
+      const float y = __uint_as_float(v[16 * q + 2 * i + 1]) * f;
+      w[i] = pack_bf16(x, y);
+      if (RES) w[i] = pack_bf16(x - bf16_lo(w[i]), y - bf16_hi(w[i]));
     }
-    *reinterpret_cast<uint4*>(stg + sw128_offset(lane, q)) = make_uint4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<uint4*>(stg + sw128_offset(lane, q + 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+    if (row) st_v8(row + 16 * q, w);
   }
-  __syncwarp();
-  const int ch = lane & 7;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int rr = (lane >> 3) + 4 * i;
-    const uint4 x = *reinterpret_cast<const uint4*>(stg + sw128_offset(rr, ch));
-    uint16_t* dst = reinterpret_cast<uint16_t*>(
-        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), rr));
-    if (dst) *reinterpret_cast<uint4*>(dst + ch * 8) = x;
-  }
-  __syncwarp();
 }
 
-// The same for a row of zeros (documents' padding), without staging: `n`
-// elements (a multiple of 8) by one thread.
+// A row of zeros (documents' padding): `n` elements (a multiple of 8) by one thread.
 __device__ __forceinline__ void dense_zero_row(uint16_t* row, int n) {
   for (int i = 0; i < n; i += 8) *reinterpret_cast<uint4*>(row + i) = make_uint4(0, 0, 0, 0);
 }
@@ -516,6 +525,23 @@ cudaError_t dense_prepare(int threads, int reg_budget, int smem) {
   e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
   return e;
+}
+
+// CTAs of a persistent kernel: one per SM, fewer if there are fewer items; with a bias a
+// multiple of the KV heads where that costs few SMs, so that a CTA keeps its tables.
+inline int dense_grid(const DenseArgs& a) {
+  static std::atomic<int> sms[64];
+  int dev = 0, n = 0;
+  cudaGetDevice(&dev);
+  if (dev < 64) n = sms[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) n = 1;
+    if (n > kDenseMaxGrid) n = kDenseMaxGrid;
+    if (dev < 64) sms[dev].store(n, std::memory_order_relaxed);
+  }
+  if (a.bias && a.hkv * 8 <= n) n -= n % a.hkv;
+  const long long items = (long long)a.nslots * a.hkv;
+  return items < n ? (int)items : n;
 }
 
 // Tensor map of a [T][heads][d] bf16 tensor with token stride `stride`

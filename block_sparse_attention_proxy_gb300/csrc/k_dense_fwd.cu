@@ -51,13 +51,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = FwdCfg<D, BIAS>;
   constexpr int NCH = D / 64, NR = C::kRing, NH = C::kHalves, W = 128 / NH;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* sQ = smem;  // [2]; after the last S also the staging of O
+  uint8_t* sQ = smem;  // [2]
   uint8_t* sKV = sQ + 2 * C::kTile;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + NR * C::kTile);
-  // [t][h]: S of tile t, half h complete; P's first / second 64 keys stored; the P V of
-  // tile t's even / odd steps complete (the softmax may be a step ahead of a product)
-  constexpr int B_Q = 0, B_F = 1, B_E = 1 + NR, B_S = 1 + 2 * NR, B_P = B_S + 4, B_PV = B_P + 4,
-                B_END = B_PV + 4;
+  // Q loaded / free | ring full / empty | [t][b]: S of tile t complete in buffer b; the
+  // first / second 64 keys of its P stored; P V of an even / odd step complete (the
+  // softmax may be a step ahead of a product)
+  constexpr int B_Q = 0, B_QE = 1, B_F = 2, B_E = B_F + NR, B_S = B_E + NR, B_P = B_S + 4,
+                B_PV = B_P + 4, B_END = B_PV + 4;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + B_END + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   static_assert((B_END + 1) * 8 + 8 <= 256, "barrier block");
@@ -66,33 +67,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (blockIdx.x == 0 && warp == 11) dense_check_docs(a);
-  const int g = blockIdx.x % a.hkv;
-  DenseItem it;
-  const int tpc = 2 * a.tpt;  // tokens per CTA
-  if (!dense_item<false>(a, (int)(blockIdx.x / a.hkv), tpc, it)) return;
-  const int q0 = it.tile * tpc;  // first token of the CTA inside the document
-  if (it.doc == a.ndoc) {
-    // padding behind the last document: zero rows
-    const int n = min(tpc, it.len - q0) * a.G;
-    for (int r = threadIdx.x; r < n; r += kThreads) {
-      const size_t row = (size_t)(it.start + q0 + r / a.G) * a.hq + g * a.G + r % a.G;
-      dense_zero_row(a.o + row * D, D);
-      if (a.o_res) dense_zero_row(a.o_res + row * D, D);
-      if (a.lse) a.lse[row] = -INFINITY;
-    }
-    return;
-  }
-  // steps of W keys of each row tile: up to its last valid token
-  int nu[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int first = q0 + t * a.tpt;
-    nu[t] = first < it.len ? (min(first + a.tpt, it.len) + W - 1) / W : 0;
-  }
-  const int ntile = (max(nu[0], nu[1]) + NH - 1) / NH;  // key tiles
+  const int tpc = 2 * a.tpt;  // tokens per item
+  DenseDocs docs;
+  if (!dense_docs(a, tpc, docs)) return;
 
   if (threadIdx.x == 0) {
     mbar_init(bar(B_Q), 1);
+    mbar_init(bar(B_QE), 1);
     for (int s = 0; s < NR; ++s) {
       mbar_init(bar(B_F + s), 1);
       mbar_init(bar(B_E + s), 1);
@@ -112,104 +93,153 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(tslot), 512);
     tmem_relinquish();
   }
-  if (BIAS && warp >= 10) dense_bias_starts<false>(a, sB, g);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *reinterpret_cast<volatile uint32_t*>(tslot);
   // TMEM: S/P of tile t at columns [128 t, 128 t + 128), O of tile t at 256 + D t
 
+  // The items of this CTA, in the same order for every role.  Ring positions, steps and
+  // barrier phases run on from item to item: the next item's loads and first products
+  // start while the softmax warps still finish the last.
+  struct Work {
+    DenseItem it;
+    int g, q0;   // KV head; first token of the item inside the document
+    int nu[2];   // steps of W keys of each row tile: up to its last valid token
+    int tiles;   // key tiles
+  };
+  const int rounds = dense_rounds(a);
+  auto work = [&](int k, Work& w) -> bool {
+    int slot;
+    if (!dense_round(a, k, &slot, &w.g) || !dense_item<false>(a, docs, slot, tpc, w.it))
+      return false;
+    w.q0 = w.it.tile * tpc;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int first = w.q0 + t * a.tpt;
+      w.nu[t] = first < w.it.len && w.it.doc < a.ndoc
+                    ? (min(first + a.tpt, w.it.len) + W - 1) / W
+                    : 0;
+    }
+    w.tiles = (max(w.nu[0], w.nu[1]) + NH - 1) / NH;
+    return true;
+  };
+
   if (warp >= 8) {
     setmaxnreg_dec<kRegsCtl>();
     if (warp == 8) {
       // ------------------------------ loads --------------------------------------
-      if (lane == 0) {
-        const uint32_t rows = (uint32_t)a.tpt * a.G * 128;  // bytes of one 64-column box
-        mbar_arrive_expect_tx(bar(B_Q), (nu[1] ? 2 : 1) * NCH * rows);
-        for (int t = 0; t < (nu[1] ? 2 : 1); ++t)
-          for (int c = 0; c < NCH; ++c)
-            tma_load_3d(smem_u32(sQ + t * C::kTile + c * 16384), &tm_q, bar(B_Q), 64 * c, g * a.G,
-                        it.start + q0 + t * a.tpt);
-        int x = 0;  // ring position: K0, V0, K1, V1, ...
-        for (; x < 2 * ntile; ++x) {
+      const uint32_t rows = (uint32_t)a.tpt * a.G * 128;  // bytes of one 64-column Q box
+      int x = 0, items = 0;  // ring position (K0, V0, K1, V1, ...), items begun
+      bool ok = true;
+      for (int k = 0; ok && k < rounds; ++k) {
+        Work w;
+        if (!work(k, w) || w.tiles == 0) continue;
+        if (items > 0 && !(ok = wait_bar_warp(bar(B_QE), (items - 1) & 1, abort_flag, a.status,
+                                              wait_site(kKerDenseFwd, B_QE, items))))
+          break;
+        const int nq = w.nu[1] ? 2 : 1;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(B_Q), nq * NCH * rows);
+          for (int t = 0; t < nq; ++t)
+            for (int c = 0; c < NCH; ++c)
+              tma_load_3d(smem_u32(sQ + t * C::kTile + c * 16384), &tm_q, bar(B_Q), 64 * c,
+                          w.g * a.G, w.it.start + w.q0 + t * a.tpt);
+        }
+        ++items;
+        for (int y = 0; y < 2 * w.tiles; ++y, ++x) {
           const int s = x % NR;
-          if (x >= NR && !wait_bar(bar(B_E + s), ((x / NR) & 1) ^ 1, abort_flag, a.status,
-                                   wait_site(kKerDenseFwd, B_E + s, x >> 1)))
+          if (x >= NR && !(ok = wait_bar_warp(bar(B_E + s), ((x / NR) & 1) ^ 1, abort_flag,
+                                              a.status, wait_site(kKerDenseFwd, B_E + s, y >> 1))))
             break;
-          mbar_arrive_expect_tx(bar(B_F + s), C::kTile);
-          const uint32_t dst = smem_u32(sKV + s * C::kTile);
-          const int tok = it.start + (x >> 1) * 128;
-          for (int c = 0; c < NCH; ++c)
-            tma_load_3d(dst + c * 16384, (x & 1) ? &tm_v : &tm_k, bar(B_F + s), 64 * c, g, tok);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(B_F + s), C::kTile);
+            const uint32_t dst = smem_u32(sKV + s * C::kTile);
+            const int tok = w.it.start + (y >> 1) * 128;
+            for (int c = 0; c < NCH; ++c)
+              tma_load_3d(dst + c * 16384, (y & 1) ? &tm_v : &tm_k, bar(B_F + s), 64 * c, w.g, tok);
+          }
         }
-        // an aborted CTA must not leave before its copies have landed
-        if (*abort_flag) {
-          drain_bar(bar(B_Q), 0);
-          for (int y = max(0, x - NR); y < x; ++y) drain_bar(bar(B_F + y % NR), (y / NR) & 1);
-        }
+        __syncwarp();
+      }
+      // an aborted CTA must not leave before its copies have landed
+      if (*abort_flag) {
+        if (items > 0) drain_bar(bar(B_Q), (items - 1) & 1);
+        for (int y = max(0, x - NR); y < x; ++y) drain_bar(bar(B_F + y % NR), (y / NR) & 1);
       }
     } else if (warp == 9) {
       // ------------------------------ MMA issue ----------------------------------
       constexpr uint32_t idS = make_idesc_bf16(128, W, false, false);
       constexpr uint32_t idO = make_idesc_bf16(128, D, false, true);
       const uint32_t el = elect_one(), tm = uniform(tbase);
-      const int len = uniform(it.len), nu0 = uniform(nu[0]), nu1 = uniform(nu[1]);
-      const int nk = uniform(ntile);
       const uint32_t q_lo = desc_lo(smem_u32(sQ), 16), k_lo = desc_lo(smem_u32(sKV), 16),
                      v_lo = desc_lo(smem_u32(sKV), 16384);
       auto wait = [&](int b, uint32_t par, int n) {
         return wait_bar_warp(bar(b), par, abort_flag, a.status, wait_site(kKerDenseFwd, b, n));
       };
       auto wait_full = [&](int x) { return wait(B_F + x % NR, (x / NR) & 1, x >> 1); };
-      auto issue_s = [&](int t, int n, int h) {
-        mma_tile_ss<D>(el, tm + 128 * t + W * h, q_lo + t * (C::kTile >> 4),
-                       k_lo + (2 * n % NR) * (C::kTile >> 4) + h * (W * 128 >> 4), idS);
-        mma_commit(el, bar(B_S + 2 * t + h));
+      int x = 0, items = 0, U[2] = {0, 0};  // ring position, items, steps of each tile so far
+      // S of a step of tile t into buffer b: keys h W .. of the K tile at ring position xk
+      auto issue_s = [&](int t, int xk, int h, int b) {
+        mma_tile_ss<D>(el, tm + 128 * t + W * b, q_lo + t * (C::kTile >> 4),
+                       k_lo + (xk % NR) * (C::kTile >> 4) + h * (W * 128 >> 4), idS);
+        mma_commit(el, bar(B_S + 2 * t + b));
       };
-      bool ok = wait(B_Q, 0, 0) && wait_full(0);
-      if (ok) {
+      bool ok = true;
+      for (int k = 0; ok && k < rounds; ++k) {
+        Work w;
+        if (!work(k, w) || w.tiles == 0) continue;
+        const int len = uniform(w.it.len), nu0 = uniform(w.nu[0]), nu1 = uniform(w.nu[1]);
+        const int nk = uniform(w.tiles);
+        if (!(ok = wait(B_Q, items & 1, items) && wait_full(x))) break;
+        ++items;
         tc_fence_after();
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-          if (h < nu0) issue_s(0, 0, h);
-          if (h < nu1) issue_s(1, 0, h);
+          if (h < nu0) issue_s(0, x, h, (U[0] + h) % NH);
+          if (h < nu1) issue_s(1, x, h, (U[1] + h) % NH);
         }
-        mma_commit(el, bar(B_E + 0));
-      }
-      for (int n = 0; ok && n < nk; ++n) {
-        const int xv = 2 * n + 1, sv = xv % NR;
-        if (!(ok = wait_full(xv))) break;
-        // keys behind the document's end: P is zero there, V must be finite
-        if ((n + 1) * 128 > len) dense_zero_rows<D>(sKV + sv * C::kTile, len - n * 128);
-        const uint32_t v = v_lo + sv * (C::kTile >> 4);
+        mma_commit(el, bar(B_E + x % NR));
+        if (nk == 1) mma_commit(el, bar(B_QE));
+        for (int n = 0; ok && n < nk; ++n) {
+          const int xv = x + 2 * n + 1, sv = xv % NR;
+          if (!(ok = wait_full(xv))) break;
+          // keys behind the document's end: P is zero there, V must be finite
+          if ((n + 1) * 128 > len) dense_zero_rows<D>(sKV + sv * C::kTile, len - n * 128);
+          const uint32_t v = v_lo + sv * (C::kTile >> 4);
 #pragma unroll
-        for (int ht = 0; ht < 2 * NH; ++ht) {
-          const int h = ht >> 1, t = ht & 1, u = n * NH + h, nut = t ? nu1 : nu0;
-          if (!ok || u >= nut) continue;
-          const uint32_t po = tm + 256 + D * t, pa = tm + 128 * t;
+          for (int ht = 0; ht < 2 * NH; ++ht) {
+            const int h = ht >> 1, t = ht & 1, u = n * NH + h, nut = t ? nu1 : nu0;
+            if (!ok || u >= nut) continue;
+            const int Ut = U[t] + u, b = Ut % NH;
+            const uint32_t po = tm + 256 + D * t, pa = tm + 128 * t + W * b;
 #pragma unroll
-          for (int q = 0; ok && q < 2 / NH; ++q) {  // 64 keys of O += P V
-            const int pb = NH == 1 ? q : h;
-            ok = wait(B_P + 2 * t + pb, n & 1, n);
+            for (int q = 0; ok && q < 2 / NH; ++q) {  // 64 keys of O += P V
+              ok = wait(B_P + 2 * t + (NH == 1 ? q : b), (Ut / NH) & 1, n);
+              if (!ok) break;
+              tc_fence_after();
+              const int vk = NH == 1 ? 4 * q : 4 * h;  // first of the V tile's 16-key steps
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ts(el, po, pa + 32 * q + 8 * kk, v + (vk + kk) * (2048 >> 4), idO,
+                       u > 0 || q > 0 || kk > 0);
+            }
             if (!ok) break;
-            tc_fence_after();
-            const uint32_t p = NH == 1 ? pa + 32 * q : pa + W * h;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_ts(el, po, p + 8 * kk, v + (4 * pb + kk) * (2048 >> 4), idO,
-                     u > 0 || q > 0 || kk > 0);
+            mma_commit(el, bar(B_PV + 2 * t + (Ut & 1)));
+            if (u + NH < nut) {
+              if (!(ok = wait_full(xv + 1))) break;
+              tc_fence_after();
+              issue_s(t, xv + 1, h, b);
+            }
           }
           if (!ok) break;
-          mma_commit(el, bar(B_PV + 2 * t + (u & 1)));
-          if (u + NH < nut) {
-            if (!(ok = wait_full(xv + 1))) break;
-            tc_fence_after();
-            issue_s(t, n + 1, h);
-          }
+          mma_commit(el, bar(B_E + sv));
+          if (n + 1 < nk) mma_commit(el, bar(B_E + (xv + 1) % NR));
+          if (n + 2 == nk) mma_commit(el, bar(B_QE));  // the last S has been issued
         }
-        if (!ok) break;
-        mma_commit(el, bar(B_E + sv));
-        if (n + 1 < nk) mma_commit(el, bar(B_E + (xv + 1) % NR));
+        x += 2 * nk;
+        U[0] += nu0;
+        U[1] += nu1;
       }
       if (!ok) {  // products in flight end before TMEM is freed
         mma_commit(el, bar(B_END));
@@ -218,10 +248,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     setmaxnreg_inc<kRegsSoftmax>();
-    if (BIAS) {
-      dense_bias_fill<false>(a, sB, g, min(q0 + tpc, it.len) - 1);
-      named_bar_sync(2, 256);
-    }
     // ------------------------------ softmax ---------------------------------------
     // A failed wait marks the warp dead: it keeps arriving on its barriers
     // without touching TMEM.
@@ -230,184 +256,204 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tbase + lane_off + 128 * t, to = tbase + lane_off + 256 + D * t;
     const int ti = r / a.G, hl = r % a.G;  // hl < G also for rows behind tpt
-    const int qi = q0 + t * a.tpt + ti;  // token inside the document
-    const bool valid = ti < a.tpt && qi < it.len;
     const float c = a.scale_log2;
-    float m = -INFINITY, l = 0.f;
     bool dead = false;
-    int bk = a.nb - 1, stk = INT_MAX;  // bucket of the next scores and its first distance
-    float v0 = 0.f;                    // its bias
-    const uint16_t* tab = a.bias + (size_t)(g * a.G + hl) * a.nb;
-    const int nut = t ? nu[1] : nu[0];
-    for (int u = 0; u < nut; ++u) {
-      const int h = u % NH, n = u / NH;
-      const int rel = qi - u * W;  // keys 0..rel of this step are visible
-      bool one = true, near = false;  // see DenseBias
-      if (BIAS) {
-        if (__any_sync(0xffffffffu, rel < stk)) {  // the row's first bucket here is another
-          bk = dense_bucket(sB, rel);
-          stk = bk > 0 ? sB->starts[bk] : INT_MIN;
-          v0 = dense_bias_log2(__ldg(tab + bk));
+    int U = 0, table_of = -1;  // steps so far; KV head the bias tables are of
+    for (int k = 0; k < rounds; ++k) {
+      Work w;
+      if (!work(k, w)) continue;
+      if (w.it.doc == a.ndoc) {  // padding behind the last document: zero rows
+        const int n = min(tpc, w.it.len - w.q0) * a.G;
+        const int rr = (int)threadIdx.x;
+        if (rr < n) {
+          const size_t row =
+              (size_t)(w.it.start + w.q0 + rr / a.G) * a.hq + w.g * a.G + rr % a.G;
+          dense_zero_row(a.o + row * D, D);
+          if (a.o_res) dense_zero_row(a.o_res + row * D, D);
+          if (a.lse) a.lse[row] = -INFINITY;
         }
-        one = __all_sync(0xffffffffu, bk == 0 || stk <= rel - (W - 1));
-        near = __all_sync(0xffffffffu, rel < a.lut_w);
+        continue;
       }
-      dead = dead || !wait_bar_warp(bar(B_S + 2 * t + h), n & 1, abort_flag, a.status,
-                                    wait_site(kKerDenseFwd, B_S + 2 * t + h, n));
-      tc_fence_after();
-      if (!dead) {
-        uint32_t x[W];
-        tmem_ld_row(ts + W * h, x);
-        if (__any_sync(0xffffffffu, rel < W - 1)) {
-#pragma unroll
-          for (int i = 0; i < W; ++i)
-            if (i > rel) x[i] = __float_as_uint(-INFINITY);
-        }
-        // P = 2^(x mul + add - m)
-        float mul = c, add = 0.f;
+      if (BIAS && table_of != w.g) {
+        dense_bias_tables<false>(a, sB, w.g);
+        table_of = w.g;
+      }
+      const int qi = w.q0 + t * a.tpt + ti;  // token inside the document
+      const bool valid = ti < a.tpt && qi < w.it.len;
+      const int nut = t ? w.nu[1] : w.nu[0];
+      float m = -INFINITY, l = 0.f;
+      int bk = a.nb - 1, stk = INT_MAX;  // bucket of the next scores and its first distance
+      float v0 = 0.f;                    // its bias
+      const uint16_t* tab = a.bias + (size_t)(w.g * a.G + hl) * a.nb;
+      for (int u = 0; u < nut; ++u, ++U) {
+        const int b = U % NH;  // buffer of this step
+        const uint32_t par = (U / NH) & 1;
+        const int rel = qi - u * W;  // keys 0..rel of this step are visible
+        bool one = true, near = false;  // see DenseBias
         if (BIAS) {
-          if (one) {
-            add = v0;  // one bucket over the row's part of the tile
-          } else {
-            mul = 1.f;
-            const float* lut = sB->lut + hl * a.lut_stride + dense_lut_pad(a) + rel;
-            int b = bk;  // the bucket of the next scores
-            float bv = v0;
+          if (__any_sync(0xffffffffu, rel < stk)) {  // the row's first bucket here is another
+            bk = dense_bucket(sB, rel);
+            stk = bk > 0 ? sB->starts[bk] : INT_MIN;
+            v0 = dense_bias_log2(__ldg(tab + bk));
+          }
+          one = __all_sync(0xffffffffu, bk == 0 || stk <= rel - (W - 1));
+          near = __all_sync(0xffffffffu, rel < a.lut_w);
+        }
+        dead = dead || !wait_bar_warp(bar(B_S + 2 * t + b), par, abort_flag, a.status,
+                                      wait_site(kKerDenseFwd, B_S + 2 * t + b, u));
+        tc_fence_after();
+        if (!dead) {
+          uint32_t x[W];
+          tmem_ld_row(ts + W * b, x);
+          if (__any_sync(0xffffffffu, rel < W - 1)) {
 #pragma unroll
-            for (int y = 0; y < W / 16; ++y) {
-              const int lowest = rel - 16 * y - 15;  // distance of the last of these 16 scores
-              const int st = b > 0 ? sB->starts[b] : INT_MIN;
-              if (near) {
+            for (int i = 0; i < W; ++i)
+              if (i > rel) x[i] = __float_as_uint(-INFINITY);
+          }
+          // P = 2^(x mul + add - m)
+          float mul = c, add = 0.f;
+          if (BIAS) {
+            if (one) {
+              add = v0;  // one bucket over the row's part of the tile
+            } else {
+              mul = 1.f;
+              const float* lut = sB->lut + hl * a.lut_stride + dense_lut_pad(a) + rel;
+              int kb = bk;  // the bucket of the next scores
+              float bv = v0;
 #pragma unroll
-                for (int i = 16 * y; i < 16 * y + 16; ++i)
-                  x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, lut[-i]));
-              } else if (!__any_sync(0xffffffffu, lowest < st)) {
+              for (int y = 0; y < W / 16; ++y) {
+                const int lowest = rel - 16 * y - 15;  // distance of the last of these 16 scores
+                const int st = kb > 0 ? sB->starts[kb] : INT_MIN;
+                if (near) {
 #pragma unroll
-                for (int i = 16 * y; i < 16 * y + 16; ++i)
-                  x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, bv));
-              } else if (__all_sync(0xffffffffu, b < 2 || sB->starts[b - 1] <= lowest)) {
-                // one start inside: scores before `cut` take bv, the others v1
-                const int cut = b > 0 ? rel - st + 1 : W;
-                const float v1 = dense_bias_log2(__ldg(tab + max(b - 1, 0)));
+                  for (int i = 16 * y; i < 16 * y + 16; ++i)
+                    x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, lut[-i]));
+                } else if (!__any_sync(0xffffffffu, lowest < st)) {
 #pragma unroll
-                for (int i = 16 * y; i < 16 * y + 16; ++i)
-                  x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, i < cut ? bv : v1));
-                if (lowest < st) {
-                  --b;
-                  bv = v1;
-                }
-              } else {
+                  for (int i = 16 * y; i < 16 * y + 16; ++i)
+                    x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, bv));
+                } else if (__all_sync(0xffffffffu, kb < 2 || sB->starts[kb - 1] <= lowest)) {
+                  // one start inside: scores before `cut` take bv, the others v1
+                  const int cut = kb > 0 ? rel - st + 1 : W;
+                  const float v1 = dense_bias_log2(__ldg(tab + max(kb - 1, 0)));
 #pragma unroll
-                for (int i = 16 * y; i < 16 * y + 16; ++i) {
-                  while (b > 0 && sB->starts[b] > rel - i) {
-                    --b;
-                    bv = dense_bias_log2(__ldg(tab + b));
+                  for (int i = 16 * y; i < 16 * y + 16; ++i)
+                    x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, i < cut ? bv : v1));
+                  if (lowest < st) {
+                    --kb;
+                    bv = v1;
                   }
-                  x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, bv));
+                } else {
+#pragma unroll
+                  for (int i = 16 * y; i < 16 * y + 16; ++i) {
+                    while (kb > 0 && sB->starts[kb] > rel - i) {
+                      --kb;
+                      bv = dense_bias_log2(__ldg(tab + kb));
+                    }
+                    x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, bv));
+                  }
+                }
+              }
+              __syncwarp();
+            }
+          }
+          float m4[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            m4[y] = __uint_as_float(x[W / 4 * y]);
+#pragma unroll
+            for (int i = W / 4 * y + 1; i + 1 < W / 4 * (y + 1); i += 2)
+              m4[y] = fmax3(m4[y], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+            m4[y] = fmaxf(m4[y], __uint_as_float(x[W / 4 * (y + 1) - 1]));
+          }
+          const float mx = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), mul, add);
+          const bool grow = mx > m + kRescale || (m == -INFINITY && mx > m);
+          if (__any_sync(0xffffffffu, grow)) {
+            const float m_new = grow ? mx : m;
+            const float f = m_new == m ? 1.f : ex2_approx(m - m_new);
+            l *= f;
+            m = m_new;
+            if (u > 0) {
+              // O is complete up to the last step once that step's P V product is
+              const int pv = B_PV + 2 * t + ((U - 1) & 1);
+              dead = dead || !wait_bar_warp(bar(pv), ((U - 1) >> 1) & 1, abort_flag, a.status,
+                                            wait_site(kKerDenseFwd, pv, u));
+              tc_fence_after();
+              if (!dead) {
+#pragma unroll 1
+                for (int q = 0; q < D / 32; ++q) {
+                  uint32_t y[32];
+                  tmem_ld32(to + 32 * q, y);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i)
+                    y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
+                  tmem_st32(to + 32 * q, y);
                 }
               }
             }
-            __syncwarp();
           }
-        }
-        float m4[4];
+          const float sub = add - (m == -INFINITY ? 0.f : m);
+          const f32x2 mul2_ = pack2(mul, mul), sub2 = pack2(sub, sub);
+          f32x2 ls[2] = {0ull, 0ull};
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          m4[y] = __uint_as_float(x[W / 4 * y]);
+          for (int q = 0; q < W / 64; ++q) {
+            uint32_t w[32];
 #pragma unroll
-          for (int i = W / 4 * y + 1; i + 1 < W / 4 * (y + 1); i += 2)
-            m4[y] = fmax3(m4[y], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-          m4[y] = fmaxf(m4[y], __uint_as_float(x[W / 4 * (y + 1) - 1]));
-        }
-        const float mx = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), mul, add);
-        const bool grow = mx > m + kRescale || (m == -INFINITY && mx > m);
-        if (__any_sync(0xffffffffu, grow)) {
-          const float m_new = grow ? mx : m;
-          const float f = m_new == m ? 1.f : ex2_approx(m - m_new);
-          l *= f;
-          m = m_new;
-          if (u > 0) {
-            // O is complete up to the last step once that step's P V product is
-            const int b = B_PV + 2 * t + ((u - 1) & 1);
-            dead = dead || !wait_bar_warp(bar(b), ((u - 1) >> 1) & 1, abort_flag, a.status,
-                                          wait_site(kKerDenseFwd, b, n));
-            tc_fence_after();
-            if (!dead) {
-#pragma unroll 1
-              for (int q = 0; q < D / 32; ++q) {
-                uint32_t y[32];
-                tmem_ld32(to + 32 * q, y);
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
-                tmem_st32(to + 32 * q, y);
-              }
+            for (int i = 0; i < 32; ++i) {
+              const int e = 64 * q + 2 * i;
+              float p0, p1;
+              unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), mul2_, sub2), p0,
+                      p1);
+              p0 = ex2_approx(p0);
+              p1 = ex2_approx(p1);
+              ls[i & 1] = add2(ls[i & 1], pack2(p0, p1));
+              w[i] = pack_bf16(p0, p1);
+            }
+            tmem_st32_async(ts + W * b + 32 * q, w);
+            tmem_wait_st();
+            // the product over the first 64 keys starts while the rest is computed
+            if (q + 1 < W / 64) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(B_P + 2 * t));
             }
           }
+          float l0, l1;
+          unpack2(add2(ls[0], ls[1]), l0, l1);
+          l += l0 + l1;
+        } else if (NH == 1 && lane == 0) {
+          mbar_arrive(bar(B_P + 2 * t));
         }
-        const float sub = add - (m == -INFINITY ? 0.f : m);
-        const f32x2 mul2_ = pack2(mul, mul), sub2 = pack2(sub, sub);
-        f32x2 ls[2] = {0ull, 0ull};
-#pragma unroll
-        for (int q = 0; q < W / 64; ++q) {
-          uint32_t w[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int e = 64 * q + 2 * i;
-            float p0, p1;
-            unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), mul2_, sub2), p0,
-                    p1);
-            p0 = ex2_approx(p0);
-            p1 = ex2_approx(p1);
-            ls[i & 1] = add2(ls[i & 1], pack2(p0, p1));
-            w[i] = pack_bf16(p0, p1);
-          }
-          tmem_st32_async(ts + W * h + 32 * q, w);
-          tmem_wait_st();
-          // the product over the first 64 keys starts while the rest is computed
-          if (q + 1 < W / 64) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_P + 2 * t));
-          }
-        }
-        float l0, l1;
-        unpack2(add2(ls[0], ls[1]), l0, l1);
-        l += l0 + l1;
-      } else if (NH == 1 && lane == 0) {
-        mbar_arrive(bar(B_P + 2 * t));
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_P + 2 * t + (NH == 1 ? 1 : b)));
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_P + 2 * t + (NH == 1 ? 1 : h)));
-    }
-    if (nut > 0) {
-      const int last = nut - 1;
-      const int b = B_PV + 2 * t + (last & 1);
-      dead = dead || !wait_bar_warp(bar(b), (last >> 1) & 1, abort_flag, a.status,
-                                    wait_site(kKerDenseFwd, b, last));
-      tc_fence_after();
-      if (!dead) {
-        const size_t row = (size_t)(it.start + qi) * a.hq + g * a.G + hl;
-        const float inv = l > 0.f ? 1.f / l : 0.f;  // 0: no key left (bias -inf)
-        uint8_t* stg = sQ + t * C::kTile + (warp & 3) * 4096;
+      if (nut > 0) {
+        const int b = B_PV + 2 * t + ((U - 1) & 1);
+        dead = dead || !wait_bar_warp(bar(b), ((U - 1) >> 1) & 1, abort_flag, a.status,
+                                      wait_site(kKerDenseFwd, b, nut));
+        tc_fence_after();
+        if (!dead) {
+          const size_t row = (size_t)(w.it.start + qi) * a.hq + w.g * a.G + hl;
+          const float inv = l > 0.f ? 1.f / l : 0.f;  // 0: no key left (bias -inf)
+          uint16_t* dst = valid ? a.o + row * D : nullptr;
+          uint16_t* res = valid && a.o_res ? a.o_res + row * D : nullptr;
 #pragma unroll 1
-        for (int u = 0; u < D / 64; ++u) {
-          uint32_t va[32], vb[32];
-          tmem_ld32x2(to + 64 * u, to + 64 * u + 32, va, vb);
-          if (BIAS && l == 0.f) {
+          for (int q = 0; q < D / 64; ++q) {
+            uint32_t v[64];
+            tmem_ld_row(to + 64 * q, v);
+            if (BIAS && l == 0.f) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) va[i] = vb[i] = 0;
+              for (int i = 0; i < 64; ++i) v[i] = 0;
+            }
+            dense_store_row(v, inv, dst ? dst + 64 * q : nullptr);
+            if (a.o_res) dense_store_row<true>(v, inv, res ? res + 64 * q : nullptr);
           }
-          dense_store_rows(va, vb, inv, stg, valid ? a.o + row * D + 64 * u : nullptr);
-          if (a.o_res)
-            dense_store_rows<true>(va, vb, inv, stg,
-                                   valid ? a.o_res + row * D + 64 * u : nullptr);
+          if (valid && a.lse) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
         }
-        if (valid && a.lse) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        tc_fence_before();
       }
     }
-    tc_fence_before();
   }
   tc_fence_before();
   __syncthreads();
@@ -424,8 +470,8 @@ cudaError_t launch_t(const DenseArgs& a, const CUtensorMap& mq, const CUtensorMa
   static_assert(kBudget <= 65536, "register budgets exceed the register file");
   cudaError_t e = dense_prepare<k_dense_fwd<D, BIAS>>(kThreads, kBudget, FwdCfg<D, BIAS>::kSmem);
   if (e != cudaSuccess) return e;
-  k_dense_fwd<D, BIAS><<<(unsigned)a.nslots * a.hkv, kThreads, FwdCfg<D, BIAS>::kSmem, st>>>(mq, mk, mv,
-                                                                                       a);
+  const int grid = dense_grid(a);
+  k_dense_fwd<D, BIAS><<<grid, kThreads, FwdCfg<D, BIAS>::kSmem, st>>>(mq, mk, mv, a);
   return cudaGetLastError();
 }
 

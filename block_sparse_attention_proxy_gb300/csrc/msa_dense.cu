@@ -8,6 +8,7 @@ namespace msa {
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
 bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1) == 0; }
 
 // Token stride of a [T][heads][d] tensor: 0 means packed.  Rows of one token
@@ -81,7 +82,7 @@ DenseWorkspace dense_workspace(const DenseArgs& a) {
   w.stats = take((size_t)a.hq * a.T * sizeof(float2));
   if (a.nb > 0) {
     const size_t n = dense_slots(a.T, a.ndoc, a.tpt);
-    w.slots = take(n * a.hkv * a.nb * 256 * sizeof(float));
+    w.slots = take((size_t)kDenseMaxGrid * a.nb * 256 * sizeof(float));  // one per CTA
     w.parts = take(n * a.hq * a.nb * sizeof(float));
   }
   return w;
@@ -112,7 +113,7 @@ msa_status msa_dense_fwd(const msa_dense_params* p, const int32_t* cu_seqlens, c
   if (!cu_seqlens || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3)) return MSA_ERR_INVALID_ARG;
   for (const void* ptr : {(const void*)q, (const void*)k, (const void*)v, (const void*)o})
     if (!ptr || !aligned16(ptr)) return MSA_ERR_INVALID_ARG;
-  if (!aligned16(lse) || !aligned16(o_res)) return MSA_ERR_INVALID_ARG;
+  if (!aligned16(lse) || !aligned32(o_res) || !aligned32(o)) return MSA_ERR_INVALID_ARG;
   if (a.nb > 0 && (!bias || !aligned2(bias))) return MSA_ERR_INVALID_ARG;
   if (bind_device(&a.status) != cudaSuccess) return MSA_ERR_CUDA;
   a.cu = cu_seqlens;
@@ -148,6 +149,7 @@ msa_status msa_dense_bwd(const msa_dense_params* p, const int32_t* cu_seqlens, c
                           (const void*)o_res, (const void*)lse, (const void*)dO, (const void*)dq, (const void*)dk,
                           (const void*)dv})
     if (!ptr || !aligned16(ptr)) return MSA_ERR_INVALID_ARG;
+  if (!aligned32(dq) || !aligned32(dk) || !aligned32(dv)) return MSA_ERR_INVALID_ARG;
   const DenseWorkspace w = dense_workspace(a);
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255)) return MSA_ERR_INVALID_ARG;
   if (ws_bytes < w.total) return MSA_ERR_WORKSPACE;

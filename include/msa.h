@@ -252,6 +252,7 @@ msa_status msa_proxy_select_noalloc(const msa_params* params, const int32_t* cu_
  * projection), their heads are d elements apart.  Gradients are summed in fp32
  * and rounded once.
  *
+ *   - o, o_res, dq, dk and dv are aligned to 32 bytes; bias and dbias to 2.
  *   - Any hq / hkv from 1 to 64, hq <= 1024, d in {64, 128}, T < 2^27.
  *   - cu_seqlens may end before T (a padded batch): the rows behind the last
  *     document get zero o, dq, dk and dv and lse = -inf.
