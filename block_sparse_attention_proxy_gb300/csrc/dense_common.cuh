@@ -61,6 +61,10 @@ struct DenseArgs {
 // over the documents is needed.  ndoc + 1 documents: the last is the padding.
 __host__ __device__ inline int dense_slots(int T, int ndoc, int bt) { return T / bt + ndoc + 1; }
 
+// The same value in every lane (lane 0's), and known to the compiler to be: control flow on
+// it does not count as divergent, which would keep operands out of uniform registers.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 struct DenseItem {
   int doc, start, len, tile;  // document, its first token and length, tile inside it
 };
@@ -163,11 +167,11 @@ __device__ __forceinline__ bool dense_item(const DenseArgs& a, const DenseDocs& 
     }
     tile = s - (b0 / bt + doc);
   }
-  it.doc = doc;
-  it.start = b0;
-  it.len = b1 - b0;
-  it.tile = tile;
-  return tile >= 0 && (long long)tile * bt < it.len;
+  it.doc = uniform(doc);
+  it.start = uniform(b0);
+  it.len = uniform(b1 - b0);
+  it.tile = uniform(tile);
+  return it.tile >= 0 && (long long)it.tile * bt < it.len;
 }
 
 // Round k of a persistent CTA over `total` = slots x KV heads items, sorted by falling work:
@@ -323,7 +327,6 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
 // every operand was moved over by itself.  Here all lanes compute the
 // (warp-uniform) operands and the instruction is predicated on one elected lane.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t e;
   asm volatile(

@@ -20,8 +20,12 @@ static_assert(kBudget <= 65536, "register budgets exceed the register file");
 // ---------------------------------------------------------------------------
 // dQ: items of 128 packed rows against their keys, tile by tile; one persistent CTA per SM.
 // Warps 0-3 and 4-7 take 64 of a tile's 128 columns each (a row is one TMEM
-// lane of both); warp 8 loads, warp 9 issues the MMAs, warps 10 and 11 bring the next
-// item's {-lse, D} (and leave them for dK, dV).  S has two TMEM buffers: while the
+// lane of both); warp 8 loads, warp 9 issues the MMAs.  {-lse, D = rowsum(dO o O)} of an
+// item's rows (which dK, dV need too) come at d = 128 from warps 10 and 11, an item ahead,
+// and at d = 64, where those two could not keep up with short items, from the softmax warps,
+// which load the next item's rows before they store an item's dQ (16384 tokens, 32 heads,
+// d 128: 1.96 against 2.04 ms; 61 documents of 24001 tokens, 8 heads, d 64: 98 against 62 us).
+// S has two TMEM buffers: while the
 // softmax warps turn S(n), dP(n) into dS(n) (bf16, over S(n)'s columns), S(n + 1) is
 // computed, and dP(n + 1) as soon as dP(n) has been read.
 // ---------------------------------------------------------------------------
@@ -43,6 +47,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                const __grid_constant__ DenseArgs a) {
   using C = DqCfg<D, BIAS>;
   constexpr int NCH = D / 64, NK = C::kNK, NV = C::kNV;
+  constexpr bool kRowWarps = D == 128;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
   uint8_t* sO = sQ + C::kTile;
@@ -225,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(el, bar(B_END));
         drain_bar(bar(B_END), 0);
       }
-    } else {
+    } else if (kRowWarps) {
       // ------------------------------ row statistics ------------------------------
       // {-lse log2(e), D} of an item's rows, D = rowsum(dO o O) with O = o + o_res: D/8
       // lanes to a row, 16 bytes each; 64 rows per warp, 8 (D = 128: 4) at a time per step.
@@ -295,21 +300,78 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* my = BIAS ? a.slots + (size_t)blockIdx.x * a.nb * 256 + w * 128 + r : nullptr;
     bool dead = false;
     int X = 0, items = 0, table_of = -1;  // table_of: KV head the bias tables are of
-    for (int k = 0; k < rounds; ++k) {
-      Work wk;
-      if (!work(k, wk)) continue;
-      float* part = BIAS ? a.parts + ((size_t)wk.slot * a.hq + wk.g * a.G) * a.nb : nullptr;
-      if (wk.N == 0) {
-        if (BIAS)
+    // D of 16 rows per warp: D/8 lanes to a row, 16 bytes each
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kSteps = 16 / kRows;
+    const int dr0 = (warp & 3) * 32 + 16 * w + lane / kLanes, part_ = lane % kLanes;
+    uint4 xo[kSteps], xr[kSteps], xd[kSteps];
+    float xl[kSteps];
+    auto load_rows = [&](const Work& wk, bool have) {
+      const int toks = min(a.tpt, wk.it.len - wk.q0);  // tokens of the item
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u) {
+        xo[u] = xr[u] = xd[u] = make_uint4(0, 0, 0, 0);
+        xl[u] = 0.f;
+      }
+      if (!have) return;
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u) {
+        // rows behind the last one read an earlier row, so that no load is conditional
+        const int rr = dr0 + u * kRows, tok = min(rr / a.G, toks - 1), hh = wk.g * a.G + rr % a.G;
+        const size_t t = (size_t)(wk.it.start + wk.q0 + tok), at = t * a.hq + hh;
+        xo[u] = ld_nc_v4(a.o + at * D + part_ * 8);
+        xr[u] = ld_nc_v4(a.o_res + at * D + part_ * 8);
+        xd[u] = ld_nc_v4(a.d_o + t * a.do_stride + (size_t)hh * D + part_ * 8);
+        xl[u] = __ldg(a.lse + at);
+      }
+    };
+    auto row_stats = [&](const Work& wk) {
+      const int toks = min(a.tpt, wk.it.len - wk.q0);
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u) {
+        auto dot = [](uint32_t o, uint32_t res, uint32_t d_o) {
+          return (bf16_lo(o) + bf16_lo(res)) * bf16_lo(d_o) +
+                 (bf16_hi(o) + bf16_hi(res)) * bf16_hi(d_o);
+        };
+        float s = (dot(xo[u].x, xr[u].x, xd[u].x) + dot(xo[u].y, xr[u].y, xd[u].y)) +
+                  (dot(xo[u].z, xr[u].z, xd[u].z) + dot(xo[u].w, xr[u].w, xd[u].w));
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (part_ == 0) {
+          const int rr = dr0 + u * kRows, tok = rr / a.G;
+          const bool there = tok < toks;
+          const float2 v = make_float2(
+              there && xl[u] != -INFINITY ? -xl[u] * kLog2E : -INFINITY, there ? s : 0.f);
+          sRow[rr] = v;
+          if (there)
+            a.stats[(size_t)(wk.g * a.G + rr % a.G) * a.T + wk.it.start + wk.q0 + tok] = v;
+        }
+      }
+      named_bar_sync(1, 256);
+    };
+    // the next item with something to compute, from round k on; what has none is written
+    auto seek = [&](int& k, Work& wk) -> bool {
+      for (; k < rounds; ++k) {
+        if (!work(k, wk)) continue;
+        if (wk.N > 0) return true;
+        if (BIAS) {
+          float* part = a.parts + ((size_t)wk.slot * a.hq + wk.g * a.G) * a.nb;
           for (int x = threadIdx.x; x < a.G * a.nb; x += 256) part[x] = 0.f;
+        }
         if (wk.it.doc == a.ndoc) {  // padding behind the last document: zero rows
           const int n = min(a.tpt, wk.it.len - wk.q0) * a.G, rr = (int)threadIdx.x;
           if (rr < n)
             dense_zero_row(a.dq + ((size_t)(wk.it.start + wk.q0 + rr / a.G) * a.hq +
                                    wk.g * a.G + rr % a.G) * D, D);
         }
-        continue;
       }
+      return false;
+    };
+    int k = 0;
+    Work wk;
+    bool have = seek(k, wk);
+    if (!kRowWarps) load_rows(wk, have);
+    while (have) {
+      float* part = BIAS ? a.parts + ((size_t)wk.slot * a.hq + wk.g * a.G) * a.nb : nullptr;
       if (BIAS && table_of != wk.g) {
         dense_bias_tables<true>(a, sB, wk.g);
         table_of = wk.g;
@@ -317,13 +379,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int qi = wk.q0 + ti;
       const bool valid = ti < a.tpt && qi < wk.it.len;
       const size_t row = (size_t)(wk.it.start + qi) * a.hq + wk.g * a.G + hl;
-      const int rb = items & 1;
-      dead = dead || !wait_bar_warp(bar(B_RF + rb), (items >> 1) & 1, abort_flag, a.status,
-                                    wait_site(kKerDenseDq, B_RF + rb, items));
-      const float2 st_ = sRow[rb * 128 + r];
-      const float nl = st_.x, dsum = st_.y;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_RE + rb));
+      const int rb = kRowWarps ? items & 1 : 0;
+      if (kRowWarps)
+        dead = dead || !wait_bar_warp(bar(B_RF + rb), (items >> 1) & 1, abort_flag, a.status,
+                                      wait_site(kKerDenseDq, B_RF + rb, items));
+      else
+        row_stats(wk);
+      const float nl = sRow[rb * 128 + r].x, dsum = sRow[rb * 128 + r].y;
+      if (kRowWarps) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_RE + rb));
+      }
       float acc = 0.f;
       uint64_t done = 0;                 // buckets stored
       int bk = a.nb - 1, stk = INT_MAX;  // bucket of the next scores and its first distance
@@ -538,6 +604,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      ++k;
+      have = seek(k, wk);
+      if (!kRowWarps) load_rows(wk, have);
       dead = dead || !wait_bar_warp(bar(B_DQ), (items - 1) & 1, abort_flag, a.status,
                                     wait_site(kKerDenseDq, B_DQ, items));
       tc_fence_after();
@@ -1016,7 +1085,10 @@ cudaError_t launch_t(const CUtensorMap& mqp, const CUtensorMap& mop, const CUten
   k_dense_dq<D, BIAS><<<dense_grid(a), kThreads, DqCfg<D, BIAS>::kSmem, st>>>(mqp, mop, mk, mv, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   a.nslots = dense_slots(a.T, a.ndoc, 128);
-  k_dense_dkv<D, BIAS><<<dense_grid(a), kThreads, DkvCfg<D, BIAS>::kSmem, st>>>(mq, mo, mk, mv, a);
+  // With a bias persistent CTAs keep their tables; without one an item per CTA, started by the
+  // hardware where an SM is free, balances better (packed 32768 tokens, 16 heads: 795
+  // against 835 us).
+  k_dense_dkv<D, BIAS><<<BIAS ? dense_grid(a) : a.nslots * a.hkv, kThreads, DkvCfg<D, BIAS>::kSmem, st>>>(mq, mo, mk, mv, a);
   return cudaGetLastError();
 }
 

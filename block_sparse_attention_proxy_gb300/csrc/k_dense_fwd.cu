@@ -18,11 +18,15 @@
 // At d = 64 a product over 128 keys takes half as long while the exponentials take the
 // same time, so the wait for the next S would show: there the softmax works on 64 keys
 // at a time (S, P and their barriers in halves), and one half's products run under the
-// other half's exponentials.
+// other half's exponentials; one warp issues the products of each row tile, so that what a
+// hand-off costs it (some hundred cycles) overlaps the other's (10007 tokens, 12 heads:
+// 110 -> 95 us), and the exponentials start ahead of the maximum (95 -> 86 us).  At d = 128,
+// where the tensor core is the bound, two issuing warps share it out between the tiles and
+// finish both later (32768 tokens, 8 heads: 1.21 -> 1.74 ms with them).
 //
 // Roles (384 threads): warps 0-3 and 4-7 are the softmax warpgroups of tile 0
 // and 1, so one tile's softmax overlaps the other's products; warp 8 loads;
-// warp 9 issues the MMAs: P V of a tile, then its next S, tile after tile.
+// warp 9 (and 10) issues the MMAs: P V of a tile, then its next S.
 // tcgen05 products of one thread run in issue order, so S(n + 1) may be issued
 // right behind the product that still reads P(n) from the same columns.
 #include "dense_common.cuh"
@@ -38,6 +42,7 @@ template <int D, bool BIAS>
 struct FwdCfg {
   static constexpr int kTile = 128 * D * 2;
   static constexpr int kHalves = D == 128 ? 1 : 2;  // softmax steps per key tile
+  static constexpr int kMmaWarps = D == 128 ? 1 : 2;
   // K and V tiles in flight; with a bias its tables take the place of one
   static constexpr int kRing = D == 128 ? (BIAS ? 4 : 5) : 8;
   static constexpr int kSmem = (2 + kRing) * kTile + 256 + (BIAS ? (int)sizeof(DenseBias) : 0);
@@ -73,10 +78,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(bar(B_Q), 1);
-    mbar_init(bar(B_QE), 1);
+    mbar_init(bar(B_QE), C::kMmaWarps);
     for (int s = 0; s < NR; ++s) {
       mbar_init(bar(B_F + s), 1);
-      mbar_init(bar(B_E + s), 1);
+      mbar_init(bar(B_E + s), C::kMmaWarps);
     }
     for (int t = 0; t < 2; ++t) {
       for (int h = 0; h < 2; ++h) {
@@ -85,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(bar(B_PV + 2 * t + h), 1);
       }
     }
-    mbar_init(bar(B_END), 1);
+    mbar_init(bar(B_END), C::kMmaWarps);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -167,8 +172,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (items > 0) drain_bar(bar(B_Q), (items - 1) & 1);
         for (int y = max(0, x - NR); y < x; ++y) drain_bar(bar(B_F + y % NR), (y / NR) & 1);
       }
-    } else if (warp == 9) {
+    } else if (warp < 9 + C::kMmaWarps) {
       // ------------------------------ MMA issue ----------------------------------
+      // One warp for both row tiles (d = 128), or one for each (d = 64).
+      const int t0 = warp - 9, t1 = C::kMmaWarps == 1 ? 2 : warp - 8;
       constexpr uint32_t idS = make_idesc_bf16(128, W, false, false);
       constexpr uint32_t idO = make_idesc_bf16(128, D, false, true);
       const uint32_t el = elect_one(), tm = uniform(tbase);
@@ -196,8 +203,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-          if (h < nu0) issue_s(0, x, h, (U[0] + h) % NH);
-          if (h < nu1) issue_s(1, x, h, (U[1] + h) % NH);
+          if (t0 == 0 && h < nu0) issue_s(0, x, h, (U[0] + h) % NH);
+          if (t1 == 2 && h < nu1) issue_s(1, x, h, (U[1] + h) % NH);
         }
         mma_commit(el, bar(B_E + x % NR));
         if (nk == 1) mma_commit(el, bar(B_QE));
@@ -210,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int ht = 0; ht < 2 * NH; ++ht) {
             const int h = ht >> 1, t = ht & 1, u = n * NH + h, nut = t ? nu1 : nu0;
-            if (!ok || u >= nut) continue;
+            if (!ok || t < t0 || t >= t1 || u >= nut) continue;
             const int Ut = U[t] + u, b = Ut % NH;
             const uint32_t po = tm + 256 + D * t, pa = tm + 128 * t + W * b;
 #pragma unroll
@@ -367,6 +374,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             m4[y] = fmaxf(m4[y], __uint_as_float(x[W / 4 * (y + 1) - 1]));
           }
           const float mx = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), mul, add);
+          // At d = 64 the first half's exponentials do not wait for the maximum: they take the
+          // running m, and again the new one in the rare step that moves it.
+          constexpr bool kEarly = D == 64;
+          const f32x2 mul2_ = pack2(mul, mul);
+          f32x2 ls[2];
+          uint32_t wp[W / 2];
+          auto exps = [&](int part, float sub) {
+            const f32x2 sub2 = pack2(sub, sub);
+#pragma unroll
+            for (int e = 0; e < W; e += 2) {
+              const int of = e / (W / 2);
+              if (of == part) {
+                float p0, p1;
+                unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), mul2_, sub2),
+                        p0, p1);
+                p0 = ex2_approx(p0);
+                p1 = ex2_approx(p1);
+                ls[(e >> 1) & 1] = add2(ls[(e >> 1) & 1], pack2(p0, p1));
+                wp[e / 2] = pack_bf16(p0, p1);
+              }
+            }
+          };
+          ls[0] = ls[1] = 0ull;
+          float sub = add - (m == -INFINITY ? 0.f : m);
+          if (kEarly) exps(0, sub);
           const bool grow = mx > m + kRescale || (m == -INFINITY && mx > m);
           if (__any_sync(0xffffffffu, grow)) {
             const float m_new = grow ? mx : m;
@@ -391,42 +423,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
             }
+            sub = add - (m == -INFINITY ? 0.f : m);
+            if (kEarly) {
+              ls[0] = ls[1] = 0ull;
+              exps(0, sub);
+            }
           }
-          const float sub = add - (m == -INFINITY ? 0.f : m);
-          const f32x2 mul2_ = pack2(mul, mul), sub2 = pack2(sub, sub);
-          f32x2 ls[2] = {0ull, 0ull};
-#pragma unroll
-          for (int q = 0; q < W / 64; ++q) {
-            uint32_t w[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int e = 64 * q + 2 * i;
-              float p0, p1;
-              unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), mul2_, sub2), p0,
-                      p1);
-              p0 = ex2_approx(p0);
-              p1 = ex2_approx(p1);
-              ls[i & 1] = add2(ls[i & 1], pack2(p0, p1));
-              w[i] = pack_bf16(p0, p1);
-            }
-            tmem_st32_async(ts + W * b + 32 * q, w);
+          if (!kEarly) exps(0, sub);
+          if (NH == 1) {
+            // the product over the first 64 keys runs while the others are computed
+            tmem_st32_async(ts, *reinterpret_cast<uint32_t(*)[32]>(wp));
             tmem_wait_st();
-            // the product over the first 64 keys starts while the rest is computed
-            if (q + 1 < W / 64) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar(B_P + 2 * t));
-            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_P + 2 * t));
+          }
+          exps(1, sub);
+          if (NH == 1) {
+            tmem_st32_async(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(wp + W / 4));
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_P + 2 * t + 1));
+          }
+          if (NH == 2) {
+            tmem_st32_async(ts + W * b, *reinterpret_cast<uint32_t(*)[32]>(wp));
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_P + 2 * t + b));
           }
           float l0, l1;
           unpack2(add2(ls[0], ls[1]), l0, l1);
           l += l0 + l1;
-        } else if (NH == 1 && lane == 0) {
-          mbar_arrive(bar(B_P + 2 * t));
+        } else {
+          if (lane == 0)
+            for (int q = 0; q < 2 / NH; ++q) mbar_arrive(bar(B_P + 2 * t + (NH == 1 ? q : b)));
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_P + 2 * t + (NH == 1 ? 1 : b)));
       }
       if (nut > 0) {
         const int b = B_PV + 2 * t + ((U - 1) & 1);
