@@ -65,6 +65,22 @@ __host__ __device__ inline int dense_slots(int T, int ndoc, int bt) { return T /
 // it does not count as divergent, which would keep operands out of uniform registers.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
+// wait_bar_warp, with a plain test first: the suspending wait costs some hundred cycles even
+// where the phase has completed already, which here is the common case.
+__device__ __forceinline__ bool dense_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                           unsigned* status, uint32_t site) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  if (__all_sync(0xffffffffu, ok)) return true;
+  return wait_bar_warp(bar, parity, abort_flag, status, site);
+}
+
 struct DenseItem {
   int doc, start, len, tile;  // document, its first token and length, tile inside it
 };

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; ok && k < rounds; ++k) {
         Work w;
         if (!work(k, w) || w.tiles == 0) continue;
-        if (items > 0 && !(ok = wait_bar_warp(bar(B_QE), (items - 1) & 1, abort_flag, a.status,
+        if (items > 0 && !(ok = dense_wait(bar(B_QE), (items - 1) & 1, abort_flag, a.status,
                                               wait_site(kKerDenseFwd, B_QE, items))))
           break;
         const int nq = w.nu[1] ? 2 : 1;
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++items;
         for (int y = 0; y < 2 * w.tiles; ++y, ++x) {
           const int s = x % NR;
-          if (x >= NR && !(ok = wait_bar_warp(bar(B_E + s), ((x / NR) & 1) ^ 1, abort_flag,
+          if (x >= NR && !(ok = dense_wait(bar(B_E + s), ((x / NR) & 1) ^ 1, abort_flag,
                                               a.status, wait_site(kKerDenseFwd, B_E + s, y >> 1))))
             break;
           if (lane == 0) {
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t q_lo = desc_lo(smem_u32(sQ), 16), k_lo = desc_lo(smem_u32(sKV), 16),
                      v_lo = desc_lo(smem_u32(sKV), 16384);
       auto wait = [&](int b, uint32_t par, int n) {
-        return wait_bar_warp(bar(b), par, abort_flag, a.status, wait_site(kKerDenseFwd, b, n));
+        return dense_wait(bar(b), par, abort_flag, a.status, wait_site(kKerDenseFwd, b, n));
       };
       auto wait_full = [&](int x) { return wait(B_F + x % NR, (x / NR) & 1, x >> 1); };
       int x = 0, items = 0, U[2] = {0, 0};  // ring position, items, steps of each tile so far
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           one = __all_sync(0xffffffffu, bk == 0 || stk <= rel - (W - 1));
           near = __all_sync(0xffffffffu, rel < a.lut_w);
         }
-        dead = dead || !wait_bar_warp(bar(B_S + 2 * t + b), par, abort_flag, a.status,
+        dead = dead || !dense_wait(bar(B_S + 2 * t + b), par, abort_flag, a.status,
                                       wait_site(kKerDenseFwd, B_S + 2 * t + b, u));
         tc_fence_after();
         if (!dead) {
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (u > 0) {
               // O is complete up to the last step once that step's P V product is
               const int pv = B_PV + 2 * t + ((U - 1) & 1);
-              dead = dead || !wait_bar_warp(bar(pv), ((U - 1) >> 1) & 1, abort_flag, a.status,
+              dead = dead || !dense_wait(bar(pv), ((U - 1) >> 1) & 1, abort_flag, a.status,
                                             wait_site(kKerDenseFwd, pv, u));
               tc_fence_after();
               if (!dead) {
@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (nut > 0) {
         const int b = B_PV + 2 * t + ((U - 1) & 1);
-        dead = dead || !wait_bar_warp(bar(b), ((U - 1) >> 1) & 1, abort_flag, a.status,
+        dead = dead || !dense_wait(bar(b), ((U - 1) >> 1) & 1, abort_flag, a.status,
                                       wait_site(kKerDenseFwd, b, nut));
         tc_fence_after();
         if (!dead) {
