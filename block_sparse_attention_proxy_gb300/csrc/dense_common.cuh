@@ -17,6 +17,8 @@ namespace msa {
 
 constexpr int kDenseMaxBuckets = 64;
 constexpr int kDenseMaxGroup = 64;     // query heads per KV head
+// One item over all keys of a document of this length ends within the bounded waits.
+constexpr int kDenseMaxTokens = 1 << 25;
 constexpr int kDenseMaxGrid = 160;     // CTAs of a persistent kernel
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;

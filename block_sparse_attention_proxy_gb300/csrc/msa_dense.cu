@@ -27,7 +27,8 @@ msa_status check_dense(const msa_dense_params* p, DenseShape* s, DenseArgs* a) {
   if (p->num_buckets < 0 || (p->num_buckets > 0 && !p->bucket_starts)) return MSA_ERR_INVALID_ARG;
   if (p->d != 64 && p->d != 128) return MSA_ERR_UNSUPPORTED;
   if (p->hq / p->hkv > kDenseMaxGroup || p->hq > 1024) return MSA_ERR_UNSUPPORTED;
-  if (p->total_tokens >= kMaxTokens || p->num_docs >= kMaxTokens) return MSA_ERR_UNSUPPORTED;
+  if (p->total_tokens >= kDenseMaxTokens || p->num_docs >= kDenseMaxTokens)
+    return MSA_ERR_UNSUPPORTED;
   if (p->num_buckets > kDenseMaxBuckets) return MSA_ERR_UNSUPPORTED;
   *a = DenseArgs{};
   for (int b = 0; b < p->num_buckets; ++b) {

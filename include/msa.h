@@ -253,7 +253,8 @@ msa_status msa_proxy_select_noalloc(const msa_params* params, const int32_t* cu_
  * and rounded once.
  *
  *   - o, o_res, dq, dk and dv are aligned to 32 bytes; bias and dbias to 2.
- *   - Any hq / hkv from 1 to 64, hq <= 1024, d in {64, 128}, T < 2^27.
+ *   - Any hq / hkv from 1 to 64, hq <= 1024, d in {64, 128}, T and the number of
+ *     documents below 2^25.
  *   - cu_seqlens may end before T (a padded batch): the rows behind the last
  *     document get zero o, dq, dk and dv and lse = -inf.
  *   - Documents do not affect one another, whatever values they hold.

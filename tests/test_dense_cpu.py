@@ -102,7 +102,7 @@ OK = dict(total_tokens=1000, num_docs=3, hq=8, hkv=2, d=64)
 
 @pytest.mark.parametrize("change", [
     dict(num_docs=0), dict(total_tokens=-1), dict(hq=7), dict(hkv=0), dict(hq=0), dict(d=96),
-    dict(hq=130, hkv=2), dict(total_tokens=1 << 27), dict(softmax_scale=0.0),
+    dict(hq=130, hkv=2), dict(total_tokens=1 << 25), dict(num_docs=1 << 25), dict(softmax_scale=0.0),
     dict(softmax_scale=-1.0), dict(softmax_scale=float("nan")), dict(softmax_scale=float("inf")),
     dict(bucket_starts=(1, 2)), dict(bucket_starts=(0, 2, 2)), dict(bucket_starts=(0, 5, 4)),
     dict(bucket_starts=tuple(range(65))), dict(flags=1), dict(q_stride=8 * 64 - 8),
@@ -142,6 +142,10 @@ def test_pointers_and_workspace_refused_on_the_host(m):
         assert bwd(good, i) == 1
     assert bwd(table, 4) == 1 and bwd(table, 12) == 1
     assert bwd(good, 13, 0x1010) == 1
+    for i in (5, 6):  # o, o_res: 32 bytes
+        assert fwd(good, i, 0x1010) == 1
+    for i in (9, 10, 11):  # dq, dk, dv
+        assert bwd(good, i, 0x1010) == 1
     assert bwd(good, size=need - 1) == 3
     empty = m.make_dense_params(**{**OK, "total_tokens": 0})
     assert fwd(empty) == 0 and bwd(empty) == 0
@@ -154,3 +158,5 @@ def test_front_end_refusals(m):
         m.dense_attention(q, q, q, cu)
     with pytest.raises(TypeError):
         m.dense_attention(q.float(), q, q, cu)
+    with pytest.raises(TypeError):
+        m.dense_attention(q, q, None, cu)

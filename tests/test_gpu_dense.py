@@ -48,6 +48,8 @@ def _compare(x, lens, starts=None, scale=1.0):
 
 
 LENS = {
+    "64 documents": [5 * i % 131 for i in range(64)],
+    "65 documents": [129] + [7 * i % 97 for i in range(64)],
     "one": [1], "two": [2], "tile": [128], "tile+1": [129], "long": [777],
     "ragged": [1, 3, 127, 128, 129, 255, 257, 64], "empty": [0, 5, 0, 300, 0, 0, 1, 0],
     "many": [7] * 70,
@@ -218,8 +220,8 @@ def test_calls_on_two_streams():
 
 
 def test_two_captured_graphs_replay_on_new_inputs():
-    """Forward and backward captured twice, replayed interleaved with new values and new
-    document boundaries, one graph while an eager graph of the same leaves is alive."""
+    """Forward and backward captured twice and replayed with new values and new document
+    boundaries."""
     starts = (0, 3, 17, 300)
     shapes = [([300, 212], [500, 12]), ([77, 435], [0, 512])]
     xs = [_inputs(a, 4, 2, 64, 20 + i, nb=4) for i, (a, _) in enumerate(shapes)]
@@ -264,6 +266,57 @@ def test_offsets_beyond_32_bits():
     for name in want:
         assert torch.equal(got[name][t0:], want[name]), name
     assert _status() == 0
+
+
+def test_more_items_than_the_gpu_holds():
+    """Persistent CTAs go through several items of different lengths and KV heads, with
+    partly filled rounds; ragged documents, 7 KV heads (no divisor of the SM count)."""
+    lens = [1900, 3, 640, 1281, 129, 2000, 77]
+    x = _inputs(lens, 21, 7, 64, 18, nb=9)
+    _compare(x, lens, (0, 1, 3, 9, 27, 81, 243, 729, 1500))
+
+
+def test_front_end_refusals():
+    from block_sparse_attention_proxy_gb300 import MsaError, dense_attention
+
+    x = _inputs([64], 4, 2, 64, 19, nb=3)
+    call = lambda **c: dense_attention(**{  # noqa: E731
+        **dict(q=x["q"], k=x["k"], v=x["v"], cu_seqlens=x["cu"]), **c})
+    for wrong, error in [
+            (dict(q=x["q"].float()), TypeError), (dict(cu_seqlens=x["cu"].float()), TypeError),
+            (dict(cu_seqlens=x["cu"].cpu()), ValueError), (dict(k=x["k"][:32]), ValueError),
+            (dict(v=x["v"][:, :1]), ValueError), (dict(q=x["q"][:, :, 0]), ValueError),
+            (dict(bias=x["bias"]), ValueError), (dict(bucket_starts=(0, 1, 2)), ValueError),
+            (dict(bias=x["bias"], bucket_starts=(0, 1)), ValueError),
+            (dict(bias=x["bias"].float(), bucket_starts=(0, 1, 2)), TypeError),
+            (dict(bias=x["bias"], bucket_starts=(0, 2, 1)), MsaError),
+            (dict(q=x["q"][:, :3]), MsaError), (dict(softmax_scale=0.0), MsaError),
+            (dict(softmax_scale=float("nan")), MsaError),
+            (dict(q=x["q"][..., :32], k=x["k"][..., :32], v=x["v"][..., :32]), MsaError)]:
+        with pytest.raises(error):
+            call(**wrong)
+    try:
+        call(softmax_scale=-1.0)
+    except MsaError as e:
+        assert e.status == 1
+    assert _status() == 0
+
+
+def test_graph_is_kept_and_differentiable_once():
+    from block_sparse_attention_proxy_gb300 import dense_attention
+
+    x = _inputs([150], 4, 2, 64, 20)
+    q = x["q"].detach().requires_grad_(True)
+    o = dense_attention(q, x["k"], x["v"], x["cu"])
+    a = torch.autograd.grad(o, q, x["do"], retain_graph=True)[0]
+    b = torch.autograd.grad(o, q, x["do"], create_graph=True)[0]
+    assert torch.equal(a, b)
+    with pytest.raises(RuntimeError):
+        b.float().sum().backward()
+    o = dense_attention(q, x["k"], x["v"], x["cu"])
+    x["k"].add_(1)  # changed in place before the backward
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(o, q, x["do"])
 
 
 def test_empty_batch():
