@@ -24,11 +24,65 @@ static_assert(kBudget <= 65536, "register budgets exceed the register file");
 // item's rows (which dK, dV need too) come at d = 128 from warps 10 and 11, an item ahead,
 // and at d = 64, where those two could not keep up with short items, from the softmax warps,
 // which load the next item's rows before they store an item's dQ (16384 tokens, 32 heads,
-// d 128: 1.96 against 2.04 ms; 61 documents of 24001 tokens, 8 heads, d 64: 98 against 62 us).
-// S has two TMEM buffers: while the
-// softmax warps turn S(n), dP(n) into dS(n) (bf16, over S(n)'s columns), S(n + 1) is
-// computed, and dP(n + 1) as soon as dP(n) has been read.
+// d 128: 1.96 ms from warps 10 and 11, 2.04 from the softmax warps; 61 documents of 24001
+// tokens, 8 heads, d 64: 98 and 62 us).
+// S has two TMEM buffers: while the softmax warps turn S(n), dP(n) into dS(n) (bf16, over
+// S(n)'s columns), S(n + 1) is computed, and dP(n + 1) as soon as dP(n) has been read.
 // ---------------------------------------------------------------------------
+// {-lse log2(e) (-inf: no key left), D} of packed rows of an item: rows first + u 256/D, u <
+// STEPS, D/8 lanes to a row, 16 bytes each, with O = o + o_res.  `load` only starts the loads.
+template <int D, int STEPS>
+struct RowStats {
+  static constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  uint4 xo[STEPS], xr[STEPS], xd[STEPS];
+  float lse[STEPS];
+  __device__ __forceinline__ void load(const DenseArgs& a, const DenseItem& it, int q0, int g,
+                                       int first) {
+    const int toks = min(a.tpt, it.len - q0), at = (threadIdx.x & 31) % kLanes * 8;
+#pragma unroll
+    for (int u = 0; u < STEPS; ++u) {
+      // rows behind the last one read an earlier row, so that no load is conditional
+      const int rr = first + u * kRows, tok = min(rr / a.G, toks - 1), hh = g * a.G + rr % a.G;
+      const size_t t = (size_t)(it.start + q0 + tok), row = t * a.hq + hh;
+      xo[u] = ld_nc_v4(a.o + row * D + at);
+      xr[u] = ld_nc_v4(a.o_res + row * D + at);
+      xd[u] = ld_nc_v4(a.d_o + t * a.do_stride + (size_t)hh * D + at);
+      lse[u] = __ldg(a.lse + row);
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int u = 0; u < STEPS; ++u) {
+      xo[u] = xr[u] = xd[u] = make_uint4(0, 0, 0, 0);
+      lse[u] = 0.f;
+    }
+  }
+  // to `rows` (by packed row) and to a.stats
+  __device__ __forceinline__ void store(const DenseArgs& a, const DenseItem& it, int q0, int g,
+                                        int first, float2* rows) const {
+    const int toks = min(a.tpt, it.len - q0);
+    auto dot = [](uint32_t o, uint32_t res, uint32_t d_o) {
+      return (bf16_lo(o) + bf16_lo(res)) * bf16_lo(d_o) +
+             (bf16_hi(o) + bf16_hi(res)) * bf16_hi(d_o);
+    };
+#pragma unroll
+    for (int u = 0; u < STEPS; ++u) {
+      float s = (dot(xo[u].x, xr[u].x, xd[u].x) + dot(xo[u].y, xr[u].y, xd[u].y)) +
+                (dot(xo[u].z, xr[u].z, xd[u].z) + dot(xo[u].w, xr[u].w, xd[u].w));
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      const int rr = first + u * kRows, tok = rr / a.G;
+      if ((threadIdx.x & 31) % kLanes == 0) {
+        const bool there = tok < toks;
+        const float2 v = make_float2(there && lse[u] != -INFINITY ? -lse[u] * kLog2E : -INFINITY,
+                                     there ? s : 0.f);
+        rows[rr] = v;
+        if (there) a.stats[(size_t)(g * a.G + rr % a.G) * a.T + it.start + q0 + tok] = v;
+      }
+    }
+  }
+};
+
 template <int D, bool BIAS>
 struct DqCfg {
   static constexpr int kTile = 128 * D * 2;
@@ -232,10 +286,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (kRowWarps) {
       // ------------------------------ row statistics ------------------------------
-      // {-lse log2(e), D} of an item's rows, D = rowsum(dO o O) with O = o + o_res: D/8
-      // lanes to a row, 16 bytes each; 64 rows per warp, 8 (D = 128: 4) at a time per step.
-      constexpr int kLanes = D / 8, kRows = 32 / kLanes, kSteps = 4;
-      const int part_ = lane % kLanes;
+      // 64 rows per warp
+      using Stats = RowStats<D, 4>;
       int items = 0;
       bool ok = true;
       for (int k = 0; ok && k < rounds; ++k) {
@@ -243,44 +295,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!work(k, w) || w.N == 0) continue;
         const int b = items & 1;
         if (items >= 2 && !(ok = dense_wait(bar(B_RE + b), ((items >> 1) & 1) ^ 1, abort_flag,
-                                               a.status, wait_site(kKerDenseDq, B_RE + b, items))))
+                                            a.status, wait_site(kKerDenseDq, B_RE + b, items))))
           break;
-        const int toks = min(a.tpt, w.it.len - w.q0);  // tokens of the item
 #pragma unroll 1
-        for (int r0 = (warp - 10) * 64; r0 < (warp - 9) * 64; r0 += kRows * kSteps) {
-          uint4 xo[kSteps], xr[kSteps], xd[kSteps];
-          float lse[kSteps];
-#pragma unroll
-          for (int u = 0; u < kSteps; ++u) {
-            // rows behind the last one read an earlier row, so that no load is conditional
-            const int rr = r0 + u * kRows + lane / kLanes, tok = min(rr / a.G, toks - 1);
-            const int hh = w.g * a.G + rr % a.G;
-            const size_t t = (size_t)(w.it.start + w.q0 + tok), row = t * a.hq + hh;
-            xo[u] = ld_nc_v4(a.o + row * D + part_ * 8);
-            xr[u] = ld_nc_v4(a.o_res + row * D + part_ * 8);
-            xd[u] = ld_nc_v4(a.d_o + t * a.do_stride + (size_t)hh * D + part_ * 8);
-            lse[u] = __ldg(a.lse + row);
-          }
-#pragma unroll
-          for (int u = 0; u < kSteps; ++u) {
-            auto dot = [](uint32_t o, uint32_t res, uint32_t d_o) {
-              return (bf16_lo(o) + bf16_lo(res)) * bf16_lo(d_o) +
-                     (bf16_hi(o) + bf16_hi(res)) * bf16_hi(d_o);
-            };
-            float s = (dot(xo[u].x, xr[u].x, xd[u].x) + dot(xo[u].y, xr[u].y, xd[u].y)) +
-                      (dot(xo[u].z, xr[u].z, xd[u].z) + dot(xo[u].w, xr[u].w, xd[u].w));
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            const int rr = r0 + u * kRows + lane / kLanes, tok = rr / a.G;
-            if (part_ == 0) {
-              const bool there = tok < toks;
-              const float2 v = make_float2(
-                  there && lse[u] != -INFINITY ? -lse[u] * kLog2E : -INFINITY, there ? s : 0.f);
-              sRow[b * 128 + rr] = v;
-              if (there)
-                a.stats[(size_t)(w.g * a.G + rr % a.G) * a.T + w.it.start + w.q0 + tok] = v;
-            }
-          }
+        for (int r0 = (warp - 10) * 64; r0 < (warp - 9) * 64; r0 += Stats::kRows * 4) {
+          const int first = r0 + lane / Stats::kLanes;
+          Stats x;
+          x.load(a, w.it, w.q0, w.g, first);
+          x.store(a, w.it, w.q0, w.g, first, sRow + b * 128);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_RF + b));
@@ -300,54 +322,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* my = BIAS ? a.slots + (size_t)blockIdx.x * a.nb * 256 + w * 128 + r : nullptr;
     bool dead = false;
     int X = 0, items = 0, table_of = -1;  // table_of: KV head the bias tables are of
-    // D of 16 rows per warp: D/8 lanes to a row, 16 bytes each
-    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kSteps = 16 / kRows;
-    const int dr0 = (warp & 3) * 32 + 16 * w + lane / kLanes, part_ = lane % kLanes;
-    uint4 xo[kSteps], xr[kSteps], xd[kSteps];
-    float xl[kSteps];
-    auto load_rows = [&](const Work& wk, bool have) {
-      const int toks = min(a.tpt, wk.it.len - wk.q0);  // tokens of the item
-#pragma unroll
-      for (int u = 0; u < kSteps; ++u) {
-        xo[u] = xr[u] = xd[u] = make_uint4(0, 0, 0, 0);
-        xl[u] = 0.f;
-      }
-      if (!have) return;
-#pragma unroll
-      for (int u = 0; u < kSteps; ++u) {
-        // rows behind the last one read an earlier row, so that no load is conditional
-        const int rr = dr0 + u * kRows, tok = min(rr / a.G, toks - 1), hh = wk.g * a.G + rr % a.G;
-        const size_t t = (size_t)(wk.it.start + wk.q0 + tok), at = t * a.hq + hh;
-        xo[u] = ld_nc_v4(a.o + at * D + part_ * 8);
-        xr[u] = ld_nc_v4(a.o_res + at * D + part_ * 8);
-        xd[u] = ld_nc_v4(a.d_o + t * a.do_stride + (size_t)hh * D + part_ * 8);
-        xl[u] = __ldg(a.lse + at);
-      }
-    };
-    auto row_stats = [&](const Work& wk) {
-      const int toks = min(a.tpt, wk.it.len - wk.q0);
-#pragma unroll
-      for (int u = 0; u < kSteps; ++u) {
-        auto dot = [](uint32_t o, uint32_t res, uint32_t d_o) {
-          return (bf16_lo(o) + bf16_lo(res)) * bf16_lo(d_o) +
-                 (bf16_hi(o) + bf16_hi(res)) * bf16_hi(d_o);
-        };
-        float s = (dot(xo[u].x, xr[u].x, xd[u].x) + dot(xo[u].y, xr[u].y, xd[u].y)) +
-                  (dot(xo[u].z, xr[u].z, xd[u].z) + dot(xo[u].w, xr[u].w, xd[u].w));
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (part_ == 0) {
-          const int rr = dr0 + u * kRows, tok = rr / a.G;
-          const bool there = tok < toks;
-          const float2 v = make_float2(
-              there && xl[u] != -INFINITY ? -xl[u] * kLog2E : -INFINITY, there ? s : 0.f);
-          sRow[rr] = v;
-          if (there)
-            a.stats[(size_t)(wk.g * a.G + rr % a.G) * a.T + wk.it.start + wk.q0 + tok] = v;
-        }
-      }
-      named_bar_sync(1, 256);
-    };
+    // row statistics, 16 rows per warp
+    using Stats = RowStats<D, D / 16>;
+    const int dr0 = (warp & 3) * 32 + 16 * w + lane / Stats::kLanes;
+    Stats rs;
     // the next item with something to compute, from round k on; what has none is written
     auto seek = [&](int& k, Work& wk) -> bool {
       for (; k < rounds; ++k) {
@@ -369,7 +347,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     int k = 0;
     Work wk;
     bool have = seek(k, wk);
-    if (!kRowWarps) load_rows(wk, have);
+    auto next_stats = [&]() {
+      rs.clear();  // kept across the tile loop otherwise
+      if (have) rs.load(a, wk.it, wk.q0, wk.g, dr0);
+    };
+    if (!kRowWarps) next_stats();
     while (have) {
       float* part = BIAS ? a.parts + ((size_t)wk.slot * a.hq + wk.g * a.G) * a.nb : nullptr;
       if (BIAS && table_of != wk.g) {
@@ -380,11 +362,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool valid = ti < a.tpt && qi < wk.it.len;
       const size_t row = (size_t)(wk.it.start + qi) * a.hq + wk.g * a.G + hl;
       const int rb = kRowWarps ? items & 1 : 0;
-      if (kRowWarps)
+      if (kRowWarps) {
         dead = dead || !dense_wait(bar(B_RF + rb), (items >> 1) & 1, abort_flag, a.status,
-                                      wait_site(kKerDenseDq, B_RF + rb, items));
-      else
-        row_stats(wk);
+                                   wait_site(kKerDenseDq, B_RF + rb, items));
+      } else {
+        rs.store(a, wk.it, wk.q0, wk.g, dr0, sRow);
+        named_bar_sync(1, 256);
+      }
       const float nl = sRow[rb * 128 + r].x, dsum = sRow[rb * 128 + r].y;
       if (kRowWarps) {
         __syncwarp();
@@ -401,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool edge = __any_sync(0xffffffffu, rel < 63);
         auto wait = [&](int bb, uint32_t par) {
           dead = dead || !dense_wait(bar(bb), par, abort_flag, a.status,
-                                        wait_site(kKerDenseDq, bb, n));
+                                     wait_site(kKerDenseDq, bb, n));
           tc_fence_after();
         };
         bool one = true, near = false;  // see DenseBias
@@ -606,9 +590,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++k;
       have = seek(k, wk);
-      if (!kRowWarps) load_rows(wk, have);
+      if (!kRowWarps) next_stats();
       dead = dead || !dense_wait(bar(B_DQ), (items - 1) & 1, abort_flag, a.status,
-                                    wait_site(kKerDenseDq, B_DQ, items));
+                                 wait_site(kKerDenseDq, B_DQ, items));
       tc_fence_after();
       if (!dead && w < D / 64) {  // 64 columns each (d = 64: the first warpgroup)
         uint32_t v[64];
@@ -628,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------------------
 // dK, dV: items of 128 keys of a KV head against the queries of its group, head by head,
-// 128 queries at a time; one persistent CTA per SM.  Transposed products, so that a key is one TMEM lane:
+// 128 queries at a time.  Transposed products, so that a key is one TMEM lane:
 // S^T = K Q^T, dP^T = V dO^T, P^T and dS^T go back as bf16 over S^T and dP^T and
 // are read from TMEM as the A operand of dV += P^T dO and dK += dS^T Q (no
 // probability passes through shared memory).  The four accumulators fill TMEM,
@@ -641,8 +625,8 @@ template <int D, bool BIAS>
 struct DkvCfg {
   static constexpr int kTile = 128 * D * 2;
   // with a bias its tables take the place of a tile
-  static constexpr int kNQ = D == 128 ? (BIAS ? 2 : 3) : 4, kNO = D == 128 ? 2 : 4;  // Q and dO rings
-  static constexpr int kNS = 2;                                           // statistics ring
+  static constexpr int kNQ = D == 128 ? (BIAS ? 2 : 3) : 4, kNO = D == 128 ? 2 : 4;  // Q, dO rings
+  static constexpr int kNS = 2;  // statistics ring
   static constexpr int kSmem =
       (2 + kNQ + kNO) * kTile + kNS * 1024 + 256 + (BIAS ? (int)sizeof(DenseBias) : 0);
   static_assert(kSmem <= 232448, "shared memory budget");
@@ -1093,7 +1077,8 @@ cudaError_t launch_t(const CUtensorMap& mqp, const CUtensorMap& mop, const CUten
   // With a bias persistent CTAs keep their tables; without one an item per CTA, started by the
   // hardware where an SM is free, balances better (packed 32768 tokens, 16 heads: 795
   // against 835 us).
-  k_dense_dkv<D, BIAS><<<BIAS ? dense_grid(a) : a.nslots * a.hkv, kThreads, DkvCfg<D, BIAS>::kSmem, st>>>(mq, mo, mk, mv, a);
+  const int grid = BIAS ? dense_grid(a) : a.nslots * a.hkv;
+  k_dense_dkv<D, BIAS><<<grid, kThreads, DkvCfg<D, BIAS>::kSmem, st>>>(mq, mo, mk, mv, a);
   return cudaGetLastError();
 }
 

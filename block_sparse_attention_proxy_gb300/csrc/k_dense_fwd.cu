@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Work w;
         if (!work(k, w) || w.tiles == 0) continue;
         if (items > 0 && !(ok = dense_wait(bar(B_QE), (items - 1) & 1, abort_flag, a.status,
-                                              wait_site(kKerDenseFwd, B_QE, items))))
+                                           wait_site(kKerDenseFwd, B_QE, items))))
           break;
         const int nq = w.nu[1] ? 2 : 1;
         if (lane == 0) {
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int y = 0; y < 2 * w.tiles; ++y, ++x) {
           const int s = x % NR;
           if (x >= NR && !(ok = dense_wait(bar(B_E + s), ((x / NR) & 1) ^ 1, abort_flag,
-                                              a.status, wait_site(kKerDenseFwd, B_E + s, y >> 1))))
+                                           a.status, wait_site(kKerDenseFwd, B_E + s, y >> 1))))
             break;
           if (lane == 0) {
             mbar_arrive_expect_tx(bar(B_F + s), C::kTile);
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           near = __all_sync(0xffffffffu, rel < a.lut_w);
         }
         dead = dead || !dense_wait(bar(B_S + 2 * t + b), par, abort_flag, a.status,
-                                      wait_site(kKerDenseFwd, B_S + 2 * t + b, u));
+                                   wait_site(kKerDenseFwd, B_S + 2 * t + b, u));
         tc_fence_after();
         if (!dead) {
           uint32_t x[W];
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               // O is complete up to the last step once that step's P V product is
               const int pv = B_PV + 2 * t + ((U - 1) & 1);
               dead = dead || !dense_wait(bar(pv), ((U - 1) >> 1) & 1, abort_flag, a.status,
-                                            wait_site(kKerDenseFwd, pv, u));
+                                         wait_site(kKerDenseFwd, pv, u));
               tc_fence_after();
               if (!dead) {
 #pragma unroll 1
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (nut > 0) {
         const int b = B_PV + 2 * t + ((U - 1) & 1);
         dead = dead || !dense_wait(bar(b), ((U - 1) >> 1) & 1, abort_flag, a.status,
-                                      wait_site(kKerDenseFwd, b, nut));
+                                   wait_site(kKerDenseFwd, b, nut));
         tc_fence_after();
         if (!dead) {
           const size_t row = (size_t)(w.it.start + qi) * a.hq + w.g * a.G + hl;
@@ -520,7 +520,8 @@ cudaError_t launch_dense_fwd(const DenseShape& s, const uint16_t* q, const uint1
   if ((e = make_tmap_rows(&mk, k, s.d, a.hkv, a.T, s.k_stride, 1, 128)) != cudaSuccess) return e;
   if ((e = make_tmap_rows(&mv, v, s.d, a.hkv, a.T, s.v_stride, 1, 128)) != cudaSuccess) return e;
   if (s.d == 128)
-    return a.bias ? launch_t<128, true>(a, mq, mk, mv, st) : launch_t<128, false>(a, mq, mk, mv, st);
+    return a.bias ? launch_t<128, true>(a, mq, mk, mv, st)
+                  : launch_t<128, false>(a, mq, mk, mv, st);
   return a.bias ? launch_t<64, true>(a, mq, mk, mv, st) : launch_t<64, false>(a, mq, mk, mv, st);
 }
 

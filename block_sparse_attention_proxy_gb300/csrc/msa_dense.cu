@@ -23,7 +23,8 @@ msa_status check_dense(const msa_dense_params* p, DenseShape* s, DenseArgs* a) {
   if (!p || p->flags != 0) return MSA_ERR_INVALID_ARG;
   if (p->total_tokens < 0 || p->num_docs < 1) return MSA_ERR_INVALID_ARG;
   if (p->hq <= 0 || p->hkv <= 0 || p->hq % p->hkv != 0) return MSA_ERR_INVALID_ARG;
-  if (!(std::isfinite(p->softmax_scale) && p->softmax_scale > 0.f)) return MSA_ERR_INVALID_ARG;
+  if (!(std::isfinite(p->softmax_scale * kLog2E) && p->softmax_scale > 0.f))
+    return MSA_ERR_INVALID_ARG;
   if (p->num_buckets < 0 || (p->num_buckets > 0 && !p->bucket_starts)) return MSA_ERR_INVALID_ARG;
   if (p->d != 64 && p->d != 128) return MSA_ERR_UNSUPPORTED;
   if (p->hq / p->hkv > kDenseMaxGroup || p->hq > 1024) return MSA_ERR_UNSUPPORTED;
@@ -147,8 +148,8 @@ msa_status msa_dense_bwd(const msa_dense_params* p, const int32_t* cu_seqlens, c
   if (a.T == 0) return MSA_OK;
   if (!cu_seqlens || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3)) return MSA_ERR_INVALID_ARG;
   for (const void* ptr : {(const void*)q, (const void*)k, (const void*)v, (const void*)o,
-                          (const void*)o_res, (const void*)lse, (const void*)dO, (const void*)dq, (const void*)dk,
-                          (const void*)dv})
+                          (const void*)o_res, (const void*)lse, (const void*)dO, (const void*)dq,
+                          (const void*)dk, (const void*)dv})
     if (!ptr || !aligned16(ptr)) return MSA_ERR_INVALID_ARG;
   if (!aligned32(dq) || !aligned32(dk) || !aligned32(dv)) return MSA_ERR_INVALID_ARG;
   const DenseWorkspace w = dense_workspace(a);

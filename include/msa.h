@@ -276,7 +276,7 @@ typedef struct msa_dense_params {
   const int32_t* bucket_starts;
   /* token strides in elements, multiples of 8 and at least heads * d; 0: contiguous */
   int64_t q_stride, k_stride, v_stride, do_stride;
-  float softmax_scale; /* finite and positive */
+  float softmax_scale; /* positive, and finite times log2(e) */
   uint32_t flags;      /* must be 0 */
 } msa_dense_params;
 

@@ -104,6 +104,7 @@ OK = dict(total_tokens=1000, num_docs=3, hq=8, hkv=2, d=64)
     dict(num_docs=0), dict(total_tokens=-1), dict(hq=7), dict(hkv=0), dict(hq=0), dict(d=96),
     dict(hq=130, hkv=2), dict(total_tokens=1 << 25), dict(num_docs=1 << 25), dict(softmax_scale=0.0),
     dict(softmax_scale=-1.0), dict(softmax_scale=float("nan")), dict(softmax_scale=float("inf")),
+    dict(softmax_scale=3e38),
     dict(bucket_starts=(1, 2)), dict(bucket_starts=(0, 2, 2)), dict(bucket_starts=(0, 5, 4)),
     dict(bucket_starts=tuple(range(65))), dict(flags=1), dict(q_stride=8 * 64 - 8),
     dict(k_stride=2 * 64 + 4), dict(v_stride=-128), dict(do_stride=1 << 38)], ids=str)
