@@ -877,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int rel = qt * 128 + 64 * w - r;  // distance of the first of this warpgroup's queries
         const bool diag = qt == 0;              // queries c with rel + c < 0 come before the key
         auto wait = [&](int bb, uint32_t par) {
-          dead = dead || !wait_bar_warp(bar(bb), par, abort_flag, a.status,
+          dead = dead || !dense_wait(bar(bb), par, abort_flag, a.status,
                                         wait_site(kKerDenseDkv, bb, n));
           tc_fence_after();
         };
@@ -1008,7 +1008,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++qt == wk.nq) qt = 0, ++hl;
       }
       ++items;
-      dead = dead || !wait_bar_warp(bar(B_G), (items - 1) & 1, abort_flag, a.status,
+      dead = dead || !dense_wait(bar(B_G), (items - 1) & 1, abort_flag, a.status,
                                     wait_site(kKerDenseDkv, B_G, items));
       tc_fence_after();
       if (!dead) {
