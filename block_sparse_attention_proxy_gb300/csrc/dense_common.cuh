@@ -92,7 +92,24 @@ struct DenseDocs {
   int first[2], len[2], n[2];  // first token, length, tiles
   int total, most;             // tiles of all documents, of the longest
 };
-// Loads them (all lanes; the same in every warp); false if cu_seqlens is malformed (flagged).
+__device__ __forceinline__ int ld_nc_s32(const int32_t* p) {
+  int v;  // volatile: issued here, ahead of what follows
+  asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+// Starts loading them (all lanes; the same in every warp): `len` holds the next one's first
+// token until dense_docs, so that the loads run while the CTA sets itself up.
+__device__ __forceinline__ void dense_docs_load(const DenseArgs& a, DenseDocs& d) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int b = lane + 32 * u;
+    d.first[u] = d.len[u] = 0;
+    if (a.ndoc <= 64 && b <= a.ndoc) d.first[u] = ld_nc_s32(a.cu + b);
+    if (a.ndoc <= 64 && b < a.ndoc) d.len[u] = ld_nc_s32(a.cu + b + 1);
+  }
+}
+// False if cu_seqlens is malformed (flagged).
 __device__ __forceinline__ bool dense_docs(const DenseArgs& a, int bt, DenseDocs& d) {
   if (a.ndoc > 64) return true;
   const int lane = threadIdx.x & 31;
@@ -100,8 +117,7 @@ __device__ __forceinline__ bool dense_docs(const DenseArgs& a, int bt, DenseDocs
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int b = lane + 32 * u;
-    d.first[u] = b <= a.ndoc ? __ldg(a.cu + b) : 0;
-    const int next = b < a.ndoc ? __ldg(a.cu + b + 1) : d.first[u];
+    const int next = b < a.ndoc ? d.len[u] : d.first[u];
     d.len[u] = next - d.first[u];
     bad |= d.first[u] < 0 || d.len[u] < 0 || next > a.T || (b == 0 && d.first[u] != 0);
     d.n[u] = (d.len[u] + bt - 1) / bt;
@@ -151,7 +167,9 @@ __device__ __forceinline__ bool dense_item(const DenseArgs& a, const DenseDocs& 
       int r = x - above;
       const bool second = r >= __popc(m0);
       if (second) r -= __popc(m0);
-      const int l = __fns(second ? m1 : m0, 0, r + 1);
+      const bool in = second ? d.n[1] > lo : d.n[0] > lo;
+      const uint32_t before = (second ? m1 : m0) & ((1u << lane) - 1);
+      const int l = __ffs(__ballot_sync(kAll, in && __popc(before) == r)) - 1;
       doc = l + (second ? 32 : 0);
       b0 = __shfl_sync(kAll, second ? d.first[1] : d.first[0], l);
       b1 = b0 + __shfl_sync(kAll, second ? d.len[1] : d.len[0], l);
@@ -196,16 +214,16 @@ __device__ __forceinline__ bool dense_item(const DenseArgs& a, const DenseDocs& 
 // even rounds run through the CTAs forwards, odd ones backwards, which evens their sums out,
 // and a CTA keeps its KV head where the grid is a multiple of hkv.
 __device__ __forceinline__ bool dense_round(const DenseArgs& a, int k, int* slot, int* g) {
-  const long long grid = gridDim.x;
-  const long long x = (k & 1) ? (k + 1) * grid - 1 - blockIdx.x : k * grid + blockIdx.x;
-  if (x >= (long long)a.nslots * a.hkv) return false;
-  *slot = (int)(x / a.hkv);
-  const int h = (int)(x % a.hkv);
-  *g = (k & 1) ? a.hkv - 1 - h : h;
+  const uint32_t grid = gridDim.x, hkv = a.hkv;  // items: below 2^31 (checked on the host)
+  const uint32_t x = (k & 1) ? (k + 1) * grid - 1 - blockIdx.x : k * grid + blockIdx.x;
+  if (x >= a.nslots * hkv) return false;
+  const uint32_t h = x % hkv;
+  *slot = x / hkv;
+  *g = (k & 1) ? hkv - 1 - h : h;
   return true;
 }
 __device__ __forceinline__ int dense_rounds(const DenseArgs& a) {
-  return (int)(((long long)a.nslots * a.hkv + gridDim.x - 1) / gridDim.x);
+  return ((uint32_t)a.nslots * a.hkv + gridDim.x - 1) / gridDim.x;
 }
 
 // Whole check of cu_seqlens (one warp of one CTA of a launch): first entry 0,

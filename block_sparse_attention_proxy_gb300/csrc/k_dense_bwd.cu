@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (blockIdx.x == 0 && warp == 11) dense_check_docs(a);
   DenseDocs docs;
+  dense_docs_load(a, docs);
   if (!dense_docs(a, a.tpt, docs)) return;
 
   if (threadIdx.x == 0) {
@@ -659,6 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   DenseDocs docs;
+  dense_docs_load(a, docs);
   if (!dense_docs(a, 128, docs)) return;
 
   if (threadIdx.x == 0) {

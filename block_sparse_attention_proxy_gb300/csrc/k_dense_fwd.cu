@@ -74,8 +74,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (blockIdx.x == 0 && warp == 11) dense_check_docs(a);
   const int tpc = 2 * a.tpt;  // tokens per item
   DenseDocs docs;
-  if (!dense_docs(a, tpc, docs)) return;
+  dense_docs_load(a, docs);
 
+  if (threadIdx.x == 256) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
   if (threadIdx.x == 0) {
     mbar_init(bar(B_Q), 1);
     mbar_init(bar(B_QE), C::kMmaWarps);
@@ -113,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int nu[2];   // steps of W keys of each row tile: up to its last valid token
     int tiles;   // key tiles
   };
-  const int rounds = dense_rounds(a);
+  const int rounds = dense_docs(a, tpc, docs) ? dense_rounds(a) : 0;
   auto work = [&](int k, Work& w) -> bool {
     int slot;
     if (!dense_round(a, k, &slot, &w.g) || !dense_item<false>(a, docs, slot, tpc, w.it))
