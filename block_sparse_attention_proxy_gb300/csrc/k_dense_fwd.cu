@@ -45,7 +45,7 @@ struct FwdCfg {
   static constexpr int kMmaWarps = D == 128 ? 1 : 2;
   // K and V tiles in flight; with a bias its tables take the place of one
   static constexpr int kRing = D == 128 ? (BIAS ? 4 : 5) : 8;
-  static constexpr int kSmem = (2 + kRing) * kTile + 288 + (BIAS ? (int)sizeof(DenseBias) : 0);
+  static constexpr int kSmem = (2 + kRing) * kTile + 256 + (BIAS ? (int)sizeof(DenseBias) : 0);
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 
@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sQ = smem;  // [2]
   uint8_t* sKV = sQ + 2 * C::kTile;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + NR * C::kTile);
-  // an item's description and Q loaded / free | ring full / empty | [t][b]: S of tile t complete in buffer b; the
+  // Q loaded / free | ring full / empty | [t][b]: S of tile t complete in buffer b; the
   // first / second 64 keys of its P stored; P V of an even / odd step complete (the
   // softmax may be a step ahead of a product)
   constexpr int B_Q = 0, B_QE = 1, B_F = 2, B_E = B_F + NR, B_S = B_E + NR, B_P = B_S + 4,
@@ -67,8 +67,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + B_END + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   static_assert((B_END + 1) * 8 + 8 <= 256, "barrier block");
-  int4* sItem = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(bars) + 256);  // [2]
-  DenseBias* sB = reinterpret_cast<DenseBias*>(sItem + 2);
+  DenseBias* sB = reinterpret_cast<DenseBias*>(reinterpret_cast<uint8_t*>(bars) + 256);
   auto bar = [&](int i) { return smem_u32(bars + i); };
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
@@ -84,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     mbar_init(bar(B_Q), 1);
-    mbar_init(bar(B_QE), C::kMmaWarps + 8);
+    mbar_init(bar(B_QE), C::kMmaWarps);
     for (int s = 0; s < NR; ++s) {
       mbar_init(bar(B_F + s), 1);
       mbar_init(bar(B_E + s), C::kMmaWarps);
@@ -110,10 +109,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tbase = *reinterpret_cast<volatile uint32_t*>(tslot);
   // TMEM: S/P of tile t at columns [128 t, 128 t + 128), O of tile t at 256 + D t
 
-  // The items of this CTA in order.  Looking one up takes about 1300 cycles, so the warp that
-  // loads does it ahead, and hands it over with Q; no steps end the list.  Ring positions,
-  // steps and barrier phases run on from item to item: the next item's loads and first
-  // products start while the softmax warps still finish the last.
+  // The items of this CTA, in the same order for every role.  Ring positions, steps and
+  // barrier phases run on from item to item: the next item's loads and first products
+  // start while the softmax warps still finish the last.
   struct Work {
     DenseItem it;
     int g, q0;   // KV head; first token of the item inside the document
@@ -152,8 +150,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         const int nq = w.nu[1] ? 2 : 1;
         if (lane == 0) {
-          sItem[0] = make_int4(w.it.start, w.it.len, w.g, w.q0);
-          sItem[1] = make_int4(w.nu[0], w.nu[1], 0, 0);
           mbar_arrive_expect_tx(bar(B_Q), nq * NCH * rows);
           for (int t = 0; t < nq; ++t)
             for (int c = 0; c < NCH; ++c)
@@ -175,13 +171,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
-      }
-      if (ok &&
-          (items == 0 || dense_wait(bar(B_QE), (items - 1) & 1, abort_flag, a.status,
-                                    wait_site(kKerDenseFwd, B_QE, items))) &&
-          lane == 0) {  // the end
-        sItem[1] = make_int4(0, 0, 0, 0);
-        mbar_arrive(bar(B_Q));
       }
       // an aborted CTA must not leave before its copies have landed
       if (*abort_flag) {
@@ -209,11 +198,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(el, bar(B_S + 2 * t + b));
       };
       bool ok = true;
-      while (ok) {
-        if (!(ok = wait(B_Q, items & 1, items))) break;
-        const int len = uniform(sItem[0].y), nu0 = uniform(sItem[1].x), nu1 = uniform(sItem[1].y);
-        const int nk = (max(nu0, nu1) + NH - 1) / NH;
-        if (nk == 0 || !(ok = wait_full(x))) break;
+      for (int k = 0; ok && k < rounds; ++k) {
+        Work w;
+        if (!work(k, w) || w.tiles == 0) continue;
+        const int len = uniform(w.it.len), nu0 = uniform(w.nu[0]), nu1 = uniform(w.nu[1]);
+        const int nk = uniform(w.tiles);
+        if (!(ok = wait(B_Q, items & 1, items) && wait_full(x))) break;
         ++items;
         tc_fence_after();
 #pragma unroll
@@ -267,20 +257,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(el, bar(B_END));
         drain_bar(bar(B_END), 0);
       }
-    } else if (warp == 11) {
-      // ------------------------------ padding ------------------------------------
-      for (int k = 0; k < rounds; ++k) {
-        Work w;
-        if (!work(k, w) || w.it.doc != a.ndoc) continue;
-        const int n = min(tpc, w.it.len - w.q0) * a.G;
-        for (int rr = lane; rr < n; rr += 32) {  // rows behind the last document: zero
-          const size_t row =
-              (size_t)(w.it.start + w.q0 + rr / a.G) * a.hq + w.g * a.G + rr % a.G;
-          dense_zero_row(a.o + row * D, D);
-          if (a.o_res) dense_zero_row(a.o_res + row * D, D);
-          if (a.lse) a.lse[row] = -INFINITY;
-        }
-      }
     }
   } else {
     setmaxnreg_inc<kRegsSoftmax>();
@@ -295,30 +271,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = a.scale_log2;
     bool dead = false;
     int U = 0, table_of = -1;  // steps so far; KV head the bias tables are of
-    for (int items = 0;; ++items) {
-      bool go = !dead && dense_wait(bar(B_Q), items & 1, abort_flag, a.status,
-                                    wait_site(kKerDenseFwd, B_Q, items));
-      const int4 d0 = sItem[0], d1 = sItem[1];
+    for (int k = 0; k < rounds; ++k) {
       Work w;
-      w.it.start = d0.x;
-      w.it.len = d0.y;
-      w.g = d0.z;
-      w.q0 = d0.w;
-      w.nu[0] = d1.x;
-      w.nu[1] = d1.y;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_QE));
-      go = go && w.nu[0] > 0;
-      // with a bias every warp leaves at the same item, also where only some of them saw a
-      // wait fail: they meet at the barriers of dense_bias_tables
-      if (BIAS ? !named_bar_all(1, 256, go) : !go) break;
+      if (!work(k, w)) continue;
+      if (w.it.doc == a.ndoc) {  // padding behind the last document: zero rows
+        const int n = min(tpc, w.it.len - w.q0) * a.G;
+        const int rr = (int)threadIdx.x;
+        if (rr < n) {
+          const size_t row =
+              (size_t)(w.it.start + w.q0 + rr / a.G) * a.hq + w.g * a.G + rr % a.G;
+          dense_zero_row(a.o + row * D, D);
+          if (a.o_res) dense_zero_row(a.o_res + row * D, D);
+          if (a.lse) a.lse[row] = -INFINITY;
+        }
+        continue;
+      }
       if (BIAS && table_of != w.g) {
         dense_bias_tables<false>(a, sB, w.g);
         table_of = w.g;
       }
       const int qi = w.q0 + t * a.tpt + ti;  // token inside the document
       const bool valid = ti < a.tpt && qi < w.it.len;
-      const int nut = uniform(t ? w.nu[1] : w.nu[0]);
+      const int nut = t ? w.nu[1] : w.nu[0];
       float m = -INFINITY, l = 0.f;
       int bk = a.nb - 1, stk = INT_MAX;  // bucket of the next scores and its first distance
       float v0 = 0.f;                    // its bias
