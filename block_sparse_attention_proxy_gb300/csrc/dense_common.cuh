@@ -83,20 +83,6 @@ __device__ __forceinline__ bool dense_wait(uint32_t bar, uint32_t parity, volati
   return wait_bar_warp(bar, parity, abort_flag, status, site);
 }
 
-// named_bar_sync that also tells whether `ok` held in every thread.
-__device__ __forceinline__ bool named_bar_all(uint32_t id, uint32_t nthreads, bool ok) {
-  uint32_t all;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 q, %3, 0;\n\t"
-      "barrier.red.and.pred p, %1, %2, q;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(all)
-      : "r"(id), "r"(nthreads), "r"((uint32_t)ok)
-      : "memory");
-  return all != 0;
-}
-
 struct DenseItem {
   int doc, start, len, tile;  // document, its first token and length, tile inside it
 };
@@ -531,7 +517,7 @@ __device__ __forceinline__ void dense_zero_rows(uint8_t* tile, int first) {
   __syncwarp();
 }
 
-// N fp32 columns of a row (one row per lane), times f, rounded to bf16, to `row` (its first
+// 64 fp32 columns of a row (one row per lane), times f, rounded to bf16, to `row` (its first
 // element; null: not stored): 32 bytes to a store, whole sectors, so that lanes need not
 // exchange rows through shared memory first.  RES: what the rounding drops, itself as
 // bf16, instead of the values.
@@ -540,10 +526,10 @@ __device__ __forceinline__ void st_v8(void* p, const uint32_t (&w)[8]) {
                "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
-template <bool RES = false, int N = 64>
-__device__ __forceinline__ void dense_store_row(const uint32_t (&v)[N], float f, uint16_t* row) {
+template <bool RES = false>
+__device__ __forceinline__ void dense_store_row(const uint32_t (&v)[64], float f, uint16_t* row) {
 #pragma unroll
-  for (int q = 0; q < N / 16; ++q) {
+  for (int q = 0; q < 4; ++q) {
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {

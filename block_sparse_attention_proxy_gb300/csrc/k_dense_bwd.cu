@@ -29,11 +29,6 @@ static_assert(kBudget <= 65536, "register budgets exceed the register file");
 // S has two TMEM buffers: while the softmax warps turn S(n), dP(n) into dS(n) (bf16, over
 // S(n)'s columns), S(n + 1) is computed, and dP(n + 1) as soon as dP(n) has been read.
 // ---------------------------------------------------------------------------
-// Two columns of dO o (o + o_res).
-__device__ __forceinline__ float dot_pair(uint32_t o, uint32_t res, uint32_t d_o) {
-  return (bf16_lo(o) + bf16_lo(res)) * bf16_lo(d_o) + (bf16_hi(o) + bf16_hi(res)) * bf16_hi(d_o);
-}
-
 // {-lse log2(e) (-inf: no key left), D} of packed rows of an item: rows first + u 256/D, u <
 // STEPS, D/8 lanes to a row, 16 bytes each, with O = o + o_res.  `load` only starts the loads.
 template <int D, int STEPS>
@@ -55,14 +50,25 @@ struct RowStats {
       lse[u] = __ldg(a.lse + row);
     }
   }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int u = 0; u < STEPS; ++u) {
+      xo[u] = xr[u] = xd[u] = make_uint4(0, 0, 0, 0);
+      lse[u] = 0.f;
+    }
+  }
   // to `rows` (by packed row) and to a.stats
   __device__ __forceinline__ void store(const DenseArgs& a, const DenseItem& it, int q0, int g,
                                         int first, float2* rows) const {
     const int toks = min(a.tpt, it.len - q0);
+    auto dot = [](uint32_t o, uint32_t res, uint32_t d_o) {
+      return (bf16_lo(o) + bf16_lo(res)) * bf16_lo(d_o) +
+             (bf16_hi(o) + bf16_hi(res)) * bf16_hi(d_o);
+    };
 #pragma unroll
     for (int u = 0; u < STEPS; ++u) {
-      float s = (dot_pair(xo[u].x, xr[u].x, xd[u].x) + dot_pair(xo[u].y, xr[u].y, xd[u].y)) +
-                (dot_pair(xo[u].z, xr[u].z, xd[u].z) + dot_pair(xo[u].w, xr[u].w, xd[u].w));
+      float s = (dot(xo[u].x, xr[u].x, xd[u].x) + dot(xo[u].y, xr[u].y, xd[u].y)) +
+                (dot(xo[u].z, xr[u].z, xd[u].z) + dot(xo[u].w, xr[u].w, xd[u].w));
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       const int rr = first + u * kRows, tok = rr / a.G;
@@ -82,9 +88,8 @@ struct DqCfg {
   static constexpr int kTile = 128 * D * 2;
   // K and V rings; with a bias its tables take the place of a tile
   static constexpr int kNK = D == 128 ? 3 : 4, kNV = D == 128 ? (BIAS ? 1 : 2) : 3;
-  static constexpr int kIn = D == 128 ? 2 : 4;  // tiles of an item: Q, dO; d = 64: o and o_res too
-  static constexpr int kScratch = 8 * 512;      // row sums of a bucket, per warp
-  static constexpr int kSmem = (kIn + kNK + kNV) * kTile + 320 + 2048 + (D == 64 ? 1024 : 0) +
+  static constexpr int kScratch = 8 * 512;  // row sums of a bucket, per warp
+  static constexpr int kSmem = (2 + kNK + kNV) * kTile + 256 + 2 * 1024 +
                                (BIAS ? (int)sizeof(DenseBias) + kScratch : 0);
   static_assert(kSmem <= 232448, "shared memory budget");
 };
@@ -93,28 +98,26 @@ template <int D, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
     k_dense_dq(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-               const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_r,
                const __grid_constant__ DenseArgs a) {
   using C = DqCfg<D, BIAS>;
   constexpr int NCH = D / 64, NK = C::kNK, NV = C::kNV;
+  constexpr bool kRowWarps = D == 128;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
   uint8_t* sO = sQ + C::kTile;
-  uint8_t* sK = sQ + C::kIn * C::kTile;
+  uint8_t* sK = sO + C::kTile;
   uint8_t* sV = sK + NK * C::kTile;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sV + NV * C::kTile);
-  // an item's description and tiles loaded / free | rings | S buffers | dP ready, read |
-  // dS buffers | dQ complete | row statistics ready, free
+  // Q and dO loaded / free | rings | S buffers | dP ready, read | dS buffers | dQ complete |
+  // row statistics ready, free
   constexpr int B_Q = 0, B_QE = 1, B_KF = 2, B_KE = B_KF + NK, B_VF = B_KE + NK, B_VE = B_VF + NV,
                 B_S = B_VE + NV, B_DP = B_S + 2, B_DPE = B_DP + 1, B_DS = B_DPE + 1,
                 B_DQ = B_DS + 2, B_RF = B_DQ + 1, B_RE = B_RF + 2, B_END = B_RE + 2;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + B_END + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
-  static_assert((B_END + 1) * 8 + 8 <= 288, "barrier block");
-  int4* sItem = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(bars) + 288);  // [2]
-  float2* sRow = reinterpret_cast<float2*>(sItem + 2);  // [2][128] {-lse log2(e), D}
-  float* sD = reinterpret_cast<float*>(sRow + 256);     // d = 64: [2][128] D of half the columns
-  DenseBias* sB = reinterpret_cast<DenseBias*>(sD + (D == 64 ? 256 : 0));
+  static_assert((B_END + 1) * 8 + 8 <= 256, "barrier block");
+  float2* sRow = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(bars) + 256);  // [2][128]
+  DenseBias* sB = reinterpret_cast<DenseBias*>(sRow + 256);
   auto bar = [&](int i) { return smem_u32(bars + i); };
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
@@ -125,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(bar(B_Q), 1);
-    mbar_init(bar(B_QE), 9);
+    mbar_init(bar(B_QE), 1);
     for (int s = 0; s < NK; ++s) mbar_init(bar(B_KF + s), 1), mbar_init(bar(B_KE + s), 1);
     for (int s = 0; s < NV; ++s) mbar_init(bar(B_VF + s), 1), mbar_init(bar(B_VE + s), 1);
     for (int b = 0; b < 2; ++b) {
@@ -152,9 +155,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // TMEM: S/dS buffer b at columns [128 b, 128 b + 128), dP at 256, dQ at 384.  dS of the
   // columns of warpgroup w starts at column 64 w of its buffer.
 
-  // The items of this CTA in order; ring positions and barrier phases run on from item to
-  // item (X: tiles so far).  Looking one up takes about 1300 cycles, so the warp that loads
-  // does it ahead, and hands it over with the tiles; N = 0 ends the list.
+  // The items of this CTA, in the same order for every role; ring positions and barrier
+  // phases run on from item to item (X: tiles so far).
   struct Work {
     DenseItem it;
     int slot, g, q0;
@@ -188,17 +190,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!work(k, w) || w.N == 0) continue;
         if (items > 0 && !(ok = wait(B_QE, (items - 1) & 1, items))) break;
         if (lane == 0) {
-          sItem[0] = make_int4(w.it.start, w.it.len, w.slot, w.g);
-          sItem[1] = make_int4(w.q0, w.N, 0, 0);
-          mbar_arrive_expect_tx(bar(B_Q), C::kIn * NCH * (uint32_t)a.tpt * a.G * 128);
-          const int head = w.g * a.G, tok = w.it.start + w.q0;
+          mbar_arrive_expect_tx(bar(B_Q), 2 * NCH * (uint32_t)a.tpt * a.G * 128);
           for (int c = 0; c < NCH; ++c) {
-            tma_load_3d(smem_u32(sQ + c * 16384), &tm_q, bar(B_Q), 64 * c, head, tok);
-            tma_load_3d(smem_u32(sO + c * 16384), &tm_do, bar(B_Q), 64 * c, head, tok);
-          }
-          if (D == 64) {
-            tma_load_3d(smem_u32(sO + C::kTile), &tm_o, bar(B_Q), 0, head, tok);
-            tma_load_3d(smem_u32(sO + 2 * C::kTile), &tm_r, bar(B_Q), 0, head, tok);
+            tma_load_3d(smem_u32(sQ + c * 16384), &tm_q, bar(B_Q), 64 * c, w.g * a.G,
+                        w.it.start + w.q0);
+            tma_load_3d(smem_u32(sO + c * 16384), &tm_do, bar(B_Q), 64 * c, w.g * a.G,
+                        w.it.start + w.q0);
           }
         }
         ++items;
@@ -222,10 +219,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           xv = X + 1;
         }
         __syncwarp();
-      }
-      if (ok && (items == 0 || wait(B_QE, (items - 1) & 1, items)) && lane == 0) {  // the end
-        sItem[1] = make_int4(0, 0, 0, 0);
-        mbar_arrive(bar(B_Q));
       }
       if (*abort_flag) {  // copies in flight land before the CTA leaves
         if (items > 0) drain_bar(bar(B_Q), (items - 1) & 1);
@@ -264,12 +257,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       bool ok = true;
-      while (ok) {
-        if (!(ok = wait(B_Q, items & 1, items))) break;
-        const int NT = uniform(sItem[1].y);
-        len = uniform(sItem[0].y);
-        if (NT == 0) break;
-        ok = s_of(X, 0) && dp_of(X, 0);
+      for (int k = 0; ok && k < rounds; ++k) {
+        Work w;
+        if (!work(k, w) || w.N == 0) continue;
+        const int NT = uniform(w.N);
+        len = uniform(w.it.len);
+        ok = wait(B_Q, items & 1, items) && s_of(X, 0) && dp_of(X, 0);
         ++items;
         if (ok && NT == 1) mma_commit(el, bar(B_QE));
         for (int n = 0; ok && n < NT; ++n, ++X) {
@@ -292,51 +285,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(el, bar(B_END));
         drain_bar(bar(B_END), 0);
       }
-    } else {
+    } else if (kRowWarps) {
       // ------------------------------ row statistics ------------------------------
-      // 64 rows per warp, an item or two ahead; and the items with nothing to compute
+      // 64 rows per warp
       using Stats = RowStats<D, 4>;
-      const int tid = (warp - 10) * 32 + lane;
       int items = 0;
       bool ok = true;
       for (int k = 0; ok && k < rounds; ++k) {
         Work w;
-        if (!work(k, w)) continue;
-        if (w.N == 0) {
-          if (BIAS) {
-            float* part = a.parts + ((size_t)w.slot * a.hq + w.g * a.G) * a.nb;
-            for (int x = tid; x < a.G * a.nb; x += 64) part[x] = 0.f;
-          }
-          if (w.it.doc == a.ndoc) {  // padding behind the last document: zero rows
-            const int n = min(a.tpt, w.it.len - w.q0) * a.G;
-            for (int rr = tid; rr < n; rr += 64)
-              dense_zero_row(a.dq + ((size_t)(w.it.start + w.q0 + rr / a.G) * a.hq + w.g * a.G +
-                                     rr % a.G) * D, D);
-          }
-          continue;
-        }
+        if (!work(k, w) || w.N == 0) continue;
         const int b = items & 1;
         if (items >= 2 && !(ok = dense_wait(bar(B_RE + b), ((items >> 1) & 1) ^ 1, abort_flag,
                                             a.status, wait_site(kKerDenseDq, B_RE + b, items))))
           break;
-        if (D == 128) {
 #pragma unroll 1
-          for (int r0 = (warp - 10) * 64; r0 < (warp - 9) * 64; r0 += Stats::kRows * 4) {
-            const int first = r0 + lane / Stats::kLanes;
-            Stats x;
-            x.load(a, w.it, w.q0, w.g, first);
-            x.store(a, w.it, w.q0, w.g, first, sRow + b * 128);
-          }
-        } else {
-          const int toks = min(a.tpt, w.it.len - w.q0);
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int rr = (warp - 10) * 64 + 32 * u + lane, tok = rr / a.G;
-            const float lse = tok < toks ? __ldg(a.lse + (size_t)(w.it.start + w.q0 + tok) * a.hq +
-                                                 w.g * a.G + rr % a.G)
-                                         : -INFINITY;
-            sRow[b * 128 + rr].x = lse != -INFINITY ? -lse * kLog2E : -INFINITY;
-          }
+        for (int r0 = (warp - 10) * 64; r0 < (warp - 9) * 64; r0 += Stats::kRows * 4) {
+          const int first = r0 + lane / Stats::kLanes;
+          Stats x;
+          x.load(a, w.it, w.q0, w.g, first);
+          x.store(a, w.it, w.q0, w.g, first, sRow + b * 128);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_RF + b));
@@ -356,44 +323,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* my = BIAS ? a.slots + (size_t)blockIdx.x * a.nb * 256 + w * 128 + r : nullptr;
     bool dead = false;
     int X = 0, items = 0, table_of = -1;  // table_of: KV head the bias tables are of
-    for (;; ++items) {
-      // Every warp leaves the loop at the same item, also where only some of them saw a wait
-      // fail: they meet at barriers inside.
-      bool go = !dead && dense_wait(bar(B_Q), items & 1, abort_flag, a.status,
-                                    wait_site(kKerDenseDq, B_Q, items));
-      const int4 d0 = sItem[0], d1 = sItem[1];
-      Work wk;
-      wk.it.start = d0.x;
-      wk.it.len = d0.y;
-      wk.slot = d0.z;
-      wk.g = d0.w;
-      wk.q0 = d1.x;
-      wk.N = uniform(d1.y);
-      go = go && wk.N > 0;
-      if (D == 64 && go) {
-        // D = rowsum(dO o O) with O = o + o_res: 32 columns each of a row
-        float s2[2] = {0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int at = r * 128 + (((4 * w + c) ^ (r & 7)) << 4);  // 128-byte swizzle
-          const uint4 g = *reinterpret_cast<const uint4*>(sO + at);
-          const uint4 o = *reinterpret_cast<const uint4*>(sO + C::kTile + at);
-          const uint4 res = *reinterpret_cast<const uint4*>(sO + 2 * C::kTile + at);
-          s2[c & 1] += (dot_pair(o.x, res.x, g.x) + dot_pair(o.y, res.y, g.y)) +
-                       (dot_pair(o.z, res.z, g.z) + dot_pair(o.w, res.w, g.w));
+    // row statistics, 16 rows per warp
+    using Stats = RowStats<D, D / 16>;
+    const int dr0 = (warp & 3) * 32 + 16 * w + lane / Stats::kLanes;
+    Stats rs;
+    // the next item with something to compute, from round k on; what has none is written
+    auto seek = [&](int& k, Work& wk) -> bool {
+      for (; k < rounds; ++k) {
+        if (!work(k, wk)) continue;
+        if (wk.N > 0) return true;
+        if (BIAS) {
+          float* part = a.parts + ((size_t)wk.slot * a.hq + wk.g * a.G) * a.nb;
+          for (int x = threadIdx.x; x < a.G * a.nb; x += 256) part[x] = 0.f;
         }
-        sD[128 * w + r] = s2[0] + s2[1];
+        if (wk.it.doc == a.ndoc) {  // padding behind the last document: zero rows
+          const int n = min(a.tpt, wk.it.len - wk.q0) * a.G, rr = (int)threadIdx.x;
+          if (rr < n)
+            dense_zero_row(a.dq + ((size_t)(wk.it.start + wk.q0 + rr / a.G) * a.hq +
+                                   wk.g * a.G + rr % a.G) * D, D);
+        }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_QE));
-      const int rb = items & 1;
-      go = go && dense_wait(bar(B_RF + rb), (items >> 1) & 1, abort_flag, a.status,
-                            wait_site(kKerDenseDq, B_RF + rb, items));
-      if (!named_bar_all(1, 256, go)) break;
-      const float nl = sRow[rb * 128 + r].x;
-      const float dsum = D == 64 ? sD[r] + sD[128 + r] : sRow[rb * 128 + r].y;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_RE + rb));
+      return false;
+    };
+    int k = 0;
+    Work wk;
+    bool have = seek(k, wk);
+    auto next_stats = [&]() {
+      rs.clear();  // kept across the tile loop otherwise
+      if (have) rs.load(a, wk.it, wk.q0, wk.g, dr0);
+    };
+    if (!kRowWarps) next_stats();
+    while (have) {
       float* part = BIAS ? a.parts + ((size_t)wk.slot * a.hq + wk.g * a.G) * a.nb : nullptr;
       if (BIAS && table_of != wk.g) {
         dense_bias_tables<true>(a, sB, wk.g);
@@ -402,8 +362,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int qi = wk.q0 + ti;
       const bool valid = ti < a.tpt && qi < wk.it.len;
       const size_t row = (size_t)(wk.it.start + qi) * a.hq + wk.g * a.G + hl;
-      if (D == 64 && w == 0 && valid)
-        a.stats[(size_t)(wk.g * a.G + hl) * a.T + wk.it.start + qi] = make_float2(nl, dsum);
+      const int rb = kRowWarps ? items & 1 : 0;
+      if (kRowWarps) {
+        dead = dead || !dense_wait(bar(B_RF + rb), (items >> 1) & 1, abort_flag, a.status,
+                                   wait_site(kKerDenseDq, B_RF + rb, items));
+      } else {
+        rs.store(a, wk.it, wk.q0, wk.g, dr0, sRow);
+        named_bar_sync(1, 256);
+      }
+      const float nl = sRow[rb * 128 + r].x, dsum = sRow[rb * 128 + r].y;
+      if (kRowWarps) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_RE + rb));
+      }
       float acc = 0.f;
       uint64_t done = 0;                 // buckets stored
       int bk = a.nb - 1, stk = INT_MAX;  // bucket of the next scores and its first distance
@@ -571,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(bar(B_DS + b));
         }
       }
+      ++items;
       if (BIAS) {
         my[bk * 256] = acc;
         done |= 1ull << bk;
@@ -617,14 +589,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      dead = dead || !dense_wait(bar(B_DQ), items & 1, abort_flag, a.status,
+      ++k;
+      have = seek(k, wk);
+      if (!kRowWarps) next_stats();
+      dead = dead || !dense_wait(bar(B_DQ), (items - 1) & 1, abort_flag, a.status,
                                  wait_site(kKerDenseDq, B_DQ, items));
       tc_fence_after();
-      if (!dead) {  // half the columns each
-        uint32_t v[D / 2];
-        if constexpr (D == 128) tmem_ld_row(tl + 384 + 64 * w, v);
-        else tmem_ld32(tl + 384 + 32 * w, v);
-        dense_store_row(v, a.scale, valid ? a.dq + row * D + D / 2 * w : nullptr);
+      if (!dead && w < D / 64) {  // 64 columns each (d = 64: the first warpgroup)
+        uint32_t v[64];
+        tmem_ld_row(tl + 384 + 64 * w, v);
+        dense_store_row(v, a.scale, valid ? a.dq + row * D + 64 * w : nullptr);
       }
       tc_fence_before();
     }
@@ -1093,15 +1067,13 @@ __global__ void __launch_bounds__(kTableThreads) k_dense_dtable(const DenseArgs 
 template <int D, bool BIAS>
 cudaError_t launch_t(const CUtensorMap& mqp, const CUtensorMap& mop, const CUtensorMap& mk,
                      const CUtensorMap& mv, const CUtensorMap& mq, const CUtensorMap& mo,
-                     const CUtensorMap& mfo, const CUtensorMap& mfr, DenseArgs a,
-                     cudaStream_t st) {
+                     DenseArgs a, cudaStream_t st) {
   cudaError_t e = dense_prepare<k_dense_dq<D, BIAS>>(kThreads, kBudget, DqCfg<D, BIAS>::kSmem);
   if (e != cudaSuccess) return e;
   e = dense_prepare<k_dense_dkv<D, BIAS>>(kThreads, kBudget, DkvCfg<D, BIAS>::kSmem);
   if (e != cudaSuccess) return e;
   a.nslots = dense_slots(a.T, a.ndoc, a.tpt);
-  k_dense_dq<D, BIAS><<<dense_grid(a), kThreads, DqCfg<D, BIAS>::kSmem, st>>>(mqp, mop, mk, mv,
-                                                                             mfo, mfr, a);
+  k_dense_dq<D, BIAS><<<dense_grid(a), kThreads, DqCfg<D, BIAS>::kSmem, st>>>(mqp, mop, mk, mv, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   a.nslots = dense_slots(a.T, a.ndoc, 128);
   // With a bias persistent CTAs keep their tables; without one an item per CTA, started by the
@@ -1126,20 +1098,12 @@ cudaError_t launch_dense_bwd(const DenseShape& s, const uint16_t* q, const uint1
   if ((e = make_tmap_rows(&mo, d_o, s.d, a.hq, a.T, s.do_stride, 1, 128)) != cudaSuccess) return e;
   if ((e = make_tmap_rows(&mk, k, s.d, a.hkv, a.T, s.k_stride, 1, 128)) != cudaSuccess) return e;
   if ((e = make_tmap_rows(&mv, v, s.d, a.hkv, a.T, s.v_stride, 1, 128)) != cudaSuccess) return e;
-  CUtensorMap mfo = mqp, mfr = mqp;  // o and o_res; d = 128 reads them without a map
-  if (s.d == 64) {
-    const long long packed = (long long)a.hq * s.d;
-    if ((e = make_tmap_rows(&mfo, a.o, s.d, a.hq, a.T, packed, a.G, a.tpt)) != cudaSuccess)
-      return e;
-    if ((e = make_tmap_rows(&mfr, a.o_res, s.d, a.hq, a.T, packed, a.G, a.tpt)) != cudaSuccess)
-      return e;
-  }
   if (s.d == 128)
-    e = a.bias ? launch_t<128, true>(mqp, mop, mk, mv, mq, mo, mfo, mfr, a, st)
-               : launch_t<128, false>(mqp, mop, mk, mv, mq, mo, mfo, mfr, a, st);
+    e = a.bias ? launch_t<128, true>(mqp, mop, mk, mv, mq, mo, a, st)
+               : launch_t<128, false>(mqp, mop, mk, mv, mq, mo, a, st);
   else
-    e = a.bias ? launch_t<64, true>(mqp, mop, mk, mv, mq, mo, mfo, mfr, a, st)
-               : launch_t<64, false>(mqp, mop, mk, mv, mq, mo, mfo, mfr, a, st);
+    e = a.bias ? launch_t<64, true>(mqp, mop, mk, mv, mq, mo, a, st)
+               : launch_t<64, false>(mqp, mop, mk, mv, mq, mo, a, st);
   if (e != cudaSuccess || !a.bias) return e;
   DenseArgs b = a;
   b.nslots = dense_slots(a.T, a.ndoc, a.tpt);
