@@ -248,6 +248,13 @@ __device__ __forceinline__ uint4 ld_nc_v4(const void* p) {
   return v;
 }
 
+// A float of global memory from L2; not moved across other volatile instructions.
+__device__ __forceinline__ float ld_cg_f32(const float* p) {
+  float v;
+  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // TMEM -> registers: 64 or 128 columns of this thread's lane, one wait for all of them.
 __device__ __forceinline__ void tmem_ld_row(uint32_t ta, uint32_t (&r)[64]) {
   asm volatile(

@@ -88,9 +88,8 @@ struct DqCfg {
   static constexpr int kTile = 128 * D * 2;
   // K and V rings; with a bias its tables take the place of a tile
   static constexpr int kNK = D == 128 ? 3 : 4, kNV = D == 128 ? (BIAS ? 1 : 2) : 3;
-  static constexpr int kScratch = 8 * 512;  // row sums of a bucket, per warp
   static constexpr int kSmem = (2 + kNK + kNV) * kTile + 256 + 2 * 1024 +
-                               (BIAS ? (int)sizeof(DenseBias) + kScratch : 0);
+                               (BIAS ? (int)sizeof(DenseBias) : 0);
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 
@@ -548,46 +547,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         done |= 1ull << bk;
         for (int b = 0; b < a.nb; ++b)  // buckets that the row does not reach
           if (!((done >> b) & 1)) my[b * 256] = 0.f;
-        // sums over the item's rows, in a fixed order: a warp takes every eighth bucket,
-        // brings its row sums (contiguous) and adds them up head by head, through shared
-        // memory where G is no power of two.  The first barrier orders the stores above before
-        // the loads, the second the loads before the next item's stores.
+        // Sums over the item's rows, head by head, in a fixed order: a warp takes every eighth
+        // bucket, four at a time; P lanes to a head add up every P-th token each, and then
+        // pairwise (more than 32 heads: one lane to a head, 32 heads at a time).  The first
+        // barrier orders the stores above before the loads, the second the loads before the
+        // next item's stores.
         __threadfence_block();
         named_bar_sync(2, 256);
-        const float* all = a.slots + (size_t)blockIdx.x * a.nb * 256 + lane;
-        float* scr = reinterpret_cast<float*>(sB + 1) + warp * 128;
-        float v[kDenseMaxBuckets / 8][4];
+        const float* all = a.slots + (size_t)blockIdx.x * a.nb * 256;
+        const int P = max(32 / a.G, 1), step = P * a.G, pt = lane / a.G;
+        for (int b0 = warp; b0 < a.nb; b0 += 32) {
+          for (int h0 = 0; h0 < a.G; h0 += 32) {
+            const int h = h0 + lane;
+            const int end = h < step ? a.tpt * a.G : 0;  // lanes left over have no rows
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int x0 = h; __any_sync(0xffffffffu, x0 < end); x0 += 5 * step) {
+              float y[4][5][2];  // all loads unconditional, so that they run together
 #pragma unroll
-        for (int u = 0; u < kDenseMaxBuckets / 8; ++u)
+              for (int j = 0; j < 5; ++j) {
+                const float* p = all + min(x0 + j * step, 127);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float* p = all + (warp + 8 * u) * 256 + 32 * i;
-            v[u][i] = warp + 8 * u < a.nb ? __ldcg(p) + __ldcg(p + 128) : 0.f;
-          }
-        named_bar_sync(2, 256);
+                for (int u = 0; u < 4; ++u)
 #pragma unroll
-        for (int u = 0; u < kDenseMaxBuckets / 8; ++u) {
-          const int b = warp + 8 * u;
-          if (b >= a.nb) break;
-          if (a.G <= 32 && (a.G & (a.G - 1)) == 0) {  // rows 32 apart belong to one head
-            float sum = (v[u][0] + v[u][1]) + (v[u][2] + v[u][3]);
+                  for (int e = 0; e < 2; ++e)
+                    y[u][j][e] = ld_cg_f32(p + min(b0 + 8 * u, a.nb - 1) * 256 + 128 * e);
+              }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-              if (o >= a.G) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (lane < a.G) part[lane * a.nb + b] = sum;
-          } else {
+              for (int j = 0; j < 5; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) scr[32 * i + lane] = v[u][i];
-            __syncwarp();
-            for (int h = lane; h < a.G; h += 32) {
-              float sum[2] = {0.f, 0.f};
-#pragma unroll 8
-              for (int i = 0; i < a.tpt; ++i) sum[i & 1] += scr[i * a.G + h];
-              part[h * a.nb + b] = sum[0] + sum[1];
+                for (int u = 0; u < 4; ++u)
+                  v[u] += x0 + j * step < end ? y[u][j][0] + y[u][j][1] : 0.f;
             }
-            __syncwarp();
+            for (int o = 16; o > 0; o >>= 1) {
+              if (o >= P) continue;
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const float other = __shfl_down_sync(0xffffffffu, v[u], o * a.G);
+                if (pt < o && pt + o < P) v[u] += other;
+              }
+            }
+            if (h < a.G) {
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                if (b0 + 8 * u < a.nb) part[h * a.nb + b0 + 8 * u] = v[u];
+            }
           }
         }
+        named_bar_sync(2, 256);
       }
       ++k;
       have = seek(k, wk);
