@@ -212,14 +212,15 @@ __device__ __forceinline__ bool dense_item(const DenseArgs& a, const DenseDocs& 
 
 // Round k of a persistent CTA over `total` = slots x KV heads items, sorted by falling work:
 // even rounds run through the CTAs forwards, odd ones backwards, which evens their sums out,
-// and a CTA keeps its KV head where the grid is a multiple of hkv.
+// and a CTA keeps its KV head where the grid is a multiple of hkv (h runs backwards in odd rounds).
 __device__ __forceinline__ bool dense_round(const DenseArgs& a, int k, int* slot, int* g) {
   const uint32_t grid = gridDim.x, hkv = a.hkv;  // items: below 2^31 (checked on the host)
   const uint32_t x = (k & 1) ? (k + 1) * grid - 1 - blockIdx.x : k * grid + blockIdx.x;
   if (x >= a.nslots * hkv) return false;
   const uint32_t h = x % hkv;
   *slot = x / hkv;
-  *g = (k & 1) ? hkv - 1 - h : h;
+  // a slot's heads must all lie in one round for this to name each once
+  *g = (k & 1) && grid % hkv == 0 ? hkv - 1 - h : h;
   return true;
 }
 __device__ __forceinline__ int dense_rounds(const DenseArgs& a) {

@@ -246,7 +246,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!ok) break;
           mma_commit(el, bar(B_E + sv));
-          if (n + 1 < nk) mma_commit(el, bar(B_E + (xv + 1) % NR));
+          if (n + 1 < nk) {
+            // a warp without a step left releases no tile that it has not seen arrive
+            if (NH == 2 && !(ok = wait_full(xv + 1))) break;
+            mma_commit(el, bar(B_E + (xv + 1) % NR));
+          }
           if (n + 2 == nk) mma_commit(el, bar(B_QE));  // the last S has been issued
         }
         x += 2 * nk;

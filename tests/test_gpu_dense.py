@@ -276,6 +276,20 @@ def test_more_items_than_the_gpu_holds():
     _compare(x, lens, (0, 1, 3, 9, 27, 81, 243, 729, 1500))
 
 
+@pytest.mark.parametrize("hq,hkv,nb", [(12, 12, 0), (10, 5, 0), (32, 16, 0), (24, 24, 4)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_kv_heads_that_do_not_divide_the_grid(hq, hkv, nb, d):
+    """More items than CTAs, rounds that end inside a slot's heads: every head of every token
+    is written (the memory that the outputs get is full of NaN)."""
+    lens = [1700, 5, 900, 1111]
+    x = _inputs(lens, hq, hkv, d, 21, nb=nb)
+    torch.cuda.synchronize()
+    spoilt = [torch.full_like(x[n], float("nan")) for n in ("q", "q", "k", "k", "v")]
+    spoilt.append(torch.full((64 << 20,), float("nan"), device="cuda"))
+    del spoilt
+    _compare(x, lens, (0, 2, 30, 400)[:nb] or None)
+
+
 def test_front_end_refusals():
     from block_sparse_attention_proxy_gb300 import MsaError, dense_attention
 
