@@ -20,9 +20,13 @@
 // at a time (S, P and their barriers in halves), and one half's products run under the
 // other half's exponentials; one warp issues the products of each row tile, so that what a
 // hand-off costs it (some hundred cycles) overlaps the other's (10007 tokens, 12 heads:
-// 110 -> 95 us), and the exponentials start ahead of the maximum (95 -> 86 us).  At d = 128,
+// 110 -> 95 us), and the exponentials start ahead of the maximum (95 -> 84 us).  At d = 128,
 // where the tensor core is the bound, two issuing warps share it out between the tiles and
 // finish both later (32768 tokens, 8 heads: 1.21 -> 1.74 ms with them).
+//
+// Bound at d = 128 by the tensor core: one document of 32768 tokens, 8 heads on 2: 1.26 ms,
+// 1.74 PFLOP/s (a library product under the same power cap: 1.73); 8 ragged documents of as
+// many tokens, 16 heads on 4: 0.41 ms, 1.47.
 //
 // Roles (384 threads): warps 0-3 and 4-7 are the softmax warpgroups of tile 0
 // and 1, so one tile's softmax overlaps the other's products; warp 8 loads;
