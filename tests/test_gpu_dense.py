@@ -82,6 +82,22 @@ def test_bias(starts, hq, hkv, d):
     _compare(_inputs(lens, hq, hkv, d, 3, nb=len(starts)), lens, starts)
 
 
+@pytest.mark.parametrize("hq,hkv", [(64, 1), (33, 1), (40, 2), (48, 4)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_bias_of_many_heads(hq, hkv, d):
+    """Groups whose table does not fit beside the tiles, up to 64 heads on one KV head."""
+    lens, starts = [260, 1, 97], tuple(range(0, 256, 4))
+    _compare(_inputs(lens, hq, hkv, d, 22, nb=64), lens, starts)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_bias_buckets_far_away(d):
+    """Buckets that begin within one tile thousands of tokens back, past the distances whose
+    starts are kept as bits."""
+    lens, starts = [9300], (0, 10, 4000, 4001, 4040, 8190, 8192, 8200, 8201, 8215, 9000, 9001)
+    _compare(_inputs(lens, 2, 1, d, 23, nb=len(starts)), lens, starts)
+
+
 def test_softmax_scale():
     lens = [190, 77]
     x = _inputs(lens, 4, 2, 64, 4, nb=4, qs=2.0)
@@ -121,8 +137,9 @@ def test_masking_bias(masked):
 
 
 @pytest.mark.parametrize("nb", [0, 3])
-def test_rows_behind_the_last_document(nb):
-    lens, starts = [130, 60], (0, 4, 50) if nb else None
+@pytest.mark.parametrize("lens", [[130, 60], [3] * 90], ids=["two", "many"])
+def test_rows_behind_the_last_document(lens, nb):
+    starts = (0, 4, 50) if nb else None
     x = _inputs(lens, 4, 2, 64, 7, nb=nb, tail=201)
     n = sum(lens)
     for name in ("q", "k", "v", "do"):
