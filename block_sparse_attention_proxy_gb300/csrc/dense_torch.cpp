@@ -3,6 +3,7 @@
 // short: a forward and backward of a small batch runs about 60 us on the GPU, and the
 // same front end written in Python kept the host busy for 270 us a step.  The
 // computation itself is in the library's kernels.
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
@@ -89,12 +90,28 @@ struct DenseAttentionBackward : torch::autograd::Node {
     return torch::autograd::DelayedError("dense_attention is differentiable once", 4)
         .apply(std::move(g));
   }
+  // Inside a capture, a gradient that goes to a node of the default stream (a leaf that a graph
+  // made outside the capture still holds) would make the engine join that stream to the
+  // capture, which ends the process: an error here instead.
+  void check_capture() {
+    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None) return;
+    const c10::Stream here = c10::cuda::getCurrentCUDAStream().unwrap();
+    const c10::Stream legacy = c10::cuda::getDefaultCUDAStream().unwrap();
+    for (const auto& e : next_edges()) {
+      const auto to = e.function ? e.function->stream() : std::nullopt;
+      if (to && *to == legacy && *to != here)
+        throw std::runtime_error(
+            "dense_attention: a backward pass is captured while an autograd graph of the same "
+            "inputs, made outside the capture on the default stream, is alive");
+    }
+  }
   variable_list compute(Tensor d_o) {
     at::NoGradGuard no_grad;
     auto self = shared_from_this();
     const Tensor q_ = q.unpack(), k_ = k.unpack(), v_ = v.unpack(), cu_ = cu.unpack();
     const Tensor bias_ = bias.unpack(), o_ = o.unpack(self), saved_ = saved.unpack();
     c10::cuda::CUDAGuard guard(q_.device());
+    check_capture();
     if (d_o.scalar_type() != at::kBFloat16) d_o = d_o.to(at::kBFloat16);
     msa_dense_params prm = call.prm;
     prm.bucket_starts = call.starts.data();

@@ -268,6 +268,34 @@ def test_two_captured_graphs_replay_on_new_inputs():
     assert _status() == 0
 
 
+def test_captured_backward_beside_an_eager_graph():
+    """A leaf that a graph made on the default stream still holds: an error, and the capture
+    ends; with that graph gone the same capture works."""
+    from block_sparse_attention_proxy_gb300 import dense_attention
+
+    x = _inputs([70], 4, 2, 64, 24)
+    want = _call(x)["dq"]
+    q = x["q"].detach().requires_grad_(True)
+    eager = dense_attention(q, x["k"], x["v"], x["cu"])
+    torch.cuda.synchronize()
+
+    def capture():
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            o = dense_attention(q, x["k"], x["v"], x["cu"])
+            return g, torch.autograd.grad(o, q, x["do"])[0]
+
+    with pytest.raises(RuntimeError, match="outside the capture"):
+        capture()
+    assert torch.equal(torch.autograd.grad(eager, q, x["do"])[0], want)
+    del eager
+    g, dq = capture()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(dq, want)
+    assert _status() == 0
+
+
 def test_offsets_beyond_32_bits():
     """More than 2^31 elements of q: the last documents equal the same documents alone."""
     n, doc, hq, hkv, d = 280000, 70, 64, 8, 128
