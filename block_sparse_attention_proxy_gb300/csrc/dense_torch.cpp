@@ -51,6 +51,13 @@ Tensor take(const Tensor& t, int64_t* stride) {
   return t.clone(at::MemoryFormat::Contiguous);
 }
 
+// A tensor that the library takes contiguous, on 32 bytes.
+Tensor whole(const Tensor& t) {
+  return t.is_contiguous() && reinterpret_cast<uintptr_t>(t.data_ptr()) % 32 == 0
+             ? t
+             : t.clone(at::MemoryFormat::Contiguous);
+}
+
 const uint16_t* in(const Tensor& t) {
   return t.defined() ? static_cast<const uint16_t*>(t.const_data_ptr()) : nullptr;
 }
@@ -105,16 +112,40 @@ struct DenseAttentionBackward : torch::autograd::Node {
             "inputs, made outside the capture on the default stream, is alive");
     }
   }
+  // What a saved tensor comes back as is up to its hooks (activation offload, compression):
+  // its values are those of the forward, its layout need not be.  Other sizes, types or devices
+  // are refused, the rest is brought into a layout that the library takes.
+  static void expect(const Tensor& t, at::IntArrayRef sizes, at::ScalarType type,
+                     const at::Device& device) {
+    if (!t.defined() || t.sizes() != sizes || t.scalar_type() != type || t.device() != device)
+      throw StatusError(MSA_ERR_INVALID_ARG, "dense_attention: a saved tensor");
+  }
   variable_list compute(Tensor d_o) {
     at::NoGradGuard no_grad;
     auto self = shared_from_this();
-    const Tensor q_ = q.unpack(), k_ = k.unpack(), v_ = v.unpack(), cu_ = cu.unpack();
-    const Tensor bias_ = bias.unpack(), o_ = o.unpack(self), saved_ = saved.unpack();
-    c10::cuda::CUDAGuard guard(q_.device());
-    check_capture();
-    if (d_o.scalar_type() != at::kBFloat16) d_o = d_o.to(at::kBFloat16);
+    Tensor q_ = q.unpack(), k_ = k.unpack(), v_ = v.unpack(), cu_ = cu.unpack();
+    Tensor bias_ = bias.unpack(), o_ = o.unpack(self), saved_ = saved.unpack();
     msa_dense_params prm = call.prm;
     prm.bucket_starts = call.starts.data();
+    const at::Device device = d_o.device();
+    const int64_t T = prm.total_tokens;
+    expect(q_, {T, prm.hq, prm.d}, at::kBFloat16, device);
+    expect(k_, {T, prm.hkv, prm.d}, at::kBFloat16, device);
+    expect(v_, {T, prm.hkv, prm.d}, at::kBFloat16, device);
+    expect(o_, {T, prm.hq, prm.d}, at::kBFloat16, device);
+    expect(cu_, {(int64_t)prm.num_docs + 1}, at::kInt, device);
+    expect(saved_, {call.saved()}, at::kByte, device);
+    if (prm.num_buckets > 0) expect(bias_, {prm.hq, prm.num_buckets}, at::kBFloat16, device);
+    c10::cuda::CUDAGuard guard(device);
+    check_capture();
+    q_ = take(q_, &prm.q_stride);
+    k_ = take(k_, &prm.k_stride);
+    v_ = take(v_, &prm.v_stride);
+    o_ = whole(o_);
+    saved_ = whole(saved_);
+    cu_ = cu_.contiguous();
+    if (bias_.defined()) bias_ = bias_.contiguous();
+    if (d_o.scalar_type() != at::kBFloat16) d_o = d_o.to(at::kBFloat16);
     d_o = take(d_o, &prm.do_stride);
     const auto opt = q_.options().requires_grad(false);
     Tensor dq = at::empty(q_.sizes(), opt), dk = at::empty(k_.sizes(), opt);
