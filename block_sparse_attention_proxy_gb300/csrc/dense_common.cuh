@@ -63,6 +63,16 @@ struct DenseArgs {
 // over the documents is needed.  ndoc + 1 documents: the last is the padding.
 __host__ __device__ inline int dense_slots(int T, int ndoc, int bt) { return T / bt + ndoc + 1; }
 
+// Ring positions, tiles and steps are counted over all the items of a CTA, and only the place
+// in a ring, the phase of its barriers and whether a ring has been filled once are taken from
+// the counts.  Between items a large one is turned back by a multiple of twice every ring's
+// length: long documents of many heads reach 2^31.  An item adds at most 2^24.
+constexpr int kDenseTurn = 240 << 21;
+__host__ __device__ constexpr int dense_turn(int x) {
+  return x >= 2 * kDenseTurn ? x - kDenseTurn : x;
+}
+__host__ __device__ constexpr bool dense_turns(int ring) { return kDenseTurn % (2 * ring) == 0; }
+
 // The same value in every lane (lane 0's), and known to the compiler to be: control flow on
 // it does not count as divergent, which would keep operands out of uniform registers.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }

@@ -94,6 +94,7 @@ struct DqCfg {
   static constexpr int kSmem = (2 + kNK + kNV) * kTile + 256 + 2 * 1024 +
                                (BIAS ? (int)sizeof(DenseBias) : 0);
   static_assert(kSmem <= 232448, "shared memory budget");
+  static_assert(dense_turns(kNK) && dense_turns(kNV) && dense_turns(2), "counts are turned back");
 };
 
 template <int D, bool BIAS>
@@ -221,6 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           xv = X + 1;
         }
         __syncwarp();
+        X = dense_turn(X);
       }
       if (*abort_flag) {  // copies in flight land before the CTA leaves
         if (items > 0) drain_bar(bar(B_Q), (items - 1) & 1);
@@ -282,6 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit(el, bar(B_KE + X % NK));
         }
         mma_commit(el, bar(B_DQ));
+        X = dense_turn(X);
       }
       if (!ok) {  // products in flight end before TMEM is freed
         mma_commit(el, bar(B_END));
@@ -545,6 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       ++items;
+      X = dense_turn(X);
       if (BIAS) {
         my[bk * 256] = acc;
         done |= 1ull << bk;
@@ -640,6 +644,7 @@ struct DkvCfg {
   static constexpr int kSmem =
       (2 + kNQ + kNO) * kTile + kNS * 1024 + 256 + (BIAS ? (int)sizeof(DenseBias) : 0);
   static_assert(kSmem <= 232448, "shared memory budget");
+  static_assert(dense_turns(kNQ) && dense_turns(kNO) && dense_turns(kNS), "counts are turned back");
 };
 
 template <int D, bool BIAS>
@@ -759,6 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (++qt == w.nq) qt = 0, ++h;
         }
         __syncwarp();
+        X = dense_turn(X);
       }
       if (*abort_flag) {  // copies in flight land before the CTA leaves
         if (items > 0) drain_bar(bar(B_KV), (items - 1) & 1);
@@ -826,6 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (n + 2 == NT) mma_commit(el, bar(B_KVE));  // the last use of K and V
         }
         mma_commit(el, bar(B_G));
+        X = dense_turn(X);
       }
       if (!ok) {  // products in flight end before TMEM is freed
         mma_commit(el, bar(B_END));
@@ -854,6 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(bar(B_TF + s));
           if (++qt == w.nq) qt = 0, ++h;
         }
+        X = dense_turn(X);
       }
     }
   } else {
@@ -1019,6 +1027,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++qt == wk.nq) qt = 0, ++hl;
       }
       ++items;
+      X = dense_turn(X);
       dead = dead || !dense_wait(bar(B_G), (items - 1) & 1, abort_flag, a.status,
                                     wait_site(kKerDenseDkv, B_G, items));
       tc_fence_after();

@@ -51,6 +51,7 @@ struct FwdCfg {
   static constexpr int kRing = D == 128 ? (BIAS ? 4 : 5) : 8;
   static constexpr int kSmem = (2 + kRing) * kTile + 256 + (BIAS ? (int)sizeof(DenseBias) : 0);
   static_assert(kSmem <= 232448, "shared memory budget");
+  static_assert(dense_turns(kRing) && dense_turns(2 * kHalves), "counts are turned back");
 };
 
 template <int D, bool BIAS>
@@ -175,6 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
+        x = dense_turn(x);
       }
       // an aborted CTA must not leave before its copies have landed
       if (*abort_flag) {
@@ -257,9 +259,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (n + 2 == nk) mma_commit(el, bar(B_QE));  // the last S has been issued
         }
-        x += 2 * nk;
-        U[0] += nu0;
-        U[1] += nu1;
+        x = dense_turn(x + 2 * nk);
+        U[0] = dense_turn(U[0] + nu0);
+        U[1] = dense_turn(U[1] + nu1);
       }
       if (!ok) {  // products in flight end before TMEM is freed
         mma_commit(el, bar(B_END));
@@ -499,6 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
       }
+      U = dense_turn(U);
     }
   }
   tc_fence_before();
