@@ -122,18 +122,24 @@ def msa_bwd(params, cu_seqlens, q, k, v, q_p, k_p, o, o_res, lse, mass, dO, sel_
                           ws.numel() * ws.element_size(), _stream(stream)), "msa_bwd")
 
 
-def _rows(t) -> int:
-    """A [tokens, heads, d] tensor whose token stride the params carry."""
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+def _rows(params, t, heads: int, stride: int) -> int:
+    """A [tokens, heads, d] tensor whose token stride (0: packed) the params carry."""
+    if tuple(t.shape) != (params.total_tokens, heads, params.d):
+        raise ValueError("the params say [%d, %d, %d]" % (params.total_tokens, heads, params.d))
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != params.d):
         raise ValueError("the heads of one token must be contiguous")
+    if params.total_tokens > 1 and t.stride(0) != (stride or heads * params.d):
+        raise ValueError("the tensor's token stride differs from the params'")
     return t.data_ptr()
 
 
 def msa_dense_fwd(params, cu_seqlens, q, k, v, bias, o, o_res, lse, stream=None) -> None:
     """Dense attention forward; q, k, v may have the token strides given in `params`."""
-    _check(load().msa_dense_fwd(ctypes.byref(params), _ptr(cu_seqlens), _rows(q), _rows(k),
-                                _rows(v), _ptr(bias), _ptr(o), _ptr(o_res), _ptr(lse),
-                                _stream(stream)), "msa_dense_fwd")
+    p = params
+    _check(load().msa_dense_fwd(ctypes.byref(p), _ptr(cu_seqlens), _rows(p, q, p.hq, p.q_stride),
+                                _rows(p, k, p.hkv, p.k_stride), _rows(p, v, p.hkv, p.v_stride),
+                                _ptr(bias), _ptr(o), _ptr(o_res), _ptr(lse), _stream(stream)),
+           "msa_dense_fwd")
 
 
 def msa_dense_bwd_workspace_size(params: MsaDenseParams) -> int:
@@ -142,10 +148,13 @@ def msa_dense_bwd_workspace_size(params: MsaDenseParams) -> int:
 
 def msa_dense_bwd(params, cu_seqlens, q, k, v, bias, o, o_res, lse, dO, dq, dk, dv, dbias, ws,
                   stream=None) -> None:
-    _check(load().msa_dense_bwd(ctypes.byref(params), _ptr(cu_seqlens), _rows(q), _rows(k),
-                                _rows(v), _ptr(bias), _ptr(o), _ptr(o_res), _ptr(lse), _rows(dO),
-                                _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dbias), _ptr(ws),
-                                ws.numel() * ws.element_size(), _stream(stream)), "msa_dense_bwd")
+    p = params
+    _check(load().msa_dense_bwd(ctypes.byref(p), _ptr(cu_seqlens), _rows(p, q, p.hq, p.q_stride),
+                                _rows(p, k, p.hkv, p.k_stride), _rows(p, v, p.hkv, p.v_stride),
+                                _ptr(bias), _ptr(o), _ptr(o_res), _ptr(lse),
+                                _rows(p, dO, p.hq, p.do_stride), _ptr(dq), _ptr(dk), _ptr(dv),
+                                _ptr(dbias), _ptr(ws), ws.numel() * ws.element_size(),
+                                _stream(stream)), "msa_dense_bwd")
 
 
 def msa_get_device_status(stream=None) -> int:
