@@ -47,12 +47,13 @@ struct DenseArgs {
   // forward outputs; in the backward o, o_res and lse are inputs
   uint16_t* o;
   uint16_t* o_res;  // bf16(O - o); null: not stored
-  float* lse;
+  float* lse;       // with o_res relative to the rows' references, as the backward takes it
   // backward
   const uint16_t* d_o;
   long long do_stride;
-  float2* stats;  // [hq][T] {lse log2(e) (+inf: no key left), D = rowsum(dO o O)}
+  float2* stats;  // [hq][T] {-lse log2(e) (-inf: no key left), D = rowsum(dO o O)}
   uint16_t *dq, *dk, *dv;
+  float* refs;    // [hq][T] the rows' references (dense_row_ref)
   float* slots;   // [CTA][nb][2][128] per-row bucket sums of dS
   float* parts;   // [nslots][hq][nb] their sums over the rows of an item
 };
@@ -436,12 +437,29 @@ __device__ __forceinline__ void mma_tile_ss(uint32_t el, uint32_t d, uint32_t a_
   }
 }
 
-// A bias in log2 units.  The lowest finite values stay finite (log2(e) times
-// them would not), so that rows in which only such values are left keep a
-// finite maximum; -inf stays -inf and masks.
-__device__ __forceinline__ float dense_bias_log2(uint16_t raw) {
-  const float b = __uint_as_float((uint32_t)raw << 16);
-  return b < -FLT_MAX ? b : fmaxf(b * kLog2E, -FLT_MAX);
+// A bias in log2 units, less the row's reference (dense_row_ref).
+__device__ __forceinline__ float dense_bias_of(uint16_t raw) {
+  return __uint_as_float((uint32_t)raw << 16);
+}
+__device__ __forceinline__ float dense_bias_log2(uint16_t raw, float ref = 0.f) {
+  return (dense_bias_of(raw) - ref) * kLog2E;
+}
+
+// Softmax does not change when a row's scores all move by the same amount, and a score next to a
+// bias of -1e9 (a mask by a large finite value) has no bits left in fp32.  So a row whose
+// largest bias within reach is that far from zero takes its biases, its maximum and its
+// log-sum-exp relative to that bias, its reference: equal biases cancel before a score is added,
+// and what lies far below the reference has no weight whether it overflows or not.  All other
+// rows have the reference 0 (a largest bias of at most 64 leaves a score 2^-17 of precision).
+// From 2^56 on, the lowest value of a type among them, a sum of bias and score holds no bit of
+// the score in 64 bits either: such a row weighs its keys equally, as that sum does.
+constexpr float kDenseModerate = 64.f, kDenseAbsorbs = 72057594037927936.f;
+__device__ __forceinline__ bool dense_extreme(float b) {
+  return fabsf(b) > kDenseModerate && fabsf(b) < INFINITY;
+}
+// What scores of such a row are multiplied by.  Not 0: a masked score is -inf.
+__device__ __forceinline__ float dense_row_scale(const DenseArgs& a, float ref) {
+  return fabsf(ref) < kDenseAbsorbs ? a.scale_log2 : 1e-30f;
 }
 
 // What a CTA keeps of the bias table in shared memory.  Tiles whose rows each lie in
@@ -460,6 +478,7 @@ struct DenseBias {
   uint32_t bits[(kDenseBits + kDenseBitsPad) / 32 + 2];
   int starts[kDenseMaxBuckets];  // INT_MAX behind the last bucket
   float table[kDenseTable];      // [G][nb] in log2 units, if it fits
+  int extreme;                   // 1: the table has entries that may be a row's reference
 };
 // Row length of the table (heads end on different banks: a warp reads 32/G tokens of G
 // heads at once) and the distances that fit.
@@ -482,6 +501,18 @@ __device__ __forceinline__ int dense_bucket(const DenseBias* s, int x) {
   return b;
 }
 
+// The reference of a row: the largest bias over the distances 0..last of its keys, if that is
+// far from zero (tab: its head's row of the table).  All buckets up to the last one's are
+// reached, so there is a key with this bias.
+__device__ __forceinline__ float dense_row_ref(const DenseArgs& a, const DenseBias* s,
+                                               const uint16_t* tab, int last) {
+  if (!s->extreme) return 0.f;
+  float m = -INFINITY;
+  for (int b = 0; b < a.nb && s->starts[b] <= last; ++b)
+    m = fmaxf(m, dense_bias_of(__ldg(tab + b)));
+  return dense_extreme(m) ? m : 0.f;
+}
+
 // Fills it for KV head g (threads 0..255, all of them; none may still read the last one's).
 template <bool BITS>
 __device__ __forceinline__ void dense_bias_tables(const DenseArgs& a, DenseBias* s, int g) {
@@ -491,11 +522,17 @@ __device__ __forceinline__ void dense_bias_tables(const DenseArgs& a, DenseBias*
   const uint16_t* tab = a.bias + (size_t)g * a.G * a.nb;
   named_bar_sync(2, 256);
   if (tid < kDenseMaxBuckets) s->starts[tid] = tid < a.nb ? a.starts[tid] : INT_MAX;
-  if (staged)
-    for (int x = tid; x < a.G * a.nb; x += 256) s->table[x] = dense_bias_log2(__ldg(tab + x));
+  if (tid == 0) s->extreme = 0;
+  bool extreme = false;
+  for (int x = tid; x < a.G * a.nb; x += 256) {
+    const uint16_t raw = __ldg(tab + x);
+    if (staged) s->table[x] = dense_bias_log2(raw);
+    extreme |= dense_extreme(dense_bias_of(raw));
+  }
   if (BITS)
     for (int x = tid; x < (kDenseBits + kDenseBitsPad) / 32 + 2; x += 256) s->bits[x] = 0;
   named_bar_sync(2, 256);
+  if (extreme) s->extreme = 1;
   if (a.lut_w > 0) {
     for (int x = tid; x < pad; x += 256)
       for (int h = 0; h < a.G; ++h) s->lut[h * a.lut_stride + x] = 0.f;

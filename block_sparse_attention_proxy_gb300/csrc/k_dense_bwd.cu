@@ -385,6 +385,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       int bk = a.nb - 1, stk = INT_MAX;  // bucket of the next scores and its first distance
       float bias0 = 0.f;                 // its bias
       const uint16_t* tab = a.bias + (size_t)(wk.g * a.G + hl) * a.nb;
+      float c = a.scale_log2, ref = 0.f;
+      if (BIAS) {
+        ref = dense_row_ref(a, sB, tab, valid ? qi : -1);
+        c = dense_row_scale(a, ref);
+        if (w == 0 && valid) a.refs[(size_t)(wk.g * a.G + hl) * a.T + wk.it.start + qi] = ref;
+      }
       for (int n = 0; n < wk.N; ++n, ++X) {
         const int b = X & 1;
         const int rel = valid ? qi - n * 128 - 64 * w : -1;  // columns 0..rel are visible
@@ -405,10 +411,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               bk = first;
             }
             stk = bk > 0 ? sB->starts[bk] : INT_MIN;
-            bias0 = dense_bias_log2(__ldg(tab + bk));
+            bias0 = dense_bias_log2(__ldg(tab + bk), ref);
           }
           one = __all_sync(0xffffffffu, bk == 0 || stk <= rel - 63);
-          near = __all_sync(0xffffffffu, rel < a.lut_w);
+          near = __all_sync(0xffffffffu, rel < a.lut_w && ref == 0.f);
         }
         uint32_t x[2][32];
         wait(B_S + b, (X >> 1) & 1);
@@ -420,32 +426,32 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 64; ++i)
               x[i >> 5][i & 31] = __float_as_uint(
-                  ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), a.scale_log2, sub)));
+                  ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), c, sub)));
           } else {
             if (near) {
               const float* lut = sB->lut + hl * a.lut_stride + dense_lut_pad(a) + rel;
 #pragma unroll
               for (int i = 0; i < 64; ++i)
                 x[i >> 5][i & 31] = __float_as_uint(ex2_approx(
-                    fmaf(__uint_as_float(x[i >> 5][i & 31]), a.scale_log2, nl + lut[-i])));
+                    fmaf(__uint_as_float(x[i >> 5][i & 31]), c, nl + lut[-i])));
             } else if (__all_sync(0xffffffffu, bk < 2 || sB->starts[bk - 1] <= rel - 63)) {
               // at most one start inside: scores before `cut` take v0, the others v1
               const int cut = bk > 0 ? rel - sB->starts[bk] + 1 : 64;
               const float v0 = nl + bias0;
-              const float v1 = nl + dense_bias_log2(__ldg(tab + max(bk - 1, 0)));
+              const float v1 = nl + dense_bias_log2(__ldg(tab + max(bk - 1, 0)), ref);
 #pragma unroll
               for (int u = 0; u < 4; ++u) {
                 if (__any_sync(0xffffffffu, cut > 16 * u && cut < 16 * u + 16)) {
 #pragma unroll
                   for (int i = 16 * u; i < 16 * u + 16; ++i)
                     x[i >> 5][i & 31] = __float_as_uint(ex2_approx(fmaf(
-                        __uint_as_float(x[i >> 5][i & 31]), a.scale_log2, i < cut ? v0 : v1)));
+                        __uint_as_float(x[i >> 5][i & 31]), c, i < cut ? v0 : v1)));
                 } else {
                   const float sub = 16 * u < cut ? v0 : v1;
 #pragma unroll
                   for (int i = 16 * u; i < 16 * u + 16; ++i)
                     x[i >> 5][i & 31] = __float_as_uint(
-                        ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), a.scale_log2, sub)));
+                        ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), c, sub)));
                 }
               }
             } else {
@@ -457,10 +463,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (rel - i < st) {
                   --q;
                   st = q > 0 ? sB->starts[q] : INT_MIN;
-                  sub = nl + dense_bias_log2(__ldg(tab + q));
+                  sub = nl + dense_bias_log2(__ldg(tab + q), ref);
                 }
                 x[i >> 5][i & 31] = __float_as_uint(
-                    ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), a.scale_log2, sub)));
+                    ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), c, sub)));
               }
             }
             __syncwarp();
@@ -642,7 +648,8 @@ struct DkvCfg {
   static constexpr int kNQ = D == 128 ? (BIAS ? 2 : 3) : 4, kNO = D == 128 ? 2 : 4;  // Q, dO rings
   static constexpr int kNS = 2;  // statistics ring
   static constexpr int kSmem =
-      (2 + kNQ + kNO) * kTile + kNS * 1024 + 256 + (BIAS ? (int)sizeof(DenseBias) : 0);
+      (2 + kNQ + kNO) * kTile + kNS * 1024 + 256 +
+      (BIAS ? kNS * 512 + 16 + (int)sizeof(DenseBias) : 0);
   static_assert(kSmem <= 232448, "shared memory budget");
   static_assert(dense_turns(kNQ) && dense_turns(kNO) && dense_turns(kNS), "counts are turned back");
 };
@@ -669,7 +676,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + B_END + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   static_assert((B_END + 1) * 8 + 8 <= 256, "barrier block");
-  DenseBias* sB = reinterpret_cast<DenseBias*>(reinterpret_cast<uint8_t*>(bars) + 256);
+  // the rows' references, and whether one of a tile's is not zero
+  float* sRef = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 256);  // [NS][128]
+  int* sFar = reinterpret_cast<int*>(sRef + NS * 128);                             // [NS]
+  static_assert(NS <= 4, "16 bytes");
+  DenseBias* sB = reinterpret_cast<DenseBias*>(sFar + 4);
   auto bar = [&](int i) { return smem_u32(bars + i); };
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
@@ -854,9 +865,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int u = 0; u < 4; ++u)
             v[u] = lane + 32 * u < left ? __ldg(src + lane + 32 * u) : make_float2(-INFINITY, 0.f);
+          float f[4];
+          bool far = false;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            f[u] = BIAS && lane + 32 * u < left
+                       ? __ldg(a.refs + (src - a.stats) + lane + 32 * u)
+                       : 0.f;
+            far |= f[u] != 0.f;
+          }
           if (X >= NS && !(ok = wait(B_TE + s, ((X / NS) & 1) ^ 1, n))) break;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) sSt[s * 128 + lane + 32 * u] = v[u];
+          for (int u = 0; u < 4; ++u) {
+            sSt[s * 128 + lane + 32 * u] = v[u];
+            if (BIAS) sRef[s * 128 + lane + 32 * u] = f[u];
+          }
+          if (BIAS) {
+            far = __any_sync(0xffffffffu, far);
+            if (lane == 0) sFar[s] = far;
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(B_TF + s));
           if (++qt == w.nq) qt = 0, ++h;
@@ -918,7 +945,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!dead) {
           tmem_ld32x2(tl + 64 * w, tl + 64 * w + 32, x[0], x[1]);
           const float c = a.scale_log2;
-          if (one) {
+          if (BIAS && sFar[s]) {
+            // a query of the tile has a reference: bucket by bucket, relative to each query's
+            const float2* sl = sSt + s * 128 + 64 * w;
+            const float* rf = sRef + s * 128 + 64 * w;
+            int q = bk;
+            int nx = q + 1 < a.nb ? sB->starts[q + 1] : INT_MAX;
+            uint16_t raw = __ldg(tab + q);
+#pragma unroll
+            for (int i = 0; i < 64; ++i) {
+              if (rel + i >= nx) {
+                ++q;
+                nx = q + 1 < a.nb ? sB->starts[q + 1] : INT_MAX;
+                raw = __ldg(tab + q);
+              }
+              x[i >> 5][i & 31] = __float_as_uint(
+                  ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), dense_row_scale(a, rf[i]),
+                                  sl[i].x + dense_bias_log2(raw, rf[i]))));
+            }
+            __syncwarp();  // the TMEM store below is warp-collective
+          } else if (one) {
             const float bv = bias0;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {

@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tbase + lane_off + 128 * t, to = tbase + lane_off + 256 + D * t;
     const int ti = r / a.G, hl = r % a.G;  // hl < G also for rows behind tpt
-    const float c = a.scale_log2;
+    float c = a.scale_log2, ref = 0.f;  // see dense_row_ref
     bool dead = false;
     int U = 0, table_of = -1;  // steps so far; KV head the bias tables are of
     for (int k = 0; k < rounds; ++k) {
@@ -307,6 +307,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int bk = a.nb - 1, stk = INT_MAX;  // bucket of the next scores and its first distance
       float v0 = 0.f;                    // its bias
       const uint16_t* tab = a.bias + (size_t)(w.g * a.G + hl) * a.nb;
+      if (BIAS) {
+        ref = dense_row_ref(a, sB, tab, qi);
+        c = dense_row_scale(a, ref);
+      }
       for (int u = 0; u < nut; ++u, ++U) {
         const int b = U % NH;  // buffer of this step
         const uint32_t par = (U / NH) & 1;
@@ -316,10 +320,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (__any_sync(0xffffffffu, rel < stk)) {  // the row's first bucket here is another
             bk = dense_bucket(sB, rel);
             stk = bk > 0 ? sB->starts[bk] : INT_MIN;
-            v0 = dense_bias_log2(__ldg(tab + bk));
+            v0 = dense_bias_log2(__ldg(tab + bk), ref);
           }
           one = __all_sync(0xffffffffu, bk == 0 || stk <= rel - (W - 1));
-          near = __all_sync(0xffffffffu, rel < a.lut_w);
+          near = __all_sync(0xffffffffu, rel < a.lut_w && ref == 0.f);
         }
         dead = dead || !dense_wait(bar(B_S + 2 * t + b), par, abort_flag, a.status,
                                    wait_site(kKerDenseFwd, B_S + 2 * t + b, u));
@@ -357,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else if (__all_sync(0xffffffffu, kb < 2 || sB->starts[kb - 1] <= lowest)) {
                   // one start inside: scores before `cut` take bv, the others v1
                   const int cut = kb > 0 ? rel - st + 1 : W;
-                  const float v1 = dense_bias_log2(__ldg(tab + max(kb - 1, 0)));
+                  const float v1 = dense_bias_log2(__ldg(tab + max(kb - 1, 0)), ref);
 #pragma unroll
                   for (int i = 16 * y; i < 16 * y + 16; ++i)
                     x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, i < cut ? bv : v1));
@@ -370,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   for (int i = 16 * y; i < 16 * y + 16; ++i) {
                     while (kb > 0 && sB->starts[kb] > rel - i) {
                       --kb;
-                      bv = dense_bias_log2(__ldg(tab + kb));
+                      bv = dense_bias_log2(__ldg(tab + kb), ref);
                     }
                     x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), c, bv));
                   }
@@ -497,7 +501,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             dense_store_row(v, inv, dst ? dst + 64 * q : nullptr);
             if (a.o_res) dense_store_row<true>(v, inv, res ? res + 64 * q : nullptr);
           }
-          if (valid && a.lse) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+          if (valid && a.lse) {
+            const float lse = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            a.lse[row] = a.o_res ? lse : lse + ref;
+          }
         }
         tc_fence_before();
       }

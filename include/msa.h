@@ -260,6 +260,10 @@ msa_status msa_proxy_select_noalloc(const msa_params* params, const int32_t* cu_
  *   - Documents do not affect one another, whatever values they hold.
  *   - A bias of -inf masks its distances.  A row without a key left has o = 0,
  *     lse = -inf and no gradient.
+ *   - Finite biases of any size are exact: the scores of a row whose keys all
+ *     carry -1e9 keep their weights.  From 2^56 in magnitude on (the lowest value of
+ *     a type), where scores would be lost in fp64 sums too, such keys
+ *     weigh the same.
  *   - Every sum has a fixed order: results repeat bit for bit.
  *   - The conventions above on ownership, alignment, streams, graph capture and
  *     errors hold; only the backward has a workspace, and calls that share none
@@ -282,7 +286,9 @@ typedef struct msa_dense_params {
 
 /* Inputs: cu_seqlens, q, k, v, bias (null without one).  Outputs: o, and what
    msa_dense_bwd needs: o_res [T, hq, d], the bf16 rounding residual of o (as
-   msa_fwd's), and lse (each null: not stored). */
+   msa_fwd's), and lse (each null: not stored).  Where o_res is stored, the lse of a row
+   whose largest bias within reach is finite and beyond 64 in magnitude is stored less
+   that bias, for the backward: one fp32 number cannot hold both. */
 msa_status msa_dense_fwd(const msa_dense_params* params, const int32_t* cu_seqlens,
                          const uint16_t* q, const uint16_t* k, const uint16_t* v,
                          const uint16_t* bias, uint16_t* o, uint16_t* o_res, float* lse,

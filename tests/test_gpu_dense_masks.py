@@ -1,0 +1,67 @@
+"""Dense attention with large finite biases: masks by a large negative value, by a type's
+lowest one, and tables whose entries are far from zero."""
+import pytest
+import torch
+
+from dense_exact import compare, dense_exact
+from test_gpu_dense import _call, _inputs, _status
+
+pytestmark = pytest.mark.gpu
+
+LOWEST = torch.finfo(torch.bfloat16).min
+LENS = [1, 2, 40, 300, 130]
+STARTS = (0, 3, 40, 150)
+
+
+def _tables(value):
+    """Where a head's large entries are; every head but the first gets them."""
+    def fill(bias, columns, values):
+        for c, x in zip(columns, values):
+            bias[1:, c] = x
+        return bias
+
+    return {
+        # a document's first tokens have no other key
+        "first": lambda b: fill(b, [0], [value]),
+        "last": lambda b: fill(b, [3], [value]),
+        "all": lambda b: fill(b, range(4), [value] * 4),
+        # a row's largest entry changes along the document
+        "falling": lambda b: fill(b, range(4), [value, value / 2, value / 4, 0.5]),
+        "apart": lambda b: fill(b, range(4), [value, -value, value, float("-inf")]),
+    }
+
+
+@pytest.mark.parametrize("where", ["first", "last", "all", "falling", "apart"])
+@pytest.mark.parametrize("value", [LOWEST, -1e9, -1e5, -100.0, 1e5])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 1, 64), (3, 3, 128), (33, 1, 128)])
+def test_large_finite_biases(hq, hkv, d, value, where):
+    """Every output against the definition, and the public log-sum-exp."""
+    from block_sparse_attention_proxy_gb300 import make_dense_params, msa_dense_fwd
+
+    x = _inputs(LENS, hq, hkv, d, 50, nb=4)
+    x["bias"] = _tables(value)[where](x["bias"])
+    got = _call(x, STARTS)
+    t = sum(LENS)
+    o, got["lse"] = torch.empty_like(x["q"]), torch.empty(t, hq, device="cuda")
+    msa_dense_fwd(make_dense_params(t, len(LENS), hq, hkv, d, 1.0, STARTS), x["cu"], x["q"],
+                  x["k"], x["v"], x["bias"], o, None, got["lse"])
+    assert _status() == 0
+    assert torch.equal(o, got["o"])
+    compare(got, dense_exact(x["q"], x["k"], x["v"], LENS, 1.0, x["bias"], STARTS, x["do"]))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_table_far_from_zero(d):
+    """A constant added to a whole table changes nothing but the log-sum-exp: a long document
+    whose buckets begin inside tiles near and far, with 512 added, where bf16 still tells
+    the entries apart."""
+    starts = (0, 1, 2, 5, 70, 200, 201, 640, 900)
+    x = _inputs([1100, 77], 4, 2, d, 51, nb=9)
+    x["bias"] = x["bias"].float().mul(4).round().mul(4).bfloat16()  # multiples of 4
+    want = _call(x, starts)
+    x["bias"] = (x["bias"].float() + 512).bfloat16()
+    got = _call(x, starts)
+    exact = dense_exact(x["q"], x["k"], x["v"], [1100, 77], 1.0, x["bias"], starts, x["do"])
+    compare(got, exact)
+    compare(want, exact)
+    assert _status() == 0
