@@ -478,7 +478,7 @@ struct DenseBias {
   uint32_t bits[(kDenseBits + kDenseBitsPad) / 32 + 2];
   int starts[kDenseMaxBuckets];  // INT_MAX behind the last bucket
   float table[kDenseTable];      // [G][nb] in log2 units, if it fits
-  int extreme;                   // 1: the table has entries that may be a row's reference
+  int extreme;                   // 1: the table has entries above 64 in magnitude, or NaN
 };
 // Row length of the table (heads end on different banks: a warp reads 32/G tokens of G
 // heads at once) and the distances that fit.
@@ -527,7 +527,8 @@ __device__ __forceinline__ void dense_bias_tables(const DenseArgs& a, DenseBias*
   for (int x = tid; x < a.G * a.nb; x += 256) {
     const uint16_t raw = __ldg(tab + x);
     if (staged) s->table[x] = dense_bias_log2(raw);
-    extreme |= dense_extreme(dense_bias_of(raw));
+    const float b = dense_bias_of(raw);
+    extreme |= !(fabsf(b) <= kDenseModerate || b == -INFINITY);
   }
   if (BITS)
     for (int x = tid; x < (kDenseBits + kDenseBitsPad) / 32 + 2; x += 256) s->bits[x] = 0;

@@ -941,30 +941,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           near = __all_sync(0xffffffffu, rel + 63 < a.lut_w);
         }
         wait(B_TF + s, (X / NS) & 1);
+        // Bucket by bucket, relative to each query's reference: where a query of the tile has
+        // one, and, if entries of the table may overflow, where the tile has queries behind the
+        // document's end, whose distances may reach buckets that no pair does.
+        const int end = wk.it.len - wk.j0 - qt * 128 - 64 * w;
+        const bool walk = BIAS && (sFar[s] || (sB->extreme && end < 64));
+        if (walk) one = near = false;
         wait(B_S, X & 1);
         if (!dead) {
           tmem_ld32x2(tl + 64 * w, tl + 64 * w + 32, x[0], x[1]);
           const float c = a.scale_log2;
-          if (BIAS && sFar[s]) {
-            // a query of the tile has a reference: bucket by bucket, relative to each query's
-            const float2* sl = sSt + s * 128 + 64 * w;
-            const float* rf = sRef + s * 128 + 64 * w;
-            int q = bk;
-            int nx = q + 1 < a.nb ? sB->starts[q + 1] : INT_MAX;
-            uint16_t raw = __ldg(tab + q);
-#pragma unroll
-            for (int i = 0; i < 64; ++i) {
-              if (rel + i >= nx) {
-                ++q;
-                nx = q + 1 < a.nb ? sB->starts[q + 1] : INT_MAX;
-                raw = __ldg(tab + q);
-              }
-              x[i >> 5][i & 31] = __float_as_uint(
-                  ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), dense_row_scale(a, rf[i]),
-                                  sl[i].x + dense_bias_log2(raw, rf[i]))));
-            }
-            __syncwarp();  // the TMEM store below is warp-collective
-          } else if (one) {
+          if (one) {
             const float bv = bias0;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -983,8 +970,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < 64; ++i)
                 x[i >> 5][i & 31] = __float_as_uint(
                     ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), c, sl[i].x + lut[i])));
-            } else if (__all_sync(0xffffffffu,
-                                  bk + 2 >= a.nb || sB->starts[bk + 2] > rel + 63)) {
+            } else if (!walk && __all_sync(0xffffffffu, bk + 2 >= a.nb ||
+                                                            sB->starts[bk + 2] > rel + 63)) {
               // at most one start inside: queries before `cut` take v0, the others v1
               const int nx = min(bk + 1, a.nb - 1);
               const int cut = bk + 1 < a.nb ? sB->starts[nx] - rel : 64;
@@ -1006,18 +993,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
             } else {
+              const float* rf = sRef + s * 128 + 64 * w;
               int q = bk;
               int nx = q + 1 < a.nb ? sB->starts[q + 1] : INT_MAX;
-              float bv = bias0;
+              uint16_t raw = __ldg(tab + q);
 #pragma unroll
               for (int i = 0; i < 64; ++i) {
                 if (rel + i >= nx) {
                   ++q;
                   nx = q + 1 < a.nb ? sB->starts[q + 1] : INT_MAX;
-                  bv = dense_bias_log2(__ldg(tab + q));
+                  raw = __ldg(tab + q);
                 }
-                x[i >> 5][i & 31] = __float_as_uint(
-                    ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), c, sl[i].x + bv)));
+                const float y =
+                    ex2_approx(fmaf(__uint_as_float(x[i >> 5][i & 31]), dense_row_scale(a, rf[i]),
+                                    sl[i].x + dense_bias_log2(raw, rf[i])));
+                x[i >> 5][i & 31] = i < end ? __float_as_uint(y) : 0;
               }
             }
             __syncwarp();  // the TMEM store below is warp-collective

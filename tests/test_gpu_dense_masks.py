@@ -8,7 +8,7 @@ from test_gpu_dense import _call, _inputs, _status
 
 pytestmark = pytest.mark.gpu
 
-LOWEST = torch.finfo(torch.bfloat16).min
+LOWEST, HIGHEST = torch.finfo(torch.bfloat16).min, torch.finfo(torch.bfloat16).max
 LENS = [1, 2, 40, 300, 130]
 STARTS = (0, 3, 40, 150)
 
@@ -32,7 +32,7 @@ def _tables(value):
 
 
 @pytest.mark.parametrize("where", ["first", "last", "all", "falling", "apart"])
-@pytest.mark.parametrize("value", [LOWEST, -1e9, -1e5, -100.0, 1e5])
+@pytest.mark.parametrize("value", [LOWEST, -1e9, -1e5, -100.0, 1e5, HIGHEST])
 @pytest.mark.parametrize("hq,hkv,d", [(4, 1, 64), (3, 3, 128), (33, 1, 128)])
 def test_large_finite_biases(hq, hkv, d, value, where):
     """Every output against the definition, and the public log-sum-exp."""
@@ -64,4 +64,20 @@ def test_table_far_from_zero(d):
     exact = dense_exact(x["q"], x["k"], x["v"], [1100, 77], 1.0, x["bias"], starts, x["do"])
     compare(got, exact)
     compare(want, exact)
+    assert _status() == 0
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan"), HIGHEST])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 1, 64), (3, 3, 128), (33, 1, 64)])
+def test_buckets_that_no_pair_reaches(hq, hkv, d, value):
+    """Whatever they hold, they change nothing: buckets behind the longest document, which the
+    idle rows and columns of its last tile would reach."""
+    lens, starts = [70, 130, 3], (0, 5, 130, 131, 200)
+    x = _inputs(lens, hq, hkv, d, 52, nb=5)
+    x["bias"][:, 2:] = 0
+    want = _call(x, starts)
+    x["bias"][:, 2:] = value
+    got = _call(x, starts)
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
     assert _status() == 0
