@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (!dead) {
           const size_t row = (size_t)(w.it.start + qi) * a.hq + w.g * a.G + hl;
-          const float inv = l > 0.f ? 1.f / l : 0.f;  // 0: no key left (bias -inf)
+          const float inv = l == 0.f ? 0.f : 1.f / l;  // l = 0: no key left (bias -inf)
           uint16_t* dst = valid ? a.o + row * D : nullptr;
           uint16_t* res = valid && a.o_res ? a.o_res + row * D : nullptr;
 #pragma unroll 1
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (a.o_res) dense_store_row<true>(v, inv, res ? res + 64 * q : nullptr);
           }
           if (valid && a.lse) {
-            const float lse = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;  // NaN stays NaN
             a.lse[row] = a.o_res ? lse : lse + ref;
           }
         }
