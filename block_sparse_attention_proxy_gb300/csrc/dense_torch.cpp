@@ -68,6 +68,14 @@ msa_stream_t current_stream() {
   return reinterpret_cast<msa_stream_t>(c10::cuda::getCurrentCUDAStream().stream());
 }
 
+// There is no forward-mode derivative: a tangent would be dropped, and a Jacobian-vector product
+// come out as zero.
+void no_tangent(const Tensor& t) {
+  TORCH_CHECK_NOT_IMPLEMENTED(
+      !t.defined() || !t._fw_grad(/*level=*/0).defined(),
+      "dense_attention has no forward-mode derivative (an input carries a tangent)");
+}
+
 // What a forward leaves for its backward, besides the tensors.
 struct Call {
   msa_dense_params prm{};
@@ -91,6 +99,7 @@ struct DenseAttentionBackward : torch::autograd::Node {
   }
   variable_list apply(variable_list&& grads) override {
     if (!grads[0].defined()) return variable_list(4);
+    no_tangent(grads[0]);
     variable_list g = compute(grads[0]);
     if (!at::GradMode::is_enabled()) return g;
     // asked for with create_graph: an error where somebody differentiates further
@@ -197,6 +206,7 @@ Tensor dense_attention(const Tensor& q, const Tensor& k, const Tensor& v, const 
   Call call;
   if (bucket_starts) call.starts = *bucket_starts;
   const Tensor bias = bias_table ? *bias_table : Tensor();
+  for (const Tensor* t : {&q, &k, &v, &bias}) no_tangent(*t);
   check(q, k, v, cu_seqlens, bias, call.starts.size());
   const bool keep = at::GradMode::is_enabled() &&
                     (q.requires_grad() || k.requires_grad() || v.requires_grad() ||
@@ -260,6 +270,8 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
     } catch (const StatusError& e) {
       auto cls = py::module_::import("block_sparse_attention_proxy_gb300").attr("MsaError");
       PyErr_SetObject(cls.ptr(), cls(e.status, e.where).ptr());
+    } catch (const c10::NotImplementedError& e) {
+      PyErr_SetString(PyExc_NotImplementedError, e.what_without_backtrace());
     }
   });
   m.def("dense_attention", &dense_attention);

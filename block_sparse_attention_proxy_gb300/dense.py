@@ -58,5 +58,6 @@ def dense_attention(q, k, v, cu_seqlens, softmax_scale: float = 1.0, bias=None,
     bias: learned table [Hq, buckets]; the score of query i and key j gets the entry of
     the last bucket whose first distance, `bucket_starts[b]`, is at most i - j.
     bucket_starts begins with 0 and increases strictly (`log_buckets` makes one).
+    Differentiable once, in reverse mode; inputs with a forward-mode tangent are refused.
     Malformed cu_seqlens are found on the device (`msa_get_device_status`)."""
     return (_call or _load())(q, k, v, cu_seqlens, softmax_scale, bias, bucket_starts)

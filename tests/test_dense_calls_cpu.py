@@ -38,3 +38,17 @@ def test_tensors_that_differ_from_the_params_are_refused(which, wrong):
 
 class _Null:
     cuda_stream = 0
+
+
+@pytest.mark.parametrize("which", ["q", "k", "v", "bias"])
+def test_forward_mode_is_refused(which):
+    """It would give a product of zero: there is no forward-mode derivative."""
+    import block_sparse_attention_proxy_gb300 as m
+
+    x = {n: torch.zeros(5, 2, 64, dtype=torch.bfloat16) for n in "qkv"}
+    x["bias"] = torch.zeros(2, 3, dtype=torch.bfloat16)
+    cu = torch.tensor([0, 5], dtype=torch.int32)
+    with torch.autograd.forward_ad.dual_level():
+        x[which] = torch.autograd.forward_ad.make_dual(x[which], torch.ones_like(x[which]))
+        with pytest.raises(NotImplementedError, match="forward-mode"):
+            m.dense_attention(x["q"], x["k"], x["v"], cu, bias=x["bias"], bucket_starts=(0, 1, 2))
