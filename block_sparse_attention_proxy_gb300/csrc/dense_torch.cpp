@@ -6,6 +6,7 @@
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/autograd/functions/utils.h>
 #include <torch/csrc/autograd/saved_variable.h>
@@ -33,6 +34,20 @@ struct StatusError : std::runtime_error {
 };
 void raise_on(msa_status s, const char* where) {
   if (s != MSA_OK) throw StatusError(s, where);
+}
+
+void set_msa_error(const StatusError& e) {
+  auto cls = py::module_::import("block_sparse_attention_proxy_gb300").attr("MsaError");
+  PyErr_SetObject(cls.ptr(), cls(e.status, e.where).ptr());
+}
+// In the form in which the engine carries a Python exception to the thread that asked for the
+// gradients; other C++ exceptions become a RuntimeError there.
+[[noreturn]] void throw_to_engine(const StatusError& e) {
+  py::gil_scoped_acquire gil;
+  set_msa_error(e);
+  python_error error;
+  error.persist();
+  throw std::move(error);
 }
 
 // Token stride the library takes for a [tokens, heads, d] tensor (0: packed), or -1 where
@@ -100,7 +115,12 @@ struct DenseAttentionBackward : torch::autograd::Node {
   variable_list apply(variable_list&& grads) override {
     if (!grads[0].defined()) return variable_list(4);
     no_tangent(grads[0]);
-    variable_list g = compute(grads[0]);
+    variable_list g;
+    try {
+      g = compute(grads[0]);
+    } catch (const StatusError& e) {
+      throw_to_engine(e);
+    }
     if (!at::GradMode::is_enabled()) return g;
     // asked for with create_graph: an error where somebody differentiates further
     return torch::autograd::DelayedError("dense_attention is differentiable once", 4)
@@ -268,8 +288,7 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
     try {
       if (p) std::rethrow_exception(p);
     } catch (const StatusError& e) {
-      auto cls = py::module_::import("block_sparse_attention_proxy_gb300").attr("MsaError");
-      PyErr_SetObject(cls.ptr(), cls(e.status, e.where).ptr());
+      set_msa_error(e);
     } catch (const c10::NotImplementedError& e) {
       PyErr_SetString(PyExc_NotImplementedError, e.what_without_backtrace());
     }
