@@ -55,7 +55,7 @@ struct DenseArgs {
   uint16_t *dq, *dk, *dv;
   float* refs;    // [hq][T] the rows' references (dense_row_ref)
   float* slots;   // [CTA][nb][2][128] per-row bucket sums of dS
-  float* parts;   // [nslots][hq][nb] their sums over the rows of an item
+  float2* parts;  // [CTA][hq][nb] their sums over the CTA's items, each a pair (add_pair)
 };
 
 // Work along the tokens is cut into slots of `bt` tokens: document b owns the
@@ -596,6 +596,15 @@ __device__ __forceinline__ void dense_store_row(const uint32_t (&v)[64], float f
     }
     if (row) st_v8(row + 16 * q, w);
   }
+}
+
+// sum += x, where sum.y collects what the roundings of sum.x drop (each is exactly
+// representable: Knuth's two-sum).  n terms are off by about n^2 2^-48 of the largest partial
+// sum at most, whatever cancels.
+__device__ __forceinline__ void add_pair(float2& sum, float x) {
+  const float s = sum.x + x, b = s - sum.x;
+  sum.y += (sum.x - (s - b)) + (x - b);
+  sum.x = s;
 }
 
 // A row of zeros (documents' padding): `n` elements (a multiple of 8) by one thread.

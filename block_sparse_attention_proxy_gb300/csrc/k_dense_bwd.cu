@@ -162,20 +162,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   // phases run on from item to item (X: tiles so far).
   struct Work {
     DenseItem it;
-    int slot, g, q0;
+    int g, q0;
     int N;  // key tiles; 0: nothing to compute
   };
   const int rounds = dense_rounds(a);
   auto work = [&](int k, Work& w) -> bool {
-    if (!dense_round(a, k, &w.slot, &w.g)) return false;
-    w.N = 0;
-    w.it.doc = -1;
-    if (dense_item<false>(a, docs, w.slot, a.tpt, w.it)) {
-      w.q0 = w.it.tile * a.tpt;
-      if (w.it.doc < a.ndoc) w.N = (min(w.q0 + a.tpt, w.it.len) + 127) >> 7;
-    } else {
-      w.it.doc = -1;
-    }
+    int slot;
+    if (!dense_round(a, k, &slot, &w.g) || !dense_item<false>(a, docs, slot, a.tpt, w.it))
+      return false;
+    w.q0 = w.it.tile * a.tpt;
+    w.N = w.it.doc < a.ndoc ? (min(w.q0 + a.tpt, w.it.len) + 127) >> 7 : 0;
     return true;
   };
 
@@ -326,6 +322,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // this row's bucket sums: a row meets the distances in falling order, so a
     // bucket is finished when the next one begins and is stored once
     float* my = BIAS ? a.slots + (size_t)blockIdx.x * a.nb * 256 + w * 128 + r : nullptr;
+    float2* sums = BIAS ? a.parts + (size_t)blockIdx.x * a.hq * a.nb : nullptr;
+    if (BIAS)
+      for (int x = threadIdx.x; x < a.hq * a.nb; x += 256) sums[x] = make_float2(0.f, 0.f);
     bool dead = false;
     int X = 0, items = 0, table_of = -1;  // table_of: KV head the bias tables are of
     // row statistics, 16 rows per warp
@@ -337,10 +336,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; k < rounds; ++k) {
         if (!work(k, wk)) continue;
         if (wk.N > 0) return true;
-        if (BIAS) {
-          float* part = a.parts + ((size_t)wk.slot * a.hq + wk.g * a.G) * a.nb;
-          for (int x = threadIdx.x; x < a.G * a.nb; x += 256) part[x] = 0.f;
-        }
         if (wk.it.doc == a.ndoc) {  // padding behind the last document: zero rows
           const int n = min(a.tpt, wk.it.len - wk.q0) * a.G, rr = (int)threadIdx.x;
           if (rr < n)
@@ -359,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (!kRowWarps) next_stats();
     while (have) {
-      float* part = BIAS ? a.parts + ((size_t)wk.slot * a.hq + wk.g * a.G) * a.nb : nullptr;
+      float2* part = BIAS ? sums + (size_t)wk.g * a.G * a.nb : nullptr;
       if (BIAS && table_of != wk.g) {
         dense_bias_tables<true>(a, sB, wk.g);
         table_of = wk.g;
@@ -562,9 +557,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!((done >> b) & 1)) my[b * 256] = 0.f;
         // Sums over the item's rows, head by head, in a fixed order: a warp takes every eighth
         // bucket, four at a time; P lanes to a head add up every P-th token each, and then
-        // pairwise (more than 32 heads: one lane to a head, 32 heads at a time).  The first
-        // barrier orders the stores above before the loads, the second the loads before the
-        // next item's stores.
+        // pairwise (more than 32 heads: one lane to a head, 32 heads at a time), and add that to
+        // the CTA's sum: the same thread for the same entry each time.  The first barrier
+        // orders the stores above before the loads, the second the loads before the next
+        // item's stores.
         __threadfence_block();
         named_bar_sync(2, 256);
         const float* all = a.slots + (size_t)blockIdx.x * a.nb * 256;
@@ -573,6 +569,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int h0 = 0; h0 < a.G; h0 += 32) {
             const int h = h0 + lane;
             const int end = h < step ? a.tpt * a.G : 0;  // lanes left over have no rows
+            float2 sum[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              sum[u] = part[min(h, a.G - 1) * a.nb + min(b0 + 8 * u, a.nb - 1)];
             float v[4] = {0.f, 0.f, 0.f, 0.f};
             for (int x0 = h; __any_sync(0xffffffffu, x0 < end); x0 += 5 * step) {
               float y[4][5][2];  // all loads unconditional, so that they run together
@@ -602,7 +602,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (h < a.G) {
 #pragma unroll
               for (int u = 0; u < 4; ++u)
-                if (b0 + 8 * u < a.nb) part[h * a.nb + b0 + 8 * u] = v[u];
+                if (b0 + 8 * u < a.nb) {
+                  add_pair(sum[u], v[u]);
+                  part[h * a.nb + b0 + 8 * u] = sum[u];
+                }
             }
           }
         }
@@ -1089,31 +1092,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// dtable[h][b] = sum over the work items, in a fixed order: one CTA per head; thread (b, c)
-// sums every nc-th item, and the nc partial sums of a bucket are added pairwise.  (fp32: at
-// most some hundred terms follow one another, and the result is rounded to bf16.  fp64 adds,
-// which are slow on this GPU, took 11 us of the 350 us of 23 documents.)
+// dtable[h][b] = sum over the CTAs of dQ, in a fixed order: one CTA per head; thread (b, c) sums
+// every nc-th CTA's pair, and the nc pairs of a bucket are added pairwise.  A CTA's sum runs over
+// all its items, hundreds of thousands for the largest batches, and dS cancels (a row's adds up
+// to zero), so the sums carry their roundings along; the result is rounded once, to bf16.
 constexpr int kTableThreads = 1024;
-__global__ void __launch_bounds__(kTableThreads) k_dense_dtable(const DenseArgs a,
+__global__ void __launch_bounds__(kTableThreads) k_dense_dtable(const DenseArgs a, int ctas,
                                                                 uint16_t* dtable) {
-  __shared__ float sum[kTableThreads];
+  __shared__ float2 sum[kTableThreads];
   int nb2 = 1;
   while (nb2 < a.nb) nb2 <<= 1;
   const int h = blockIdx.x, b = threadIdx.x % nb2, c = threadIdx.x / nb2, nc = kTableThreads / nb2;
-  const float* src = a.parts + (size_t)h * a.nb + b;
-  const size_t step = (size_t)a.hq * a.nb;
-  float s = 0.f;
-  if (b < a.nb) {
-#pragma unroll 8
-    for (int x = c; x < a.nslots; x += nc) s += __ldg(src + x * step);
-  }
+  float2 s = make_float2(0.f, 0.f);
+  auto add = [&](float2 x) {
+    add_pair(s, x.x);
+    s.y += x.y;
+  };
+  if (b < a.nb)
+    for (int x = c; x < ctas; x += nc) add(__ldg(a.parts + ((size_t)x * a.hq + h) * a.nb + b));
   sum[threadIdx.x] = s;
   for (int half = nc / 2; half > 0; half >>= 1) {
     __syncthreads();
-    if (c < half) sum[threadIdx.x] += sum[threadIdx.x + half * nb2];
+    if (c < half) {
+      add(sum[threadIdx.x + half * nb2]);
+      sum[threadIdx.x] = s;
+    }
   }
   if (c == 0 && b < a.nb) {
-    const __nv_bfloat16 y = __float2bfloat16(sum[threadIdx.x]);
+    const __nv_bfloat16 y = __float2bfloat16(s.x + s.y);
     dtable[(size_t)h * a.nb + b] = *reinterpret_cast<const uint16_t*>(&y);
   }
 }
@@ -1161,7 +1167,7 @@ cudaError_t launch_dense_bwd(const DenseShape& s, const uint16_t* q, const uint1
   if (e != cudaSuccess || !a.bias) return e;
   DenseArgs b = a;
   b.nslots = dense_slots(a.T, a.ndoc, a.tpt);
-  k_dense_dtable<<<a.hq, kTableThreads, 0, st>>>(b, dtable);
+  k_dense_dtable<<<a.hq, kTableThreads, 0, st>>>(b, dense_grid(b), dtable);
   return cudaGetLastError();
 }
 

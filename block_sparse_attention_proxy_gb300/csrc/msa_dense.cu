@@ -83,10 +83,9 @@ DenseWorkspace dense_workspace(const DenseArgs& a) {
   };
   w.stats = take((size_t)a.hq * a.T * sizeof(float2));
   if (a.nb > 0) {
-    const size_t n = dense_slots(a.T, a.ndoc, a.tpt);
     w.refs = take((size_t)a.hq * a.T * sizeof(float));
     w.slots = take((size_t)kDenseMaxGrid * a.nb * 256 * sizeof(float));  // one per CTA
-    w.parts = take(n * a.hq * a.nb * sizeof(float));
+    w.parts = take((size_t)kDenseMaxGrid * a.hq * a.nb * sizeof(float2));
   }
   return w;
 }
@@ -168,7 +167,7 @@ msa_status msa_dense_bwd(const msa_dense_params* p, const int32_t* cu_seqlens, c
   a.stats = reinterpret_cast<float2*>(base + w.stats);
   a.refs = reinterpret_cast<float*>(base + w.refs);
   a.slots = reinterpret_cast<float*>(base + w.slots);
-  a.parts = reinterpret_cast<float*>(base + w.parts);
+  a.parts = reinterpret_cast<float2*>(base + w.parts);
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;

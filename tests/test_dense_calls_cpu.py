@@ -52,3 +52,15 @@ def test_forward_mode_is_refused(which):
         x[which] = torch.autograd.forward_ad.make_dual(x[which], torch.ones_like(x[which]))
         with pytest.raises(NotImplementedError, match="forward-mode"):
             m.dense_attention(x["q"], x["k"], x["v"], cu, bias=x["bias"], bucket_starts=(0, 1, 2))
+
+
+@pytest.mark.parametrize("hq,hkv", [(64, 1), (16, 16), (1024, 16)])
+def test_workspace_of_the_table_gradient(hq, hkv):
+    """The sums for 64 buckets take some MB beside the rows' statistics (12 bytes each), however
+    many tokens there are."""
+    import block_sparse_attention_proxy_gb300 as m
+
+    for tokens in (1000, 1 << 20):
+        size = m.msa_dense_bwd_workspace_size(m.make_dense_params(
+            tokens, 5, hq, hkv, 64, bucket_starts=tuple(range(64))))
+        assert 0 < size - 12 * tokens * hq < (12 << 20) + 160 * hq * 64 * 8

@@ -1,0 +1,40 @@
+"""The gradient of the bias table over many items."""
+import pytest
+import torch
+
+from test_gpu_dense import _call, _inputs, _status
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_sums_over_many_items(d):
+    """8192 documents of 8 tokens under 64 heads of one KV head, two tokens to a tile: documents
+    A, then B, then A and B with the opposite gradient.  Items of a pair have exactly opposite
+    sums, so the table's gradient is zero but for the addition of some 32768 items.  n terms
+    of a CTA, about 220 items of which half build up, are off by n^2 2^-48 of n/2 terms: 2^-33 of
+    all CTAs' terms together.  Sums rounded to fp32 after each item are off by some 2^-22."""
+    n, doc, hq, starts = 2048, 8, 64, (0, 1, 3, 5)
+    x = _inputs([doc, doc], hq, 1, d, 80, nb=4)
+    one = []
+    for i in (0, 1):  # one document alone
+        y = {m: t[i * doc:(i + 1) * doc] for m, t in x.items() if m not in ("cu", "bias")}
+        y.update(bias=x["bias"], cu=torch.tensor([0, doc], dtype=torch.int32, device="cuda"))
+        one.append(_call(y, starts)["dbias"].double())
+    y = {m: torch.cat([x[m][:doc].repeat(n, 1, 1), x[m][doc:].repeat(n, 1, 1)] * 2)
+         for m in ("q", "k", "v", "do")}
+    y["do"][2 * n * doc:] *= -1
+    y.update(bias=x["bias"],
+             cu=torch.arange(4 * n + 1, dtype=torch.int32, device="cuda") * doc)
+    got = _call(y, starts)["dbias"].double()
+    assert _status() == 0
+    terms = 2 * n * float(one[0].abs().max() + one[1].abs().max())
+    assert float(got.abs().max()) <= 2.0 ** -32 * terms, (float(got.abs().max()), terms)
+    # and the sum itself: A and B only
+    y = {m: (t if m == "bias" else t[:2 * n * doc + (m == "cu") * (2 * n + 1 - 2 * n * doc)])
+         for m, t in y.items()}
+    got = _call(y, starts)["dbias"].double()
+    want = n * (one[0] + one[1])
+    # the single documents' gradients are rounded to bf16, and so is the sum
+    limit = 2.0 ** -8 * (n * (one[0].abs() + one[1].abs()) + want.abs()) + 2.0 ** -20 * terms
+    assert ((got - want).abs() <= limit).all()
