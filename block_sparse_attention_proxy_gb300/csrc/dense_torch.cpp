@@ -247,7 +247,10 @@ Tensor dense_attention(const Tensor& q, const Tensor& k, const Tensor& v, const 
     q_ = take(q, &prm.q_stride);
     k_ = take(k, &prm.k_stride);
     v_ = take(v, &prm.v_stride);
-    cu = cu_seqlens.scalar_type() == at::kInt ? cu_seqlens : cu_seqlens.to(at::kInt);
+    // out of range stays out of range in 32 bits, so that the kernels find it
+    cu = cu_seqlens.scalar_type() == at::kInt
+             ? cu_seqlens
+             : cu_seqlens.clamp(-1, std::numeric_limits<int32_t>::max()).to(at::kInt);
     cu = cu.contiguous();
     if (bias.defined()) b = bias.contiguous();
     const auto opt = q.options().requires_grad(false);
