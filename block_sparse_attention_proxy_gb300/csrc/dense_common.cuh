@@ -488,7 +488,7 @@ __host__ inline void dense_lut_shape(DenseArgs* a) {
   const int w = a->lut_stride - (127 + a->tpt), last = a->nb > 0 ? a->starts[a->nb - 1] : 0;
   a->lut_w = w < 0 ? 0 : w;
   // a warp's part of a tile spans fewer than 256 distances: beyond this it lies in one bucket
-  if (a->lut_w > last + 256) a->lut_w = last + 256;
+  if (a->lut_w - 256 > last) a->lut_w = last + 256;  // the last start may be INT_MAX
 }
 __device__ __forceinline__ int dense_lut_pad(const DenseArgs& a) { return 127 + a.tpt; }
 

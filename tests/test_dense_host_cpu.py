@@ -31,6 +31,32 @@ int main() {
 """
 
 
+TABLE = r"""
+#include <cstdio>
+#include "dense_common.cuh"
+using namespace msa;
+// A last bucket that begins where no distance lies: the same table by distance wherever that is.
+int main() {
+  for (int G = 1; G <= kDenseMaxGroup; ++G) {
+    DenseArgs a{};
+    a.G = G, a.tpt = 128 / G, a.nb = 3, a.starts[1] = 7, a.starts[2] = 1 << 20;
+    dense_lut_shape(&a);
+    for (int last : {INT_MAX - 257, INT_MAX - 256, INT_MAX - 255, INT_MAX}) {
+      DenseArgs b = a;
+      b.starts[2] = last;
+      dense_lut_shape(&b);
+      if (a.lut_w < 0 || b.lut_w != a.lut_w || b.lut_stride != a.lut_stride)
+        return std::printf("G %d, last start %d: %d distances, %d expected\n", G, last, b.lut_w,
+                           a.lut_w), 1;
+      if (b.lut_w > 0 && 127 + b.tpt + b.lut_w > b.lut_stride)
+        return std::printf("G %d: the row of the table is too short\n", G), 1;
+    }
+  }
+  return 0;
+}
+"""
+
+
 def run(tmp_path, source):
     """Compiles a host program against the kernels' header and runs it."""
     from block_sparse_attention_proxy_gb300 import build
@@ -44,6 +70,6 @@ def run(tmp_path, source):
     assert r.returncode == 0, r.stdout
 
 
-@pytest.mark.parametrize("source", [TURNS], ids=["counts past 32 bits"])
+@pytest.mark.parametrize("source", [TURNS, TABLE], ids=["counts past 32 bits", "last start"])
 def test_host_rules(tmp_path, source):
     run(tmp_path, source)
