@@ -58,9 +58,7 @@ def _compile_torch(newest: float) -> str:
     import torch
     from torch.utils import cpp_extension
 
-    obj = os.path.join(BUILD, "dense_torch.o")
-    if os.path.exists(obj) and os.path.getmtime(obj) >= newest:
-        return obj
+    obj, stamp = (os.path.join(BUILD, "dense_torch" + x) for x in (".o", ".stamp"))
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     dirs = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"],
             os.path.join(cuda, "include")]
@@ -68,9 +66,19 @@ def _compile_torch(newest: float) -> str:
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
            *(x for d in dirs for x in ("-isystem", d)), "-c",
            os.path.join(CSRC, "dense_torch.cpp"), "-o", obj]
+    # the object is tied to the C++ interface of this torch and this Python
+    made_for = "\n".join([torch.__version__, str(sysconfig.get_config_var("SOABI")), *cmd])
+    if os.path.exists(obj) and os.path.getmtime(obj) >= newest and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read() == made_for:
+                return obj
+    if os.path.exists(stamp):
+        os.remove(stamp)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for dense_torch.cpp:\n{r.stdout}\n{r.stderr}")
+    with open(stamp, "w") as f:
+        f.write(made_for)
     return obj
 
 
