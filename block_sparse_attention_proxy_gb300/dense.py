@@ -17,22 +17,28 @@ and v may be slices of a fused projection (any token stride that keeps rows on
 """
 from __future__ import annotations
 
+import os
+
 import torch
 
 from ._abi import load
+from .build import TORCH_LIB
 
 _call = None
 
 
 def _load():
-    """The front end's extension.  Raises if it has not been built: there is no fallback."""
+    """The front end's extension.  Raises if it has not been built, or does not load: there is
+    no fallback."""
     global _call
     load()  # the kernels' library, with its own message where that is missing
+    if not os.path.exists(TORCH_LIB):
+        raise RuntimeError(f"{TORCH_LIB} is missing: build the library first "
+                           "(python -c 'import __graft_entry__ as g; g.build()')")
     try:
         from ._dense_torch import dense_attention as call
     except ImportError as e:
-        raise RuntimeError("_dense_torch.so is missing: build the library first "
-                           "(python -c 'import __graft_entry__ as g; g.build()')") from e
+        raise RuntimeError(f"{TORCH_LIB} does not load: {e}") from e
     _call = call
     return call
 

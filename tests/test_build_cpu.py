@@ -64,3 +64,22 @@ def test_a_failed_compile_leaves_nothing_to_reuse(compiles, monkeypatch):
         compiles()
     monkeypatch.setattr(build.subprocess, "run", good)
     assert compiles() == 1
+
+
+def test_a_front_end_that_does_not_load_says_why(monkeypatch, tmp_path):
+    import sys
+
+    from block_sparse_attention_proxy_gb300 import dense
+
+    there, absent = tmp_path / "there.so", tmp_path / "absent.so"
+    there.touch()
+    monkeypatch.setattr(dense, "load", lambda: None)
+    monkeypatch.setattr(dense, "_call", None)
+    monkeypatch.setitem(sys.modules, "block_sparse_attention_proxy_gb300._dense_torch", None)
+    monkeypatch.setattr(dense, "TORCH_LIB", str(there))
+    with pytest.raises(RuntimeError, match="does not load: .*_dense_torch") as error:
+        dense._load()
+    assert "missing" not in str(error.value)
+    monkeypatch.setattr(dense, "TORCH_LIB", str(absent))
+    with pytest.raises(RuntimeError, match="is missing: build the library"):
+        dense._load()
