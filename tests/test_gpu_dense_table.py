@@ -2,6 +2,8 @@
 import pytest
 import torch
 
+from dense_exact import compare, dense_exact
+from test_dense_exact_cpu import LAYOUTS, finds_mistakes
 from test_gpu_dense import _call, _inputs, _status
 
 pytestmark = pytest.mark.gpu
@@ -38,3 +40,33 @@ def test_sums_over_many_items(d):
     # the single documents' gradients are rounded to bf16, and so is the sum
     limit = 2.0 ** -8 * (n * (one[0].abs() + one[1].abs()) + want.abs()) + 2.0 ** -20 * terms
     assert ((got - want).abs() <= limit).all()
+
+
+def _against_definition(lens, hq, hkv, d, starts, seed):
+    """Within limits so tight that planted mistakes in the table's gradient are found."""
+    x = _inputs(lens, hq, hkv, d, seed, nb=len(starts))
+    got = _call(x, starts)
+    assert _status() == 0
+    want = dense_exact(x["q"], x["k"], x["v"], lens, 1.0, x["bias"], starts, x["do"])
+    compare(got, want)
+    finds_mistakes([{n: t.cpu() for n, t in y.items()} if i < 2 else y
+                    for i, y in enumerate(want)])
+
+
+@pytest.mark.parametrize("starts", LAYOUTS.values(), ids=LAYOUTS.keys())
+@pytest.mark.parametrize("hq,hkv,d", [(4, 1, 64), (3, 3, 128), (6, 2, 128)])
+def test_bucket_layouts(starts, hq, hkv, d):
+    _against_definition([1, 200, 65, 513], hq, hkv, d, starts, 81)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_buckets_far_away(d):
+    """Past the distances whose starts are kept as bits."""
+    _against_definition([9300], 2, 1, d,
+                        (0, 10, 4000, 4001, 4040, 8190, 8192, 8200, 8201, 8215, 9000, 9001), 82)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (8, 1, 128), (12, 4, 64)])
+def test_more_than_64_documents(hq, hkv, d):
+    lens = [300, 0, 17] + [(13 * i) % 71 for i in range(70)]
+    _against_definition(lens, hq, hkv, d, (0, 1, 2, 4, 8, 30, 100, 250), 83)
