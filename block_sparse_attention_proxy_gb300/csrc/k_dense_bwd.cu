@@ -7,8 +7,8 @@
 // over its group's queries.  S and dP are computed in both (7 products per
 // tile pair instead of 5); in exchange there are no fp32 partial gradients in
 // HBM and no atomics, and every sum has a fixed order.  Bound at d = 128 by the tensor core
-// (16384 tokens, 32 heads on 8: dQ 1.85 ms, 1.78 PFLOP/s of its 3 products; dK, dV 2.65 ms,
-// 1.66 of their 4); at d = 64 by the exponentials and the hand-offs between the roles, and for
+// (16384 tokens, 32 heads on 8: dQ 1.90 ms, 1.74 PFLOP/s of its 3 products; dK, dV 2.64 ms,
+// 1.67 of their 4); at d = 64 by the exponentials and the hand-offs between the roles, and for
 // short documents by what an item costs outside its tiles.
 #include "dense_common.cuh"
 
@@ -27,8 +27,8 @@ static_assert(kBudget <= 65536, "register budgets exceed the register file");
 // item's rows (which dK, dV need too) come at d = 128 from warps 10 and 11, an item ahead,
 // and at d = 64, where those two could not keep up with short items, from the softmax warps,
 // which load the next item's rows before they store an item's dQ (16384 tokens, 32 heads,
-// d 128: 1.96 ms from warps 10 and 11, 2.04 from the softmax warps; 61 documents of 24001
-// tokens, 8 heads, d 64: 98 and 62 us).
+// d 128, as the kernel was when that was tried: 1.96 ms from warps 10 and 11, 2.04 from the
+// softmax warps; 61 documents of 24001 tokens, 8 heads, d 64: 98 and 62 us).
 // S has two TMEM buffers: while the softmax warps turn S(n), dP(n) into dS(n) (bf16, over
 // S(n)'s columns), S(n + 1) is computed, and dP(n + 1) as soon as dP(n) has been read.
 // ---------------------------------------------------------------------------

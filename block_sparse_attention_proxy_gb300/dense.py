@@ -46,7 +46,8 @@ def _load():
 def log_buckets(num_buckets: int, max_distance: int) -> tuple[int, ...]:
     """First distance of each of `num_buckets` buckets: one distance per bucket for
     the first half, then spaced evenly in the logarithm; the last bucket begins
-    at `max_distance`.  Needs num_buckets >= 4 and max_distance >= num_buckets."""
+    at `max_distance`.  This package's own rule: a table trained with another one, whose
+    last bucket may begin earlier, needs that rule's first distances.  Needs num_buckets >= 4 and max_distance >= num_buckets."""
     if num_buckets < 4 or max_distance < num_buckets:
         raise ValueError("num_buckets >= 4 and max_distance >= num_buckets expected")
     half = num_buckets // 2
@@ -65,5 +66,6 @@ def dense_attention(q, k, v, cu_seqlens, softmax_scale: float = 1.0, bias=None,
     the last bucket whose first distance, `bucket_starts[b]`, is at most i - j.
     bucket_starts begins with 0 and increases strictly (`log_buckets` makes one).
     Differentiable once, in reverse mode; inputs with a forward-mode tangent are refused.
-    Malformed cu_seqlens are found on the device (`msa_get_device_status`)."""
+    Finite biases of any size are exact, -inf masks.  Malformed cu_seqlens are found on the
+    device (`msa_get_device_status`); the results are undefined then."""
     return (_call or _load())(q, k, v, cu_seqlens, softmax_scale, bias, bucket_starts)
