@@ -1119,7 +1119,8 @@ __global__ void __launch_bounds__(kTableThreads) k_dense_dtable(const DenseArgs 
     }
   }
   if (c == 0 && b < a.nb) {
-    const __nv_bfloat16 y = __float2bfloat16(s.x + s.y);
+    // what an infinite sum's roundings drop is NaN
+    const __nv_bfloat16 y = __float2bfloat16(fabsf(s.x) < INFINITY ? s.x + s.y : s.x);
     dtable[(size_t)h * a.nb + b] = *reinterpret_cast<const uint16_t*>(&y);
   }
 }

@@ -70,3 +70,16 @@ def test_buckets_far_away(d):
 def test_more_than_64_documents(hq, hkv, d):
     lens = [300, 0, 17] + [(13 * i) % 71 for i in range(70)]
     _against_definition(lens, hq, hkv, d, (0, 1, 2, 4, 8, 30, 100, 250), 83)
+
+
+def test_sums_beyond_the_largest_number():
+    """A gradient that overflows is infinite with its sign, as a plain sum is: 400 documents of
+    two tokens, each of whose second rows adds some 6e36 to bucket 0 and takes it from bucket 1."""
+    lens = [2] * 400
+    x = _inputs(lens, 4, 4, 64, 84, nb=2)
+    x["do"] = x["v"] * 1e36
+    got = _call(x, (0, 1))["dbias"]
+    want = dense_exact(x["q"], x["k"], x["v"], lens, 1.0, x["bias"], (0, 1), x["do"])[0]["dbias"]
+    assert float(want[:, 0].min()) > 3.5e38 and float(want[:, 1].max()) < -3.5e38
+    assert torch.equal(got.double(), want.sign() * float("inf"))
+    assert _status() == 0
