@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint16_t* tab = a.bias + (size_t)(wk.g * a.G + hl) * a.nb;
       float c = a.scale_log2, ref = 0.f;
       if (BIAS) {
-        ref = dense_row_ref(a, sB, tab, valid ? qi : -1);
+        ref = dense_row_ref(a, sB, hl, tab, valid ? qi : -1);
         c = dense_row_scale(a, ref);
         if (w == 0 && valid) a.refs[(size_t)(wk.g * a.G + hl) * a.T + wk.it.start + qi] = ref;
       }
@@ -945,10 +945,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         wait(B_TF + s, (X / NS) & 1);
         // Bucket by bucket, relative to each query's reference: where a query of the tile has
-        // one, and, if entries of the table may overflow, where the tile has queries behind the
-        // document's end, whose distances may reach buckets that no pair does.
+        // one, and, if the table has NaN, +inf or entries that overflow, where the tile has queries
+        // behind the document's end, whose distances may reach buckets that no pair does.
         const int end = wk.it.len - wk.j0 - qt * 128 - 64 * w;
-        const bool walk = BIAS && (sFar[s] || (sB->extreme && end < 64));
+        const bool walk = BIAS && (sFar[s] || (sB->loose && end < 64));
         if (walk) one = near = false;
         wait(B_S, X & 1);
         if (!dead) {

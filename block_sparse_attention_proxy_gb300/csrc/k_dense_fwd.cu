@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float v0 = 0.f;                    // its bias
       const uint16_t* tab = a.bias + (size_t)(w.g * a.G + hl) * a.nb;
       if (BIAS) {
-        ref = dense_row_ref(a, sB, tab, qi);
+        ref = dense_row_ref(a, sB, hl, tab, qi);
         c = dense_row_scale(a, ref);
       }
       for (int u = 0; u < nut; ++u, ++U) {

@@ -81,3 +81,16 @@ def test_buckets_that_no_pair_reaches(hq, hkv, d, value):
     for n in want:
         assert torch.equal(got[n], want[n]), n
     assert _status() == 0
+
+
+@pytest.mark.parametrize("value", [LOWEST, -1e9, 1e5])
+@pytest.mark.parametrize("hq,hkv,d", [(64, 1, 64), (40, 2, 128), (8, 2, 64)])
+def test_large_tables_and_many_documents(hq, hkv, d, value):
+    """Tables that do not fit beside the tiles, in batches that go document by document."""
+    lens, starts = [150, 0, 3] + [(11 * i) % 23 for i in range(66)], tuple(range(0, 128, 2))
+    x = _inputs(lens, hq, hkv, d, 53, nb=64)
+    x["bias"][1::3, :20] = value
+    x["bias"][2::3, 5:] = value
+    got = _call(x, starts)
+    assert _status() == 0
+    compare(got, dense_exact(x["q"], x["k"], x["v"], lens, 1.0, x["bias"], starts, x["do"]))
