@@ -206,8 +206,18 @@ def allocate_outputs(params: MsaParams, device="cuda") -> dict:
     )
 
 
+from ._cache_calls import (make_cache, make_paged_params, make_rotary_params,  # noqa: E402
+                           make_table, msa_cache_append, msa_cache_evict,
+                           msa_cache_evict_workspace_size, msa_paged_attention,
+                           msa_paged_attention_workspace_size, msa_rotary)
 # autograd front end (imported last: it builds on the calls above)
+from .cache import (PagedCache, cache_append, cache_evict, paged_attention,  # noqa: E402
+                    paged_cache, rotary, rotary_plan)
 from .dense import dense_attention, log_buckets  # noqa: E402
 from .function import MSAFunction, last_kl_loss, msa_attention  # noqa: E402
 
-__all__ += ["MSAFunction", "msa_attention", "last_kl_loss", "dense_attention", "log_buckets"]
+__all__ += ["MSAFunction", "msa_attention", "last_kl_loss", "dense_attention", "log_buckets",
+            "rotary_plan", "rotary", "PagedCache", "paged_cache", "cache_append", "paged_attention",
+            "cache_evict", "make_cache", "make_paged_params", "make_rotary_params", "make_table",
+            "msa_cache_append", "msa_cache_evict", "msa_cache_evict_workspace_size",
+            "msa_paged_attention", "msa_paged_attention_workspace_size", "msa_rotary"]

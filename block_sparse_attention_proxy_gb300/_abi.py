@@ -32,6 +32,12 @@ EXPORTS = (
     "msa_dense_fwd",
     "msa_dense_bwd_workspace_size",
     "msa_dense_bwd",
+    "msa_rotary",
+    "msa_cache_append",
+    "msa_paged_attention_workspace_size",
+    "msa_paged_attention",
+    "msa_cache_evict_workspace_size",
+    "msa_cache_evict",
     "msa_get_device_status",
     "msa_last_status_word",
     "msa_launch_count",
@@ -78,6 +84,65 @@ class MsaDenseParams(ctypes.Structure):
     ]
 
 
+class MsaRotaryParams(ctypes.Structure):
+    _fields_ = [
+        ("total_tokens", ctypes.c_int32),
+        ("num_docs", ctypes.c_int32),
+        ("hq", ctypes.c_int32),
+        ("hkv", ctypes.c_int32),
+        ("d", ctypes.c_int32),
+        ("dims", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("inverse", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("position_bytes", ctypes.c_int32),
+        ("freq", ctypes.POINTER(ctypes.c_uint64)),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("amplitude", ctypes.c_float),
+        ("flags", ctypes.c_uint32),
+    ]
+
+
+class MsaCache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("weight", ctypes.c_void_p),
+        ("position", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("hkv", ctypes.c_int32),
+        ("d", ctypes.c_int32),
+        ("k_page_stride", ctypes.c_int64),
+        ("k_slot_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("v_page_stride", ctypes.c_int64),
+        ("v_slot_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+    ]
+
+
+class MsaTable(ctypes.Structure):
+    _fields_ = [
+        ("pages", ctypes.c_void_p),
+        ("lens", ctypes.c_void_p),
+        ("num_seqs", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("stride", ctypes.c_int64),
+    ]
+
+
+class MsaPagedParams(ctypes.Structure):
+    _fields_ = [
+        ("hq", ctypes.c_int32),
+        ("accumulate", ctypes.c_int32),
+        ("q_stride", ctypes.c_int64),
+        ("softmax_scale", ctypes.c_float),
+        ("flags", ctypes.c_uint32),
+    ]
+
+
 class MsaError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -118,6 +183,20 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.msa_dense_bwd_workspace_size.restype = sz
     lib.msa_dense_bwd.argtypes = [DP] + [vp] * 13 + [vp, sz, vp]
     lib.msa_dense_bwd.restype = i32
+    RP, CP, TP, PP = (ctypes.POINTER(t) for t in (MsaRotaryParams, MsaCache, MsaTable,
+                                                  MsaPagedParams))
+    lib.msa_rotary.argtypes = [RP] + [vp] * 7
+    lib.msa_rotary.restype = i32
+    lib.msa_cache_append.argtypes = [CP, TP, RP, ctypes.c_int64] + [vp] * 7
+    lib.msa_cache_append.restype = i32
+    lib.msa_paged_attention_workspace_size.argtypes = [CP, TP, PP]
+    lib.msa_paged_attention_workspace_size.restype = sz
+    lib.msa_paged_attention.argtypes = [CP, TP, PP] + [vp] * 3 + [sz, vp]
+    lib.msa_paged_attention.restype = i32
+    lib.msa_cache_evict_workspace_size.argtypes = [CP, TP, ctypes.c_int32]
+    lib.msa_cache_evict_workspace_size.restype = sz
+    lib.msa_cache_evict.argtypes = [CP, TP, ctypes.c_int32, ctypes.c_int32, vp, vp, sz, vp]
+    lib.msa_cache_evict.restype = i32
     lib.msa_get_device_status.argtypes = [vp]
     lib.msa_get_device_status.restype = i32
     lib.msa_last_status_word.argtypes = []

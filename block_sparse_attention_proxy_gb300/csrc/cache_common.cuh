@@ -1,0 +1,114 @@
+// Shared by the kernels around the paged key-value cache: rotary positions, append,
+// attention of one new token, eviction.
+#pragma once
+#include <atomic>
+#include <climits>
+
+#include "msa_internal.cuh"
+
+namespace msa {
+
+constexpr int kRotaryMaxPairs = 128;     // head dim 256
+constexpr int kCacheMaxSeqs = 1 << 20;
+constexpr int kCacheMaxEntries = 1 << 30;  // of one sequence: max_pages * page_size
+constexpr int kPagedMaxGroup = 64;         // query heads per KV head
+
+// Where the cache's rows lie.  Strides in elements.
+struct CacheArgs {
+  uint16_t *k, *v;
+  float* weight;
+  int32_t* position;
+  int num_pages, page_shift, hkv, d;
+  long long kp, ks, kh, vp, vs, vh;  // page, slot and head strides of k and v
+  const int32_t* table;
+  long long table_stride;
+  const int32_t* lens;
+  int nseq, capacity;  // entries that a row of the table can name
+  unsigned* status;
+  __device__ __forceinline__ uint16_t* k_row(int page, int slot, int h) const {
+    return k + page * kp + slot * ks + h * kh;
+  }
+  __device__ __forceinline__ uint16_t* v_row(int page, int slot, int h) const {
+    return v + page * vp + slot * vs + h * vh;
+  }
+  // index into weight and position
+  __device__ __forceinline__ long long meta(int page, int slot, int h) const {
+    return (((long long)page * hkv + h) << page_shift) + slot;
+  }
+};
+
+// Length of sequence b within what the table can name; others are flagged.
+__device__ __forceinline__ int cache_len(const CacheArgs& c, int b) {
+  const int n = __ldg(c.lens + b);
+  if (n >= 0 && n <= c.capacity) return n;
+  set_status(c.status, MSA_ERR_DEVICE_CHECK);
+  return n < 0 ? 0 : c.capacity;
+}
+// Page of entry i of sequence b, or -1 (flagged) where the table names none of the cache's.
+__device__ __forceinline__ int cache_page(const CacheArgs& c, int b, int i) {
+  const int page = __ldg(c.table + (long long)b * c.table_stride + (i >> c.page_shift));
+  if ((unsigned)page < (unsigned)c.num_pages) return page;
+  set_status(c.status, MSA_ERR_DEVICE_CHECK);
+  return -1;
+}
+
+// Rows to rotate.  A row is a (token, head) pair; heads are those of q, then of k, then (append)
+// of v.
+struct RotaryArgs {
+  int T, ndoc, hq, hkv, d, dims;
+  float sign, amplitude;
+  const int32_t* cu;       // null: positions
+  const void* positions;   // null: cu, or (append) the entries' numbers
+  int position_bytes;
+  const void *q, *k, *v;
+  void *q_out, *k_out;     // append writes k to the cache
+  long long qs, ks, vs;    // token strides, elements
+  int slots, per;          // threads along the heads of a token, heads of each
+  unsigned* status;
+  uint64_t freq[kRotaryMaxPairs];
+};
+
+cudaError_t launch_rotary(RotaryArgs& a, int dtype, bool interleaved, cudaStream_t st);
+cudaError_t launch_append(RotaryArgs& a, const CacheArgs& c, bool interleaved, cudaStream_t st);
+
+// Attention of one new token (k_paged.cu).
+constexpr int kPagedMaxGrid = 320;  // CTAs: bounds the workspace on every device
+struct PagedArgs {
+  CacheArgs cache;
+  int hq, G, grid;
+  float scale_log2;
+  uint16_t* o;
+  float* parts;        // [CTA][2][G][d] sums of rows that CTAs share
+  float2* part_stats;  // [CTA][2][G] their references and normalisers
+  float2* stats;       // [nseq][hq] reference and 1 / normaliser of whole rows (with scores)
+  float* scores;       // [tile][G][128] in log2 units; null: no weights asked for
+};
+int paged_grid(const CacheArgs& c, int G);
+cudaError_t launch_paged(const PagedArgs& a, const uint16_t* q, long long q_stride,
+                         cudaStream_t st);
+
+// Eviction (k_evict.cu).
+struct EvictArgs {
+  CacheArgs cache;
+  int keep, recent;
+  int32_t* new_lens;
+  int32_t* count;  // [nseq][hkv] entries that move
+  int32_t* pairs;  // [nseq][hkv][2][most] where from, where to
+  int most;        // pairs of a row at most
+};
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st, int* launches);
+
+// Streaming multiprocessors of the current device.
+inline int sm_count() {
+  static std::atomic<int> sms[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 1;
+  if (dev < 64) n = sms[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) n = 1;
+    if (dev < 64) sms[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+}  // namespace msa

@@ -3,93 +3,12 @@
 // short: a forward and backward of a small batch runs about 60 us on the GPU, and the
 // same front end written in Python kept the host busy for 270 us a step.  The
 // computation itself is in the library's kernels.
-#include <c10/cuda/CUDAGraphsC10Utils.h>
-#include <c10/cuda/CUDAGuard.h>
-#include <c10/cuda/CUDAStream.h>
-#include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/functions/basic_ops.h>
-#include <torch/csrc/autograd/functions/utils.h>
-#include <torch/csrc/autograd/saved_variable.h>
-#include <torch/extension.h>
-
-#include <limits>
-#include <vector>
-
-#include "msa.h"
+#include "torch_front.h"
 
 namespace {
 
-using at::Tensor;
-using torch::autograd::SavedVariable;
-using torch::autograd::variable_list;
-
-// A status of the library; becomes the package's MsaError.
-struct StatusError : std::runtime_error {
-  int status;
-  const char* where;
-  StatusError(int s, const char* w)
-      : std::runtime_error(std::string(w) + ": " + msa_status_string((msa_status)s)),
-        status(s),
-        where(w) {}
-};
-void raise_on(msa_status s, const char* where) {
-  if (s != MSA_OK) throw StatusError(s, where);
-}
-
-void set_msa_error(const StatusError& e) {
-  auto cls = py::module_::import("block_sparse_attention_proxy_gb300").attr("MsaError");
-  PyErr_SetObject(cls.ptr(), cls(e.status, e.where).ptr());
-}
-// In the form in which the engine carries a Python exception to the thread that asked for the
-// gradients; other C++ exceptions become a RuntimeError there.
-[[noreturn]] void throw_to_engine(const StatusError& e) {
-  py::gil_scoped_acquire gil;
-  set_msa_error(e);
-  python_error error;
-  error.persist();
-  throw std::move(error);
-}
-
-// Token stride the library takes for a [tokens, heads, d] tensor (0: packed), or -1 where
-// the layout has to be copied: heads not packed, rows that overlap or are off 16 bytes.
-int64_t row_stride(const Tensor& t) {
-  const int64_t heads = t.size(1), d = t.size(2);
-  if (t.stride(2) != 1 || (heads > 1 && t.stride(1) != d)) return -1;
-  if (reinterpret_cast<uintptr_t>(t.data_ptr()) % 16) return -1;
-  if (t.size(0) <= 1) return 0;
-  return t.stride(0) < heads * d || t.stride(0) % 8 ? -1 : t.stride(0);
-}
-Tensor take(const Tensor& t, int64_t* stride) {
-  *stride = row_stride(t);
-  if (*stride >= 0) return t;
-  *stride = 0;
-  return t.clone(at::MemoryFormat::Contiguous);
-}
-
-// A tensor that the library takes contiguous, on 32 bytes.
-Tensor whole(const Tensor& t) {
-  return t.is_contiguous() && reinterpret_cast<uintptr_t>(t.data_ptr()) % 32 == 0
-             ? t
-             : t.clone(at::MemoryFormat::Contiguous);
-}
-
-const uint16_t* in(const Tensor& t) {
-  return t.defined() ? static_cast<const uint16_t*>(t.const_data_ptr()) : nullptr;
-}
-uint16_t* out(const Tensor& t) {
-  return t.defined() ? static_cast<uint16_t*>(t.mutable_data_ptr()) : nullptr;
-}
-msa_stream_t current_stream() {
-  return reinterpret_cast<msa_stream_t>(c10::cuda::getCurrentCUDAStream().stream());
-}
-
-// There is no forward-mode derivative: a tangent would be dropped, and a Jacobian-vector product
-// come out as zero.
-void no_tangent(const Tensor& t) {
-  TORCH_CHECK_NOT_IMPLEMENTED(
-      !t.defined() || !t._fw_grad(/*level=*/0).defined(),
-      "dense_attention has no forward-mode derivative (an input carries a tangent)");
-}
+using namespace msa_front;
+constexpr const char* kName = "dense_attention";
 
 // What a forward leaves for its backward, besides the tensors.
 struct Call {
@@ -114,7 +33,7 @@ struct DenseAttentionBackward : torch::autograd::Node {
   }
   variable_list apply(variable_list&& grads) override {
     if (!grads[0].defined()) return variable_list(4);
-    no_tangent(grads[0]);
+    no_tangent(grads[0], kName);
     variable_list g;
     try {
       g = compute(grads[0]);
@@ -125,21 +44,6 @@ struct DenseAttentionBackward : torch::autograd::Node {
     // asked for with create_graph: an error where somebody differentiates further
     return torch::autograd::DelayedError("dense_attention is differentiable once", 4)
         .apply(std::move(g));
-  }
-  // Inside a capture, a gradient that goes to a node of the default stream (a leaf that a graph
-  // made outside the capture still holds) would make the engine join that stream to the
-  // capture, which ends the process: an error here instead.
-  void check_capture() {
-    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None) return;
-    const c10::Stream here = c10::cuda::getCurrentCUDAStream().unwrap();
-    const c10::Stream legacy = c10::cuda::getDefaultCUDAStream().unwrap();
-    for (const auto& e : next_edges()) {
-      const auto to = e.function ? e.function->stream() : std::nullopt;
-      if (to && *to == legacy && *to != here)
-        throw std::runtime_error(
-            "dense_attention: a backward pass is captured while an autograd graph of the same "
-            "inputs, made outside the capture on the default stream, is alive");
-    }
   }
   // What a saved tensor comes back as is up to its hooks (activation offload, compression):
   // its values are those of the forward, its layout need not be.  Other sizes, types or devices
@@ -166,7 +70,7 @@ struct DenseAttentionBackward : torch::autograd::Node {
     expect(saved_, {call.saved()}, at::kByte, device);
     if (prm.num_buckets > 0) expect(bias_, {prm.hq, prm.num_buckets}, at::kBFloat16, device);
     c10::cuda::CUDAGuard guard(device);
-    check_capture();
+    check_capture(*this, kName);
     q_ = take(q_, &prm.q_stride);
     k_ = take(k_, &prm.k_stride);
     v_ = take(v_, &prm.v_stride);
@@ -226,7 +130,7 @@ Tensor dense_attention(const Tensor& q, const Tensor& k, const Tensor& v, const 
   Call call;
   if (bucket_starts) call.starts = *bucket_starts;
   const Tensor bias = bias_table ? *bias_table : Tensor();
-  for (const Tensor* t : {&q, &k, &v, &bias}) no_tangent(*t);
+  for (const Tensor* t : {&q, &k, &v, &bias}) no_tangent(*t, kName);
   check(q, k, v, cu_seqlens, bias, call.starts.size());
   const bool keep = at::GradMode::is_enabled() &&
                     (q.requires_grad() || k.requires_grad() || v.requires_grad() ||
@@ -247,11 +151,7 @@ Tensor dense_attention(const Tensor& q, const Tensor& k, const Tensor& v, const 
     q_ = take(q, &prm.q_stride);
     k_ = take(k, &prm.k_stride);
     v_ = take(v, &prm.v_stride);
-    // out of range stays out of range in 32 bits, so that the kernels find it
-    cu = cu_seqlens.scalar_type() == at::kInt
-             ? cu_seqlens
-             : cu_seqlens.clamp(-1, std::numeric_limits<int32_t>::max()).to(at::kInt);
-    cu = cu.contiguous();
+    cu = ints(cu_seqlens).contiguous();
     if (bias.defined()) b = bias.contiguous();
     const auto opt = q.options().requires_grad(false);
     o = at::empty(q.sizes(), opt);
@@ -286,6 +186,8 @@ Tensor dense_attention(const Tensor& q, const Tensor& k, const Tensor& v, const 
 
 }  // namespace
 
+void bind_cache(py::module_& m);  // cache_torch.cpp
+
 PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
   py::register_exception_translator([](std::exception_ptr p) {
     try {
@@ -297,4 +199,5 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
     }
   });
   m.def("dense_attention", &dense_attention);
+  bind_cache(m);
 }

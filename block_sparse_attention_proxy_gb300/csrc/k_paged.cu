@@ -1,0 +1,815 @@
+// Attention of one new token of each sequence over a paged key-value cache:
+//   s_j = scale q . k_j,  p = softmax_j(s),  o = sum_j p_j v_j  over the sequence's entries.
+//
+// Bound: HBM, every key and value read once (4 d bytes for 4 d G operations: below the tensor
+// core's rate by far, but beyond what fp32 units sustain at G = 8).  So the products run on the
+// tensor core with the entries as rows, which wastes none of it on the G queries of a KV head:
+//   S^T [128 entries x G] = K Q^T,   O^T [d x G] += V^T P^T,
+// K and V as they lie in the cache (TMA boxes of a page, or of 128 entries of a larger one), Q and
+// P as the narrow operand (G padded to 16, 32 or 64 columns).  A thread of the softmax
+// warpgroup owns one entry's G scores, later one row of O^T.
+//
+// The work is cut evenly: the tiles of 128 entries of all (sequence, KV head) rows are counted
+// through, and CTA c takes tiles [W c / C, W (c + 1) / C) of the W, whatever rows they fall in.  A
+// row inside one CTA's range is finished there; of the others each CTA leaves a partial result
+// (fp32 sums, maximum, normaliser; at most two a CTA), which k_paged_join adds up in a fixed order.
+// No prefix sum is stored and nothing is read back: every CTA adds up the tiles of all sequences
+// by itself.
+//
+// The reference m of a head's exponentials moves only when a score exceeds it by more than 8
+// (a factor of 256): one vote over the warpgroup a tile, and O is rescaled in TMEM in the
+// rare tile that raises it.  P enters its product as two bf16 parts (its rounding and what that
+// drops, 16 bits together) in columns of their own, of which G <= 8 leaves enough idle; with
+// one part the result's error was 1.4 times that of rounding it once (64 sequences of 4096 entries: 2.3e-3 against 1.7e-3).  With weights asked for, the scores go out in fp32 and the join adds
+// 2^(s - m) / l of the group's heads to each entry's weight.
+#include "cache_common.cuh"
+#include "dense_common.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kThreads = 192;  // softmax warps 0-3, loads 4, products 5
+constexpr int kJoinThreads = 256;
+constexpr float kRaise = 8.f;
+constexpr float kLowest = -FLT_MAX;  // reference of a row that has no score above it yet
+
+// GC: query heads that are computed (G rounded up), D: head dim
+template <int D, int GC>
+struct PagedCfg {
+  static constexpr int kN = GC < 16 ? 16 : GC;   // columns of S
+  static constexpr int kHi = GC < 8 ? 8 : GC;    // columns of O: those of P's upper parts, then
+  static constexpr int kNo = 2 * kHi;            // those of its lower ones
+  static constexpr int kTile = 128 * D * 2;
+  static constexpr int kQ = kN * D * 2, kP = kNo * 256;
+  static constexpr int kCtas = 3 * kTile + 2 * kQ + 2 * kP <= 114688 ? 2 : 1;  // per SM
+  static constexpr int kMisc = GC <= 16 ? 1024 : 2560;  // barriers, sums over the warps
+  static constexpr int kRoom = kCtas == 2 ? 115712 : 232448;
+  static constexpr int kRing = (kRoom - 2 * kQ - 2 * kP - kMisc) / kTile;
+  static constexpr int kSmem = kRing * kTile + 2 * kQ + 2 * kP + kMisc;
+  static constexpr int kUsed = 2 * kN + 2 * kNo;  // TMEM: two S, two O
+  static constexpr int kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+  static_assert(kRing >= 3 && 400 + 32 * GC <= kMisc && kCols * kCtas <= 512, "budgets");
+};
+
+// Tiles of all rows, and where tile x lies.
+struct PagedSpan {
+  long long total;  // W
+  long long x0, x1; // this CTA's tiles
+  int b, off;       // sequence of tile x0, tiles of it before x0 (over its KV heads)
+};
+__device__ __forceinline__ int tiles_of(const CacheArgs& c, int b) {
+  return (cache_len(c, b) + 127) >> 7;
+}
+__device__ __forceinline__ long long cut(const PagedArgs& a, long long total, int c) {
+  return total * c / a.grid;
+}
+
+// Counts the tiles of all sequences (every thread of the block, n of them) and looks tile
+// [W c / C] up.  `sm`: n / 32 + 1 numbers of 8 bytes and 2 of 4 behind them.
+__device__ PagedSpan paged_span(const PagedArgs& a, int c, long long* sm, int n) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = n / 32;
+  const int per = (a.cache.nseq + n - 1) / n, first = min(tid * per, a.cache.nseq),
+            last = min(first + per, a.cache.nseq);
+  long long mine = 0;
+  for (int b = first; b < last; ++b) mine += tiles_of(a.cache, b);
+  mine *= a.cache.hkv;
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  int* at = reinterpret_cast<int*>(sm + nw + 1);
+  if (lane == 31) sm[warp] = incl;
+  if (tid == 0) at[0] = a.cache.nseq, at[1] = 0;
+  __syncthreads();
+  PagedSpan s;
+  s.total = 0;
+  long long before = incl - mine;
+  for (int w = 0; w < nw; ++w) {
+    if (w < warp) before += sm[w];
+    s.total += sm[w];
+  }
+  s.x0 = cut(a, s.total, c);
+  s.x1 = cut(a, s.total, c + 1);
+  if (mine > 0 && s.x0 >= before && s.x0 < before + mine) {
+    long long left = s.x0 - before;
+    int b = first;
+    for (; b < last - 1; ++b) {
+      const long long t = (long long)tiles_of(a.cache, b) * a.cache.hkv;
+      if (left < t) break;
+      left -= t;
+    }
+    at[0] = b;
+    at[1] = (int)left;
+  }
+  __syncthreads();
+  s.b = at[0];
+  s.off = at[1];
+  __syncthreads();
+  return s;
+}
+
+// The rows (sequence, KV head) that a range of tiles runs through.
+struct PagedWalk {
+  int b, h, t;      // next tile
+  long long left;   // tiles of the range that are left
+  int len, tiles;   // of sequence b
+  int t1;           // end of the current part of the row: tiles [t0, t1)
+  int t0;
+  int sb, sh;       // sequence and KV head of the current part
+  __device__ __forceinline__ void seek(const PagedArgs& a) {
+    while (b < a.cache.nseq) {
+      len = cache_len(a.cache, b);
+      tiles = (len + 127) >> 7;
+      if (tiles > 0) return;
+      ++b;
+    }
+    left = 0;
+  }
+  __device__ __forceinline__ PagedWalk(const PagedArgs& a, const PagedSpan& s) {
+    b = s.b;
+    left = s.x1 - s.x0;
+    len = tiles = h = t = t0 = t1 = sb = sh = 0;
+    if (left <= 0) return;
+    seek(a);
+    if (left > 0) {
+      h = s.off / tiles;
+      t = s.off - h * tiles;
+    }
+  }
+  // The next part; false at the end.  len and tiles are its sequence's.
+  __device__ __forceinline__ bool next(const PagedArgs& a) {
+    if (t == 0 && h == a.cache.hkv) {
+      h = 0;
+      ++b;
+      if (left > 0) seek(a);
+    }
+    if (left <= 0) return false;
+    sb = b;
+    sh = h;
+    t0 = t;
+    t1 = (int)min((long long)tiles, t + left);
+    left -= t1 - t0;
+    t = t1;
+    if (t == tiles) t = 0, ++h;
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
+};
+
+// Whether `x` holds for one of the softmax warps' 128 threads; a barrier for them.
+__device__ __forceinline__ bool any128(bool x) {
+  uint32_t y;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(y)
+      : "r"((uint32_t)x)
+      : "memory");
+  return y != 0;
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t ta, float (&f)[N]) {
+  uint32_t r[N];
+  if constexpr (N == 4) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(ta)
+        : "memory");
+  } else if constexpr (N == 8) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7])
+        : "r"(ta)
+        : "memory");
+  } else if constexpr (N == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(ta)
+        : "memory");
+  } else if constexpr (N == 32) {
+    tmem_ld32(ta, r);
+  } else {
+    tmem_ld_row(ta, r);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = __uint_as_float(r[i]);
+}
+template <int N>
+__device__ __forceinline__ void tmem_st_cols(uint32_t ta, const float (&f)[N]) {
+  if constexpr (N == 64) {
+    uint32_t r[32];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(f[32 * h + i]);
+      tmem_st32(ta + 32 * h, r);
+    }
+  } else {
+    uint32_t r[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = __float_as_uint(f[i]);
+    if constexpr (N == 4) {
+      asm volatile(
+          "tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};\n\t"
+          "tcgen05.wait::st.sync.aligned;" ::"r"(ta),
+          "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+          : "memory");
+    } else if constexpr (N == 8) {
+      asm volatile(
+          "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\t"
+          "tcgen05.wait::st.sync.aligned;" ::"r"(ta),
+          "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+          : "memory");
+    } else if constexpr (N == 16) {
+      tmem_st16(ta, r);
+    } else {
+      tmem_st32(ta, r);
+    }
+  }
+}
+
+// Reduces N columns over the lanes of a warp: halves of the columns are exchanged, so that each
+// step works on half as many.  Afterwards lane l holds, in x[0 .. max(1, N / 32)), the
+// columns column_of<N>(l) and following.
+template <int N, bool MAX>
+__device__ __forceinline__ void reduce_cols(float (&x)[N]) {
+  const int lane = threadIdx.x & 31;
+  int n = N;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    if (n > 1) {
+      n /= 2;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        if (i < n) {
+          const bool up = lane & o;
+          const float give = up ? x[i] : x[i + n], own = up ? x[i + n] : x[i];
+          const float got = __shfl_xor_sync(0xffffffffu, give, o);
+          x[i] = MAX ? fmaxf(own, got) : own + got;
+        }
+      }
+    } else {
+      const float got = __shfl_xor_sync(0xffffffffu, x[0], o);
+      x[0] = MAX ? fmaxf(x[0], got) : x[0] + got;
+    }
+  }
+}
+template <int N>
+__device__ __forceinline__ int column_of(int lane) {
+  int c = 0, n = N;
+#pragma unroll
+  for (int o = 16; o > 0 && n > 1; o >>= 1) {
+    n /= 2;
+    if (lane & o) c += n;
+  }
+  return c;
+}
+
+template <int D, int GC, bool WEIGHTS>
+__global__ void __launch_bounds__(kThreads, PagedCfg<D, GC>::kCtas)
+    k_paged(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedArgs a) {
+  using C = PagedCfg<D, GC>;
+  constexpr int NCH = D / 64, NR = C::kRing, N = C::kN, NO = C::kNo, HI = C::kHi,
+                CH = GC < 16 ? GC : 16;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sKV = smem;
+  uint8_t* sQ = sKV + NR * C::kTile;  // [2][chunk][N rows][128 bytes]
+  uint8_t* sP = sQ + 2 * C::kQ;       // [2][64 entries][NO rows][128 bytes]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sP + 2 * C::kP);
+  // ring full / empty | queries loaded / free | S complete | P stored | P V complete | O read
+  constexpr int B_F = 0, B_E = B_F + NR, B_Q = B_E + NR, B_QE = B_Q + 2, B_S = B_QE + 2,
+                B_P = B_S + 2, B_PV = B_P + 2, B_OE = B_PV + 2, B_END = B_OE + 2;
+  static_assert((B_END + 1) * 8 <= 320, "barrier block");
+  long long* scan = reinterpret_cast<long long*>(bars + 40);  // see paged_span
+  static_assert(kThreads / 32 + 2 <= 8, "scan block");
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 48);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+  float* sMax = reinterpret_cast<float*>(bars + 50);  // [4][GC] maxima of the warps
+  float* sSum = sMax + 4 * GC;                        // [4][GC] their sums
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 128) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NR; ++s) {
+      mbar_init(bar(B_F + s), 1);
+      mbar_init(bar(B_E + s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(B_Q + i), 1);
+      mbar_init(bar(B_QE + i), 1);
+      mbar_init(bar(B_S + i), 1);
+      mbar_init(bar(B_P + i), 4);
+      mbar_init(bar(B_PV + i), 1);
+      mbar_init(bar(B_OE + i), 4);
+    }
+    mbar_init(bar(B_END), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 5) {
+    tmem_alloc(smem_u32(tslot), C::kCols);
+    tmem_relinquish();
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // sequences without an entry: no tile names them
+  for (int b = blockIdx.x; b < a.cache.nseq; b += gridDim.x)
+    if (cache_len(a.cache, b) == 0)
+      for (int i = threadIdx.x; i < a.hq * D / 8; i += kThreads)
+        reinterpret_cast<uint4*>(a.o + (size_t)b * a.hq * D)[i] = make_uint4(0, 0, 0, 0);
+  const PagedSpan span = paged_span(a, blockIdx.x, scan, kThreads);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *reinterpret_cast<volatile uint32_t*>(tslot);
+  // TMEM: S of tile u at columns N (u & 1), O of part i at 2 N + NO (i & 1)
+  auto wait = [&](int b, uint32_t parity, int n) {
+    return wait_bar_warp(bar(b), parity, abort_flag, a.cache.status, wait_site(kKerPaged, b, n));
+  };
+
+  // The loads run in the order K0, K1, V0, K2, V1, ...: that in which the products take them, with
+  // the scores of one tile ahead of the values of the one before it.
+  if (warp == 4) {
+    // ------------------------------ loads ----------------------------------------
+    const int rows = min(128, 1 << a.cache.page_shift);  // of a box
+    const int box = lane / NCH, ch = lane % NCH;         // one box of a tile per lane
+    int s = 0, round = 0, part = 0;
+    bool ok = true;
+    auto load = [&](const CUtensorMap* tm, int b, int h, int len, int t) {
+      const int valid = min(128, len - t * 128), n = (valid + rows - 1) / rows;  // entries, boxes
+      int page = 0;
+      const int e = t * 128 + box * rows;
+      if (box < n) page = max(0, cache_page(a.cache, b, e));
+      if (round > 0 && !(ok = wait(B_E + s, (round & 1) ^ 1, t))) return;
+      if (lane == 0) mbar_arrive_expect_tx(bar(B_F + s), n * rows * NCH * 128);
+      __syncwarp();
+      if (box < n)
+        tma_load_4d(smem_u32(sKV + s * C::kTile) + ch * 16384 + box * rows * 128, tm, bar(B_F + s),
+                    64 * ch, h, e & ((1 << a.cache.page_shift) - 1), page);
+      if (++s == NR) s = 0, ++round;
+    };
+    struct { int b, h, len, t; } last{-1, 0, 0, 0};
+    PagedWalk w(a, span);
+    while (ok && w.next(a)) {
+      if (part >= 2 && !(ok = wait(B_QE + (part & 1), ((part >> 1) & 1) ^ 1, part))) break;
+      if (lane == 0) mbar_arrive_expect_tx(bar(B_Q + (part & 1)), C::kQ);
+      __syncwarp();
+      if (lane < NCH)
+        tma_load_4d(smem_u32(sQ + (part & 1) * C::kQ) + lane * N * 128, &tm_q,
+                    bar(B_Q + (part & 1)), 64 * lane, 0, w.sh, w.sb);
+      ++part;
+      for (int t = w.t0; ok && t < w.t1; ++t) {
+        load(&tm_k, w.sb, w.sh, w.len, t);
+        if (ok && last.b >= 0) load(&tm_v, last.b, last.h, last.len, last.t);
+        last = {w.sb, w.sh, w.len, t};
+      }
+    }
+    if (ok && last.b >= 0) load(&tm_v, last.b, last.h, last.len, last.t);
+    // an aborted CTA must not leave before its copies have landed
+    if (*abort_flag) {
+      for (int i = max(0, part - 2); i < part; ++i) drain_bar(bar(B_Q + (i & 1)), (i >> 1) & 1);
+      for (int i = 0; i < NR; ++i)
+        if (i < s || round > 0) drain_bar(bar(B_F + i), (i < s ? round : round - 1) & 1);
+    }
+  } else if (warp == 5) {
+    // ------------------------------ products -------------------------------------
+    constexpr uint32_t idS = make_idesc_bf16(128, N, false, false);
+    constexpr uint32_t idO = make_idesc_bf16(128, NO, true, false);
+    const uint32_t el = elect_one(), tm = uniform(tbase);
+    const uint32_t k_lo = desc_lo(smem_u32(sKV), 16), q_lo = desc_lo(smem_u32(sQ), 16),
+                   p_lo = desc_lo(smem_u32(sP), 16);
+    // d = 64 fills half of the 128 rows of V^T: the other half repeats it and is not read
+    const uint32_t v_lo = desc_lo(smem_u32(sKV), D == 128 ? 16384 : 0);
+    int s = 0, round = 0, part = 0, u = 0;  // ring position, parts, tiles
+    bool ok = true, first = false, pending = false, new_part = false;
+    int valid = 0;
+    // O += V^T P^T of tile u - 1, which has `valid` entries; the first of part `part - 1`, or of
+    // the one before where a new part's first scores have been issued since
+    auto values = [&](int of) {
+      if (!(ok = wait(B_F + s, round & 1, u))) return;
+      const int steps = (valid + 15) / 16;
+      if (valid < 16 * steps) {  // entries behind the end: P is zero there, V must be finite
+        uint8_t* tile = sKV + s * C::kTile;
+        const int pieces = (16 * steps - valid) * 8;
+        for (int x = lane; x < NCH * pieces; x += 32)
+          *reinterpret_cast<uint4*>(tile + (x / pieces) * 16384 + valid * 128 +
+                                    (x % pieces) * 16) = make_uint4(0, 0, 0, 0);
+        fence_async_smem();
+        __syncwarp();
+      }
+      const int up = u - 1;
+      if (first && of >= 2 && !(ok = wait(B_OE + (of & 1), ((of >> 1) & 1) ^ 1, of))) return;
+      if (!(ok = wait(B_P + (up & 1), (up >> 1) & 1, up))) return;
+      tc_fence_after();
+      const uint32_t v = v_lo + s * (C::kTile >> 4), p = p_lo + (up & 1) * (C::kP >> 4);
+      const uint32_t d = tm + 2 * N + NO * (of & 1);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        if (kk < steps)
+          mma_ss(el, d, v + kk * (2048 >> 4), p + (((kk >> 2) * NO * 128 + (kk & 3) * 32) >> 4),
+                 idO, !first || kk > 0);
+      mma_commit(el, bar(B_PV + (up & 1)));
+      mma_commit(el, bar(B_E + s));
+      if (++s == NR) s = 0, ++round;
+    };
+    PagedWalk w(a, span);
+    while (ok && w.next(a)) {
+      if (!(ok = wait(B_Q + (part & 1), (part >> 1) & 1, part))) break;
+      new_part = true;
+      for (int t = w.t0; ok && t < w.t1; ++t) {
+        if (!(ok = wait(B_F + s, round & 1, u))) break;
+        tc_fence_after();
+        const uint32_t k = k_lo + s * (C::kTile >> 4), q = q_lo + (part & 1) * (C::kQ >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss(el, tm + N * (u & 1), k + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                 q + (((kk >> 2) * N * 128 + (kk & 3) * 32) >> 4), idS, kk > 0);
+        mma_commit(el, bar(B_S + (u & 1)));
+        mma_commit(el, bar(B_E + s));
+        if (t + 1 == w.t1) mma_commit(el, bar(B_QE + (part & 1)));
+        if (++s == NR) s = 0, ++round;
+        if (pending) values(new_part ? part - 1 : part);
+        if (!ok) break;
+        pending = true;
+        first = new_part;
+        new_part = false;
+        valid = min(128, w.len - t * 128);
+        ++u;
+      }
+      ++part;
+    }
+    if (ok && pending) values(part - 1);
+    if (!ok) {  // products in flight end before TMEM is freed
+      mma_commit(el, bar(B_END));
+      drain_bar(bar(B_END), 0);
+    }
+  } else {
+    // ------------------------------ softmax --------------------------------------
+    // A failed wait marks the warp dead: it keeps to its barriers without touching TMEM.
+    const int r = threadIdx.x;  // entry of a tile; row of O^T
+    const uint32_t lanes = tbase + ((uint32_t)(warp * 32) << 16);
+    const float c = a.scale_log2;
+    bool dead = false;
+    int u = 0, part = 0;
+    long long x = span.x0;  // tile over all rows
+    PagedWalk w(a, span);
+    while (w.next(a)) {
+      float m[GC], l[GC];
+#pragma unroll
+      for (int g = 0; g < GC; ++g) m[g] = kLowest, l[g] = 0.f;
+      for (int t = w.t0; t < w.t1; ++t, ++u, ++x) {
+        const int b = u & 1;
+        dead = dead || !wait(B_S + b, (u >> 1) & 1, u);
+        tc_fence_after();
+        float y[GC];
+#pragma unroll
+        for (int g = 0; g < GC; ++g) y[g] = -INFINITY;
+        if (!dead) tmem_ld_cols<GC>(lanes + N * b, y);
+        __syncwarp();
+        const bool there = r < w.len - t * 128;
+        bool raise = false;
+#pragma unroll
+        for (int g = 0; g < GC; ++g) {
+          y[g] = there && g < a.G ? y[g] * c : -INFINITY;
+          raise |= y[g] > m[g] + kRaise;
+        }
+        if (WEIGHTS && there) {
+          float* out = a.scores + ((size_t)x * a.G) * 128 + r;
+#pragma unroll
+          for (int g = 0; g < GC; ++g)
+            if (g < a.G) out[g * 128] = y[g];
+        }
+        __syncwarp();
+        if (any128(raise)) {
+          // the tile's maxima of all heads; O of the tiles before it moves to the new reference
+          float z[GC];
+#pragma unroll
+          for (int g = 0; g < GC; ++g) z[g] = y[g];
+          reduce_cols<GC, true>(z);
+          const int col = column_of<GC>(lane);
+#pragma unroll
+          for (int i = 0; i < (GC > 32 ? GC / 32 : 1); ++i) sMax[warp * GC + col + i] = z[i];
+          named_bar_sync(2, 128);
+          if (t > w.t0) {
+            dead = dead || !wait(B_PV + (b ^ 1), ((u - 1) >> 1) & 1, u);
+            tc_fence_after();
+          }
+#pragma unroll
+          for (int g0 = 0; g0 < GC; g0 += CH) {
+            float f[CH];
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+              const int g = g0 + i;
+              const float top = fmaxf(fmaxf(sMax[g], sMax[GC + g]),
+                                      fmaxf(sMax[2 * GC + g], sMax[3 * GC + g]));
+              f[i] = 1.f;
+              if (top > m[g]) {
+                f[i] = ex2_approx(m[g] - top);
+                m[g] = top;
+              }
+              l[g] *= f[i];
+            }
+            if (t > w.t0 && !dead) {
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const uint32_t to = lanes + 2 * N + NO * (part & 1) + HI * half + g0;
+                float o[CH];
+                tmem_ld_cols<CH>(to, o);
+#pragma unroll
+                for (int i = 0; i < CH; ++i) o[i] *= f[i];
+                tmem_st_cols<CH>(to, o);
+              }
+            }
+          }
+        }
+        // the buffer of P was last read by the product of tile u - 2
+        if (u >= 2) dead = dead || !wait(B_PV + b, ((u - 2) >> 1) & 1, u);
+        uint8_t* p = sP + b * C::kP + (r >> 6) * NO * 128 + (r & 7) * 2;
+#pragma unroll
+        for (int g = 0; g < GC; ++g) {
+          if (g < a.G) {
+            const float e = ex2_approx(y[g] - m[g]);
+            l[g] += e;
+            const __nv_bfloat16 hi = __float2bfloat16_rn(e);
+            const __nv_bfloat16 lo = __float2bfloat16_rn(e - __bfloat162float(hi));
+            uint8_t* to = p + g * 128 + ((((r & 63) >> 3) ^ (g & 7)) << 4);  // HI is a multiple of 8
+            *reinterpret_cast<__nv_bfloat16*>(to) = hi;
+            *reinterpret_cast<__nv_bfloat16*>(to + HI * 128) = lo;
+          }
+        }
+        fence_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_P + b));
+      }
+      // normalisers over the entries
+      reduce_cols<GC, false>(l);
+      const int col = column_of<GC>(lane);
+#pragma unroll
+      for (int i = 0; i < (GC > 32 ? GC / 32 : 1); ++i) sSum[warp * GC + col + i] = l[i];
+      named_bar_sync(2, 128);
+      dead = dead || !wait(B_PV + ((u - 1) & 1), ((u - 1) >> 1) & 1, u);
+      tc_fence_after();
+      const bool whole = w.whole();
+      const size_t row0 = (size_t)w.sb * a.hq + w.sh * a.G;
+      // a part of a row: the first of this CTA's range, or the last
+      const size_t at = ((size_t)blockIdx.x * 2 + (part > 0)) * a.G;
+#pragma unroll
+      for (int g0 = 0; g0 < GC; g0 += CH) {
+        float o[CH], lo[CH];
+#pragma unroll
+        for (int i = 0; i < CH; ++i) o[i] = lo[i] = 0.f;
+        if (!dead) {
+          const uint32_t from = lanes + 2 * N + NO * (part & 1) + g0;
+          tmem_ld_cols<CH>(from, o);
+          tmem_ld_cols<CH>(from + HI, lo);
+        }
+#pragma unroll
+        for (int i = 0; i < CH; ++i) o[i] += lo[i];
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          const int g = g0 + i;
+          if (g >= a.G) continue;
+          const float sum = (sSum[g] + sSum[GC + g]) + (sSum[2 * GC + g] + sSum[3 * GC + g]);
+          if (whole) {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const __nv_bfloat16 h = __float2bfloat16_rn(sum == 0.f ? 0.f : o[i] * inv);
+            if (r < D) a.o[(row0 + g) * D + r] = *reinterpret_cast<const uint16_t*>(&h);
+            if (WEIGHTS && r == 0) a.stats[row0 + g] = make_float2(m[g], inv);
+          } else {
+            if (r < D) a.parts[(at + g) * D + r] = o[i];
+            if (r == 0) a.part_stats[at + g] = make_float2(m[g], sum);
+          }
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_OE + (part & 1)));
+      ++part;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tbase, C::kCols);
+  }
+}
+
+// Adds up the rows that several CTAs share, and the weights of CTA c's tiles.
+//
+// Row (b, h) with tiles [r0, r1) belongs to block c of the first cut x_c inside it.  Its parts are
+// those of CTA c - 1 (the last of its range), c, c + 1, ... (the first of theirs) up to the one
+// that reaches r1; they are added in this order.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_constant__ PagedArgs a) {
+  constexpr int V = D / 4;  // pieces of a head's row
+  __shared__ long long scan[kJoinThreads / 32 + 4];
+  __shared__ float s_m[kPagedMaxGroup], s_inv[kPagedMaxGroup];
+  __shared__ float4 s_sum[kJoinThreads];
+  const int c = blockIdx.x, tid = threadIdx.x, G = a.G;
+  const PagedSpan span = paged_span(a, c, scan, kJoinThreads);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // m and 1 / l of the shared row that holds tile x (of sequence b, row starting at r0), from its
+  // parts [c0, c1]
+  auto part_of = [&](int i, long long r0) -> size_t {  // of CTA i in the row
+    return ((size_t)i * 2 + (cut(a, span.total, i) < r0)) * G;
+  };
+  auto first_cta = [&](long long r0) {  // whose range holds tile r0
+    int i = (int)((r0 * a.grid) / span.total);
+    while (i > 0 && cut(a, span.total, i) > r0) --i;
+    while (cut(a, span.total, i + 1) <= r0) ++i;
+    return i;
+  };
+  auto stats = [&](int c0, int c1, long long r0) {
+    const int warp = tid >> 5, lane = tid & 31;
+    for (int g = warp; g < G; g += kJoinThreads / 32) {
+      float m = kLowest, l = 0.f;
+      for (int i = c0 + lane; i <= c1; i += 32) {
+        if (cut(a, span.total, i) == cut(a, span.total, i + 1)) continue;
+        m = fmaxf(m, __ldcg(&a.part_stats[part_of(i, r0) + g].x));
+      }
+      m = warp_max(m);
+      for (int i = c0 + lane; i <= c1; i += 32) {
+        if (cut(a, span.total, i) == cut(a, span.total, i + 1)) continue;
+        const float2 p = __ldcg(&a.part_stats[part_of(i, r0) + g]);
+        l += p.y * (p.x == m ? 1.f : ex2_approx(p.x - m));
+      }
+      l = warp_sum(l);
+      if (lane == 0) {
+        s_m[g] = m;
+        s_inv[g] = l == 0.f ? 0.f : 1.f / l;
+      }
+    }
+    __syncthreads();
+  };
+
+  if (c > 0 && span.b < a.cache.nseq && span.x0 < span.total) {
+    const int tiles = tiles_of(a.cache, span.b), h = span.off / tiles;
+    const long long r0 = span.x0 - (span.off - h * tiles), r1 = r0 + tiles;
+    if (span.x0 > r0 && cut(a, span.total, c - 1) <= r0) {
+      const int c1 = first_cta(r1 - 1);
+      stats(c - 1, c1, r0);
+      const size_t row0 = (size_t)span.b * a.hq + h * G;
+      // threads: pieces of the G rows, and where those are few, several runs over the parts
+      const int items = G * V, runs = max(1, kJoinThreads / items);
+      for (int i0 = 0; i0 < items; i0 += kJoinThreads) {
+        const int item = i0 + (runs > 1 ? tid % items : tid), run = runs > 1 ? tid / items : 0;
+        const bool on = item < items && run < runs;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (on) {
+          const int g = item / V, v = item % V;
+#pragma unroll 4
+          for (int i = c - 1 + run; i <= c1; i += runs) {
+            if (cut(a, span.total, i) == cut(a, span.total, i + 1)) continue;
+            const size_t at = part_of(i, r0) + g;
+            const float pm = __ldcg(&a.part_stats[at].x);
+            const float f = (pm == s_m[g] ? 1.f : ex2_approx(pm - s_m[g])) * s_inv[g];
+            const float4 p = __ldcg(reinterpret_cast<const float4*>(a.parts + at * D) + v);
+            sum.x += p.x * f, sum.y += p.y * f, sum.z += p.z * f, sum.w += p.w * f;
+          }
+        }
+        if (runs > 1) {
+          s_sum[tid] = sum;
+          __syncthreads();
+          if (run == 0)
+            for (int j = 1; j < runs; ++j) {
+              const float4 p = s_sum[j * items + item];
+              sum.x += p.x, sum.y += p.y, sum.z += p.z, sum.w += p.w;
+            }
+        }
+        if (on && run == 0) {
+          const int g = item / V, v = item % V;
+          if (s_inv[g] == 0.f) sum = make_float4(0.f, 0.f, 0.f, 0.f);
+          reinterpret_cast<uint2*>(a.o + (row0 + g) * D)[v] =
+              make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
+        }
+      }
+      __syncthreads();
+    }
+  }
+
+  if (!a.scores) return;
+  PagedWalk w(a, span);
+  long long x = span.x0;
+  while (w.next(a)) {
+    const size_t row0 = (size_t)w.sb * a.hq + w.sh * G;
+    if (w.whole()) {
+      if (tid < G) {
+        const float2 p = __ldcg(&a.stats[row0 + tid]);
+        s_m[tid] = p.x;
+        s_inv[tid] = p.y;
+      }
+      __syncthreads();
+    } else {
+      const long long r0 = x - w.t0;
+      stats(first_cta(r0), first_cta(r0 + w.tiles - 1), r0);
+    }
+    const int n = min(w.len, w.t1 * 128) - w.t0 * 128;
+    for (int i = tid; i < n; i += kJoinThreads) {
+      const float* s = a.scores + (size_t)(x + (i >> 7)) * G * 128 + (i & 127);
+      float sum = 0.f;
+#pragma unroll 4
+      for (int g = 0; g < G; ++g) sum += ex2_approx(__ldcg(s + g * 128) - s_m[g]) * s_inv[g];
+      const int e = w.t0 * 128 + i, page = cache_page(a.cache, w.sb, e);
+      if (page >= 0)
+        atomicAdd(a.cache.weight +
+                      a.cache.meta(page, e & ((1 << a.cache.page_shift) - 1), w.sh), sum);
+    }
+    x += w.t1 - w.t0;
+    __syncthreads();
+  }
+}
+
+template <int D, int GC, bool WEIGHTS>
+cudaError_t launch_t(const PagedArgs& a, const CUtensorMap& mq, const CUtensorMap& mk,
+                     const CUtensorMap& mv, cudaStream_t st) {
+  using C = PagedCfg<D, GC>;
+  cudaError_t e = dense_prepare<k_paged<D, GC, WEIGHTS>>(kThreads, 0, C::kSmem);
+  if (e != cudaSuccess) return e;
+  k_paged<D, GC, WEIGHTS><<<a.grid, kThreads, C::kSmem, st>>>(mq, mk, mv, a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (a.grid == 1 && !WEIGHTS) return e;  // every row whole
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.grid);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_paged_join<D>, a);
+}
+
+template <int D, bool WEIGHTS>
+cudaError_t launch_d(const PagedArgs& a, const CUtensorMap& mq, const CUtensorMap& mk,
+                     const CUtensorMap& mv, cudaStream_t st) {
+  if (a.G <= 4) return launch_t<D, 4, WEIGHTS>(a, mq, mk, mv, st);
+  if (a.G <= 8) return launch_t<D, 8, WEIGHTS>(a, mq, mk, mv, st);
+  if (a.G <= 16) return launch_t<D, 16, WEIGHTS>(a, mq, mk, mv, st);
+  if (a.G <= 32) return launch_t<D, 32, WEIGHTS>(a, mq, mk, mv, st);
+  return launch_t<D, 64, WEIGHTS>(a, mq, mk, mv, st);
+}
+
+template <int D>
+int ctas_of(int G) {  // per SM
+  return G <= 4    ? PagedCfg<D, 4>::kCtas
+         : G <= 8  ? PagedCfg<D, 8>::kCtas
+         : G <= 16 ? PagedCfg<D, 16>::kCtas
+         : G <= 32 ? PagedCfg<D, 32>::kCtas
+                   : PagedCfg<D, 64>::kCtas;
+}
+
+}  // namespace
+
+int paged_grid(const CacheArgs& c, int G) {
+  const int ctas = G <= 8 || (G <= 16 && c.d == 64) ? 2 : 1;  // PagedCfg::kCtas
+
+  const int most = sm_count() * ctas;
+  const long long tiles = (long long)c.nseq * c.hkv * ((c.capacity + 127) / 128);
+  return (int)(tiles < 1 ? 1 : tiles < most ? tiles : most < kPagedMaxGrid ? most : kPagedMaxGrid);
+}
+
+cudaError_t launch_paged(const PagedArgs& a, const uint16_t* q, long long q_stride,
+                         cudaStream_t st) {
+  const CacheArgs& c = a.cache;
+  const int page = 1 << c.page_shift, rows = page < 128 ? page : 128;
+  const int n = a.G <= 16 ? 16 : a.G <= 32 ? 32 : 64;
+  CUtensorMap mq, mk, mv;
+  cudaError_t e;
+  if ((e = make_tmap_4d(&mq, q, c.d, a.G, c.hkv, c.nseq, c.d, (long long)a.G * c.d, q_stride, n,
+                        1)) != cudaSuccess ||
+      (e = make_tmap_4d(&mk, c.k, c.d, c.hkv, page, c.num_pages, c.kh, c.ks, c.kp, 1, rows)) !=
+          cudaSuccess ||
+      (e = make_tmap_4d(&mv, c.v, c.d, c.hkv, page, c.num_pages, c.vh, c.vs, c.vp, 1, rows)) !=
+          cudaSuccess)
+    return e;
+  if (a.scores)
+    return c.d == 128 ? launch_d<128, true>(a, mq, mk, mv, st) : launch_d<64, true>(a, mq, mk, mv, st);
+  return c.d == 128 ? launch_d<128, false>(a, mq, mk, mv, st)
+                    : launch_d<64, false>(a, mq, mk, mv, st);
+}
+
+}  // namespace msa

@@ -193,6 +193,21 @@ cudaError_t make_tmap_rows(CUtensorMap* map, const void* base, int d, int heads,
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t make_tmap_4d(CUtensorMap* map, const void* base, int d, int n1, int n2, int n3,
+                         long long s1, long long s2, long long s3, int box1, int box2) {
+  if (!encode_fn()) return cudaErrorNotSupported;
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)n1, (cuuint64_t)n2, (cuuint64_t)n3};
+  const cuuint64_t strides[3] = {(cuuint64_t)(n1 > 1 ? s1 : d) * 2, (cuuint64_t)(n2 > 1 ? s2 : d) * 2,
+                                 (cuuint64_t)(n3 > 1 ? s3 : d) * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)box1, (cuuint32_t)box2, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  const CUresult r =
+      g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides,
+               box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t make_tmap_3d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t mid,
                          uint64_t outer, uint32_t box_inner, uint32_t box_mid, uint32_t box_outer,
                          int swizzle_bytes) {

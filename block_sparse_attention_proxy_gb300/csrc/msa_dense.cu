@@ -5,6 +5,18 @@
 #include "dense_common.cuh"
 
 namespace msa {
+
+// Device status word, with the device's context made current on this thread: a
+// thread's first CUDA call may be this one (autograd runs backwards on threads of its own),
+// and encoding a tensor map does not do that by itself.
+cudaError_t bind_device(unsigned** status) {
+  static thread_local int bound = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev != bound && (e = cudaSetDevice(dev)) == cudaSuccess) bound = dev;
+  return e == cudaSuccess ? status_ptr(status) : e;
+}
+
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -57,17 +69,6 @@ msa_status check_dense(const msa_dense_params* p, DenseShape* s, DenseArgs* a) {
   if ((long long)dense_slots(a->T, a->ndoc, a->tpt) * a->hkv > 0x7fffffffll)
     return MSA_ERR_UNSUPPORTED;
   return MSA_OK;
-}
-
-// Device status word, with the device's context made current on this thread: a
-// thread's first CUDA call may be this one (autograd runs backwards on threads of its own),
-// and encoding a tensor map does not do that by itself.
-cudaError_t bind_device(unsigned** status) {
-  static thread_local int bound = -1;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess && dev != bound && (e = cudaSetDevice(dev)) == cudaSuccess) bound = dev;
-  return e == cudaSuccess ? status_ptr(status) : e;
 }
 
 struct DenseWorkspace {

@@ -23,7 +23,7 @@ constexpr long long kWaitCycles = 1000000000ll;
 // Where a bounded wait gave up, stored above the status code in the status
 // word: kernel id (4 bits), barrier index (8 bits), tile or block index (12 bits).
 enum : uint32_t { kKerSelect = 1, kKerFwd = 2, kKerBwd = 3, kKerSelArg = 4,
-                kKerDenseFwd = 5, kKerDenseDq = 6, kKerDenseDkv = 7 };
+                kKerDenseFwd = 5, kKerDenseDq = 6, kKerDenseDkv = 7, kKerPaged = 8 };
 __host__ __device__ constexpr uint32_t wait_site(uint32_t kernel, uint32_t bar, int n) {
   return kernel | (bar << 4) | ((uint32_t)(n < 0 ? 0 : (n > 4095 ? 4095 : n)) << 12);
 }
@@ -215,6 +215,8 @@ Workspace workspace_layout(const Shape& s, WsKind kind);
 msa_status check_params(const msa_params* p, Shape* s);
 // Address of the current device's status word.
 cudaError_t status_ptr(unsigned** out);
+// The same, with the device's context made current on the calling thread (tensor maps need that).
+cudaError_t bind_device(unsigned** out);
 // Adds to the process-wide count of launched kernels (msa_launch_count).
 void add_launches(uint64_t n);
 
@@ -225,6 +227,10 @@ struct TmapEncoder;  // opaque; resolves cuTensorMapEncodeTiled once
 cudaError_t make_tmap_3d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t mid,
                          uint64_t outer, uint32_t box_inner, uint32_t box_mid, uint32_t box_outer,
                          int swizzle_bytes);
+// Tensor map of a [n3][n2][n1][d] bf16 tensor with strides s1, s2, s3 elements (of a dimension of
+// size 1: any): boxes of 64 columns x box1 x box2 x 1, 128-byte swizzle.
+cudaError_t make_tmap_4d(CUtensorMap* map, const void* base, int d, int n1, int n2, int n3,
+                         long long s1, long long s2, long long s3, int box1, int box2);
 
 cudaError_t launch_meta(const Shape& s, const int32_t* cu_seqlens, int32_t* cu_blocks,
                         unsigned* status, cudaStream_t st);

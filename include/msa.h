@@ -307,6 +307,136 @@ msa_status msa_dense_bwd(const msa_dense_params* params, const int32_t* cu_seqle
                          size_t workspace_bytes, msa_stream_t stream);
 
 /*
+ * Rotary positions: pair i of a row (i < dims / 2) at position p turns by the angle
+ * p f_i and grows by `amplitude`,
+ *   a' = amplitude (a cos(p f_i) - b sin(p f_i)),  b' = amplitude (b cos(p f_i) + a sin(p f_i)),
+ * elements `dims` and later of the row stay as they are.  A pair is elements (i, i + dims / 2),
+ * or (2 i, 2 i + 1) where `interleaved` is set.  `inverse` turns by -p f_i: the gradient.
+ * Frequencies are turns (2 pi) a position as fractions of 2^64, so that p f_i modulo a turn
+ * is exact for any position.  Angles' cosines and sines and the products are fp32, each
+ * result is rounded once.
+ *
+ * q, q_out [T, hq, d], k, k_out [T, hkv, d] (null with hkv = 0), one type; the outputs are
+ * contiguous and must not overlap the inputs.  Either cu_seqlens is given (a position is the
+ * place in the document; rows behind the last document come out zero) or positions [T],
+ * int32 or int64, of any sign.
+ */
+typedef enum msa_dtype { MSA_BF16 = 0, MSA_FP16 = 1, MSA_FP32 = 2 } msa_dtype;
+
+typedef struct msa_rotary_params {
+  int32_t total_tokens; /* T, below 2^25 */
+  int32_t num_docs;     /* documents of cu_seqlens; 0 with positions */
+  int32_t hq, hkv;      /* heads of q and k, hq + hkv <= 2048 */
+  int32_t d;            /* head dim, a multiple of 16 up to 256 */
+  int32_t dims;         /* rotated elements of a head, a multiple of 16 up to d; 0: none */
+  int32_t interleaved, inverse; /* 0 or 1 */
+  int32_t dtype;                /* msa_dtype */
+  int32_t position_bytes;       /* 4 or 8: type of positions */
+  /* host pointer, read during the call: dims / 2 frequencies */
+  const uint64_t* freq;
+  /* token strides in elements, multiples of 16 bytes and at least heads * d; 0: contiguous */
+  int64_t q_stride, k_stride;
+  float amplitude; /* finite */
+  uint32_t flags;  /* must be 0 */
+} msa_rotary_params;
+
+msa_status msa_rotary(const msa_rotary_params* params, const int32_t* cu_seqlens,
+                      const void* positions, const void* q, const void* k, void* q_out,
+                      void* k_out, msa_stream_t stream);
+
+/*
+ * A key-value cache in pages, shared by many sequences: entry i of sequence b lies in page
+ * table[b][i / page_size], slot i % page_size.
+ *   k, v      [num_pages, page_size, hkv, d] bf16 with any strides that are multiples of 8
+ *             elements, the last dimension contiguous
+ *   weight    [num_pages, hkv, page_size] fp32, the attention weight that the entry has
+ *             received (null: not kept)
+ *   position  [num_pages, hkv, page_size] int32, the entry's position in its text (null: not
+ *             kept)
+ *   table     [num_seqs, max_pages] int32 with a row stride, lens [num_seqs] int32
+ * page_size is 16, 32, 64, 128 or 256, d 64 or 128.  Keys are stored as they are scored
+ * (rotated), so the order of a sequence's entries carries no meaning.  Sequences may share
+ * pages that are only read; pages that a call writes (msa_cache_append, msa_cache_evict, the
+ * weights) belong to one sequence.  What the table names behind a sequence's length is not
+ * read.  A page out of range, a length below 0 or beyond max_pages * page_size is recorded as
+ * MSA_ERR_DEVICE_CHECK, nothing out of the cache is touched, and the call's results are undefined.
+ */
+typedef struct msa_cache {
+  uint16_t *k, *v;
+  float* weight;
+  int32_t* position;
+  int32_t num_pages, page_size, hkv, d;
+  int64_t k_page_stride, k_slot_stride, k_head_stride; /* elements, below 2^38 */
+  int64_t v_page_stride, v_slot_stride, v_head_stride;
+} msa_cache;
+
+typedef struct msa_table {
+  const int32_t* pages; /* [num_seqs, max_pages] */
+  const int32_t* lens;  /* [num_seqs] */
+  int32_t num_seqs;     /* below 2^20 */
+  int32_t max_pages;    /* max_pages * page_size below 2^30 */
+  int64_t stride;       /* elements between rows of the table, at least max_pages */
+} msa_table;
+
+/*
+ * New entries for the cache.  Token t of sequence b (cu_seqlens [num_seqs + 1]; null: one token
+ * a sequence, T = num_seqs) becomes entry lens[b] + (its place among the sequence's new
+ * tokens); lens are the lengths before the call and are not written.  Its position is
+ * positions[t], or, with positions null, the entry's number; k is rotated by it as by msa_rotary
+ * and v copied, weight starts at 0.  With hq > 0 the queries q [T, hq, d] are rotated too, to q_out.
+ * rotary->hkv and d are the cache's, dtype is MSA_BF16, inverse 0 and num_docs num_seqs or, without
+ * cu_seqlens, 0; its strides are those of q and k, v_stride that of v.  Tokens behind the last
+ * sequence enter nowhere, their rows of q_out come out zero.
+ */
+msa_status msa_cache_append(const msa_cache* cache, const msa_table* table,
+                            const msa_rotary_params* rotary, int64_t v_stride,
+                            const int32_t* cu_seqlens, const void* positions, const uint16_t* q,
+                            const uint16_t* k, const uint16_t* v, uint16_t* q_out,
+                            msa_stream_t stream);
+
+/*
+ * Attention of one new token of each sequence over its entries (its own among them, if it has been
+ * appended):
+ *   s_j = softmax_scale q . k_j,  j < lens[b],  p = softmax(s),  o = sum_j p_j v_j.
+ * q, o [num_seqs, hq, d] bf16, o contiguous; any hq / hkv from 1 to 64, hq <= 1024.  A sequence
+ * without entries gets o = 0.  With `accumulate` the weights that an entry gets from the hq / hkv
+ * heads of its KV head are added to cache->weight.  A score of -inf takes no weight; a sequence all
+ * of whose scores are -inf gets o = 0.  Sums have a fixed order (the weights too, unless
+ * sequences share pages): results repeat bit for bit.
+ */
+typedef struct msa_paged_params {
+  int32_t hq;
+  int32_t accumulate;  /* 0 or 1 */
+  int64_t q_stride;    /* token stride in elements, a multiple of 8; 0: contiguous */
+  float softmax_scale; /* positive, and finite times log2(e) */
+  uint32_t flags;      /* must be 0 */
+} msa_paged_params;
+
+/* Workspace bytes of msa_paged_attention (0 if an argument is invalid).  With
+   `accumulate` 4 bytes a query head for every entry that the table can name: a view of the
+   table's first columns makes it smaller. */
+size_t msa_paged_attention_workspace_size(const msa_cache* cache, const msa_table* table,
+                                          const msa_paged_params* params);
+msa_status msa_paged_attention(const msa_cache* cache, const msa_table* table,
+                               const msa_paged_params* params, const uint16_t* q, uint16_t* o,
+                               void* workspace, size_t workspace_bytes, msa_stream_t stream);
+
+/*
+ * Cuts every sequence of more than `keep` entries down to `keep`, for each KV head by itself: the
+ * entries whose position is above the newest one's less `recent` stay, and of the others those
+ * with the largest weights (a NaN counts as largest; equal ones: the lower entry).  Entries that
+ * stay and lie behind the first `keep` move, k, v, weight and position, into the places of
+ * entries that leave, both taken in ascending order; nothing else is written.  new_lens [num_seqs]
+ * gets min(lens, keep); it must not overlap the table's lens.  Needs weight, and position with
+ * recent > 0; 0 <= recent <= keep, keep >= 1.
+ */
+size_t msa_cache_evict_workspace_size(const msa_cache* cache, const msa_table* table,
+                                      int32_t keep);
+msa_status msa_cache_evict(const msa_cache* cache, const msa_table* table, int32_t keep,
+                           int32_t recent, int32_t* new_lens, void* workspace,
+                           size_t workspace_bytes, msa_stream_t stream);
+
+/*
  * Synchronises `stream`, returns the device status word of the current device
  * (MSA_OK, MSA_ERR_TIMEOUT or MSA_ERR_DEVICE_CHECK; the first error recorded
  * wins) and resets it to MSA_OK.  Returns MSA_ERR_CUDA if the stream itself
@@ -319,7 +449,7 @@ msa_status msa_get_device_status(msa_stream_t stream);
  * calling host thread.  Bits 0-7 hold the status code.  For MSA_ERR_TIMEOUT,
  * bits 8-11 name the kernel whose wait ran out (1 proxy select, 2 forward,
  * 3 backward, 4 selection argmax, 5 dense forward, 6 dense dQ, 7 dense dK and
- * dV), bits 12-19 the barrier index inside it and bits 20-31 the tile
+ * dV, 8 paged attention), bits 12-19 the barrier index inside it and bits 20-31 the tile
  * (or key block) it was working on, saturated at 4095.
  */
 uint32_t msa_last_status_word(void);

@@ -1,0 +1,231 @@
+"""Rotary positions and the paged cache without a GPU: plans, and what the C entry points refuse
+before any CUDA call."""
+import ctypes
+import math
+import os
+from fractions import Fraction
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def m():
+    import block_sparse_attention_proxy_gb300 as m
+
+    if not os.path.exists(m.LIB_PATH):
+        from block_sparse_attention_proxy_gb300 import build
+
+        build.build()
+    m.load()
+    return m
+
+
+# ------------------------------ plans -------------------------------------------
+
+
+@pytest.mark.parametrize("dims,kw", [(64, {}), (128, dict(base=1e6)), (32, dict(stretch=4.0)),
+                                     (128, dict(stretch=8.0, trained_length=4096)),
+                                     (16, dict(frequencies=[0.0, -1.0, 1e-9, 7.5, 6.25, 1, 2, 3]))])
+def test_plan_frequencies(m, dims, kw):
+    """Whole numbers within half of 2^-64 of a turn of the frequency, and the rule behind it."""
+    plan = m.rotary_plan(dims, **kw)
+    assert plan.dims == dims and len(plan.frequencies) == dims // 2
+    two_pi = Fraction(int("6283185307179586476925286766559005768394338798750"), 10 ** 48)
+    for i, word in enumerate(plan.frequencies):
+        if "frequencies" in kw:
+            f = kw["frequencies"][i]
+        else:
+            f = kw.get("base", 10000.0) ** (-2 * i / dims)
+            s, part = kw.get("stretch", 1.0), 0.0
+            if "trained_length" in kw:
+                part = min(1.0, max(0.0, (4096 * f / (2 * math.pi) - 1) / 31))
+            f *= part + (1 - part) / s
+        off = Fraction(word, 2 ** 64) - Fraction(f) / two_pi
+        off -= round(off)
+        assert abs(off) <= Fraction(1, 2 ** 60) * 2 + abs(Fraction(f)) * Fraction(1, 2 ** 50)
+
+
+def test_plan_stretch_leaves_fast_pairs(m):
+    plain, far = m.rotary_plan(128), m.rotary_plan(128, stretch=16.0, trained_length=2048)
+    assert far.frequencies[0] == plain.frequencies[0]
+    assert abs(far.frequencies[-1] * 16 - plain.frequencies[-1]) <= 16
+    ratio = [a / b for a, b in zip(plain.frequencies, far.frequencies)]
+    assert all(1 - 1e-9 <= x <= 16 + 1e-9 for x in ratio)
+    assert all(a <= b + 1e-9 for a, b in zip(ratio, ratio[1:]))
+
+
+def test_plan_refusals(m):
+    for kw in (dict(dims=8), dict(dims=24), dict(dims=-16), dict(dims=272), dict(dims=16, base=0),
+               dict(dims=16, stretch=0), dict(dims=16, stretch=float("inf")),
+               dict(dims=16, amplitude=float("nan")), dict(dims=16, trained_length=0),
+               dict(dims=16, trained_length=10, low=3, high=3), dict(dims=16, frequencies=[1.0] * 7),
+               dict(dims=16, frequencies=[float("nan")] * 8),
+               dict(dims=16, frequencies=[1.0] * 8, stretch=2.0)):
+        with pytest.raises(ValueError):
+            m.rotary_plan(**kw)
+
+
+def test_cpu_tensors_are_refused(m):
+    q = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        m.rotary(q, None, m.rotary_plan(64), positions=torch.arange(4))
+    cache = m.paged_cache(2, 16, 2, 64, scores=True, device="cpu")
+    table, lens = torch.zeros(4, 1, dtype=torch.int32), torch.ones(4, dtype=torch.int32)
+    for call in (lambda: m.paged_attention(q, cache, table, lens),
+                 lambda: m.cache_append(cache, q, q, table, lens),
+                 lambda: m.cache_evict(cache, table, lens, 1, 0)):
+        with pytest.raises(TypeError):
+            call()
+
+
+# ------------------------------ C entry points ----------------------------------
+
+P = 0x10000  # never read: every call below is refused first
+
+
+def _cache(m, **kw):
+    given = dict(k=P, v=P, weight=P, position=P, num_pages=9, page_size=64, hkv=2, d=64,
+                 k_page_stride=8192, k_slot_stride=128, k_head_stride=64, v_page_stride=8192,
+                 v_slot_stride=128, v_head_stride=64)
+    return m._abi.MsaCache(**{**given, **kw})
+
+
+def _table(m, **kw):
+    return m._abi.MsaTable(**{**dict(pages=P, lens=P, num_seqs=3, max_pages=4, stride=4), **kw})
+
+
+BAD_CACHES = [(1, dict(num_pages=0)), (1, dict(hkv=0)), (2, dict(d=96)), (2, dict(d=256)),
+              (2, dict(page_size=8)), (2, dict(page_size=48)), (2, dict(page_size=512)),
+              (2, dict(page_size=0)), (2, dict(hkv=1025)), (1, dict(k_page_stride=0)),
+              (1, dict(k_slot_stride=-128)), (1, dict(v_head_stride=60)),
+              (1, dict(v_page_stride=1 << 38))]
+BAD_TABLES = [(1, dict(num_seqs=-1)), (1, dict(max_pages=0)), (1, dict(stride=3)),
+              (2, dict(num_seqs=1 << 20)), (2, dict(max_pages=1 << 24, stride=1 << 24))]
+
+
+def _calls(m, cache, table, hq=4, keep=10, recent=2, ws=1 << 30, **ptr):
+    """Status of attention and eviction with everything else in order."""
+    lib, by = m.load(), ctypes.byref
+    p = m.make_paged_params(hq)
+    at = {**dict(q=P, o=P, room=P, new=2 * P), **ptr}
+    return (lib.msa_paged_attention(by(cache), by(table), by(p), at["q"], at["o"], at["room"], ws, None),
+            lib.msa_cache_evict(by(cache), by(table), keep, recent, at["new"], at["room"], ws, None))
+
+
+@pytest.mark.parametrize("status,kw", BAD_CACHES)
+def test_bad_caches(m, status, kw):
+    assert _calls(m, _cache(m, **kw), _table(m)) == (status, status)
+    rp = m.make_rotary_params(3, 4, kw.get("hkv", 2), kw.get("d", 64), [1] * 8)
+    assert m.load().msa_cache_append(ctypes.byref(_cache(m, **kw)), ctypes.byref(_table(m)),
+                                     ctypes.byref(rp), 0, None, None, P, P, P, P, None) == status
+    assert m.msa_paged_attention_workspace_size(_cache(m, **kw), _table(m), m.make_paged_params(4)) == 0
+    assert m.msa_cache_evict_workspace_size(_cache(m, **kw), _table(m), 10) == 0
+
+
+@pytest.mark.parametrize("status,kw", BAD_TABLES)
+def test_bad_tables(m, status, kw):
+    assert _calls(m, _cache(m), _table(m, **kw)) == (status, status)
+
+
+def test_strides_of_single_rows_do_not_matter(m):
+    """Of a dimension of size 1; the calls get as far as their workspace."""
+    cache = _cache(m, num_pages=1, hkv=1, k_page_stride=1, v_head_stride=-3)
+    assert _calls(m, cache, _table(m, num_seqs=1, stride=0), ws=0) == (3, 3)
+
+
+def test_bad_pointers_and_workspaces(m):
+    ok = _cache(m), _table(m)
+    for kw in (dict(k=0), dict(v=P + 8), dict(weight=P + 2)):
+        assert _calls(m, _cache(m, **kw), ok[1]) == (1, 1)
+    for kw in (dict(pages=0), dict(lens=0), dict(lens=P + 1)):
+        assert _calls(m, ok[0], _table(m, **kw)) == (1, 1)
+    for kw in (dict(q=0), dict(q=P + 8), dict(o=0), dict(room=0), dict(room=P + 16)):
+        assert _calls(m, *ok, **kw)[0] == 1
+    for kw in (dict(new=0), dict(new=P), dict(new=P + 8), dict(room=0)):  # new lengths over the old
+        assert _calls(m, *ok, **kw)[1] == 1
+    prm = m.make_paged_params(4)
+    assert _calls(m, *ok, ws=m.msa_paged_attention_workspace_size(*ok, prm) - 1)[0] == 3
+    assert _calls(m, *ok, ws=m.msa_cache_evict_workspace_size(*ok, 10) - 1)[1] == 3
+
+
+def test_bad_numbers(m):
+    ok = _cache(m), _table(m)
+    for hq, status in ((0, 1), (3, 1), (-2, 1), (130, 2), (2048, 2)):
+        assert _calls(m, *ok, hq=hq)[0] == status
+    for keep, recent in ((0, 0), (-1, 0), (5, 6), (5, -1)):
+        assert _calls(m, *ok, keep=keep, recent=recent)[1] == 1
+    assert _calls(m, _cache(m, weight=0), ok[1])[1] == 1
+    assert _calls(m, _cache(m, position=0), ok[1])[1] == 1
+    lib, by = m.load(), ctypes.byref
+    for kw, status in ((dict(softmax_scale=0.0), 1), (dict(softmax_scale=float("inf")), 1),
+                       (dict(softmax_scale=3e38), 1), (dict(flags=1), 1), (dict(q_stride=252), 1),
+                       (dict(q_stride=64), 1)):
+        p = m.make_paged_params(4, **kw)
+        assert lib.msa_paged_attention(by(ok[0]), by(ok[1]), by(p), P, P, P, 1 << 30, None) == status
+    p = m.make_paged_params(4, accumulate=True)
+    assert m.msa_paged_attention_workspace_size(_cache(m, weight=0), ok[1], p) == 0
+    huge = _table(m, num_seqs=(1 << 20) - 1, max_pages=1 << 20, stride=1 << 20)
+    assert m.msa_paged_attention_workspace_size(_cache(m), huge, p) == 0
+    empty = _table(m, num_seqs=0)
+    assert _calls(m, ok[0], empty, ws=0) == (0, 0)
+
+
+def test_workspace_of_the_weights(m):
+    """4 bytes a query head for every entry that the table names, beside the shared rows' parts."""
+    plain = m.msa_paged_attention_workspace_size(_cache(m), _table(m), m.make_paged_params(4))
+    prm = m.make_paged_params(4, accumulate=True)
+    for pages in (2, 4, 64):
+        more = m.msa_paged_attention_workspace_size(_cache(m), _table(m, max_pages=pages, stride=pages),
+                                                    prm) - plain
+        assert 0 <= more - 3 * 4 * pages * 64 * 4 <= 512
+    assert plain < 4 << 20
+
+
+def test_bad_rotations(m):
+    lib, by = m.load(), ctypes.byref
+    base = dict(total_tokens=10, hq=2, hkv=1, d=64, frequencies=[1] * 16)
+
+    def call(cu=None, pos=P, q=P, k=8 * P, qo=32 * P, ko=64 * P, **kw):
+        p = m.make_rotary_params(**{**base, **kw})
+        return lib.msa_rotary(by(p), cu, pos, q, k, qo, ko, None)
+
+    for kw in (dict(pos=None), dict(cu=P, num_docs=1), dict(num_docs=1), dict(cu=P, pos=None),
+               dict(total_tokens=-1), dict(hq=-1), dict(hq=0, hkv=0), dict(interleaved=2),
+               dict(inverse=2), dict(dtype=3), dict(position_bytes=2), dict(flags=1),
+               dict(amplitude=float("inf")), dict(frequencies=[1] * 40), dict(q_stride=100),
+               dict(q_stride=64), dict(k_stride=60), dict(q=0), dict(k=0), dict(qo=0), dict(ko=0),
+               dict(q=P + 8), dict(ko=64 * P + 2), dict(pos=P + 1),
+               dict(pos=P + 4, position_bytes=8), dict(qo=P), dict(ko=P + 32), dict(qo=8 * P),
+               dict(cu=P + 2, pos=None, num_docs=1)):
+        assert call(**kw) == 1, kw
+    for kw in (dict(d=72, frequencies=[1] * 16), dict(d=272), dict(frequencies=[1] * 4),
+               dict(hq=2048), dict(hq=3000), dict(total_tokens=1 << 25), dict(d=0, frequencies=[])):
+        assert call(**kw) == 2, kw
+    assert call(total_tokens=0, q=0, k=0) == 0
+
+
+def test_bad_appends(m):
+    lib, by = m.load(), ctypes.byref
+
+    def call(cu=None, pos=None, q=P, k=8 * P, v=9 * P, qo=32 * P, v_stride=0, **kw):
+        p = m.make_rotary_params(**{**dict(total_tokens=3, hq=4, hkv=2, d=64, frequencies=[1] * 16),
+                                    **kw})
+        return lib.msa_cache_append(by(_cache(m)), by(_table(m)), by(p), v_stride, cu, pos, q, k, v,
+                                    qo, None)
+
+    for kw in (dict(hkv=1), dict(d=128), dict(dtype=1), dict(inverse=True), dict(total_tokens=4),
+               dict(cu=P, num_docs=2), dict(cu=P), dict(num_docs=3), dict(v_stride=100),
+               dict(v_stride=64), dict(k=0), dict(v=0), dict(v=9 * P + 8), dict(q=0), dict(qo=0),
+               dict(qo=8 * P), dict(qo=9 * P), dict(pos=P + 2)):
+        assert call(**kw) == 1, kw
+    assert call(cu=P, num_docs=3, total_tokens=0, q=0, k=0, v=0) == 0
+
+
+def test_struct_layouts(m):
+    """As in the header on both machines: 10 + 1 (padding none) words, pointers and strides of 8 bytes."""
+    a = m._abi
+    assert ctypes.sizeof(a.MsaRotaryParams) == 10 * 4 + 8 + 2 * 8 + 2 * 4
+    assert ctypes.sizeof(a.MsaCache) == 4 * 8 + 4 * 4 + 6 * 8
+    assert ctypes.sizeof(a.MsaTable) == 2 * 8 + 2 * 4 + 8
+    assert ctypes.sizeof(a.MsaPagedParams) == 2 * 4 + 8 + 2 * 4
