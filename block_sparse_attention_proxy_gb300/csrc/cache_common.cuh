@@ -76,6 +76,8 @@ constexpr int kPagedMaxGrid = 320;  // CTAs: bounds the workspace on every devic
 struct PagedArgs {
   CacheArgs cache;
   int hq, G, grid;
+  int side, groups;  // CTAs of a team, each on a KV head of its own; groups of so many KV heads
+  bool whole;        // rows are not shared between CTAs
   float scale_log2;
   uint16_t* o;
   float* parts;        // [CTA][2][G][d] sums of rows that CTAs share
@@ -83,7 +85,7 @@ struct PagedArgs {
   float2* stats;       // [nseq][hq] reference and 1 / normaliser of whole rows (with scores)
   float* scores;       // [tile][G][128] in log2 units; null: no weights asked for
 };
-int paged_grid(const CacheArgs& c, int G);
+void paged_shape(PagedArgs* a);
 cudaError_t launch_paged(const PagedArgs& a, const uint16_t* q, long long q_stride,
                          cudaStream_t st);
 
@@ -93,7 +95,7 @@ struct EvictArgs {
   int keep, recent;
   int32_t* new_lens;
   int32_t* count;  // [nseq][hkv] entries that move
-  int32_t* pairs;  // [nseq][hkv][2][most] where from, where to
+  long long* pairs;  // [nseq][hkv][2][most] places in the cache: from, to
   int most;        // pairs of a row at most
 };
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st, int* launches);

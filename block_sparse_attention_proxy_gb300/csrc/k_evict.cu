@@ -14,12 +14,17 @@
 #include "cache_common.cuh"
 #include "dense_common.cuh"
 
+#include <algorithm>
+
 namespace msa {
 namespace {
 
-constexpr int kMostKeys = 49152;  // of a row in shared memory
-constexpr int kMostFused = 256;   // moves that the listing block makes itself
-constexpr int kMoveThreads = 256;
+constexpr int kListThreads = 512;
+constexpr int kMostBlocks = 8;    // of a cluster: one row
+constexpr int kMostKeys = 24576;  // entries of a block whose ranks and positions it keeps
+constexpr int kMostFused = 256;   // moves that the listing blocks make themselves
+constexpr int kFew = 8;           // entries that leave and are looked for one by one
+constexpr int kAtOnce = 8;        // rows that a warp has on their way, of the second kernel
 constexpr uint32_t kRecent = 0xFFFFFFFFu, kNaN = 0xFFFFFFFEu;
 
 // Order of weights as whole numbers; zeros of both signs are equal.
@@ -29,63 +34,45 @@ __device__ __forceinline__ uint32_t rank_of(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Moves entry `from` of a row to `to`: LP lanes, 16 bytes of k or v each.
-struct Move {
-  const uint4* src;
-  uint4* dst;
-  long long from, to;  // places in weight and position
-  bool ok;
-};
-__device__ __forceinline__ Move move_of(const CacheArgs& c, int b, int h, int from, int to,
-                                        int lane) {
-  Move m;
-  const int p0 = cache_page(c, b, from), p1 = cache_page(c, b, to);
-  const int mask = (1 << c.page_shift) - 1, half = c.d / 8;
-  m.ok = p0 >= 0 && p1 >= 0;
-  const int x = lane < half ? lane : lane - half;
-  const uint16_t *s, *d;
-  if (lane < half) {
-    s = c.k_row(p0, from & mask, h);
-    d = c.k_row(p1, to & mask, h);
-  } else {
-    s = c.v_row(p0, from & mask, h);
-    d = c.v_row(p1, to & mask, h);
+// Moves between entries of a row, given by their places in the cache (page * page size + slot; -1:
+// none): d / 4 lanes of a warp have 16 bytes of k or of v each, and a warp has kAtOnce moves of each
+// such group on their way.  They are moves i0 and up of the row's n.
+template <int kAtOnce>
+__device__ __forceinline__ void move_warp(const CacheArgs& c, int h, const long long* from,
+                                          const long long* to, int i0, int n) {
+  const int lane = threadIdx.x & 31, lp = c.d / 4, group = lane / lp, groups = 32 / lp;
+  const int x = lane % lp, half = lp / 2, mask = (1 << c.page_shift) - 1;
+  // lane l has the places of move i0 + l
+  const int mine = i0 + lane;
+  const bool there = lane < kAtOnce * groups && mine < n;
+  const long long f = there ? from[mine] : -1, t = there ? to[mine] : -1;
+  uint16_t* base = (x < half ? c.k : c.v) + 8 * (x < half ? x : x - half);
+  const long long ps = x < half ? c.kp : c.vp, ss = x < half ? c.ks : c.vs,
+                  at = h * (x < half ? c.kh : c.vh);
+  uint4 row[kAtOnce];
+  float w = 0.f;
+  int p = 0;
+  if (f >= 0 && t >= 0) {
+    w = __ldcg(c.weight + c.meta((int)(f >> c.page_shift), (int)f & mask, h));
+    if (c.position) p = __ldcg(c.position + c.meta((int)(f >> c.page_shift), (int)f & mask, h));
   }
-  m.src = reinterpret_cast<const uint4*>(s) + x;
-  m.dst = reinterpret_cast<uint4*>(const_cast<uint16_t*>(d)) + x;
-  m.from = c.meta(p0, from & mask, h);
-  m.to = c.meta(p1, to & mask, h);
-  return m;
-}
-
-// Pairs i0, i0 + step, ... below n of a row, by the LP lanes of a group; N in flight.
-template <int N>
-__device__ __forceinline__ void move_pairs(const CacheArgs& c, int b, int h, const int* from,
-                                           const int* to, int i0, int step, int n, int lane) {
-  for (int i = i0; i < n; i += N * step) {
-    Move m[N];
-    uint4 v[N];
-    float w[N];
-    int p[N];
+  long long dst[kAtOnce];
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      m[j].ok = false;
-      if (i + j * step < n) m[j] = move_of(c, b, h, from[i + j * step], to[i + j * step], lane);
-    }
+  for (int j = 0; j < kAtOnce; ++j) {
+    const long long fj = __shfl_sync(0xffffffffu, f, j * groups + group);
+    const long long tj = __shfl_sync(0xffffffffu, t, j * groups + group);
+    dst[j] = fj < 0 || tj < 0 ? -1 : (tj >> c.page_shift) * ps + (tj & mask) * ss + at;
+    if (dst[j] >= 0)
+      row[j] = __ldcg(reinterpret_cast<const uint4*>(base + (fj >> c.page_shift) * ps +
+                                                     (fj & mask) * ss + at));
+  }
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (m[j].ok) {
-        v[j] = *m[j].src;
-        if (lane == 0) w[j] = c.weight[m[j].from];
-        if (lane == 1 && c.position) p[j] = c.position[m[j].from];
-      }
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (m[j].ok) {
-        *m[j].dst = v[j];
-        if (lane == 0) c.weight[m[j].to] = w[j];
-        if (lane == 1 && c.position) c.position[m[j].to] = p[j];
-      }
+  for (int j = 0; j < kAtOnce; ++j)
+    if (dst[j] >= 0) *reinterpret_cast<uint4*>(base + dst[j]) = row[j];
+  if (f >= 0 && t >= 0) {
+    const long long m = c.meta((int)(t >> c.page_shift), (int)t & mask, h);
+    c.weight[m] = w;
+    if (c.position) c.position[m] = p;
   }
 }
 
@@ -105,69 +92,207 @@ __device__ __forceinline__ int warp_base(int x, int* sm, int* total) {
   return __shfl_sync(0xffffffffu, incl - y, warp);
 }
 
+// A word of another block's shared memory (of the cluster).
+__device__ __forceinline__ uint32_t ld_peer(const void* p, uint32_t rank) {
+  uint32_t at, x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+  return x;
+}
+
+// One cluster per row, each of its blocks with a run of `slice` entries.
 template <bool KEYS, bool FUSED>
-__global__ void __launch_bounds__(1024) k_evict_list(const __grid_constant__ EvictArgs a) {
-  extern __shared__ uint32_t s_key[];
-  __shared__ int s_hist[256], s_sum[32], s_pick[2];
-  __shared__ int s_from[FUSED ? kMostFused : 1], s_to[FUSED ? kMostFused : 1];
+__global__ void __launch_bounds__(kListThreads, 2)
+    k_evict_list(const __grid_constant__ EvictArgs a, int blocks, int slice) {
+  extern __shared__ __align__(16) uint32_t s_key[];  // slice ranks, slice positions
+  __shared__ int s_hist[4][256], s_all[256], s_sum[32], s_pick[3], s_share[4];
+  int* s_pos = reinterpret_cast<int*>(s_key + (KEYS ? slice : 0));
   const CacheArgs& c = a.cache;
-  const int b = blockIdx.x / c.hkv, h = blockIdx.x - b * c.hkv;
+  const int row = blockIdx.x / blocks, rank = blockIdx.x - row * blocks;
+  const int b = row / c.hkv, h = row - b * c.hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int n = cache_len(c, b);
-  if (h == 0 && tid == 0) a.new_lens[b] = min(n, a.keep);
+  if (h == 0 && rank == 0 && tid == 0) a.new_lens[b] = min(n, a.keep);
   if (n <= a.keep) {
-    if (!FUSED && tid == 0) a.count[blockIdx.x] = 0;
-    return;
+    if (!FUSED && rank == 0 && tid == 0) a.count[row] = 0;
+    return;  // all blocks of the cluster
   }
   const int mask = (1 << c.page_shift) - 1;
+  const int begin = min(rank * slice, n), end = min(begin + slice, n);  // entries of this block
   auto place = [&](int i) -> long long {
     const int page = cache_page(c, b, i);
     return page < 0 ? -1 : c.meta(page, i & mask, h);
   };
+  auto sync = [&] {
+    __syncwarp();
+    if (blocks > 1) cluster_sync(); else __syncthreads();
+  };
+  // Sum of word `p` of all blocks' shared memory, and that of the blocks before this one.
+  auto gather = [&](const int* p, int* before) {
+    int x[kMostBlocks], all = 0;
+    *before = 0;
+#pragma unroll
+    for (int r = 0; r < kMostBlocks; ++r) {  // all on their way at once
+      x[r] = 0;
+      if (r < blocks) x[r] = blocks > 1 ? (int)ld_peer(p, r) : *p;
+    }
+#pragma unroll
+    for (int r = 0; r < kMostBlocks; ++r) {
+      if (r < rank) *before += x[r];
+      all += x[r];
+    }
+    return all;
+  };
 
+  for (int i = tid; i < 4 * 256; i += threads) (&s_hist[0][0])[i] = 0;
+  // Weights and positions, four entries at a time: pages begin at multiples of 16.
+  int newest = INT_MIN;
+#pragma unroll 4
+  for (int i = begin + 4 * tid; i < end; i += 4 * threads) {
+    const long long m = place(i);
+    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+    int4 p = make_int4(INT_MIN, INT_MIN, INT_MIN, INT_MIN);
+    if (m >= 0) {
+      if (KEYS) w = __ldcg(reinterpret_cast<const float4*>(c.weight + m));
+      if (a.recent > 0) p = __ldcg(reinterpret_cast<const int4*>(c.position + m));
+    }
+    const int k = end - i;
+    newest = max(newest, p.x);
+    if (k > 1) newest = max(newest, p.y);
+    if (k > 2) newest = max(newest, p.z);
+    if (k > 3) newest = max(newest, p.w);
+    if (KEYS) {
+      // a page that the table does not name ranks lowest
+      const uint4 x = m < 0 ? make_uint4(0, 0, 0, 0)
+                            : make_uint4(rank_of(w.x), rank_of(w.y), rank_of(w.z), rank_of(w.w));
+      *reinterpret_cast<uint4*>(s_key + i - begin) = x;
+      *reinterpret_cast<int4*>(s_pos + i - begin) = p;
+    }
+  }
   long long limit = LLONG_MAX;  // positions from here on stay
   if (a.recent > 0) {
-    int newest = INT_MIN;
-#pragma unroll 4
-    for (int i = tid; i < n; i += threads) {
-      const long long m = place(i);
-      if (m >= 0) newest = max(newest, c.position[m]);
-    }
     newest = __reduce_max_sync(0xffffffffu, newest);
     if (lane == 0) s_sum[warp] = newest;
     __syncthreads();
     newest = __reduce_max_sync(0xffffffffu, lane < threads / 32 ? s_sum[lane] : INT_MIN);
+    if (blocks > 1) {
+      if (tid == 0) s_share[0] = newest;
+      sync();
+      for (int r = 0; r < blocks; ++r) newest = max(newest, (int)ld_peer(&s_share[0], r));
+    }
     limit = (long long)newest - a.recent + 1;
+  } else {
+    __syncthreads();
   }
-  auto load = [&](int i) -> uint32_t {
+  auto key = [&](int i) -> uint32_t {
+    if (KEYS) return s_key[i - begin];
     const long long m = place(i);
     if (m < 0) return 0;
-    if (a.recent > 0 && c.position[m] >= limit) return kRecent;
-    return rank_of(c.weight[m]);
+    if (a.recent > 0 && __ldcg(c.position + m) >= limit) return kRecent;
+    return rank_of(__ldcg(c.weight + m));
   };
-  if (KEYS) {
-#pragma unroll 4
-    for (int i = tid; i < n; i += threads) s_key[i] = load(i);
-  }
-  auto key = [&](int i) -> uint32_t { return KEYS ? s_key[i] : load(i); };
-
-  // the keep-th largest number `edge`, and how many of those equal to it stay
-  uint32_t edge = 0;
-  int left = a.keep;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) s_hist[tid] = 0;
+  if (KEYS && a.recent > 0) {  // each thread its own entries
+    for (int i = 4 * tid; i < end - begin; i += 4 * threads) {
+      const int4 p = *reinterpret_cast<const int4*>(s_pos + i);
+      if (p.x >= limit) s_key[i] = kRecent;
+      if (p.y >= limit) s_key[i + 1] = kRecent;
+      if (p.z >= limit) s_key[i + 2] = kRecent;
+      if (p.w >= limit) s_key[i + 3] = kRecent;
+    }
     __syncthreads();
-    const uint32_t done = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-    for (int i = tid; i < n; i += threads) {
+  }
+
+  long long* from = a.pairs + (size_t)row * 2 * a.most;
+  long long* to = from + a.most;
+  auto entry = [&](int i) -> long long {  // its place in the cache
+    const int page = cache_page(c, b, i);
+    return page < 0 ? -1 : ((long long)page << c.page_shift) + (i & mask);
+  };
+
+  // A cache a step or a few over its budget: those that leave are found one after the other, by
+  // (rank, the last entry first) as one number.
+  if (KEYS && n - a.keep <= kFew) {
+    __shared__ uint32_t s_min[2][32][2], s_best[kFew][2];
+    __shared__ int s_gone[kFew];
+    __shared__ long long s_from[kFew], s_to[kFew];
+    const int leave = n - a.keep, warps = threads / 32;
+    uint64_t mine;
+    auto look = [&](uint64_t behind) {  // the least of this thread's behind that one
+      mine = ~0ull;
+#pragma unroll 4
+      for (int i = begin + tid; i < end; i += threads) {
+        const uint64_t o = (uint64_t)s_key[i - begin] << 32 | (uint32_t)~i;
+        if (o >= behind && o < mine) mine = o;
+      }
+    };
+    auto least = [](uint64_t x) {  // of the warp
+      const uint32_t hi = __reduce_min_sync(0xffffffffu, (uint32_t)(x >> 32));
+      const uint32_t lo =
+          __reduce_min_sync(0xffffffffu, (uint32_t)(x >> 32) == hi ? (uint32_t)x : 0xFFFFFFFFu);
+      return (uint64_t)hi << 32 | lo;
+    };
+    look(0);
+    for (int j = 0; j < leave; ++j) {
+      uint64_t best = least(mine);
+      if (lane == 0) s_min[j & 1][warp][0] = (uint32_t)(best >> 32), s_min[j & 1][warp][1] = (uint32_t)best;
+      __syncthreads();
+      best = lane < warps ? (uint64_t)s_min[j & 1][lane][0] << 32 | s_min[j & 1][lane][1] : ~0ull;
+      best = least(best);
+      if (blocks > 1) {
+        if (tid == 0) s_best[j][0] = (uint32_t)(best >> 32), s_best[j][1] = (uint32_t)best;
+        sync();
+        best = lane < blocks ? (uint64_t)ld_peer(&s_best[j][0], lane) << 32 | ld_peer(&s_best[j][1], lane)
+                             : ~0ull;
+        best = least(best);
+      }
+      if (tid == 0) s_gone[j] = (int)~(uint32_t)best;
+      if (mine == best) look(best + 1);
+    }
+    if (rank == 0 && warp == 0) {
+      __syncwarp();
+      const int gone = lane < leave ? s_gone[lane] : INT_MAX, i = a.keep + lane;
+      bool stays = lane < leave;
+      int before = 0;
+      for (int j = 0; j < leave; ++j) {
+        stays &= s_gone[j] != i;
+        before += s_gone[j] < gone;
+      }
+      const uint32_t vo = __ballot_sync(0xffffffffu, stays);
+      const int moves = __popc(vo);
+      if (stays) (FUSED ? s_from : from)[__popc(vo & ((1u << lane) - 1))] = entry(i);
+      if (gone < a.keep) (FUSED ? s_to : to)[before] = entry(gone);
+      __syncwarp();
+      if (FUSED)
+        for (int k = 0; k < moves; k += 2 * (128 / c.d)) move_warp<2>(c, h, s_from, s_to, k, moves);
+      else if (lane == 0)
+        a.count[row] = moves;
+    }
+    sync();  // nobody reads a block's shared memory any more
+    return;
+  }
+
+  // the keep-th largest rank `edge`, and how many of those equal to it stay
+  uint32_t edge = 0;
+  int left = a.keep, equal = 0;
+  for (int d = 0; d < 4; ++d) {
+    const int shift = 24 - 8 * d;
+    const uint32_t done = d == 0 ? 0u : 0xFFFFFFFFu << (shift + 8);
+#pragma unroll 4
+    for (int i = begin + tid; i < end; i += threads) {
       const uint32_t x = key(i);
-      if ((x & done) == edge) atomicAdd(&s_hist[(x >> shift) & 255], 1);
+      if ((x & done) == edge) atomicAdd(&s_hist[d][(x >> shift) & 255], 1);
+    }
+    sync();
+    for (int i = tid; i < 256; i += threads) {
+      int before;
+      s_all[i] = gather(&s_hist[d][i], &before);
     }
     __syncthreads();
     if (warp == 0) {  // from the top: the first digit at which `left` are reached
       int x[8], mine = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) mine += x[i] = s_hist[255 - 8 * lane - i];
+      for (int i = 0; i < 8; ++i) mine += x[i] = s_all[255 - 8 * lane - i];
       int incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -181,6 +306,7 @@ __global__ void __launch_bounds__(1024) k_evict_list(const __grid_constant__ Evi
           if (before < left && left <= before + x[i]) {
             s_pick[0] = 255 - 8 * lane - i;
             s_pick[1] = left - before;
+            s_pick[2] = x[i];
           }
           before += x[i];
         }
@@ -189,17 +315,29 @@ __global__ void __launch_bounds__(1024) k_evict_list(const __grid_constant__ Evi
     __syncthreads();
     edge |= (uint32_t)s_pick[0] << shift;
     left = s_pick[1];
+    equal = s_pick[2];
+    if (equal == left) break;  // the lower digits decide nothing
   }
 
   // Each warp has a run of entries and votes on 32 at a time.
-  const int per = ((n + 31) / 32 + threads / 32 - 1) / (threads / 32) * 32;
-  const int first = min(warp * per, n), last = min(first + per, n);
+  const int per = ((end - begin + 31) / 32 + threads / 32 - 1) / (threads / 32) * 32;
+  const int first = min(begin + warp * per, end), last = min(first + per, end);
   const uint32_t below = (1u << lane) - 1;
-  int ties = 0;
-  for (int i = first; i < last; i += 32)
-    ties += __popc(__ballot_sync(0xffffffffu, i + lane < last && key(i + lane) == edge));
-  int total;
-  const int tie0 = warp_base(ties, s_sum, &total);
+  int tie0 = 0, total, before;
+  if (equal > left) {  // not all of them stay: those of the lowest entries
+    int ties = 0;
+    for (int i = first; i < last; i += 32)
+      ties += __popc(__ballot_sync(0xffffffffu, i + lane < last && key(i + lane) == edge));
+    tie0 = warp_base(ties, s_sum, &total);
+    if (blocks > 1) {
+      if (tid == 0) s_share[1] = total;
+      sync();
+      gather(&s_share[1], &before);
+      tie0 += before;
+    }
+  } else {
+    left = INT_MAX;
+  }
   auto walk = [&](auto each) {  // each(entry, in range, stays)
     int tie = tie0;
     for (int i = first; i < last; i += 32) {
@@ -216,45 +354,59 @@ __global__ void __launch_bounds__(1024) k_evict_list(const __grid_constant__ Evi
     outs += __popc(__ballot_sync(0xffffffffu, in && stays && i >= a.keep));
     ins += __popc(__ballot_sync(0xffffffffu, in && !stays && i < a.keep));
   });
-  int out = warp_base(outs, s_sum, &total), into = warp_base(ins, s_sum, &total);
-  int* from = FUSED ? s_from : a.pairs + (size_t)blockIdx.x * 2 * a.most;
-  int* to = FUSED ? s_to : from + a.most;
+  int all_in, into = warp_base(ins, s_sum, &all_in), out = warp_base(outs, s_sum, &total);
+  if (blocks > 1) {
+    if (tid == 0) s_share[2] = total, s_share[3] = all_in;
+    sync();
+    total = gather(&s_share[2], &before);
+    out += before;
+    gather(&s_share[3], &before);
+    into += before;
+  }
   walk([&](int i, bool in, bool stays) {
     const bool o = in && stays && i >= a.keep, t = in && !stays && i < a.keep;
     const uint32_t vo = __ballot_sync(0xffffffffu, o), vt = __ballot_sync(0xffffffffu, t);
-    if (o) from[out + __popc(vo & below)] = i;
-    if (t) to[into + __popc(vt & below)] = i;
+    if (o) from[out + __popc(vo & below)] = entry(i);
+    if (t) to[into + __popc(vt & below)] = entry(i);
     out += __popc(vo);
     into += __popc(vt);
   });
+  if (!FUSED && rank == 0 && tid == 0) a.count[row] = total;
+  sync();  // the lists are whole; nobody reads a block's shared memory any more
   if (FUSED) {
-    __syncthreads();
-    const int lp = c.d / 4;  // lanes of a move
-    move_pairs<4>(c, b, h, s_from, s_to, tid / lp, threads / lp, total, tid % lp);
-  } else if (tid == 0) {
-    a.count[blockIdx.x] = total;
+    const int step = 2 * (128 / c.d), warps = threads / 32;
+    for (int i = (rank * warps + warp) * step; i < total; i += blocks * warps * step)
+      move_warp<2>(c, h, from, to, i, total);
   }
 }
 
-constexpr int kPairsPerBlock = 64;
-__global__ void __launch_bounds__(kMoveThreads)
-    k_evict_move(const __grid_constant__ EvictArgs a, int chunks) {
-  const CacheArgs& c = a.cache;
+// One warp a block, so that a block's registers are free as soon as its moves are done.
+__global__ void __launch_bounds__(32) k_evict_move(const __grid_constant__ EvictArgs a, int chunks) {
   const int row = blockIdx.x / chunks, chunk = blockIdx.x - row * chunks;
-  const int b = row / c.hkv, h = row - b * c.hkv, lp = c.d / 4;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int n = min(__ldcg(a.count + row), (chunk + 1) * kPairsPerBlock);
-  const int* from = a.pairs + (size_t)row * 2 * a.most;
-  move_pairs<4>(c, b, h, from, from + a.most, chunk * kPairsPerBlock + threadIdx.x / lp,
-                kMoveThreads / lp, n, threadIdx.x % lp);
+  const int n = __ldcg(a.count + row), i0 = chunk * kAtOnce * (128 / a.cache.d);
+  if (i0 >= n) return;
+  const long long* from = a.pairs + (size_t)row * 2 * a.most;
+  move_warp<kAtOnce>(a.cache, row % a.cache.hkv, from, from + a.most, i0, n);
 }
 
 template <bool KEYS, bool FUSED>
-cudaError_t list(const EvictArgs& a, int rows, int threads, int smem, cudaStream_t st) {
-  const cudaError_t e = dense_prepare<k_evict_list<KEYS, FUSED>>(0, 0, KEYS ? kMostKeys * 4 : 0);
+cudaError_t list(const EvictArgs& a, int rows, int blocks, int slice, int threads,
+                 cudaStream_t st) {
+  const cudaError_t e = dense_prepare<k_evict_list<KEYS, FUSED>>(0, 0, KEYS ? kMostKeys * 8 : 0);
   if (e != cudaSuccess) return e;
-  k_evict_list<KEYS, FUSED><<<rows, threads, smem, st>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * blocks));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = KEYS ? slice * 8 : 0;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = blocks;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_evict_list<KEYS, FUSED>, a, blocks, slice);
 }
 
 }  // namespace
@@ -262,19 +414,26 @@ cudaError_t list(const EvictArgs& a, int rows, int threads, int smem, cudaStream
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st, int* launches) {
   const CacheArgs& c = a.cache;
   const int rows = c.nseq * c.hkv;
-  const bool keys = c.capacity <= kMostKeys, fused = a.most <= kMostFused;
-  const int threads = c.capacity <= 8192 ? 256 : 1024, smem = keys ? c.capacity * 4 : 0;
-  const cudaError_t e =
-      keys ? (fused ? list<true, true>(a, rows, threads, smem, st)
-                    : list<true, false>(a, rows, threads, smem, st))
-           : (fused ? list<false, true>(a, rows, threads, smem, st)
-                    : list<false, false>(a, rows, threads, smem, st));
+  // Several blocks to a row where the rows alone leave SMs idle (and where a row's ranks do not
+  // fit one block), each with a few thousand entries at least.
+  int blocks = 1;
+  while (blocks < kMostBlocks &&
+         ((long long)rows * blocks * 2 <= 2 * sm_count() ? c.capacity / (2 * blocks) >= 2048
+                                                         : c.capacity > blocks * kMostKeys))
+    blocks *= 2;
+  const int slice = (int)((((long long)c.capacity + blocks - 1) / blocks + 31) / 32 * 32);
+  const bool keys = slice <= kMostKeys, fused = a.most <= kMostFused;
+  const int threads = std::min(std::max((slice / 16 + 31) / 32 * 32, 128), kListThreads);
+  const cudaError_t e = keys ? (fused ? list<true, true>(a, rows, blocks, slice, threads, st)
+                                      : list<true, false>(a, rows, blocks, slice, threads, st))
+                             : (fused ? list<false, true>(a, rows, blocks, slice, threads, st)
+                                      : list<false, false>(a, rows, blocks, slice, threads, st));
   *launches = fused ? 1 : 2;
   if (e != cudaSuccess || fused) return e;
-  const int chunks = (a.most + kPairsPerBlock - 1) / kPairsPerBlock;
+  const int step = kAtOnce * (128 / c.d), chunks = (a.most + step - 1) / step;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * chunks));
-  cfg.blockDim = dim3(kMoveThreads);
+  cfg.blockDim = dim3(32);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -10,11 +10,16 @@
 // warpgroup owns one entry's G scores, later one row of O^T.
 //
 // The work is cut evenly: the tiles of 128 entries of all (sequence, KV head) rows are counted
-// through, and CTA c takes tiles [W c / C, W (c + 1) / C) of the W, whatever rows they fall in.  A
-// row inside one CTA's range is finished there; of the others each CTA leaves a partial result
-// (fp32 sums, maximum, normaliser; at most two a CTA), which k_paged_join adds up in a fixed order.
-// No prefix sum is stored and nothing is read back: every CTA adds up the tiles of all sequences
-// by itself.
+// through, and each CTA takes as many of them, whatever rows they fall in.  A row inside one CTA's
+// range is finished there; of the others each CTA leaves a partial result (fp32 sums, maximum,
+// normaliser; at most two a CTA), which k_paged_join adds up in a fixed order.  No prefix sum is
+// stored and nothing is read back: every CTA adds up the tiles of all sequences by itself.  Where
+// no row can have more than kWholeTiles tiles they stay whole, and no join is needed.
+//
+// Neighbouring KV heads of one entry lie side by side in the cache.  The CTAs of a team (`side` of
+// them, the largest divisor of the KV heads up to 8) have the same range of tiles, each for its
+// own head, so that neighbours in memory are read at about the same time: 64 sequences of 4096
+// entries, 8 heads of d = 64: 103 us alone, 92 in twos, 91 in fours, 88 in eights; d = 128: 170 -> 165.
 //
 // The reference m of a head's exponentials moves only when a score exceeds it by more than 8
 // (a factor of 256): one vote over the warpgroup a tile, and O is rescaled in TMEM in the
@@ -30,6 +35,7 @@ namespace {
 
 constexpr int kThreads = 192;  // softmax warps 0-3, loads 4, products 5
 constexpr int kJoinThreads = 256;
+constexpr int kWholeTiles = 4, kMostSide = 8;
 constexpr float kRaise = 8.f;
 constexpr float kLowest = -FLT_MAX;  // reference of a row that has no score above it yet
 
@@ -51,68 +57,98 @@ struct PagedCfg {
   static_assert(kRing >= 3 && 400 + 32 * GC <= kMisc && kCols * kCtas <= 512, "budgets");
 };
 
-// Tiles of all rows, and where tile x lies.
+// How the tiles of all rows are shared out.  Team c of the n that get any takes the tiles from
+// cut(c) on: per or per + 1 of them.
+struct PagedCuts {
+  long long total, per;
+  int more, n;  // teams with per + 1 tiles; teams with tiles
+  __host__ __device__ PagedCuts(long long tiles, int teams) : total(tiles) {
+    n = tiles < teams ? (int)tiles : teams;
+    per = n > 0 ? tiles / n : 0;
+    more = n > 0 ? (int)(tiles - per * n) : 0;
+  }
+  __host__ __device__ long long cut(int c) const {
+    return c >= n ? total : per * c + (c < more ? c : more);
+  }
+  // The team that has tile x.
+  __host__ __device__ int team_of(long long x) const {
+    const long long big = (per + 1) * more;
+    return (int)(x < big ? x / (per + 1) : more + (x - big) / per);
+  }
+};
+
+// A team's tiles [x0, x1): x0 is tile `off` of sequence b, counted over its groups of KV heads.
 struct PagedSpan {
-  long long total;  // W
-  long long x0, x1; // this CTA's tiles
-  int b, off;       // sequence of tile x0, tiles of it before x0 (over its KV heads)
+  long long x0, x1;
+  int b, off;
 };
 __device__ __forceinline__ int tiles_of(const CacheArgs& c, int b) {
   return (cache_len(c, b) + 127) >> 7;
 }
-__device__ __forceinline__ long long cut(const PagedArgs& a, long long total, int c) {
-  return total * c / a.grid;
-}
 
-// Counts the tiles of all sequences (every thread of the block, n of them) and looks tile
-// [W c / C] up.  `sm`: n / 32 + 1 numbers of 8 bytes and 2 of 4 behind them.
-__device__ PagedSpan paged_span(const PagedArgs& a, int c, long long* sm, int n) {
+// Counts the tiles of all sequences (every thread of the block, n of them) and looks up the tiles
+// of team c.  With `whole` its range begins and ends with rows: at the first row that begins
+// at or behind the cut.  `sm`: n / 32 + 2 numbers.
+__device__ PagedCuts paged_span(const PagedArgs& a, int c, long long* sm, int n, PagedSpan* span) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = n / 32;
+  int *s_b = reinterpret_cast<int*>(sm + nw), *s_off = s_b + 2;
   const int per = (a.cache.nseq + n - 1) / n, first = min(tid * per, a.cache.nseq),
             last = min(first + per, a.cache.nseq);
   long long mine = 0;
   for (int b = first; b < last; ++b) mine += tiles_of(a.cache, b);
-  mine *= a.cache.hkv;
+  mine *= a.groups;
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
-  int* at = reinterpret_cast<int*>(sm + nw + 1);
   if (lane == 31) sm[warp] = incl;
-  if (tid == 0) at[0] = a.cache.nseq, at[1] = 0;
+  if (tid < 2) s_b[tid] = a.cache.nseq, s_off[tid] = 0;
   __syncthreads();
-  PagedSpan s;
-  s.total = 0;
-  long long before = incl - mine;
+  long long before = incl - mine, total = 0;
   for (int w = 0; w < nw; ++w) {
     if (w < warp) before += sm[w];
-    s.total += sm[w];
+    total += sm[w];
   }
-  s.x0 = cut(a, s.total, c);
-  s.x1 = cut(a, s.total, c + 1);
-  if (mine > 0 && s.x0 >= before && s.x0 < before + mine) {
-    long long left = s.x0 - before;
-    int b = first;
-    for (; b < last - 1; ++b) {
-      const long long t = (long long)tiles_of(a.cache, b) * a.cache.hkv;
-      if (left < t) break;
-      left -= t;
+  const PagedCuts cuts(total, a.grid / a.side);
+  long long x[2] = {cuts.cut(c), cuts.cut(c + 1)};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (i == 1 && !a.whole) break;
+    if (mine > 0 && x[i] >= before && x[i] < before + mine) {
+      long long left = x[i] - before;
+      int b = first;
+      for (; b < last - 1; ++b) {
+        const long long t = (long long)tiles_of(a.cache, b) * a.groups;
+        if (left < t) break;
+        left -= t;
+      }
+      s_b[i] = b;
+      s_off[i] = (int)left;
     }
-    at[0] = b;
-    at[1] = (int)left;
   }
   __syncthreads();
-  s.b = at[0];
-  s.off = at[1];
-  __syncthreads();
-  return s;
+  span->b = s_b[0];
+  span->off = s_off[0];
+  if (a.whole) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (s_b[i] >= a.cache.nseq) continue;
+      const int tiles = tiles_of(a.cache, s_b[i]), t = s_off[i] % tiles;
+      if (t == 0) continue;
+      x[i] += tiles - t;
+      if (i == 0) span->off += tiles - t;
+    }
+  }
+  span->x0 = x[0];
+  span->x1 = x[1];
+  return cuts;
 }
 
-// The rows (sequence, KV head) that a range of tiles runs through.
+// The rows (sequence, KV head) that a CTA's range of tiles runs through.
 struct PagedWalk {
-  int b, h, t;      // next tile
+  int b, h, t;      // next tile; h: group of KV heads
   long long left;   // tiles of the range that are left
   int len, tiles;   // of sequence b
   int t1;           // end of the current part of the row: tiles [t0, t1)
@@ -140,14 +176,14 @@ struct PagedWalk {
   }
   // The next part; false at the end.  len and tiles are its sequence's.
   __device__ __forceinline__ bool next(const PagedArgs& a) {
-    if (t == 0 && h == a.cache.hkv) {
+    if (t == 0 && h == a.groups) {
       h = 0;
       ++b;
       if (left > 0) seek(a);
     }
     if (left <= 0) return false;
     sb = b;
-    sh = h;
+    sh = h * a.side + blockIdx.x % a.side;
     t0 = t;
     t1 = (int)min((long long)tiles, t + left);
     left -= t1 - t0;
@@ -331,12 +367,8 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, GC>::kCtas)
     tmem_relinquish();
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // sequences without an entry: no tile names them
-  for (int b = blockIdx.x; b < a.cache.nseq; b += gridDim.x)
-    if (cache_len(a.cache, b) == 0)
-      for (int i = threadIdx.x; i < a.hq * D / 8; i += kThreads)
-        reinterpret_cast<uint4*>(a.o + (size_t)b * a.hq * D)[i] = make_uint4(0, 0, 0, 0);
-  const PagedSpan span = paged_span(a, blockIdx.x, scan, kThreads);
+  PagedSpan span;
+  paged_span(a, blockIdx.x / a.side, scan, kThreads, &span);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -384,6 +416,11 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, GC>::kCtas)
       }
     }
     if (ok && last.b >= 0) load(&tm_v, last.b, last.h, last.len, last.t);
+    // sequences without an entry: no tile names them
+    for (int b = blockIdx.x; b < a.cache.nseq; b += gridDim.x)
+      if (cache_len(a.cache, b) == 0)
+        for (int i = lane; i < a.hq * D / 8; i += 32)
+          reinterpret_cast<uint4*>(a.o + (size_t)b * a.hq * D)[i] = make_uint4(0, 0, 0, 0);
     // an aborted CTA must not leave before its copies have landed
     if (*abort_flag) {
       for (int i = max(0, part - 2); i < part; ++i) drain_bar(bar(B_Q + (i & 1)), (i >> 1) & 1);
@@ -493,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, GC>::kCtas)
           raise |= y[g] > m[g] + kRaise;
         }
         if (WEIGHTS && there) {
-          float* out = a.scores + ((size_t)x * a.G) * 128 + r;
+          float* out = a.scores + ((size_t)x * a.side + blockIdx.x % a.side) * a.G * 128 + r;
 #pragma unroll
           for (int g = 0; g < GC; ++g)
             if (g < a.G) out[g * 128] = y[g];
@@ -616,129 +653,150 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, GC>::kCtas)
   }
 }
 
-// Adds up the rows that several CTAs share, and the weights of CTA c's tiles.
+// Adds four values to four floats, on 16 bytes, without a result.
+__device__ __forceinline__ void red_add_v4(float* p, float4 x) {
+  asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(x.x), "f"(x.y),
+               "f"(x.z), "f"(x.w)
+               : "memory");
+}
+
+// Adds up the rows that several CTAs share, and the weights of a CTA's tiles.
 //
-// Row (b, h) with tiles [r0, r1) belongs to block c of the first cut x_c inside it.  Its parts are
-// those of CTA c - 1 (the last of its range), c, c + 1, ... (the first of theirs) up to the one
-// that reaches r1; they are added in this order.
+// The parts of a row that begins inside team i's range and ends inside team j's are i's last, and
+// the first of i + 1 .. j: added in this order.  The blocks of i + 1 .. j share the row's heads
+// between them.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_constant__ PagedArgs a) {
-  constexpr int V = D / 4;  // pieces of a head's row
-  __shared__ long long scan[kJoinThreads / 32 + 4];
-  __shared__ float s_m[kPagedMaxGroup], s_inv[kPagedMaxGroup];
+  constexpr int V = D / 4;                  // pieces of a head's row
+  constexpr int R = kJoinThreads / V;       // runs over the parts
+  __shared__ long long scan[kJoinThreads / 32 + 2];
   __shared__ float4 s_sum[kJoinThreads];
-  const int c = blockIdx.x, tid = threadIdx.x, G = a.G;
-  const PagedSpan span = paged_span(a, c, scan, kJoinThreads);
+  __shared__ float2 s_run[R], s_ref[2][kPagedMaxGroup];
+  const int c = blockIdx.x / a.side, at_side = blockIdx.x % a.side, G = a.G;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  PagedSpan span;
+  const PagedCuts cuts = paged_span(a, c, scan, kJoinThreads, &span);
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // m and 1 / l of the shared row that holds tile x (of sequence b, row starting at r0), from its
-  // parts [c0, c1]
-  auto part_of = [&](int i, long long r0) -> size_t {  // of CTA i in the row
-    return ((size_t)i * 2 + (cut(a, span.total, i) < r0)) * G;
+  // Where team i keeps its part of a row whose first tile is team c0's: see k_paged.
+  auto part_of = [&](int i, int c0, bool behind) {
+    return (((size_t)i * a.side + at_side) * 2 + (i == c0 && behind)) * G;
   };
-  auto first_cta = [&](long long r0) {  // whose range holds tile r0
-    int i = (int)((r0 * a.grid) / span.total);
-    while (i > 0 && cut(a, span.total, i) > r0) --i;
-    while (cut(a, span.total, i + 1) <= r0) ++i;
-    return i;
-  };
-  auto stats = [&](int c0, int c1, long long r0) {
-    const int warp = tid >> 5, lane = tid & 31;
-    for (int g = warp; g < G; g += kJoinThreads / 32) {
-      float m = kLowest, l = 0.f;
-      for (int i = c0 + lane; i <= c1; i += 32) {
-        if (cut(a, span.total, i) == cut(a, span.total, i + 1)) continue;
-        m = fmaxf(m, __ldcg(&a.part_stats[part_of(i, r0) + g].x));
-      }
-      m = warp_max(m);
-      for (int i = c0 + lane; i <= c1; i += 32) {
-        if (cut(a, span.total, i) == cut(a, span.total, i + 1)) continue;
-        const float2 p = __ldcg(&a.part_stats[part_of(i, r0) + g]);
-        l += p.y * (p.x == m ? 1.f : ex2_approx(p.x - m));
-      }
-      l = warp_sum(l);
-      if (lane == 0) {
-        s_m[g] = m;
-        s_inv[g] = l == 0.f ? 0.f : 1.f / l;
-      }
-    }
-    __syncthreads();
-  };
-
-  if (c > 0 && span.b < a.cache.nseq && span.x0 < span.total) {
-    const int tiles = tiles_of(a.cache, span.b), h = span.off / tiles;
-    const long long r0 = span.x0 - (span.off - h * tiles), r1 = r0 + tiles;
-    if (span.x0 > r0 && cut(a, span.total, c - 1) <= r0) {
-      const int c1 = first_cta(r1 - 1);
-      stats(c - 1, c1, r0);
-      const size_t row0 = (size_t)span.b * a.hq + h * G;
-      // threads: pieces of the G rows, and where those are few, several runs over the parts
-      const int items = G * V, runs = max(1, kJoinThreads / items);
-      for (int i0 = 0; i0 < items; i0 += kJoinThreads) {
-        const int item = i0 + (runs > 1 ? tid % items : tid), run = runs > 1 ? tid / items : 0;
-        const bool on = item < items && run < runs;
+  if (!a.whole && c > 0 && c < cuts.n) {
+    const int tiles = tiles_of(a.cache, span.b), h = span.off / tiles, t = span.off - h * tiles;
+    const long long r0 = span.x0 - t;
+    if (t > 0) {  // the row of this team's first tile begins before it
+      const int c0 = cuts.team_of(r0), c1 = cuts.team_of(r0 + tiles - 1);
+      const bool behind = cuts.cut(c0) < r0;
+      const size_t row0 = (size_t)span.b * a.hq + (h * a.side + at_side) * G;
+      const int v = tid % V, run = tid / V;
+      for (int g = c - c0 - 1; g < G; g += c1 - c0) {
+        // every run with a reference of its own, so that sums need not wait for the references
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (on) {
-          const int g = item / V, v = item % V;
+        float m = kLowest, l = 0.f;
 #pragma unroll 4
-          for (int i = c - 1 + run; i <= c1; i += runs) {
-            if (cut(a, span.total, i) == cut(a, span.total, i + 1)) continue;
-            const size_t at = part_of(i, r0) + g;
-            const float pm = __ldcg(&a.part_stats[at].x);
-            const float f = (pm == s_m[g] ? 1.f : ex2_approx(pm - s_m[g])) * s_inv[g];
-            const float4 p = __ldcg(reinterpret_cast<const float4*>(a.parts + at * D) + v);
-            sum.x += p.x * f, sum.y += p.y * f, sum.z += p.z * f, sum.w += p.w * f;
+        for (int i = c0 + run; i <= c1; i += R) {
+          const size_t at = part_of(i, c0, behind) + g;
+          const float2 st = __ldcg(&a.part_stats[at]);
+          const float4 p = __ldcg(reinterpret_cast<const float4*>(a.parts + at * D) + v);
+          const float to = fmaxf(m, st.x);
+          const float f = m == to ? 1.f : ex2_approx(m - to), e = st.x == to ? 1.f : ex2_approx(st.x - to);
+          m = to;
+          l = l * f + st.y * e;
+          sum.x = sum.x * f + p.x * e, sum.y = sum.y * f + p.y * e;
+          sum.z = sum.z * f + p.z * e, sum.w = sum.w * f + p.w * e;
+        }
+        s_sum[tid] = sum;
+        if (v == 0) s_run[run] = make_float2(m, l);
+        __syncthreads();
+        if (run == 0) {
+          float top = kLowest, all = 0.f;
+#pragma unroll
+          for (int j = 0; j < R; ++j) top = fmaxf(top, s_run[j].x);
+          sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int j = 0; j < R; ++j) {
+            const float2 st = s_run[j];
+            const float e = st.x == top ? 1.f : ex2_approx(st.x - top);
+            const float4 p = s_sum[j * V + v];
+            all += st.y * e;
+            sum.x += p.x * e, sum.y += p.y * e, sum.z += p.z * e, sum.w += p.w * e;
           }
+          const float inv = all == 0.f ? 0.f : 1.f / all;
+          const uint2 o = make_uint2(pack_bf16(sum.x * inv, sum.y * inv),
+                                     pack_bf16(sum.z * inv, sum.w * inv));
+          reinterpret_cast<uint2*>(a.o + (row0 + g) * D)[v] = all == 0.f ? make_uint2(0, 0) : o;
         }
-        if (runs > 1) {
-          s_sum[tid] = sum;
-          __syncthreads();
-          if (run == 0)
-            for (int j = 1; j < runs; ++j) {
-              const float4 p = s_sum[j * items + item];
-              sum.x += p.x, sum.y += p.y, sum.z += p.z, sum.w += p.w;
-            }
-        }
-        if (on && run == 0) {
-          const int g = item / V, v = item % V;
-          if (s_inv[g] == 0.f) sum = make_float4(0.f, 0.f, 0.f, 0.f);
-          reinterpret_cast<uint2*>(a.o + (row0 + g) * D)[v] =
-              make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
-        }
+        __syncthreads();
       }
-      __syncthreads();
     }
   }
 
+  // Weights.  A warp has a tile, a lane four of its entries (they share a page).  Rows that are
+  // shared are the first and the last of the range: their references come first.
   if (!a.scores) return;
+  int parts = 0;
+  {
+    PagedWalk w(a, span);
+    long long x = span.x0;
+    while (w.next(a)) {
+      if (!w.whole() && (parts == 0 || w.left == 0)) {
+        const long long r0 = x - w.t0;
+        const int c0 = cuts.team_of(r0), c1 = cuts.team_of(r0 + w.tiles - 1);
+        const bool behind = cuts.cut(c0) < r0;
+        for (int g = warp; g < G; g += kJoinThreads / 32) {
+          float m = kLowest, l = 0.f;
+          for (int i = c0 + lane; i <= c1; i += 32) {
+            const float2 st = __ldcg(&a.part_stats[part_of(i, c0, behind) + g]);
+            const float to = fmaxf(m, st.x);
+            l = l * (m == to ? 1.f : ex2_approx(m - to)) +
+                st.y * (st.x == to ? 1.f : ex2_approx(st.x - to));
+            m = to;
+          }
+          const float top = warp_max(m);
+          l = warp_sum(l * (m == top ? 1.f : ex2_approx(m - top)));
+          if (lane == 0) s_ref[parts > 0][g] = make_float2(top, l == 0.f ? 0.f : 1.f / l);
+        }
+      }
+      x += w.t1 - w.t0;
+      ++parts;
+    }
+  }
+  __syncthreads();
   PagedWalk w(a, span);
   long long x = span.x0;
+  int part = 0, next = warp;  // tile of this warp, counted over the range
   while (w.next(a)) {
-    const size_t row0 = (size_t)w.sb * a.hq + w.sh * G;
-    if (w.whole()) {
-      if (tid < G) {
-        const float2 p = __ldcg(&a.stats[row0 + tid]);
-        s_m[tid] = p.x;
-        s_inv[tid] = p.y;
-      }
-      __syncthreads();
-    } else {
-      const long long r0 = x - w.t0;
-      stats(first_cta(r0), first_cta(r0 + w.tiles - 1), r0);
-    }
-    const int n = min(w.len, w.t1 * 128) - w.t0 * 128;
-    for (int i = tid; i < n; i += kJoinThreads) {
-      const float* s = a.scores + (size_t)(x + (i >> 7)) * G * 128 + (i & 127);
-      float sum = 0.f;
+    const int n = w.t1 - w.t0, done = (int)(x - span.x0);
+    const float2* ref = w.whole() ? a.stats + (size_t)w.sb * a.hq + w.sh * G : s_ref[part > 0];
+    for (; next < done + n; next += kJoinThreads / 32) {
+      const int e = (w.t0 + next - done) * 128 + 4 * lane;
+      if (e >= w.len) continue;
+      const float* s =
+          a.scores + ((size_t)(span.x0 + next) * a.side + at_side) * G * 128 + 4 * lane;
+      const int page = cache_page(a.cache, w.sb, e);
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-      for (int g = 0; g < G; ++g) sum += ex2_approx(__ldcg(s + g * 128) - s_m[g]) * s_inv[g];
-      const int e = w.t0 * 128 + i, page = cache_page(a.cache, w.sb, e);
-      if (page >= 0)
-        atomicAdd(a.cache.weight +
-                      a.cache.meta(page, e & ((1 << a.cache.page_shift) - 1), w.sh), sum);
+      for (int g = 0; g < G; ++g) {
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(s + g * 128));
+        const float2 st = ref[g];
+        sum.x += ex2_approx(y.x - st.x) * st.y;
+        sum.y += ex2_approx(y.y - st.x) * st.y;
+        sum.z += ex2_approx(y.z - st.x) * st.y;
+        sum.w += ex2_approx(y.w - st.x) * st.y;
+      }
+      if (page < 0) continue;
+      float* to = a.cache.weight + a.cache.meta(page, e & ((1 << a.cache.page_shift) - 1), w.sh);
+      if (e + 4 <= w.len) {
+        red_add_v4(to, sum);
+      } else {  // the scores behind the last entry are not written
+        atomicAdd(to, sum.x);
+        if (e + 1 < w.len) atomicAdd(to + 1, sum.y);
+        if (e + 2 < w.len) atomicAdd(to + 2, sum.z);
+      }
     }
-    x += w.t1 - w.t0;
-    __syncthreads();
+    x += n;
+    ++part;
   }
 }
 
@@ -750,7 +808,7 @@ cudaError_t launch_t(const PagedArgs& a, const CUtensorMap& mq, const CUtensorMa
   if (e != cudaSuccess) return e;
   k_paged<D, GC, WEIGHTS><<<a.grid, kThreads, C::kSmem, st>>>(mq, mk, mv, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (a.grid == 1 && !WEIGHTS) return e;  // every row whole
+  if (a.whole && !WEIGHTS) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.grid);
   cfg.blockDim = dim3(kJoinThreads);
@@ -784,12 +842,20 @@ int ctas_of(int G) {  // per SM
 
 }  // namespace
 
-int paged_grid(const CacheArgs& c, int G) {
-  const int ctas = G <= 8 || (G <= 16 && c.d == 64) ? 2 : 1;  // PagedCfg::kCtas
-
-  const int most = sm_count() * ctas;
-  const long long tiles = (long long)c.nseq * c.hkv * ((c.capacity + 127) / 128);
-  return (int)(tiles < 1 ? 1 : tiles < most ? tiles : most < kPagedMaxGrid ? most : kPagedMaxGrid);
+// Teams, their size and the grid for these shapes.
+void paged_shape(PagedArgs* a) {
+  const CacheArgs& c = a->cache;
+  a->side = kMostSide;
+  while (c.hkv % a->side) --a->side;
+  a->groups = c.hkv / a->side;
+  const long long row = (c.capacity + 127) / 128;
+  a->whole = row <= kWholeTiles;
+  int most = sm_count() * (c.d == 128 ? ctas_of<128>(a->G) : ctas_of<64>(a->G));
+  if (most > kPagedMaxGrid) most = kPagedMaxGrid;
+  const long long tiles = (long long)c.nseq * a->groups * (a->whole ? 1 : row);
+  const int teams = most / a->side > 0 ? most / a->side : 1;
+  a->grid = (int)(tiles < teams ? tiles : teams) * a->side;
+  if (a->grid == a->side) a->whole = true;
 }
 
 cudaError_t launch_paged(const PagedArgs& a, const uint16_t* q, long long q_stride,

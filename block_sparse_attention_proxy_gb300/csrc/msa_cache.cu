@@ -94,7 +94,7 @@ msa_status check_cache(const msa_cache* c, const msa_table* t, CacheArgs* a) {
 }
 msa_status check_cache_pointers(const CacheArgs& a) {
   if (!a.k || !a.v || !aligned(a.k, 16) || !aligned(a.v, 16)) return MSA_ERR_INVALID_ARG;
-  if (!aligned(a.weight, 4) || !aligned(a.position, 4)) return MSA_ERR_INVALID_ARG;
+  if (!aligned(a.weight, 16) || !aligned(a.position, 16)) return MSA_ERR_INVALID_ARG;
   if (!a.table || !a.lens || !aligned(a.table, 4) || !aligned(a.lens, 4))
     return MSA_ERR_INVALID_ARG;
   return MSA_OK;
@@ -158,10 +158,10 @@ msa_status evict_workspace(const CacheArgs& a, int keep, EvictWorkspace* w) {
   Carve c;
   w->most = most;
   w->count = c.take((size_t)a.nseq * a.hkv * sizeof(int32_t));
-  w->pairs = c.take((size_t)a.nseq * a.hkv * 2 * most * sizeof(int32_t));
+  w->pairs = c.take((size_t)a.nseq * a.hkv * 2 * most * sizeof(int64_t));
   w->total = c.total;
-  // blocks of the largest grid: 64 pairs each
-  return (long long)a.nseq * a.hkv * ((most + 63) / 64 + 1) > 0x7fffffffll ? MSA_ERR_UNSUPPORTED
+  // blocks of the largest grid: 8 of a row, or one for 8 pairs
+  return (long long)a.nseq * a.hkv * std::max((most + 7) / 8, 8) > 0x7fffffffll ? MSA_ERR_UNSUPPORTED
                                                                          : MSA_OK;
 }
 
@@ -280,10 +280,10 @@ msa_status msa_paged_attention(const msa_cache* cache, const msa_table* table,
     a.stats = reinterpret_cast<float2*>(base + w.stats);
     a.scores = reinterpret_cast<float*>(base + w.scores);
   }
-  a.grid = paged_grid(a.cache, a.G);
+  paged_shape(&a);
   if (launch_paged(a, q, qs, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
     return MSA_ERR_CUDA;
-  add_launches(a.grid == 1 && !p->accumulate ? 1 : 2);
+  add_launches(a.whole && !p->accumulate ? 1 : 2);
   return MSA_OK;
 }
 
@@ -318,7 +318,7 @@ msa_status msa_cache_evict(const msa_cache* cache, const msa_table* table, int32
   a.recent = recent;
   a.new_lens = new_lens;
   a.count = reinterpret_cast<int32_t*>(base + w.count);
-  a.pairs = reinterpret_cast<int32_t*>(base + w.pairs);
+  a.pairs = reinterpret_cast<long long*>(base + w.pairs);
   a.most = w.most;
   int launches = 0;
   if (launch_evict(a, reinterpret_cast<cudaStream_t>(stream), &launches) != cudaSuccess)

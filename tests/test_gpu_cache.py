@@ -379,7 +379,9 @@ def _evict(lens, keep, recent, page, hkv, d, seed=40, change=None):
 @pytest.mark.parametrize("lens,keep,recent", [
     ([1], 1, 0), ([2], 1, 1), ([5, 4, 3, 0], 4, 2), ([129, 128, 127, 300], 128, 16),
     ([129] * 9, 128, 128), ([1000, 999, 64, 3], 64, 0), ([1000, 700, 640], 600, 599),
-    ([5000, 100, 4001], 400, 33), ([9001], 9000, 100), ([20003, 600], 1500, 7)])
+    ([5000, 100, 4001], 400, 33), ([9001], 9000, 100), ([20003, 600], 1500, 7),
+    ([70, 67, 65, 64, 72, 73, 74], 65, 3), ([8, 7, 2, 1], 1, 1), ([4100, 4097], 4096, 4096),
+    ([30005, 30008, 30009], 30001, 0)])
 @pytest.mark.parametrize("page,d", [(16, 64), (64, 128)])
 def test_evict(lens, keep, recent, page, d):
     _evict(lens, keep, recent, page, 3, d)
