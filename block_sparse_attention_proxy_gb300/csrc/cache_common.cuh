@@ -78,6 +78,7 @@ struct PagedArgs {
   int hq, G, grid;
   int side, groups;  // CTAs of a team, each on a KV head of its own; groups of so many KV heads
   bool whole;        // rows are not shared between CTAs
+  bool direct;       // and team c has row c at most
   float scale_log2;
   uint16_t* o;
   float* parts;        // [CTA][2][G][d] sums of rows that CTAs share
@@ -98,6 +99,8 @@ struct EvictArgs {
   long long* pairs;  // [nseq][hkv][2][most] places in the cache: from, to
   int most;        // pairs of a row at most
 };
+// Whether the lists of the moves need no workspace, for `most` moves of a row at most.
+bool evict_on_chip(const CacheArgs& c, int most);
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st, int* launches);
 
 // Streaming multiprocessors of the current device.

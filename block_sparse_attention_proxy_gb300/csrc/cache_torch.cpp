@@ -361,9 +361,10 @@ Tensor paged_attention(const Tensor& q, const Tensor& ck, const Tensor& cv,
   const auto opt = q.options().requires_grad(false);
   Tensor o = at::empty(q.sizes(), opt);
   const size_t need = msa_paged_attention_workspace_size(&c.cache, &c.table, &p);
-  Tensor ws = at::empty({std::max<int64_t>((int64_t)need, 256)}, opt.dtype(at::kByte));
-  raise_on(msa_paged_attention(&c.cache, &c.table, &p, in(q_), out(o), ws.mutable_data_ptr(),
-                               (size_t)ws.numel(), current_stream()),
+  Tensor ws;
+  if (need > 256) ws = at::empty({(int64_t)need}, opt.dtype(at::kByte));
+  raise_on(msa_paged_attention(&c.cache, &c.table, &p, in(q_), out(o), any_out(ws), need,
+                               current_stream()),
            "msa_paged_attention");
   if (accumulate) c.changed(false, false);
   return o;
@@ -384,11 +385,10 @@ Tensor cache_evict(const Tensor& ck, const Tensor& cv, const std::optional<Tenso
   c.describe(table, lens);
   Tensor left = at::empty(c.lens.sizes(), c.lens.options());
   const size_t need = msa_cache_evict_workspace_size(&c.cache, &c.table, (int32_t)keep);
-  Tensor ws = at::empty({std::max<int64_t>((int64_t)need, 256)},
-                        c.lens.options().dtype(at::kByte));
+  Tensor ws;
+  if (need > 256) ws = at::empty({(int64_t)need}, c.lens.options().dtype(at::kByte));
   raise_on(msa_cache_evict(&c.cache, &c.table, (int32_t)keep, (int32_t)recent,
-                           left.mutable_data_ptr<int32_t>(), ws.mutable_data_ptr(),
-                           (size_t)ws.numel(), current_stream()),
+                           left.mutable_data_ptr<int32_t>(), any_out(ws), need, current_stream()),
            "msa_cache_evict");
   c.changed(true, true);
   return left;

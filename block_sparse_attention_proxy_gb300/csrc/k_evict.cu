@@ -19,6 +19,7 @@
 namespace msa {
 namespace {
 
+constexpr int kSms = 152;          // of a GB300
 constexpr int kListThreads = 512;
 constexpr int kMostBlocks = 8;    // of a cluster: one row
 constexpr int kMostKeys = 24576;  // entries of a block whose ranks and positions it keeps
@@ -203,8 +204,10 @@ __global__ void __launch_bounds__(kListThreads, 2)
     __syncthreads();
   }
 
-  long long* from = a.pairs + (size_t)row * 2 * a.most;
-  long long* to = from + a.most;
+  __shared__ long long s_pairs[FUSED ? 2 * kMostFused : 1];
+  const bool on_chip = FUSED && blocks == 1;  // the lists; else in the workspace
+  long long* from = on_chip ? s_pairs : a.pairs + (size_t)row * 2 * a.most;
+  long long* to = from + (on_chip ? kMostFused : a.most);
   auto entry = [&](int i) -> long long {  // its place in the cache
     const int page = cache_page(c, b, i);
     return page < 0 ? -1 : ((long long)page << c.page_shift) + (i & mask);
@@ -395,6 +398,10 @@ cudaError_t list(const EvictArgs& a, int rows, int blocks, int slice, int thread
                  cudaStream_t st) {
   const cudaError_t e = dense_prepare<k_evict_list<KEYS, FUSED>>(0, 0, KEYS ? kMostKeys * 8 : 0);
   if (e != cudaSuccess) return e;
+  if (blocks == 1) {
+    k_evict_list<KEYS, FUSED><<<rows, threads, KEYS ? slice * 8 : 0, st>>>(a, 1, slice);
+    return cudaGetLastError();
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * blocks));
   cfg.blockDim = dim3(threads);
@@ -411,16 +418,24 @@ cudaError_t list(const EvictArgs& a, int rows, int blocks, int slice, int thread
 
 }  // namespace
 
+// Several blocks to a row where the rows alone leave SMs idle (and where a row's ranks do not fit
+// one block), each with a few thousand entries at least.
+int evict_blocks(const CacheArgs& c) {
+  const long long rows = (long long)c.nseq * c.hkv;
+  int blocks = 1;
+  while (blocks < kMostBlocks && (rows * blocks * 2 <= 2 * kSms ? c.capacity / (2 * blocks) >= 2048
+                                                               : c.capacity > blocks * kMostKeys))
+    blocks *= 2;
+  return blocks;
+}
+bool evict_on_chip(const CacheArgs& c, int most) {
+  return most <= kMostFused && evict_blocks(c) == 1;
+}
+
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st, int* launches) {
   const CacheArgs& c = a.cache;
   const int rows = c.nseq * c.hkv;
-  // Several blocks to a row where the rows alone leave SMs idle (and where a row's ranks do not
-  // fit one block), each with a few thousand entries at least.
-  int blocks = 1;
-  while (blocks < kMostBlocks &&
-         ((long long)rows * blocks * 2 <= 2 * sm_count() ? c.capacity / (2 * blocks) >= 2048
-                                                         : c.capacity > blocks * kMostKeys))
-    blocks *= 2;
+  const int blocks = evict_blocks(c);
   const int slice = (int)((((long long)c.capacity + blocks - 1) / blocks + 31) / 32 * 32);
   const bool keys = slice <= kMostKeys, fused = a.most <= kMostFused;
   const int threads = std::min(std::max((slice / 16 + 31) / 32 * 32, 128), kListThreads);

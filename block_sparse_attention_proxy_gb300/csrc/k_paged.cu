@@ -6,8 +6,8 @@
 // tensor core with the entries as rows, which wastes none of it on the G queries of a KV head:
 //   S^T [128 entries x G] = K Q^T,   O^T [d x G] += V^T P^T,
 // K and V as they lie in the cache (TMA boxes of a page, or of 128 entries of a larger one), Q and
-// P as the narrow operand (G padded to 16, 32 or 64 columns).  A thread of the softmax
-// warpgroup owns one entry's G scores, later one row of O^T.
+// P as the narrow operand (G padded to 16, 32 or 64 columns).  A thread of a softmax
+// warpgroup owns one entry's scores of up to 16 heads, later one row of O^T.
 //
 // The work is cut evenly: the tiles of 128 entries of all (sequence, KV head) rows are counted
 // through, and each CTA takes as many of them, whatever rows they fall in.  A row inside one CTA's
@@ -22,7 +22,7 @@
 // entries, 8 heads of d = 64: 103 us alone, 92 in twos, 91 in fours, 88 in eights; d = 128: 170 -> 165.
 //
 // The reference m of a head's exponentials moves only when a score exceeds it by more than 8
-// (a factor of 256): one vote over the warpgroup a tile, and O is rescaled in TMEM in the
+// (a factor of 256): one vote over a warpgroup a tile, and O is rescaled in TMEM in the
 // rare tile that raises it.  P enters its product as two bf16 parts (its rounding and what that
 // drops, 16 bits together) in columns of their own, of which G <= 8 leaves enough idle; with
 // one part the result's error was 1.4 times that of rounding it once (64 sequences of 4096 entries: 2.3e-3 against 1.7e-3).  With weights asked for, the scores go out in fp32 and the join adds
@@ -33,9 +33,10 @@
 namespace msa {
 namespace {
 
-constexpr int kThreads = 192;  // softmax warps 0-3, loads 4, products 5
 constexpr int kJoinThreads = 256;
-constexpr int kWholeTiles = 4, kMostSide = 8;
+constexpr int kWeightBlocks = 2;  // blocks that add the weights of one CTA's tiles
+constexpr int kWholeTiles = 12, kMostSide = 8;
+constexpr int kBarStart = 15;  // named barrier; 1 to 8: votes and sums of the softmax warpgroups
 constexpr float kRaise = 8.f;
 constexpr float kLowest = -FLT_MAX;  // reference of a row that has no score above it yet
 
@@ -43,18 +44,20 @@ constexpr float kLowest = -FLT_MAX;  // reference of a row that has no score abo
 template <int D, int GC>
 struct PagedCfg {
   static constexpr int kN = GC < 16 ? 16 : GC;   // columns of S
+  static constexpr int kGroups = GC <= 16 ? 1 : GC / 16;  // softmax warpgroups, 16 heads each
+  static constexpr int kThreads = 128 * kGroups + 64;     // and a warp for loads, one for products
   static constexpr int kHi = GC < 8 ? 8 : GC;    // columns of O: those of P's upper parts, then
   static constexpr int kNo = 2 * kHi;            // those of its lower ones
   static constexpr int kTile = 128 * D * 2;
   static constexpr int kQ = kN * D * 2, kP = kNo * 256;
-  static constexpr int kCtas = 3 * kTile + 2 * kQ + 2 * kP <= 114688 ? 2 : 1;  // per SM
+  static constexpr int kCtas = GC <= 16 && 3 * kTile + 2 * kQ + 2 * kP <= 114688 ? 2 : 1;  // per SM
   static constexpr int kMisc = GC <= 16 ? 1024 : 2560;  // barriers, sums over the warps
   static constexpr int kRoom = kCtas == 2 ? 115712 : 232448;
-  static constexpr int kRing = (kRoom - 2 * kQ - 2 * kP - kMisc) / kTile;
+  static constexpr int kRing = (kRoom - 2 * kQ - 2 * kP - kMisc) / kTile;  // K and V tiles in flight
   static constexpr int kSmem = kRing * kTile + 2 * kQ + 2 * kP + kMisc;
   static constexpr int kUsed = 2 * kN + 2 * kNo;  // TMEM: two S, two O
   static constexpr int kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
-  static_assert(kRing >= 3 && 400 + 32 * GC <= kMisc && kCols * kCtas <= 512, "budgets");
+  static_assert(kRing >= 3 && kCols * kCtas <= 512, "budgets");
 };
 
 // How the tiles of all rows are shared out.  Team c of the n that get any takes the tiles from
@@ -90,6 +93,14 @@ __device__ __forceinline__ int tiles_of(const CacheArgs& c, int b) {
 // of team c.  With `whole` its range begins and ends with rows: at the first row that begins
 // at or behind the cut.  `sm`: n / 32 + 2 numbers.
 __device__ PagedCuts paged_span(const PagedArgs& a, int c, long long* sm, int n, PagedSpan* span) {
+  if (a.direct) {  // a row for each team at most: nothing to count
+    span->b = c / a.groups;
+    const int tiles = span->b < a.cache.nseq ? tiles_of(a.cache, span->b) : 0;
+    span->off = (c - span->b * a.groups) * tiles;
+    span->x0 = (long long)c * ((a.cache.capacity + 127) / 128);
+    span->x1 = span->x0 + tiles;
+    return PagedCuts(0, 1);
+  }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = n / 32;
   int *s_b = reinterpret_cast<int*>(sm + nw), *s_off = s_b + 2;
   const int per = (a.cache.nseq + n - 1) / n, first = min(tid * per, a.cache.nseq),
@@ -154,6 +165,7 @@ struct PagedWalk {
   int t1;           // end of the current part of the row: tiles [t0, t1)
   int t0;
   int sb, sh;       // sequence and KV head of the current part
+  int at_side;      // of the CTA
   __device__ __forceinline__ void seek(const PagedArgs& a) {
     while (b < a.cache.nseq) {
       len = cache_len(a.cache, b);
@@ -163,7 +175,8 @@ struct PagedWalk {
     }
     left = 0;
   }
-  __device__ __forceinline__ PagedWalk(const PagedArgs& a, const PagedSpan& s) {
+  __device__ __forceinline__ PagedWalk(const PagedArgs& a, const PagedSpan& s, int cta) {
+    at_side = cta % a.side;
     b = s.b;
     left = s.x1 - s.x0;
     len = tiles = h = t = t0 = t1 = sb = sh = 0;
@@ -183,7 +196,7 @@ struct PagedWalk {
     }
     if (left <= 0) return false;
     sb = b;
-    sh = h * a.side + blockIdx.x % a.side;
+    sh = h * a.side + at_side;
     t0 = t;
     t1 = (int)min((long long)tiles, t + left);
     left -= t1 - t0;
@@ -194,16 +207,16 @@ struct PagedWalk {
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
 };
 
-// Whether `x` holds for one of the softmax warps' 128 threads; a barrier for them.
-__device__ __forceinline__ bool any128(bool x) {
+// Whether `x` holds for one of a warpgroup's 128 threads; a barrier for them.
+__device__ __forceinline__ bool any128(uint32_t id, bool x) {
   uint32_t y;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(y)
-      : "r"((uint32_t)x)
+      : "r"((uint32_t)x), "r"(id)
       : "memory");
   return y != 0;
 }
@@ -226,7 +239,8 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t ta, float (&f)[N]) {
           "=r"(r[7])
         : "r"(ta)
         : "memory");
-  } else if constexpr (N == 16) {
+  } else {
+    static_assert(N == 16, "");
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
@@ -236,51 +250,34 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t ta, float (&f)[N]) {
           "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(ta)
         : "memory");
-  } else if constexpr (N == 32) {
-    tmem_ld32(ta, r);
-  } else {
-    tmem_ld_row(ta, r);
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) f[i] = __uint_as_float(r[i]);
 }
 template <int N>
 __device__ __forceinline__ void tmem_st_cols(uint32_t ta, const float (&f)[N]) {
-  if constexpr (N == 64) {
-    uint32_t r[32];
+  uint32_t r[N];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(f[32 * h + i]);
-      tmem_st32(ta + 32 * h, r);
-    }
+  for (int i = 0; i < N; ++i) r[i] = __float_as_uint(f[i]);
+  if constexpr (N == 4) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(ta),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+        : "memory");
+  } else if constexpr (N == 8) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(ta),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+        : "memory");
   } else {
-    uint32_t r[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = __float_as_uint(f[i]);
-    if constexpr (N == 4) {
-      asm volatile(
-          "tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};\n\t"
-          "tcgen05.wait::st.sync.aligned;" ::"r"(ta),
-          "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-          : "memory");
-    } else if constexpr (N == 8) {
-      asm volatile(
-          "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\t"
-          "tcgen05.wait::st.sync.aligned;" ::"r"(ta),
-          "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-          : "memory");
-    } else if constexpr (N == 16) {
-      tmem_st16(ta, r);
-    } else {
-      tmem_st32(ta, r);
-    }
+    tmem_st16(ta, r);
   }
 }
 
-// Reduces N columns over the lanes of a warp: halves of the columns are exchanged, so that each
-// step works on half as many.  Afterwards lane l holds, in x[0 .. max(1, N / 32)), the
-// columns column_of<N>(l) and following.
+// Reduces N <= 16 columns over the lanes of a warp: halves of the columns are exchanged, so that
+// each step works on half as many.  Afterwards lane l holds column column_of<N>(l) in x[0].
 template <int N, bool MAX>
 __device__ __forceinline__ void reduce_cols(float (&x)[N]) {
   const int lane = threadIdx.x & 31;
@@ -316,12 +313,12 @@ __device__ __forceinline__ int column_of(int lane) {
 }
 
 template <int D, int GC, bool WEIGHTS>
-__global__ void __launch_bounds__(kThreads, PagedCfg<D, GC>::kCtas)
+__global__ void __launch_bounds__(PagedCfg<D, GC>::kThreads, PagedCfg<D, GC>::kCtas)
     k_paged(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedArgs a) {
   using C = PagedCfg<D, GC>;
-  constexpr int NCH = D / 64, NR = C::kRing, N = C::kN, NO = C::kNo, HI = C::kHi,
-                CH = GC < 16 ? GC : 16;
+  constexpr int NCH = D / 64, NR = C::kRing, N = C::kN, NO = C::kNo, HI = C::kHi;
+  constexpr int CH = GC < 16 ? GC : 16, kLoads = 4 * C::kGroups, kProducts = kLoads + 1;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sKV = smem;
   uint8_t* sQ = sKV + NR * C::kTile;  // [2][chunk][N rows][128 bytes]
@@ -330,22 +327,20 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, GC>::kCtas)
   // ring full / empty | queries loaded / free | S complete | P stored | P V complete | O read
   constexpr int B_F = 0, B_E = B_F + NR, B_Q = B_E + NR, B_QE = B_Q + 2, B_S = B_QE + 2,
                 B_P = B_S + 2, B_PV = B_P + 2, B_OE = B_PV + 2, B_END = B_OE + 2;
-  static_assert((B_END + 1) * 8 <= 320, "barrier block");
-  long long* scan = reinterpret_cast<long long*>(bars + 40);  // see paged_span
-  static_assert(kThreads / 32 + 2 <= 8, "scan block");
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 48);
+  constexpr int kScan = B_END + 1, kSlot = kScan + C::kThreads / 32 + 2, kMax = kSlot + 1;
+  long long* scan = reinterpret_cast<long long*>(bars + kScan);  // see paged_span
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + kSlot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
-  float* sMax = reinterpret_cast<float*>(bars + 50);  // [4][GC] maxima of the warps
-  float* sSum = sMax + 4 * GC;                        // [4][GC] their sums
+  float* sMax = reinterpret_cast<float*>(bars + kMax);  // [group][4][CH] maxima of the warps
+  float* sSum = sMax + 4 * GC;                          // [group][4][CH] their sums
+  static_assert(8 * kMax + 32 * GC <= C::kMisc, "shared memory budget");
   auto bar = [&](int i) { return smem_u32(bars + i); };
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
-  if (threadIdx.x == 128) {
+  if (warp == kLoads && lane == 0) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
-  }
-  if (threadIdx.x == 0) {
     for (int s = 0; s < NR; ++s) {
       mbar_init(bar(B_F + s), 1);
       mbar_init(bar(B_E + s), 1);
@@ -354,25 +349,30 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, GC>::kCtas)
       mbar_init(bar(B_Q + i), 1);
       mbar_init(bar(B_QE + i), 1);
       mbar_init(bar(B_S + i), 1);
-      mbar_init(bar(B_P + i), 4);
+      mbar_init(bar(B_P + i), 4 * C::kGroups);
       mbar_init(bar(B_PV + i), 1);
-      mbar_init(bar(B_OE + i), 4);
+      mbar_init(bar(B_OE + i), 4 * C::kGroups);
     }
     mbar_init(bar(B_END), 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 5) {
+  if (warp == kProducts) {
     tmem_alloc(smem_u32(tslot), C::kCols);
     tmem_relinquish();
   }
+  __syncwarp();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   PagedSpan span;
-  paged_span(a, blockIdx.x / a.side, scan, kThreads, &span);
+  paged_span(a, blockIdx.x / a.side, scan, C::kThreads, &span);
+  // The loading warp has what it needs and starts; the others wait for its barriers.
   tc_fence_before();
-  __syncthreads();
+  if (warp == kLoads)
+    asm volatile("barrier.cta.arrive %0, %1;" ::"n"(kBarStart), "n"(C::kThreads) : "memory");
+  else
+    asm volatile("barrier.cta.sync %0, %1;" ::"n"(kBarStart), "n"(C::kThreads) : "memory");
   tc_fence_after();
-  const uint32_t tbase = *reinterpret_cast<volatile uint32_t*>(tslot);
+  const uint32_t tbase = warp == kLoads ? 0 : *reinterpret_cast<volatile uint32_t*>(tslot);
   // TMEM: S of tile u at columns N (u & 1), O of part i at 2 N + NO (i & 1)
   auto wait = [&](int b, uint32_t parity, int n) {
     return wait_bar_warp(bar(b), parity, abort_flag, a.cache.status, wait_site(kKerPaged, b, n));
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, GC>::kCtas)
 
   // The loads run in the order K0, K1, V0, K2, V1, ...: that in which the products take them, with
   // the scores of one tile ahead of the values of the one before it.
-  if (warp == 4) {
+  if (warp == kLoads) {
     // ------------------------------ loads ----------------------------------------
     const int rows = min(128, 1 << a.cache.page_shift);  // of a box
     const int box = lane / NCH, ch = lane % NCH;         // one box of a tile per lane
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, GC>::kCtas)
       if (++s == NR) s = 0, ++round;
     };
     struct { int b, h, len, t; } last{-1, 0, 0, 0};
-    PagedWalk w(a, span);
+    PagedWalk w(a, span, blockIdx.x);
     while (ok && w.next(a)) {
       if (part >= 2 && !(ok = wait(B_QE + (part & 1), ((part >> 1) & 1) ^ 1, part))) break;
       if (lane == 0) mbar_arrive_expect_tx(bar(B_Q + (part & 1)), C::kQ);
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, GC>::kCtas)
       for (int i = 0; i < NR; ++i)
         if (i < s || round > 0) drain_bar(bar(B_F + i), (i < s ? round : round - 1) & 1);
     }
-  } else if (warp == 5) {
+  } else if (warp == kProducts) {
     // ------------------------------ products -------------------------------------
     constexpr uint32_t idS = make_idesc_bf16(128, N, false, false);
     constexpr uint32_t idO = make_idesc_bf16(128, NO, true, false);
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, GC>::kCtas)
       mma_commit(el, bar(B_E + s));
       if (++s == NR) s = 0, ++round;
     };
-    PagedWalk w(a, span);
+    PagedWalk w(a, span, blockIdx.x);
     while (ok && w.next(a)) {
       if (!(ok = wait(B_Q + (part & 1), (part >> 1) & 1, part))) break;
       new_part = true;
@@ -502,77 +502,75 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, GC>::kCtas)
   } else {
     // ------------------------------ softmax --------------------------------------
     // A failed wait marks the warp dead: it keeps to its barriers without touching TMEM.
-    const int r = threadIdx.x;  // entry of a tile; row of O^T
-    const uint32_t lanes = tbase + ((uint32_t)(warp * 32) << 16);
+    const int quarter = warp & 3, group = warp >> 2;
+    const int r = quarter * 32 + lane;  // entry of a tile; row of O^T
+    const int h0 = group * CH;          // heads h0 .. h0 + CH are this warpgroup's
+    const uint32_t lanes = tbase + ((uint32_t)(quarter * 32) << 16) + h0;
+    const uint32_t id_vote = 1 + 2 * group, id_join = 2 + 2 * group;
+    float *wMax = sMax + 4 * h0, *wSum = sSum + 4 * h0;
     const float c = a.scale_log2;
     bool dead = false;
     int u = 0, part = 0;
     long long x = span.x0;  // tile over all rows
-    PagedWalk w(a, span);
+    PagedWalk w(a, span, blockIdx.x);
     while (w.next(a)) {
-      float m[GC], l[GC];
+      float m[CH], l[CH];
 #pragma unroll
-      for (int g = 0; g < GC; ++g) m[g] = kLowest, l[g] = 0.f;
+      for (int g = 0; g < CH; ++g) m[g] = kLowest, l[g] = 0.f;
       for (int t = w.t0; t < w.t1; ++t, ++u, ++x) {
         const int b = u & 1;
         dead = dead || !wait(B_S + b, (u >> 1) & 1, u);
         tc_fence_after();
-        float y[GC];
+        float y[CH];
 #pragma unroll
-        for (int g = 0; g < GC; ++g) y[g] = -INFINITY;
-        if (!dead) tmem_ld_cols<GC>(lanes + N * b, y);
+        for (int g = 0; g < CH; ++g) y[g] = -INFINITY;
+        if (!dead) tmem_ld_cols<CH>(lanes + N * b, y);
         __syncwarp();
         const bool there = r < w.len - t * 128;
         bool raise = false;
 #pragma unroll
-        for (int g = 0; g < GC; ++g) {
-          y[g] = there && g < a.G ? y[g] * c : -INFINITY;
+        for (int g = 0; g < CH; ++g) {
+          y[g] = there && h0 + g < a.G ? y[g] * c : -INFINITY;
           raise |= y[g] > m[g] + kRaise;
         }
         if (WEIGHTS && there) {
-          float* out = a.scores + ((size_t)x * a.side + blockIdx.x % a.side) * a.G * 128 + r;
+          float* out = a.scores + (((size_t)x * a.side + blockIdx.x % a.side) * a.G + h0) * 128 + r;
 #pragma unroll
-          for (int g = 0; g < GC; ++g)
-            if (g < a.G) out[g * 128] = y[g];
+          for (int g = 0; g < CH; ++g)
+            if (h0 + g < a.G) out[g * 128] = y[g];
         }
         __syncwarp();
-        if (any128(raise)) {
+        if (any128(id_vote, raise)) {
           // the tile's maxima of all heads; O of the tiles before it moves to the new reference
-          float z[GC];
+          float z[CH];
 #pragma unroll
-          for (int g = 0; g < GC; ++g) z[g] = y[g];
-          reduce_cols<GC, true>(z);
-          const int col = column_of<GC>(lane);
+          for (int g = 0; g < CH; ++g) z[g] = y[g];
+          reduce_cols<CH, true>(z);
+          wMax[quarter * CH + column_of<CH>(lane)] = z[0];
+          named_bar_sync(id_join, 128);
+          float f[CH];
 #pragma unroll
-          for (int i = 0; i < (GC > 32 ? GC / 32 : 1); ++i) sMax[warp * GC + col + i] = z[i];
-          named_bar_sync(2, 128);
+          for (int g = 0; g < CH; ++g) {
+            const float top = fmaxf(fmaxf(wMax[g], wMax[CH + g]),
+                                    fmaxf(wMax[2 * CH + g], wMax[3 * CH + g]));
+            f[g] = 1.f;
+            if (top > m[g]) {
+              f[g] = ex2_approx(m[g] - top);
+              m[g] = top;
+            }
+            l[g] *= f[g];
+          }
           if (t > w.t0) {
             dead = dead || !wait(B_PV + (b ^ 1), ((u - 1) >> 1) & 1, u);
             tc_fence_after();
-          }
-#pragma unroll
-          for (int g0 = 0; g0 < GC; g0 += CH) {
-            float f[CH];
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-              const int g = g0 + i;
-              const float top = fmaxf(fmaxf(sMax[g], sMax[GC + g]),
-                                      fmaxf(sMax[2 * GC + g], sMax[3 * GC + g]));
-              f[i] = 1.f;
-              if (top > m[g]) {
-                f[i] = ex2_approx(m[g] - top);
-                m[g] = top;
-              }
-              l[g] *= f[i];
-            }
-            if (t > w.t0 && !dead) {
+            if (!dead) {
 #pragma unroll
               for (int half = 0; half < 2; ++half) {
-                const uint32_t to = lanes + 2 * N + NO * (part & 1) + HI * half + g0;
+                const uint32_t to = lanes + 2 * N + NO * (part & 1) + HI * half;
                 float o[CH];
                 tmem_ld_cols<CH>(to, o);
 #pragma unroll
-                for (int i = 0; i < CH; ++i) o[i] *= f[i];
+                for (int g = 0; g < CH; ++g) o[g] *= f[g];
                 tmem_st_cols<CH>(to, o);
               }
             }
@@ -580,15 +578,16 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, GC>::kCtas)
         }
         // the buffer of P was last read by the product of tile u - 2
         if (u >= 2) dead = dead || !wait(B_PV + b, ((u - 2) >> 1) & 1, u);
-        uint8_t* p = sP + b * C::kP + (r >> 6) * NO * 128 + (r & 7) * 2;
+        uint8_t* p = sP + b * C::kP + (r >> 6) * NO * 128 + h0 * 128 + (r & 7) * 2;
 #pragma unroll
-        for (int g = 0; g < GC; ++g) {
-          if (g < a.G) {
+        for (int g = 0; g < CH; ++g) {
+          if (h0 + g < a.G) {
             const float e = ex2_approx(y[g] - m[g]);
             l[g] += e;
             const __nv_bfloat16 hi = __float2bfloat16_rn(e);
             const __nv_bfloat16 lo = __float2bfloat16_rn(e - __bfloat162float(hi));
-            uint8_t* to = p + g * 128 + ((((r & 63) >> 3) ^ (g & 7)) << 4);  // HI is a multiple of 8
+            // h0 and HI are multiples of 8 (h0 = 0 below 16 heads)
+            uint8_t* to = p + g * 128 + ((((r & 63) >> 3) ^ (g & 7)) << 4);
             *reinterpret_cast<__nv_bfloat16*>(to) = hi;
             *reinterpret_cast<__nv_bfloat16*>(to + HI * 128) = lo;
           }
@@ -599,55 +598,48 @@ __global__ void __launch_bounds__(kThreads, PagedCfg<D, GC>::kCtas)
         if (lane == 0) mbar_arrive(bar(B_P + b));
       }
       // normalisers over the entries
-      reduce_cols<GC, false>(l);
-      const int col = column_of<GC>(lane);
-#pragma unroll
-      for (int i = 0; i < (GC > 32 ? GC / 32 : 1); ++i) sSum[warp * GC + col + i] = l[i];
-      named_bar_sync(2, 128);
+      reduce_cols<CH, false>(l);
+      wSum[quarter * CH + column_of<CH>(lane)] = l[0];
+      named_bar_sync(id_join, 128);
       dead = dead || !wait(B_PV + ((u - 1) & 1), ((u - 1) >> 1) & 1, u);
       tc_fence_after();
-      const bool whole = w.whole();
-      const size_t row0 = (size_t)w.sb * a.hq + w.sh * a.G;
-      // a part of a row: the first of this CTA's range, or the last
-      const size_t at = ((size_t)blockIdx.x * 2 + (part > 0)) * a.G;
+      float o[CH], lo[CH];
 #pragma unroll
-      for (int g0 = 0; g0 < GC; g0 += CH) {
-        float o[CH], lo[CH];
-#pragma unroll
-        for (int i = 0; i < CH; ++i) o[i] = lo[i] = 0.f;
-        if (!dead) {
-          const uint32_t from = lanes + 2 * N + NO * (part & 1) + g0;
-          tmem_ld_cols<CH>(from, o);
-          tmem_ld_cols<CH>(from + HI, lo);
-        }
-#pragma unroll
-        for (int i = 0; i < CH; ++i) o[i] += lo[i];
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          const int g = g0 + i;
-          if (g >= a.G) continue;
-          const float sum = (sSum[g] + sSum[GC + g]) + (sSum[2 * GC + g] + sSum[3 * GC + g]);
-          if (whole) {
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            const __nv_bfloat16 h = __float2bfloat16_rn(sum == 0.f ? 0.f : o[i] * inv);
-            if (r < D) a.o[(row0 + g) * D + r] = *reinterpret_cast<const uint16_t*>(&h);
-            if (WEIGHTS && r == 0) a.stats[row0 + g] = make_float2(m[g], inv);
-          } else {
-            if (r < D) a.parts[(at + g) * D + r] = o[i];
-            if (r == 0) a.part_stats[at + g] = make_float2(m[g], sum);
-          }
-        }
-        __syncwarp();
+      for (int g = 0; g < CH; ++g) o[g] = lo[g] = 0.f;
+      if (!dead) {
+        const uint32_t from = lanes + 2 * N + NO * (part & 1);
+        tmem_ld_cols<CH>(from, o);
+        tmem_ld_cols<CH>(from + HI, lo);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_OE + (part & 1)));
+      const bool whole = w.whole();
+      const size_t row0 = (size_t)w.sb * a.hq + w.sh * a.G + h0;
+      // a part of a row: the first of this CTA's range, or the last
+      const size_t at = ((size_t)blockIdx.x * 2 + (part > 0)) * a.G + h0;
+#pragma unroll
+      for (int g = 0; g < CH; ++g) {
+        if (h0 + g >= a.G) continue;
+        const float sum = (wSum[g] + wSum[CH + g]) + (wSum[2 * CH + g] + wSum[3 * CH + g]);
+        const float v = o[g] + lo[g];
+        if (whole) {
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          const __nv_bfloat16 h = __float2bfloat16_rn(sum == 0.f ? 0.f : v * inv);
+          if (r < D) a.o[(row0 + g) * D + r] = *reinterpret_cast<const uint16_t*>(&h);
+          if (WEIGHTS && r == 0) a.stats[row0 + g] = make_float2(m[g], inv);
+        } else {
+          if (r < D) a.parts[(at + g) * D + r] = v;
+          if (r == 0) a.part_stats[at + g] = make_float2(m[g], sum);
+        }
+      }
+      __syncwarp();
       ++part;
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == kProducts) {
     tc_fence_after();
     tmem_dealloc(tbase, C::kCols);
   }
@@ -672,7 +664,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
   __shared__ long long scan[kJoinThreads / 32 + 2];
   __shared__ float4 s_sum[kJoinThreads];
   __shared__ float2 s_run[R], s_ref[2][kPagedMaxGroup];
-  const int c = blockIdx.x / a.side, at_side = blockIdx.x % a.side, G = a.G;
+  // blocks of the first grid join rows, those of the others add weights
+  const int job = blockIdx.x / a.grid, cta = blockIdx.x - job * a.grid;
+  const int c = cta / a.side, at_side = cta % a.side, G = a.G;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   PagedSpan span;
   const PagedCuts cuts = paged_span(a, c, scan, kJoinThreads, &span);
@@ -682,7 +676,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
   auto part_of = [&](int i, int c0, bool behind) {
     return (((size_t)i * a.side + at_side) * 2 + (i == c0 && behind)) * G;
   };
-  if (!a.whole && c > 0 && c < cuts.n) {
+  if (job == 0) {
+    if (a.whole || c == 0 || c >= cuts.n) return;
     const int tiles = tiles_of(a.cache, span.b), h = span.off / tiles, t = span.off - h * tiles;
     const long long r0 = span.x0 - t;
     if (t > 0) {  // the row of this team's first tile begins before it
@@ -711,10 +706,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
         __syncthreads();
         if (run == 0) {
           float top = kLowest, all = 0.f;
-#pragma unroll
+#pragma unroll 8
           for (int j = 0; j < R; ++j) top = fmaxf(top, s_run[j].x);
           sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
+#pragma unroll 8
           for (int j = 0; j < R; ++j) {
             const float2 st = s_run[j];
             const float e = st.x == top ? 1.f : ex2_approx(st.x - top);
@@ -730,14 +725,14 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
         __syncthreads();
       }
     }
+    return;
   }
 
   // Weights.  A warp has a tile, a lane four of its entries (they share a page).  Rows that are
   // shared are the first and the last of the range: their references come first.
-  if (!a.scores) return;
   int parts = 0;
   {
-    PagedWalk w(a, span);
+    PagedWalk w(a, span, cta);
     long long x = span.x0;
     while (w.next(a)) {
       if (!w.whole() && (parts == 0 || w.left == 0)) {
@@ -763,13 +758,14 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
     }
   }
   __syncthreads();
-  PagedWalk w(a, span);
+  PagedWalk w(a, span, cta);
   long long x = span.x0;
-  int part = 0, next = warp;  // tile of this warp, counted over the range
+  constexpr int kStep = kWeightBlocks * kJoinThreads / 32;
+  int part = 0, next = (job - 1) * (kJoinThreads / 32) + warp;  // this warp's tile of the range
   while (w.next(a)) {
     const int n = w.t1 - w.t0, done = (int)(x - span.x0);
     const float2* ref = w.whole() ? a.stats + (size_t)w.sb * a.hq + w.sh * G : s_ref[part > 0];
-    for (; next < done + n; next += kJoinThreads / 32) {
+    for (; next < done + n; next += kStep) {
       const int e = (w.t0 + next - done) * 128 + 4 * lane;
       if (e >= w.len) continue;
       const float* s =
@@ -804,13 +800,13 @@ template <int D, int GC, bool WEIGHTS>
 cudaError_t launch_t(const PagedArgs& a, const CUtensorMap& mq, const CUtensorMap& mk,
                      const CUtensorMap& mv, cudaStream_t st) {
   using C = PagedCfg<D, GC>;
-  cudaError_t e = dense_prepare<k_paged<D, GC, WEIGHTS>>(kThreads, 0, C::kSmem);
+  cudaError_t e = dense_prepare<k_paged<D, GC, WEIGHTS>>(C::kThreads, 0, C::kSmem);
   if (e != cudaSuccess) return e;
-  k_paged<D, GC, WEIGHTS><<<a.grid, kThreads, C::kSmem, st>>>(mq, mk, mv, a);
+  k_paged<D, GC, WEIGHTS><<<a.grid, C::kThreads, C::kSmem, st>>>(mq, mk, mv, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (a.whole && !WEIGHTS) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.grid);
+  cfg.gridDim = dim3(a.grid * (WEIGHTS ? 1 + kWeightBlocks : 1));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -849,13 +845,19 @@ void paged_shape(PagedArgs* a) {
   while (c.hkv % a->side) --a->side;
   a->groups = c.hkv / a->side;
   const long long row = (c.capacity + 127) / 128;
-  a->whole = row <= kWholeTiles;
+  // One CTA takes a row's tiles one after the other in some 0.85 us each (d = 128); shared out, all
+  // rows together take as long as their bytes, and the join 4 us more.  Measured at 8 heads of
+  // d = 128 (shared, whole, in us): 1 sequence of 3 tiles 8.2, 6.7, of 5 7.9, 8.6; 16 sequences of up
+  // to 7 tiles 16.9, 12.5, 14 tiles 23.4, 20.0, 26 tiles 34.9, 33.0, 51 tiles 56.7, 59.5.
+  const long long rows = (long long)c.nseq * c.hkv;
+  const double tile = c.d == 128 ? 0.85 : 0.7, share = c.d == 128 ? 0.007 : 0.0035;
+  a->whole = row <= kWholeTiles && row * (tile - share * rows) <= 3.5;
   int most = sm_count() * (c.d == 128 ? ctas_of<128>(a->G) : ctas_of<64>(a->G));
   if (most > kPagedMaxGrid) most = kPagedMaxGrid;
   const long long tiles = (long long)c.nseq * a->groups * (a->whole ? 1 : row);
   const int teams = most / a->side > 0 ? most / a->side : 1;
   a->grid = (int)(tiles < teams ? tiles : teams) * a->side;
-  if (a->grid == a->side) a->whole = true;
+  a->direct = a->whole && (long long)c.nseq * a->groups <= a->grid / a->side;
 }
 
 cudaError_t launch_paged(const PagedArgs& a, const uint16_t* q, long long q_stride,

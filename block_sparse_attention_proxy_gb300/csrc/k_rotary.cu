@@ -4,8 +4,8 @@
 //   a' = a cos t - b sin t,  b' = b cos t + a sin t.
 // f is in turns a position, as a fraction of 2^64, so p f modulo a turn is one product of whole
 // numbers that drops what lies above 64 bits: exact at any position, where an angle in fp32
-// is off by radians from some 2^24 on.  The turn's upper 32 bits become half turns in [-1, 1) for
-// sincospif (2^-32 of a turn, below fp32's own step).
+// is off by radians from some 2^24 on.  The turn's upper 32 bits become half turns in [-1, 1)
+// (2^-32 of a turn, below fp32's own step).
 //
 // A thread has 16 elements of a row: 8 pairs (two runs of 8 elements half the rotated part apart,
 // or 16 neighbours), or 16 elements that only move.  It takes 8 sines and cosines once
@@ -18,6 +18,7 @@ namespace msa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr float kPi = 3.14159265358979f;
 
 // Eight elements as fp32.
 template <typename T>
@@ -97,14 +98,23 @@ __device__ __forceinline__ long long position_of(const RotaryArgs& a, int t) {
                                : (long long)__ldg(static_cast<const int*>(a.positions) + t);
 }
 
-// Cosines and sines of 8 pairs from `pair` on at position p.
+// Cosines and sines of 8 pairs from `pair` on at position p.  Results of 16 bits take the hardware's
+// functions, whose error over a turn (2^-21) is far below their rounding: sincospif's
+// instructions for 8 pairs outnumbered those for the rows where a thread has few heads.
+template <typename T>
 __device__ __forceinline__ void turns(const RotaryArgs& a, int pair, long long p, float (&c)[8],
                                       float (&s)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint64_t turn = a.freq[pair + i] * (uint64_t)p;
+    const float half = (float)(int32_t)(turn >> 32);  // 2^-31 half turns, in [-1, 1)
     float sn, cs;
-    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &sn, &cs);
+    if (sizeof(T) == 2) {
+      sn = __sinf(half * (0x1p-31f * kPi));
+      cs = __cosf(half * (0x1p-31f * kPi));
+    } else {
+      sincospif(half * 0x1p-31f, &sn, &cs);
+    }
     c[i] = cs * a.amplitude;
     s[i] = sn * a.amplitude * a.sign;
   }
@@ -179,7 +189,7 @@ __global__ void __launch_bounds__(kThreads)
     pos = position_of(a, p.token);
   }
   float c[8], s[8];
-  if (p.turn) turns(a, p.pair, pos, c, s);
+  if (p.turn) turns<T>(a, p.pair, pos, c, s);
   constexpr int N = 4;  // heads in flight
   for (int h0 = p.slot; h0 < H; h0 += N * a.slots) {
     Eight<T> x[N], y[N];
@@ -240,7 +250,7 @@ __global__ void __launch_bounds__(kThreads)
   const long long pos = a.positions ? position_of(a, t) : entry;
   const int slot = entry & ((1 << cache.page_shift) - 1);
   float c[8], s[8];
-  if (p.turn) turns(a, p.pair, pos, c, s);
+  if (p.turn) turns<T>(a, p.pair, pos, c, s);
   const T* q = static_cast<const T*>(a.q) + (long long)t * a.qs;
   const T* k = static_cast<const T*>(a.k) + (long long)t * a.ks;
   const T* v = static_cast<const T*>(a.v) + (long long)t * a.vs;
@@ -290,10 +300,11 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Threads along a token's heads: as few as still fill the GPU twice over, since each of them
-// takes the sines again.
+// Threads along a token's heads: as few as give each SM 512 threads, since each of them looks its
+// document up and takes the sines again (24001 tokens of 9 heads: 19.1 us with 4096, 14.2 with
+// 2048, 11.6 with 512; 6000 tokens of 40: 17.2, 11.3, 7.8, and 8.7 with 256).
 unsigned grid_of(RotaryArgs& a, int heads) {
-  const long long cols = a.d / 16, want = 2ll * sm_count() * 2048;
+  const long long cols = a.d / 16, want = 512ll * sm_count();
   const long long rows = cols * a.T;
   long long slots = (want + rows - 1) / rows;
   if (slots > heads) slots = heads;

@@ -120,6 +120,7 @@ msa_status check_paged(const msa_cache* c, const msa_table* t, const msa_paged_p
   a->hq = p->hq;
   a->G = p->hq / c->hkv;
   a->scale_log2 = p->softmax_scale * kLog2E;
+  paged_shape(a);
   return MSA_OK;
 }
 
@@ -137,8 +138,10 @@ struct PagedWorkspace {
 PagedWorkspace paged_workspace(const PagedArgs& a, bool accumulate) {
   PagedWorkspace w{};
   Carve c;
-  w.parts = c.take((size_t)kPagedMaxGrid * 2 * a.G * a.cache.d * sizeof(float));
-  w.part_stats = c.take((size_t)kPagedMaxGrid * 2 * a.G * sizeof(float2));
+  if (!a.whole) {
+    w.parts = c.take((size_t)kPagedMaxGrid * 2 * a.G * a.cache.d * sizeof(float));
+    w.part_stats = c.take((size_t)kPagedMaxGrid * 2 * a.G * sizeof(float2));
+  }
   if (accumulate) {
     w.stats = c.take((size_t)a.cache.nseq * a.hq * sizeof(float2));
     w.scores = c.take((size_t)a.cache.nseq * a.cache.hkv * ((a.cache.capacity + 127) / 128) * a.G *
@@ -157,8 +160,10 @@ msa_status evict_workspace(const CacheArgs& a, int keep, EvictWorkspace* w) {
   const int most = std::max(0, std::min(keep, a.capacity - keep));
   Carve c;
   w->most = most;
-  w->count = c.take((size_t)a.nseq * a.hkv * sizeof(int32_t));
-  w->pairs = c.take((size_t)a.nseq * a.hkv * 2 * most * sizeof(int64_t));
+  if (!evict_on_chip(a, most)) {
+    w->count = c.take((size_t)a.nseq * a.hkv * sizeof(int32_t));
+    w->pairs = c.take((size_t)a.nseq * a.hkv * 2 * most * sizeof(int64_t));
+  }
   w->total = c.total;
   // blocks of the largest grid: 8 of a row, or one for 8 pairs
   return (long long)a.nseq * a.hkv * std::max((most + 7) / 8, 8) > 0x7fffffffll ? MSA_ERR_UNSUPPORTED
@@ -255,7 +260,7 @@ size_t msa_paged_attention_workspace_size(const msa_cache* cache, const msa_tabl
   PagedArgs a;
   long long qs;
   if (check_paged(cache, table, p, &a, &qs) != MSA_OK) return 0;
-  return paged_workspace(a, p->accumulate != 0).total;
+  return std::max<size_t>(paged_workspace(a, p->accumulate != 0).total, 256);
 }
 
 msa_status msa_paged_attention(const msa_cache* cache, const msa_table* table,
@@ -269,7 +274,7 @@ msa_status msa_paged_attention(const msa_cache* cache, const msa_table* table,
   if ((st = check_cache_pointers(a.cache)) != MSA_OK) return st;
   if (!q || !o || !aligned(q, 16) || !aligned(o, 16)) return MSA_ERR_INVALID_ARG;
   const PagedWorkspace w = paged_workspace(a, p->accumulate != 0);
-  if (!ws || !aligned(ws, 256)) return MSA_ERR_INVALID_ARG;
+  if ((w.total > 0 && !ws) || !aligned(ws, 256)) return MSA_ERR_INVALID_ARG;
   if (ws_bytes < w.total) return MSA_ERR_WORKSPACE;
   if (bind_device(&a.cache.status) != cudaSuccess) return MSA_ERR_CUDA;
   uint8_t* base = static_cast<uint8_t*>(ws);
@@ -280,7 +285,6 @@ msa_status msa_paged_attention(const msa_cache* cache, const msa_table* table,
     a.stats = reinterpret_cast<float2*>(base + w.stats);
     a.scores = reinterpret_cast<float*>(base + w.scores);
   }
-  paged_shape(&a);
   if (launch_paged(a, q, qs, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
     return MSA_ERR_CUDA;
   add_launches(a.whole && !p->accumulate ? 1 : 2);
@@ -310,7 +314,7 @@ msa_status msa_cache_evict(const msa_cache* cache, const msa_table* table, int32
   const size_t bytes = (size_t)a.cache.nseq * 4;
   if (!new_lens || !aligned(new_lens, 4) || overlap(new_lens, bytes, a.cache.lens, bytes))
     return MSA_ERR_INVALID_ARG;
-  if (!ws || !aligned(ws, 256)) return MSA_ERR_INVALID_ARG;
+  if ((w.total > 0 && !ws) || !aligned(ws, 256)) return MSA_ERR_INVALID_ARG;
   if (ws_bytes < w.total) return MSA_ERR_WORKSPACE;
   if (status_ptr(&a.cache.status) != cudaSuccess) return MSA_ERR_CUDA;
   uint8_t* base = static_cast<uint8_t*>(ws);

@@ -414,7 +414,7 @@ typedef struct msa_paged_params {
 
 /* Workspace bytes of msa_paged_attention (0 if an argument is invalid).  With
    `accumulate` 4 bytes a query head for every entry that the table can name: a view of the
-   table's first columns makes it smaller. */
+   table's first columns makes it smaller.  Where it says 256 none is used, and it may be null. */
 size_t msa_paged_attention_workspace_size(const msa_cache* cache, const msa_table* table,
                                           const msa_paged_params* params);
 msa_status msa_paged_attention(const msa_cache* cache, const msa_table* table,
@@ -428,7 +428,8 @@ msa_status msa_paged_attention(const msa_cache* cache, const msa_table* table,
  * stay and lie behind the first `keep` move, k, v, weight and position, into the places of
  * entries that leave, both taken in ascending order; nothing else is written.  new_lens [num_seqs]
  * gets min(lens, keep); it must not overlap the table's lens.  Needs weight, and position with
- * recent > 0; 0 <= recent <= keep, keep >= 1.
+ * recent > 0; 0 <= recent <= keep, keep >= 1.  A workspace size of 256 says that none is used; it
+ * may then be null.
  */
 size_t msa_cache_evict_workspace_size(const msa_cache* cache, const msa_table* table,
                                       int32_t keep);

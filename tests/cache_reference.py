@@ -4,7 +4,9 @@ results of kernels that compute in fp32 from 16-bit operands.
 Rotary.  A turn is exact to 2^-32 before it becomes a float in [-1, 1) (2^-25 of half a turn:
 less than 2^-23 radians), sine and cosine are off by at most 2^-23 more, the amplitude's product
 and the two products' sum by 2^-24 each of |a| + |b|: together 2^-21 amplitude (|a| + |b|),
-and the rounding of the result, half a step.
+and the rounding of the result, half a step.  For 16-bit results sine and cosine are the hardware's,
+whose error is given as at most 2^-21.19 between -pi and pi: 2^-21.19 + 2^-23 + 2 * 2^-24 = 1.13 *
+2^-21, within 2^-20.
 
 Attention.  U = 2^-8, half a bf16 step.  A score is a sum of at most 128 products accumulated in
 fp32, each addition off by at most 2^-23 of A = sum |q||k| scale: 2^-16 A; exponentials, sums
@@ -41,7 +43,7 @@ def rotary_exact(x, positions, frequencies, interleaved=False, amplitude=1.0, in
             (slice(0, n), slice(n, 2 * n)))
     out, lim = y.clone(), torch.zeros_like(y)
     out[..., a], out[..., b] = y[..., a] * c - y[..., b] * s, y[..., b] * c + y[..., a] * s
-    size = 2.0 ** -21 * abs(amplitude) * (y[..., a].abs() + y[..., b].abs())
+    size = 2.0 ** (-21 if x.dtype == torch.float32 else -20) * abs(amplitude) * (y[..., a].abs() + y[..., b].abs())
     lim[..., a] = lim[..., b] = size
     turned = torch.zeros(y.shape[-1], dtype=torch.bool)
     turned[:2 * n] = True

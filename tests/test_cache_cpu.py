@@ -92,7 +92,7 @@ def _cache(m, **kw):
 
 
 def _table(m, **kw):
-    return m._abi.MsaTable(**{**dict(pages=P, lens=P, num_seqs=3, max_pages=4, stride=4), **kw})
+    return m._abi.MsaTable(**{**dict(pages=P, lens=P, num_seqs=3, max_pages=16, stride=16), **kw})
 
 
 BAD_CACHES = [(1, dict(num_pages=0)), (1, dict(hkv=0)), (2, dict(d=96)), (2, dict(d=256)),
@@ -100,11 +100,11 @@ BAD_CACHES = [(1, dict(num_pages=0)), (1, dict(hkv=0)), (2, dict(d=96)), (2, dic
               (2, dict(page_size=0)), (2, dict(hkv=1025)), (1, dict(k_page_stride=0)),
               (1, dict(k_slot_stride=-128)), (1, dict(v_head_stride=60)),
               (1, dict(v_page_stride=1 << 38))]
-BAD_TABLES = [(1, dict(num_seqs=-1)), (1, dict(max_pages=0)), (1, dict(stride=3)),
+BAD_TABLES = [(1, dict(num_seqs=-1)), (1, dict(max_pages=0)), (1, dict(stride=15)),
               (2, dict(num_seqs=1 << 20)), (2, dict(max_pages=1 << 24, stride=1 << 24))]
 
 
-def _calls(m, cache, table, hq=4, keep=10, recent=2, ws=1 << 30, **ptr):
+def _calls(m, cache, table, hq=4, keep=500, recent=2, ws=1 << 30, **ptr):
     """Status of attention and eviction with everything else in order."""
     lib, by = m.load(), ctypes.byref
     p = m.make_paged_params(hq)
@@ -146,7 +146,7 @@ def test_bad_pointers_and_workspaces(m):
         assert _calls(m, *ok, **kw)[1] == 1
     prm = m.make_paged_params(4)
     assert _calls(m, *ok, ws=m.msa_paged_attention_workspace_size(*ok, prm) - 1)[0] == 3
-    assert _calls(m, *ok, ws=m.msa_cache_evict_workspace_size(*ok, 10) - 1)[1] == 3
+    assert _calls(m, *ok, ws=m.msa_cache_evict_workspace_size(*ok, 500) - 1)[1] == 3
 
 
 def test_bad_numbers(m):
@@ -172,14 +172,19 @@ def test_bad_numbers(m):
 
 
 def test_workspace_of_the_weights(m):
-    """4 bytes a query head for every entry that the table names, beside the shared rows' parts."""
+    """4 bytes a query head for every entry that the table names (a row's rounded up to 128), beside
+    the shared rows' parts."""
     plain = m.msa_paged_attention_workspace_size(_cache(m), _table(m), m.make_paged_params(4))
     prm = m.make_paged_params(4, accumulate=True)
-    for pages in (2, 4, 64):
+    for pages in (16, 17, 64):
         more = m.msa_paged_attention_workspace_size(_cache(m), _table(m, max_pages=pages, stride=pages),
                                                     prm) - plain
-        assert 0 <= more - 3 * 4 * pages * 64 * 4 <= 512
-    assert plain < 4 << 20
+        assert 0 <= more - 3 * 4 * -(-pages * 64 // 128) * 128 * 4 <= 512
+    assert 256 < plain < 4 << 20
+    short = _table(m, max_pages=8, stride=8)  # rows that one CTA takes whole need none
+    assert m.msa_paged_attention_workspace_size(_cache(m), short, m.make_paged_params(4)) == 256
+    assert m.msa_cache_evict_workspace_size(_cache(m), short, 256) == 256  # few moves
+    assert m.msa_cache_evict_workspace_size(_cache(m), _table(m), 257) > 6 * 2 * 257 * 8
 
 
 def test_bad_rotations(m):

@@ -620,7 +620,7 @@ def test_refusals():
 def test_c_entry_points_give_the_functions_results():
     """With workspaces of the size that is asked for, full of NaN; one byte less is refused."""
     m = _m()
-    lens, hq = [190, 77, 0], 6
+    lens, hq = [1900, 770, 0], 6
     cache, table, n = _filled([x + 1 for x in lens], 32, 2, 64, 58)
     n = n - 1
     q, k, v = (_normal(3, h, 64, seed=59 + h) for h in (hq, 2, 3))
@@ -628,7 +628,7 @@ def test_c_entry_points_give_the_functions_results():
     plan, other = m.rotary_plan(32), m.PagedCache(*(x.clone() for x in cache))
     rq = m.cache_append(cache, k, v, table, n, plan=plan, q=q)
     o = m.paged_attention(rq, cache, table, n + 1, 0.3, accumulate=True)
-    left = m.cache_evict(cache, table, n + 1, 60, 9)
+    left = m.cache_evict(cache, table, n + 1, 600, 9)
 
     c, t = m.make_cache(other), m.make_table(table, n)
     rp = m.make_rotary_params(3, hq, 2, 64, plan.frequencies)
@@ -643,8 +643,8 @@ def test_c_entry_points_give_the_functions_results():
     nan = lambda size: torch.full((-(-size // 4),), float("nan"), device="cuda").view(torch.uint8)[:size]  # noqa: E731
     for call, size in ((lambda ws: m.msa_paged_attention(c, t, prm, rq, got, ws),
                         m.msa_paged_attention_workspace_size(c, t, prm)),
-                       (lambda ws: m.msa_cache_evict(c, t, 60, 9, n, ws),
-                        m.msa_cache_evict_workspace_size(c, t, 60))):
+                       (lambda ws: m.msa_cache_evict(c, t, 600, 9, n, ws),
+                        m.msa_cache_evict_workspace_size(c, t, 600))):
         with pytest.raises(m.MsaError) as error:
             call(nan(size)[:-1])
         assert error.value.status == 3
