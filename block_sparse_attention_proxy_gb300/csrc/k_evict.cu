@@ -105,14 +105,27 @@ __device__ __forceinline__ uint32_t ld_peer(const void* p, uint32_t rank) {
 template <bool KEYS, bool FUSED>
 __global__ void __launch_bounds__(kListThreads, 2)
     k_evict_list(const __grid_constant__ EvictArgs a, int blocks, int slice) {
-  extern __shared__ __align__(16) uint32_t s_key[];  // slice ranks, slice positions
-  __shared__ int s_hist[4][256], s_all[256], s_sum[32], s_pick[3], s_share[4];
+  // ranks, positions, and the pages of 16 entries each
+  extern __shared__ __align__(16) uint32_t s_key[];
+  __shared__ int s_hist[4][256], s_all[256], s_sum[32], s_share[4];
   int* s_pos = reinterpret_cast<int*>(s_key + (KEYS ? slice : 0));
+  int* s_page = s_pos + (KEYS ? slice : 0);
   const CacheArgs& c = a.cache;
   const int row = blockIdx.x / blocks, rank = blockIdx.x - row * blocks;
   const int b = row / c.hkv, h = row - b * c.hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // The first pages that this thread needs do not wait for the length.
+  constexpr int kBatch = 4;
+  const int* table = c.table + (long long)b * c.table_stride;
+  int early[kBatch];
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j) {
+    const int i = 4 * (tid + j * threads);
+    early[j] = i < slice && i < c.capacity - rank * slice
+                   ? __ldg(table + ((rank * slice + i) >> c.page_shift))
+                   : -1;
+  }
   const int n = cache_len(c, b);
   if (h == 0 && rank == 0 && tid == 0) a.new_lens[b] = min(n, a.keep);
   if (n <= a.keep) {
@@ -149,26 +162,43 @@ __global__ void __launch_bounds__(kListThreads, 2)
   for (int i = tid; i < 4 * 256; i += threads) (&s_hist[0][0])[i] = 0;
   // Weights and positions, four entries at a time: pages begin at multiples of 16.
   int newest = INT_MIN;
-#pragma unroll 4
-  for (int i = begin + 4 * tid; i < end; i += 4 * threads) {
-    const long long m = place(i);
-    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-    int4 p = make_int4(INT_MIN, INT_MIN, INT_MIN, INT_MIN);
-    if (m >= 0) {
-      if (KEYS) w = __ldcg(reinterpret_cast<const float4*>(c.weight + m));
-      if (a.recent > 0) p = __ldcg(reinterpret_cast<const int4*>(c.position + m));
+  for (int i0 = begin + 4 * tid; i0 < end; i0 += 4 * kBatch * threads) {
+    int page[kBatch];
+    float4 w[kBatch];
+    int4 p[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = i0 + 4 * j * threads;
+      page[j] = -1;
+      if (i < end) page[j] = i0 == begin + 4 * tid ? early[j] : __ldg(table + (i >> c.page_shift));
+      if (i < end && (unsigned)page[j] >= (unsigned)c.num_pages) {
+        set_status(c.status, MSA_ERR_DEVICE_CHECK);
+        page[j] = -1;
+      }
     }
-    const int k = end - i;
-    newest = max(newest, p.x);
-    if (k > 1) newest = max(newest, p.y);
-    if (k > 2) newest = max(newest, p.z);
-    if (k > 3) newest = max(newest, p.w);
-    if (KEYS) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      w[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      p[j] = make_int4(INT_MIN, INT_MIN, INT_MIN, INT_MIN);
+      if (page[j] < 0) continue;
+      const long long m = c.meta(page[j], (i0 + 4 * j * threads) & mask, h);
+      if (KEYS) w[j] = __ldcg(reinterpret_cast<const float4*>(c.weight + m));
+      if (a.recent > 0) p[j] = __ldcg(reinterpret_cast<const int4*>(c.position + m));
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = i0 + 4 * j * threads, k = end - i;
+      if (k > 0) newest = max(newest, p[j].x);
+      if (k > 1) newest = max(newest, p[j].y);
+      if (k > 2) newest = max(newest, p[j].z);
+      if (k > 3) newest = max(newest, p[j].w);
+      if (!KEYS || k <= 0) continue;
       // a page that the table does not name ranks lowest
-      const uint4 x = m < 0 ? make_uint4(0, 0, 0, 0)
-                            : make_uint4(rank_of(w.x), rank_of(w.y), rank_of(w.z), rank_of(w.w));
-      *reinterpret_cast<uint4*>(s_key + i - begin) = x;
-      *reinterpret_cast<int4*>(s_pos + i - begin) = p;
+      *reinterpret_cast<uint4*>(s_key + i - begin) =
+          page[j] < 0 ? make_uint4(0, 0, 0, 0)
+                      : make_uint4(rank_of(w[j].x), rank_of(w[j].y), rank_of(w[j].z), rank_of(w[j].w));
+      *reinterpret_cast<int4*>(s_pos + i - begin) = p[j];
+      if (i % 16 == 0) s_page[(i - begin) / 16] = page[j];
     }
   }
   long long limit = LLONG_MAX;  // positions from here on stay
@@ -180,7 +210,7 @@ __global__ void __launch_bounds__(kListThreads, 2)
     if (blocks > 1) {
       if (tid == 0) s_share[0] = newest;
       sync();
-      for (int r = 0; r < blocks; ++r) newest = max(newest, (int)ld_peer(&s_share[0], r));
+      newest = __reduce_max_sync(0xffffffffu, (int)ld_peer(&s_share[0], lane & (blocks - 1)));
     }
     limit = (long long)newest - a.recent + 1;
   } else {
@@ -209,7 +239,7 @@ __global__ void __launch_bounds__(kListThreads, 2)
   long long* from = on_chip ? s_pairs : a.pairs + (size_t)row * 2 * a.most;
   long long* to = from + (on_chip ? kMostFused : a.most);
   auto entry = [&](int i) -> long long {  // its place in the cache
-    const int page = cache_page(c, b, i);
+    const int page = KEYS && i >= begin && i < end ? s_page[(i - begin) / 16] : cache_page(c, b, i);
     return page < 0 ? -1 : ((long long)page << c.page_shift) + (i & mask);
   };
 
@@ -292,33 +322,27 @@ __global__ void __launch_bounds__(kListThreads, 2)
       s_all[i] = gather(&s_hist[d][i], &before);
     }
     __syncthreads();
-    if (warp == 0) {  // from the top: the first digit at which `left` are reached
-      int x[8], mine = 0;
+    // from the top: the first digit at which `left` are reached
+    int x[8], mine = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) mine += x[i] = s_all[255 - 8 * lane - i];
-      int incl = mine;
+    for (int i = 0; i < 8; ++i) mine += x[i] = s_all[255 - 8 * lane - i];
+    int incl = mine;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int z = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += z;
-      }
-      int before = incl - mine;
-      if (before < left && left <= incl) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (before < left && left <= before + x[i]) {
-            s_pick[0] = 255 - 8 * lane - i;
-            s_pick[1] = left - before;
-            s_pick[2] = x[i];
-          }
-          before += x[i];
-        }
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += z;
     }
-    __syncthreads();
-    edge |= (uint32_t)s_pick[0] << shift;
-    left = s_pick[1];
-    equal = s_pick[2];
+    int before = incl - mine, digit = 0, of = 0, rest = 0;
+    const uint32_t here = __ballot_sync(0xffffffffu, before < left && left <= incl);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (before < left && left <= before + x[i]) digit = 255 - 8 * lane - i, rest = left - before, of = x[i];
+      before += x[i];
+    }
+    const int at = __ffs(here) - 1;
+    edge |= (uint32_t)__shfl_sync(0xffffffffu, digit, at) << shift;
+    left = __shfl_sync(0xffffffffu, rest, at);
+    equal = __shfl_sync(0xffffffffu, of, at);
     if (equal == left) break;  // the lower digits decide nothing
   }
 
@@ -341,22 +365,25 @@ __global__ void __launch_bounds__(kListThreads, 2)
   } else {
     left = INT_MAX;
   }
-  auto walk = [&](auto each) {  // each(entry, in range, stays)
-    int tie = tie0;
-    for (int i = first; i < last; i += 32) {
-      const bool in = i + lane < last;
-      const uint32_t x = in ? key(i + lane) : 0;
-      const uint32_t eq = __ballot_sync(0xffffffffu, in && x == edge);
-      const bool stays = in && (x > edge || (x == edge && tie + __popc(eq & below) < left));
-      tie += __popc(eq);
-      each(i + lane, in, stays);
-    }
+  // Whether entries i + lane of this warp's run stay; `tie` counts those equal to the edge.
+  const bool all_equal = left == INT_MAX;
+  auto stay = [&](int i, int& tie) {
+    const uint32_t x = i + lane < last ? key(i + lane) : 0;
+    if (all_equal) return x >= edge;
+    const uint32_t eq = __ballot_sync(0xffffffffu, i + lane < last && x == edge);
+    const bool s = x > edge || (x == edge && tie + __popc(eq & below) < left);
+    tie += __popc(eq);
+    return s;
   };
-  int outs = 0, ins = 0;
-  walk([&](int i, bool in, bool stays) {
-    outs += __popc(__ballot_sync(0xffffffffu, in && stays && i >= a.keep));
-    ins += __popc(__ballot_sync(0xffffffffu, in && !stays && i < a.keep));
-  });
+  int outs = 0, ins = 0, tie = tie0;
+#pragma unroll 4
+  for (int i = first; i < last; i += 32) {
+    const bool s = stay(i, tie), in = i + lane < last;
+    outs += in && s && i + lane >= a.keep;
+    ins += in && !s && i + lane < a.keep;
+  }
+  outs = __reduce_add_sync(0xffffffffu, outs);
+  ins = __reduce_add_sync(0xffffffffu, ins);
   int all_in, into = warp_base(ins, s_sum, &all_in), out = warp_base(outs, s_sum, &total);
   if (blocks > 1) {
     if (tid == 0) s_share[2] = total, s_share[3] = all_in;
@@ -366,14 +393,17 @@ __global__ void __launch_bounds__(kListThreads, 2)
     gather(&s_share[3], &before);
     into += before;
   }
-  walk([&](int i, bool in, bool stays) {
-    const bool o = in && stays && i >= a.keep, t = in && !stays && i < a.keep;
+  tie = tie0;
+#pragma unroll 4
+  for (int i = first; i < last; i += 32) {
+    const bool s = stay(i, tie), in = i + lane < last;
+    const bool o = in && s && i + lane >= a.keep, t = in && !s && i + lane < a.keep;
     const uint32_t vo = __ballot_sync(0xffffffffu, o), vt = __ballot_sync(0xffffffffu, t);
-    if (o) from[out + __popc(vo & below)] = entry(i);
-    if (t) to[into + __popc(vt & below)] = entry(i);
+    if (o) from[out + __popc(vo & below)] = entry(i + lane);
+    if (t) to[into + __popc(vt & below)] = entry(i + lane);
     out += __popc(vo);
     into += __popc(vt);
-  });
+  }
   if (!FUSED && rank == 0 && tid == 0) a.count[row] = total;
   sync();  // the lists are whole; nobody reads a block's shared memory any more
   if (FUSED) {
@@ -396,16 +426,16 @@ __global__ void __launch_bounds__(32) k_evict_move(const __grid_constant__ Evict
 template <bool KEYS, bool FUSED>
 cudaError_t list(const EvictArgs& a, int rows, int blocks, int slice, int threads,
                  cudaStream_t st) {
-  const cudaError_t e = dense_prepare<k_evict_list<KEYS, FUSED>>(0, 0, KEYS ? kMostKeys * 8 : 0);
+  const cudaError_t e = dense_prepare<k_evict_list<KEYS, FUSED>>(0, 0, KEYS ? kMostKeys * 8 + kMostKeys / 4 : 0);
   if (e != cudaSuccess) return e;
   if (blocks == 1) {
-    k_evict_list<KEYS, FUSED><<<rows, threads, KEYS ? slice * 8 : 0, st>>>(a, 1, slice);
+    k_evict_list<KEYS, FUSED><<<rows, threads, KEYS ? slice * 8 + slice / 4 : 0, st>>>(a, 1, slice);
     return cudaGetLastError();
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * blocks));
   cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = KEYS ? slice * 8 : 0;
+  cfg.dynamicSmemBytes = KEYS ? slice * 8 + slice / 4 : 0;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;

@@ -60,6 +60,11 @@ struct PagedCfg {
   static_assert(kRing >= 3 && kCols * kCtas <= 512, "budgets");
 };
 
+// a / b of numbers that are not negative; in 32 bits, a fifth of the instructions, where they fit.
+__host__ __device__ inline long long quotient(long long a, long long b) {
+  return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
 // How the tiles of all rows are shared out.  Team c of the n that get any takes the tiles from
 // cut(c) on: per or per + 1 of them.
 struct PagedCuts {
@@ -67,7 +72,7 @@ struct PagedCuts {
   int more, n;  // teams with per + 1 tiles; teams with tiles
   __host__ __device__ PagedCuts(long long tiles, int teams) : total(tiles) {
     n = tiles < teams ? (int)tiles : teams;
-    per = n > 0 ? tiles / n : 0;
+    per = n > 0 ? quotient(tiles, n) : 0;
     more = n > 0 ? (int)(tiles - per * n) : 0;
   }
   __host__ __device__ long long cut(int c) const {
@@ -76,7 +81,7 @@ struct PagedCuts {
   // The team that has tile x.
   __host__ __device__ int team_of(long long x) const {
     const long long big = (per + 1) * more;
-    return (int)(x < big ? x / (per + 1) : more + (x - big) / per);
+    return (int)(x < big ? quotient(x, per + 1) : more + quotient(x - big, per));
   }
 };
 
@@ -386,22 +391,25 @@ __global__ void __launch_bounds__(PagedCfg<D, GC>::kThreads, PagedCfg<D, GC>::kC
     const int box = lane / NCH, ch = lane % NCH;         // one box of a tile per lane
     int s = 0, round = 0, part = 0;
     bool ok = true;
-    auto load = [&](const CUtensorMap* tm, int b, int h, int len, int t) {
-      const int valid = min(128, len - t * 128), n = (valid + rows - 1) / rows;  // entries, boxes
-      int page = 0;
+    // The page of this lane's box of a tile.  It is looked up a tile ahead, and kept for the values.
+    auto page_of = [&](int b, int len, int t) {
       const int e = t * 128 + box * rows;
-      if (box < n) page = max(0, cache_page(a.cache, b, e));
+      return box * rows < 128 && e < len ? max(0, cache_page(a.cache, b, e)) : 0;
+    };
+    auto load = [&](const CUtensorMap* tm, int h, int len, int t, int page) {
+      const int valid = min(128, len - t * 128), n = (valid + rows - 1) / rows;  // entries, boxes
       if (round > 0 && !(ok = wait(B_E + s, (round & 1) ^ 1, t))) return;
       if (lane == 0) mbar_arrive_expect_tx(bar(B_F + s), n * rows * NCH * 128);
       __syncwarp();
       if (box < n)
         tma_load_4d(smem_u32(sKV + s * C::kTile) + ch * 16384 + box * rows * 128, tm, bar(B_F + s),
-                    64 * ch, h, e & ((1 << a.cache.page_shift) - 1), page);
+                    64 * ch, h, (t * 128 + box * rows) & ((1 << a.cache.page_shift) - 1), page);
       if (++s == NR) s = 0, ++round;
     };
-    struct { int b, h, len, t; } last{-1, 0, 0, 0};
+    struct { int h, len, t, page; } last{0, 0, -1, 0};
     PagedWalk w(a, span, blockIdx.x);
     while (ok && w.next(a)) {
+      int page = page_of(w.sb, w.len, w.t0);
       if (part >= 2 && !(ok = wait(B_QE + (part & 1), ((part >> 1) & 1) ^ 1, part))) break;
       if (lane == 0) mbar_arrive_expect_tx(bar(B_Q + (part & 1)), C::kQ);
       __syncwarp();
@@ -410,12 +418,13 @@ __global__ void __launch_bounds__(PagedCfg<D, GC>::kThreads, PagedCfg<D, GC>::kC
                     bar(B_Q + (part & 1)), 64 * lane, 0, w.sh, w.sb);
       ++part;
       for (int t = w.t0; ok && t < w.t1; ++t) {
-        load(&tm_k, w.sb, w.sh, w.len, t);
-        if (ok && last.b >= 0) load(&tm_v, last.b, last.h, last.len, last.t);
-        last = {w.sb, w.sh, w.len, t};
+        load(&tm_k, w.sh, w.len, t, page);
+        if (ok && last.t >= 0) load(&tm_v, last.h, last.len, last.t, last.page);
+        last = {w.sh, w.len, t, page};
+        page = page_of(w.sb, w.len, min(t + 1, w.t1 - 1));
       }
     }
-    if (ok && last.b >= 0) load(&tm_v, last.b, last.h, last.len, last.t);
+    if (ok && last.t >= 0) load(&tm_v, last.h, last.len, last.t, last.page);
     // sequences without an entry: no tile names them
     for (int b = blockIdx.x; b < a.cache.nseq; b += gridDim.x)
       if (cache_len(a.cache, b) == 0)
@@ -689,7 +698,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
         // every run with a reference of its own, so that sums need not wait for the references
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
         float m = kLowest, l = 0.f;
-#pragma unroll 4
+#pragma unroll 8
         for (int i = c0 + run; i <= c1; i += R) {
           const size_t at = part_of(i, c0, behind) + g;
           const float2 st = __ldcg(&a.part_stats[at]);
