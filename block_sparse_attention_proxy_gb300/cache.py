@@ -22,7 +22,6 @@ table [sequences, pages] and lens [sequences] integers on the device (int32 is t
 from __future__ import annotations
 
 import math
-from fractions import Fraction
 from typing import NamedTuple, Optional
 
 import torch
@@ -31,8 +30,14 @@ from . import dense
 
 _front = None
 
-# 2 pi to 60 digits, from the arctangents of 1/5 and 1/239 (Machin)
-_TWO_PI = None
+_DIGITS = 10 ** 60
+
+
+def _arctan(n):  # of 1 / n, times 10^60, rounded down term by term: off by less than 100
+    return sum((-1) ** i * _DIGITS // ((2 * i + 1) * n ** (2 * i + 1)) for i in range(45))
+
+
+_TWO_PI = 32 * _arctan(5) - 8 * _arctan(239)  # times 10^60, right to 56 digits (Machin's formula)
 
 
 def _load():
@@ -45,14 +50,10 @@ def _load():
     return _front
 
 
-def _two_pi() -> Fraction:
-    global _TWO_PI
-    if _TWO_PI is None:
-        def arctan(n):
-            return sum(Fraction((-1) ** i, (2 * i + 1) * n ** (2 * i + 1)) for i in range(45))
-
-        _TWO_PI = Fraction(round((32 * arctan(5) - 8 * arctan(239)) * 10 ** 60), 10 ** 60)
-    return _TWO_PI
+def _turns(f: float) -> int:
+    """Radians a position as turns a position modulo one, a fraction of 2^64."""
+    n, d = f.as_integer_ratio()
+    return ((n * _DIGITS << 65) // (d * _TWO_PI) + 1 >> 1) % 2 ** 64
 
 
 def rotary_plan(dims: int, base: float = 10000.0, interleaved: bool = False, stretch: float = 1.0,
@@ -88,9 +89,8 @@ def rotary_plan(dims: int, base: float = 10000.0, interleaved: bool = False, str
     frequencies = [float(f) for f in frequencies]
     if len(frequencies) != dims // 2 or not all(map(math.isfinite, frequencies)):
         raise ValueError("dims / 2 finite frequencies expected")
-    # turns a position modulo one, as fractions of 2^64
-    words = [round(Fraction(f) / _two_pi() * 2 ** 64) % 2 ** 64 for f in frequencies]
-    return (_front or _load()).RotaryPlan(words, bool(interleaved), float(amplitude))
+    return (_front or _load()).RotaryPlan([_turns(f) for f in frequencies], bool(interleaved),
+                                          float(amplitude))
 
 
 def rotary(q, k, plan, cu_seqlens=None, positions=None):

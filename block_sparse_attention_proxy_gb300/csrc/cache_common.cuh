@@ -86,6 +86,31 @@ struct PagedArgs {
   float2* stats;       // [nseq][hq] reference and 1 / normaliser of whole rows (with scores)
   float* scores;       // [tile][G][128] in log2 units; null: no weights asked for
 };
+// a / b of numbers that are not negative; in 32 bits, a fifth of the instructions, where they fit.
+__host__ __device__ inline long long quotient(long long a, long long b) {
+  return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
+// How the tiles of all rows are shared out.  Team c of the n that get any takes the tiles from
+// cut(c) on: per or per + 1 of them.
+struct PagedCuts {
+  long long total, per;
+  int more, n;  // teams with per + 1 tiles; teams with tiles
+  __host__ __device__ PagedCuts(long long tiles, int teams) : total(tiles) {
+    n = tiles < teams ? (int)tiles : teams;
+    per = n > 0 ? quotient(tiles, n) : 0;
+    more = n > 0 ? (int)(tiles - per * n) : 0;
+  }
+  __host__ __device__ long long cut(int c) const {
+    return c >= n ? total : per * c + (c < more ? c : more);
+  }
+  // The team that has tile x.
+  __host__ __device__ int team_of(long long x) const {
+    const long long big = (per + 1) * more;
+    return (int)(x < big ? quotient(x, per + 1) : more + quotient(x - big, per));
+  }
+};
+
 void paged_shape(PagedArgs* a);
 cudaError_t launch_paged(const PagedArgs& a, const uint16_t* q, long long q_stride,
                          cudaStream_t st);

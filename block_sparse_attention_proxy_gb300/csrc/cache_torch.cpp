@@ -246,7 +246,8 @@ struct Pages {
     table.max_pages = (int32_t)pages.size(1);
     table.stride = pages.stride(0);
   }
-  // what a call has written in place
+  // What a call writes in place; said before it does, so that a tensor that must not be written
+  // is refused.
   void changed(bool rows, bool position_too) {
     if (rows) {
       torch::autograd::impl::bump_version(k);
@@ -330,10 +331,10 @@ std::optional<Tensor> cache_append(const Tensor& ck, const Tensor& cv,
     p.hq = (int32_t)q.size(1);
     qo = at::empty(q.sizes(), q.options().requires_grad(false));
   }
+  c.changed(true, true);
   raise_on(msa_cache_append(&c.cache, &c.table, &p, v_stride, ints_in(cu32), any_in(at_), in(q__),
                             in(k_), in(v_), out(qo), current_stream()),
            "msa_cache_append");
-  c.changed(true, true);
   if (!qo.defined()) return std::nullopt;
   return qo;
 }
@@ -363,10 +364,10 @@ Tensor paged_attention(const Tensor& q, const Tensor& ck, const Tensor& cv,
   const size_t need = msa_paged_attention_workspace_size(&c.cache, &c.table, &p);
   Tensor ws;
   if (need > 256) ws = at::empty({(int64_t)need}, opt.dtype(at::kByte));
+  if (accumulate) c.changed(false, false);
   raise_on(msa_paged_attention(&c.cache, &c.table, &p, in(q_), out(o), any_out(ws), need,
                                current_stream()),
            "msa_paged_attention");
-  if (accumulate) c.changed(false, false);
   return o;
 }
 
@@ -387,10 +388,10 @@ Tensor cache_evict(const Tensor& ck, const Tensor& cv, const std::optional<Tenso
   const size_t need = msa_cache_evict_workspace_size(&c.cache, &c.table, (int32_t)keep);
   Tensor ws;
   if (need > 256) ws = at::empty({(int64_t)need}, c.lens.options().dtype(at::kByte));
+  c.changed(true, true);
   raise_on(msa_cache_evict(&c.cache, &c.table, (int32_t)keep, (int32_t)recent,
                            left.mutable_data_ptr<int32_t>(), any_out(ws), need, current_stream()),
            "msa_cache_evict");
-  c.changed(true, true);
   return left;
 }
 

@@ -227,6 +227,42 @@ def test_bad_appends(m):
     assert call(cu=P, num_docs=3, total_tokens=0, q=0, k=0, v=0) == 0
 
 
+CUTS = r"""
+#include <cstdio>
+#include "cache_common.cuh"
+using namespace msa;
+// Every tile belongs to one team, every team with tiles has per or per + 1 of them in a row.
+int main() {
+  uint64_t r = 1;
+  for (int k = 0; k < 4000; ++k) {
+    r = r * 6364136223846793005ull + 1442695040888963407ull;
+    const int teams = 1 + (int)((r >> 33) % 320);
+    const long long total = k < 1000 ? k : (long long)((r >> 20) % (k % 2 ? 100000 : 1ll << 40));
+    const PagedCuts c(total, teams);
+    if (c.n != (total < teams ? total : teams) || c.cut(0) != 0 || c.cut(c.n) != total ||
+        c.cut(c.n + 5) != total)
+      return std::printf("%lld tiles, %d teams: ends\n", total, teams), 1;
+    for (int i = 0; i < c.n; ++i) {
+      const long long a = c.cut(i), b = c.cut(i + 1), n = b - a;
+      if (n < 1 || n < c.per || n > c.per + 1 || c.team_of(a) != i || c.team_of(b - 1) != i ||
+          c.team_of(a + n / 2) != i)
+        return std::printf("%lld tiles, %d teams: team %d\n", total, teams, i), 1;
+    }
+  }
+  for (long long a : {0ll, 7ll, 1ll << 31, (1ll << 32) - 1, 1ll << 32, 1ll << 52})
+    for (long long b : {1ll, 3ll, (1ll << 32) - 1, 1ll << 32, 1ll << 33})
+      if (quotient(a, b) != a / b) return std::printf("%lld / %lld\n", a, b), 1;
+  return 0;
+}
+"""
+
+
+def test_tiles_are_shared_out_without_gaps(tmp_path):
+    from test_dense_host_cpu import run
+
+    run(tmp_path, CUTS)
+
+
 def test_struct_layouts(m):
     """As in the header on both machines: 10 + 1 (padding none) words, pointers and strides of 8 bytes."""
     a = m._abi

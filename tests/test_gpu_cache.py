@@ -350,9 +350,9 @@ def test_append_equals_rotary():
 # ------------------------------ eviction ----------------------------------------
 
 
-def _evict(lens, keep, recent, page, hkv, d, seed=40, change=None):
+def _evict(lens, keep, recent, page, hkv, d, seed=40, change=None, spare=1):
     m = _m()
-    cache, table, n = _filled(lens, page, hkv, d, seed)
+    cache, table, n = _filled(lens, page, hkv, d, seed, spare=spare)
     if change:
         change(cache, table)
     moves = evict_exact(cache.weight, cache.position, table.cpu(), lens, keep, recent)
@@ -387,8 +387,13 @@ def test_evict(lens, keep, recent, page, d):
     _evict(lens, keep, recent, page, 3, d)
 
 
-def test_evict_more_than_fits_on_chip():
-    _evict([60000, 49153], 2000, 100, 256, 1, 64)
+@pytest.mark.parametrize("lens,keep,recent,spare", [
+    ([60000, 49153], 2000, 100, 1), ([200001], 3001, 50, 1), ([200100], 200001, 50, 1),
+    ([26000, 30000] + [50] * 160, 500, 20, 1), ([1000, 7, 903], 900, 20, 50),
+    ([904, 900, 901], 900, 20, 50), ([9010, 9003], 9002, 0, 300)])
+def test_evict_long_rows_and_wide_tables(lens, keep, recent, spare):
+    """Ranks that fit no block, rows of several blocks, tables much wider than the lengths."""
+    _evict(lens, keep, recent, 256, 1, 64, spare=spare)
 
 
 def test_evict_ties_and_unusual_weights():
@@ -653,6 +658,27 @@ def test_c_entry_points_give_the_functions_results():
     assert torch.equal(got, o) and torch.equal(n, left)
     for x, y in zip(cache, other):
         assert torch.equal(x, y)
+
+
+def test_inference_mode():
+    m = _m()
+    with torch.inference_mode():
+        cache = m.paged_cache(8, 16, 2, 64, scores=True)
+        table = torch.arange(8, device="cuda", dtype=torch.int32).view(2, 4)
+        lens = torch.tensor([0, 0], device="cuda", dtype=torch.int32)
+        q, kv = _normal(2, 4, 64, seed=62), _normal(2, 2, 64, seed=63)
+        plan = m.rotary_plan(64)
+        for step in range(3):
+            r = m.cache_append(cache, kv, kv, table, lens, plan=plan, q=q)
+            lens = lens + 1
+            o = m.paged_attention(r, cache, table, lens, accumulate=True)
+        assert m.cache_evict(cache, table, lens, 2, 1).tolist() == [2, 2]
+        assert (o.view(2, 2, 2, 64) == kv[:, :, None]).all()  # all values are the same
+        assert m.rotary(q, None, plan, positions=lens)[0].shape == q.shape
+    before = cache.k.clone()
+    with torch.no_grad(), pytest.raises(RuntimeError, match="[Ii]nference"):
+        m.cache_append(cache, kv, kv, table, lens)
+    assert torch.equal(cache.k, before) and _status() == 0
 
 
 def test_two_streams():
