@@ -46,12 +46,15 @@ struct PagedCfg {
   static constexpr int kN = GC < 16 ? 16 : GC;   // columns of S
   static constexpr int kGroups = GC <= 16 ? 1 : GC / 16;  // softmax warpgroups, 16 heads each
   static constexpr int kThreads = 128 * kGroups + 64;     // and a warp for loads, one for products
+  // Many threads leave each of them few registers, and the tiles leave L1 too small for what
+  // does not fit: there the references, the same for a whole warpgroup, are in shared memory.
+  static constexpr bool kShared = kGroups > 2;
   static constexpr int kHi = GC < 8 ? 8 : GC;    // columns of O: those of P's upper parts, then
   static constexpr int kNo = 2 * kHi;            // those of its lower ones
   static constexpr int kTile = 128 * D * 2;
   static constexpr int kQ = kN * D * 2, kP = kNo * 256;
   static constexpr int kCtas = GC <= 16 && 3 * kTile + 2 * kQ + 2 * kP <= 114688 ? 2 : 1;  // per SM
-  static constexpr int kMisc = GC <= 16 ? 1024 : 2560;  // barriers, sums over the warps
+  static constexpr int kMisc = GC <= 16 ? 1024 : 3072;  // barriers, sums over the warps
   static constexpr int kRoom = kCtas == 2 ? 115712 : 232448;
   static constexpr int kRing = (kRoom - 2 * kQ - 2 * kP - kMisc) / kTile;  // K and V tiles in flight
   static constexpr int kSmem = kRing * kTile + 2 * kQ + 2 * kP + kMisc;
@@ -298,7 +301,7 @@ __global__ void __launch_bounds__(PagedCfg<D, GC>::kThreads, PagedCfg<D, GC>::kC
             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedArgs a) {
   using C = PagedCfg<D, GC>;
   constexpr int NCH = D / 64, NR = C::kRing, N = C::kN, NO = C::kNo, HI = C::kHi;
-  constexpr int CH = GC < 16 ? GC : 16, kLoads = 4 * C::kGroups, kProducts = kLoads + 1;
+  constexpr int CH = GC / C::kGroups, kLoads = 4 * C::kGroups, kProducts = kLoads + 1;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sKV = smem;
   uint8_t* sQ = sKV + NR * C::kTile;  // [2][chunk][N rows][128 bytes]
@@ -313,7 +316,8 @@ __global__ void __launch_bounds__(PagedCfg<D, GC>::kThreads, PagedCfg<D, GC>::kC
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   float* sMax = reinterpret_cast<float*>(bars + kMax);  // [group][4][CH] maxima of the warps
   float* sSum = sMax + 4 * GC;                          // [group][4][CH] their sums
-  static_assert(8 * kMax + 32 * GC <= C::kMisc, "shared memory budget");
+  // and, where they are shared, [group][CH] the references
+  static_assert(8 * kMax + (C::kShared ? 36 : 32) * GC <= C::kMisc, "shared memory budget");
   auto bar = [&](int i) { return smem_u32(bars + i); };
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
@@ -491,16 +495,21 @@ __global__ void __launch_bounds__(PagedCfg<D, GC>::kThreads, PagedCfg<D, GC>::kC
     const int h0 = group * CH;          // heads h0 .. h0 + CH are this warpgroup's
     const uint32_t lanes = tbase + ((uint32_t)(quarter * 32) << 16) + h0;
     const uint32_t id_vote = 1 + 2 * group, id_join = 2 + 2 * group;
-    float *wMax = sMax + 4 * h0, *wSum = sSum + 4 * h0;
+    float *wMax = sMax + 4 * h0, *wSum = sSum + 4 * h0, *wRef = sSum + 4 * GC + h0;
     const float c = a.scale_log2;
     bool dead = false;
     int u = 0, part = 0;
     long long x = span.x0;  // tile over all rows
     PagedWalk w(a, span, blockIdx.x);
     while (w.next(a)) {
-      float m[CH], l[CH];
+      // references: of this thread, or (kShared) of the warpgroup
+      float own[C::kShared ? 1 : CH], l[CH];
+      float* m = C::kShared ? wRef : own;
 #pragma unroll
-      for (int g = 0; g < CH; ++g) m[g] = kLowest, l[g] = 0.f;
+      for (int g = 0; g < CH; ++g) {
+        l[g] = 0.f;
+        if (!C::kShared) m[g] = kLowest;
+      }
       for (int t = w.t0; t < w.t1; ++t, ++u, ++x) {
         const int b = u & 1;
         dead = dead || !wait(B_S + b, (u >> 1) & 1, u);
@@ -511,11 +520,11 @@ __global__ void __launch_bounds__(PagedCfg<D, GC>::kThreads, PagedCfg<D, GC>::kC
         if (!dead) tmem_ld_cols<CH>(lanes + N * b, y);
         __syncwarp();
         const bool there = r < w.len - t * 128;
-        bool raise = false;
+        bool raise = C::kShared && t == w.t0;  // the first tile sets shared references
 #pragma unroll
         for (int g = 0; g < CH; ++g) {
           y[g] = there && h0 + g < a.G ? y[g] * c : -INFINITY;
-          raise |= y[g] > m[g] + kRaise;
+          if (!C::kShared || t > w.t0) raise |= y[g] > m[g] + kRaise;
         }
         if (WEIGHTS && there) {
           float* out = a.scores + (((size_t)x * a.side + blockIdx.x % a.side) * a.G + h0) * 128 + r;
@@ -537,12 +546,20 @@ __global__ void __launch_bounds__(PagedCfg<D, GC>::kThreads, PagedCfg<D, GC>::kC
           for (int g = 0; g < CH; ++g) {
             const float top = fmaxf(fmaxf(wMax[g], wMax[CH + g]),
                                     fmaxf(wMax[2 * CH + g], wMax[3 * CH + g]));
-            f[g] = 1.f;
-            if (top > m[g]) {
-              f[g] = ex2_approx(m[g] - top);
-              m[g] = top;
-            }
+            const float old = C::kShared && t == w.t0 ? kLowest : m[g];
+            f[g] = top > old ? ex2_approx(old - top) : 1.f;
+            if (!C::kShared) m[g] = top > old ? top : old;
             l[g] *= f[g];
+          }
+          if (C::kShared) {
+            named_bar_sync(id_join, 128);  // all have read the old ones
+            if (quarter == 0 && lane < CH) {
+              const float top = fmaxf(fmaxf(wMax[lane], wMax[CH + lane]),
+                                      fmaxf(wMax[2 * CH + lane], wMax[3 * CH + lane]));
+              const float old = t == w.t0 ? kLowest : wRef[lane];
+              wRef[lane] = top > old ? top : old;
+            }
+            named_bar_sync(id_join, 128);
           }
           if (t > w.t0) {
             dead = dead || !wait(B_PV + (b ^ 1), ((u - 1) >> 1) & 1, u);
