@@ -63,7 +63,7 @@ struct RotaryArgs {
   const void *q, *k, *v;
   void *q_out, *k_out;     // append writes k to the cache
   long long qs, ks, vs;    // token strides, elements
-  int slots, per;          // threads along the heads of a token, heads of each
+  int slots;               // threads along the heads of a token
   unsigned* status;
   uint64_t freq[kRotaryMaxPairs];
 };

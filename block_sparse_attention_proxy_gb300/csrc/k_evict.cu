@@ -8,9 +8,14 @@
 // only entries that stay and lie behind `keep` move, each into the place of one that leaves; both
 // are listed in ascending order by counting votes, so results do not depend on timing.
 //
-// Bound: HBM: weights and positions read once, the rows that move read and written once.  Few
-// moves (a cache one step over its budget) are made by the block that lists them, many by a second
-// kernel over all SMs.
+// A row one step or a few over its budget needs no digits: the entries that leave are found one
+// after the other (48 sequences of 4097 entries, 8 heads: 24 -> 10 us), and their places are filled
+// by the block itself.  Many moves are made by a second kernel over all SMs.
+//
+// Bound: HBM for the bytes (weights and positions read once, the rows that move read and written
+// once), the chain of dependent steps for the search: four prompts of 32768 entries cut to 4096 (8
+// heads, a cluster of 8 blocks a row): listing 17 us, of which loads 2.4, the newest position 1.2, each
+// digit 1.7, counting and listing 4; moving 54 MB 20 us (16 at a copy's rate).
 #include "cache_common.cuh"
 #include "dense_common.cuh"
 
@@ -36,30 +41,32 @@ __device__ __forceinline__ uint32_t rank_of(float w) {
 }
 
 // Moves between entries of a row, given by their places in the cache (page * page size + slot; -1:
-// none): d / 4 lanes of a warp have 16 bytes of k or of v each, and a warp has kAtOnce moves of each
-// such group on their way.  They are moves i0 and up of the row's n.
-template <int kAtOnce>
+// none): d / 4 lanes of a warp have 16 bytes of k or of v each, and a warp has N moves of each such
+// group on their way.  They are moves i0 and up of the row's n; the lists lie in shared memory
+// (`on_chip`) or in the workspace.
+template <int N>
 __device__ __forceinline__ void move_warp(const CacheArgs& c, int h, const long long* from,
-                                          const long long* to, int i0, int n) {
+                                          const long long* to, bool on_chip, int i0, int n) {
   const int lane = threadIdx.x & 31, lp = c.d / 4, group = lane / lp, groups = 32 / lp;
   const int x = lane % lp, half = lp / 2, mask = (1 << c.page_shift) - 1;
   // lane l has the places of move i0 + l
   const int mine = i0 + lane;
-  const bool there = lane < kAtOnce * groups && mine < n;
-  const long long f = there ? from[mine] : -1, t = there ? to[mine] : -1;
+  const bool there = lane < N * groups && mine < n;
+  const long long f = there ? (on_chip ? from[mine] : __ldcg(from + mine)) : -1;
+  const long long t = there ? (on_chip ? to[mine] : __ldcg(to + mine)) : -1;
   uint16_t* base = (x < half ? c.k : c.v) + 8 * (x < half ? x : x - half);
   const long long ps = x < half ? c.kp : c.vp, ss = x < half ? c.ks : c.vs,
                   at = h * (x < half ? c.kh : c.vh);
-  uint4 row[kAtOnce];
+  uint4 row[N];
   float w = 0.f;
   int p = 0;
   if (f >= 0 && t >= 0) {
     w = __ldcg(c.weight + c.meta((int)(f >> c.page_shift), (int)f & mask, h));
     if (c.position) p = __ldcg(c.position + c.meta((int)(f >> c.page_shift), (int)f & mask, h));
   }
-  long long dst[kAtOnce];
+  long long dst[N];
 #pragma unroll
-  for (int j = 0; j < kAtOnce; ++j) {
+  for (int j = 0; j < N; ++j) {
     const long long fj = __shfl_sync(0xffffffffu, f, j * groups + group);
     const long long tj = __shfl_sync(0xffffffffu, t, j * groups + group);
     dst[j] = fj < 0 || tj < 0 ? -1 : (tj >> c.page_shift) * ps + (tj & mask) * ss + at;
@@ -68,7 +75,7 @@ __device__ __forceinline__ void move_warp(const CacheArgs& c, int h, const long 
                                                      (fj & mask) * ss + at));
   }
 #pragma unroll
-  for (int j = 0; j < kAtOnce; ++j)
+  for (int j = 0; j < N; ++j)
     if (dst[j] >= 0) *reinterpret_cast<uint4*>(base + dst[j]) = row[j];
   if (f >= 0 && t >= 0) {
     const long long m = c.meta((int)(t >> c.page_shift), (int)t & mask, h);
@@ -297,7 +304,7 @@ __global__ void __launch_bounds__(kListThreads, 2)
       if (gone < a.keep) (FUSED ? s_to : to)[before] = entry(gone);
       __syncwarp();
       if (FUSED)
-        for (int k = 0; k < moves; k += 2 * (128 / c.d)) move_warp<2>(c, h, s_from, s_to, k, moves);
+        for (int k = 0; k < moves; k += 2 * (128 / c.d)) move_warp<2>(c, h, s_from, s_to, true, k, moves);
       else if (lane == 0)
         a.count[row] = moves;
     }
@@ -409,7 +416,7 @@ __global__ void __launch_bounds__(kListThreads, 2)
   if (FUSED) {
     const int step = 2 * (128 / c.d), warps = threads / 32;
     for (int i = (rank * warps + warp) * step; i < total; i += blocks * warps * step)
-      move_warp<2>(c, h, from, to, i, total);
+      move_warp<2>(c, h, from, to, on_chip, i, total);
   }
 }
 
@@ -420,7 +427,8 @@ __global__ void __launch_bounds__(32) k_evict_move(const __grid_constant__ Evict
   const int n = __ldcg(a.count + row), i0 = chunk * kAtOnce * (128 / a.cache.d);
   if (i0 >= n) return;
   const long long* from = a.pairs + (size_t)row * 2 * a.most;
-  move_warp<kAtOnce>(a.cache, row % a.cache.hkv, from, from + a.most, i0, n);
+  move_warp<kAtOnce>(a.cache, row % a.cache.hkv, from, from + a.most, false,
+                     i0, n);
 }
 
 template <bool KEYS, bool FUSED>

