@@ -39,7 +39,6 @@ namespace msa {
 namespace {
 
 constexpr int kJoinThreads = 256;
-constexpr int kWeightBlocks = 2;  // blocks that add the weights of one CTA's tiles
 constexpr int kWholeTiles = 12, kMostSide = 8;
 constexpr int kBarStart = 15;  // named barrier; 1 to 8: votes and sums of the softmax warpgroups
 constexpr float kRaise = 8.f;
@@ -666,121 +665,94 @@ __device__ __forceinline__ void red_add_v4(float* p, float4 x) {
 // The parts of a row that begins inside team i's range and ends inside team j's are i's last, and
 // the first of i + 1 .. j: added in this order.  The blocks of i + 1 .. j share the row's heads
 // between them.
-template <int D>
+template <int D, bool WEIGHTS>
 __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_constant__ PagedArgs a) {
   constexpr int V = D / 4;                  // pieces of a head's row
   constexpr int R = kJoinThreads / V;       // runs over the parts
   __shared__ long long scan[kJoinThreads / 32 + 2];
   __shared__ float4 s_sum[kJoinThreads];
   __shared__ float2 s_run[R], s_ref[2][kPagedMaxGroup];
-  // blocks of the first grid join rows, those of the others add weights
-  const int job = blockIdx.x / a.grid, cta = blockIdx.x - job * a.grid;
-  const int c = cta / a.side, at_side = cta % a.side, G = a.G;
+  const int c = blockIdx.x / a.side, at_side = blockIdx.x % a.side, G = a.G;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   PagedSpan span;
   const PagedCuts cuts = paged_span(a, c, scan, kJoinThreads, &span);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-
   // Where team i keeps its part of a row whose first tile is team c0's: see k_paged.
   auto part_of = [&](int i, int c0, bool behind) {
     return (((size_t)i * a.side + at_side) * 2 + (i == c0 && behind)) * G;
   };
-  if (job == 0) {
-    if (a.whole || c == 0 || c >= cuts.n) return;
+  // What follows from the lengths alone is worked out before k_paged's results are waited for.
+  // The row of this team's first tile, if it begins before that:
+  int c0 = 0, c1 = 0;
+  bool behind = false;
+  size_t row0 = 0;
+  if (!a.whole && c > 0 && c < cuts.n) {
     const int tiles = tiles_of(a.cache, span.b), h = span.off / tiles, t = span.off - h * tiles;
     const long long r0 = span.x0 - t;
-    if (t > 0) {  // the row of this team's first tile begins before it
-      const int c0 = cuts.team_of(r0), c1 = cuts.team_of(r0 + tiles - 1);
-      const bool behind = cuts.cut(c0) < r0;
-      const size_t row0 = (size_t)span.b * a.hq + (h * a.side + at_side) * G;
-      const int v = tid % V, run = tid / V;
-      for (int g = c - c0 - 1; g < G; g += c1 - c0) {
-        // every run with a reference of its own, so that sums need not wait for the references
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        float m = kLowest, l = 0.f;
-#pragma unroll 8
-        for (int i = c0 + run; i <= c1; i += R) {
-          const size_t at = part_of(i, c0, behind) + g;
-          const float2 st = __ldcg(&a.part_stats[at]);
-          const float4 p = __ldcg(reinterpret_cast<const float4*>(a.parts + at * D) + v);
-          const float to = fmaxf(m, st.x);
-          const float f = m == to ? 1.f : ex2_approx(m - to), e = st.x == to ? 1.f : ex2_approx(st.x - to);
-          m = to;
-          l = l * f + st.y * e;
-          sum.x = sum.x * f + p.x * e, sum.y = sum.y * f + p.y * e;
-          sum.z = sum.z * f + p.z * e, sum.w = sum.w * f + p.w * e;
-        }
-        s_sum[tid] = sum;
-        if (v == 0) s_run[run] = make_float2(m, l);
-        __syncthreads();
-        if (run == 0) {
-          float top = kLowest, all = 0.f;
-#pragma unroll 8
-          for (int j = 0; j < R; ++j) top = fmaxf(top, s_run[j].x);
-          sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int j = 0; j < R; ++j) {
-            const float2 st = s_run[j];
-            const float e = st.x == top ? 1.f : ex2_approx(st.x - top);
-            const float4 p = s_sum[j * V + v];
-            all += st.y * e;
-            sum.x += p.x * e, sum.y += p.y * e, sum.z += p.z * e, sum.w += p.w * e;
-          }
-          const float inv = all == 0.f ? 0.f : 1.f / all;
-          const uint2 o = make_uint2(pack_bf16(sum.x * inv, sum.y * inv),
-                                     pack_bf16(sum.z * inv, sum.w * inv));
-          reinterpret_cast<uint2*>(a.o + (row0 + g) * D)[v] = all == 0.f ? make_uint2(0, 0) : o;
-        }
-        __syncthreads();
-      }
+    if (t > 0) {
+      c0 = cuts.team_of(r0);
+      c1 = cuts.team_of(r0 + tiles - 1);
+      behind = cuts.cut(c0) < r0;
+      row0 = (size_t)span.b * a.hq + (h * a.side + at_side) * G;
     }
-    return;
   }
-
-  // Weights.  A warp has a tile, a lane four of its entries (they share a page).  Rows that are
-  // shared are the first and the last of the range: their references come first.
-  int parts = 0;
-  {
-    PagedWalk w(a, span, cta);
-    long long x = span.x0;
-    while (w.next(a)) {
-      if (!w.whole() && (parts == 0 || w.left == 0)) {
+  if constexpr (WEIGHTS) {
+    // A warp has a tile, a lane four of its entries (they share a page).  Rows that are shared are
+    // the first and the last of the range.
+    struct { int c0, c1; bool on, behind; } shared[2] = {};
+    {
+      PagedWalk w(a, span, blockIdx.x);
+      long long x = span.x0;
+      for (int parts = 0; w.next(a); ++parts, x += w.t1 - w.t0) {
+        if (w.whole()) continue;
         const long long r0 = x - w.t0;
-        const int c0 = cuts.team_of(r0), c1 = cuts.team_of(r0 + w.tiles - 1);
-        const bool behind = cuts.cut(c0) < r0;
-        for (int g = warp; g < G; g += kJoinThreads / 32) {
-          float m = kLowest, l = 0.f;
-          for (int i = c0 + lane; i <= c1; i += 32) {
-            const float2 st = __ldcg(&a.part_stats[part_of(i, c0, behind) + g]);
-            const float to = fmaxf(m, st.x);
-            l = l * (m == to ? 1.f : ex2_approx(m - to)) +
-                st.y * (st.x == to ? 1.f : ex2_approx(st.x - to));
-            m = to;
-          }
-          const float top = warp_max(m);
-          l = warp_sum(l * (m == top ? 1.f : ex2_approx(m - top)));
-          if (lane == 0) s_ref[parts > 0][g] = make_float2(top, l == 0.f ? 0.f : 1.f / l);
-        }
+        auto& s = shared[parts > 0];
+        s.on = true;
+        s.c0 = cuts.team_of(r0);
+        s.c1 = cuts.team_of(r0 + w.tiles - 1);
+        s.behind = cuts.cut(s.c0) < r0;
       }
-      x += w.t1 - w.t0;
-      ++parts;
     }
-  }
-  __syncthreads();
-  PagedWalk w(a, span, cta);
-  long long x = span.x0;
-  constexpr int kStep = kWeightBlocks * kJoinThreads / 32;
-  int part = 0, next = (job - 1) * (kJoinThreads / 32) + warp;  // this warp's tile of the range
-  while (w.next(a)) {
-    const int n = w.t1 - w.t0, done = (int)(x - span.x0);
-    const float2 *of_row = a.stats + (size_t)w.sb * a.hq + w.sh * G, *of_part = s_ref[part > 0];
-    const bool whole = w.whole();
-    for (; next < done + n; next += kStep) {
-      const int e = (w.t0 + next - done) * 128 + 4 * lane;
-      if (e >= w.len) continue;
+    PagedWalk w(a, span, blockIdx.x);
+    int next = warp;                 // this warp's tile, counted over the range
+    int part = -1, done = 0, n = 0;  // tiles before the part, of the part
+    auto seek = [&] {
+      while (next >= done + n) {
+        done += n;
+        if (!w.next(a)) return false;
+        n = w.t1 - w.t0;
+        ++part;
+      }
+      return true;
+    };
+    auto first_entry = [&] { return (w.t0 + next - done) * 128 + 4 * lane; };
+    bool more = seek();
+    int page = more && first_entry() < w.len ? cache_page(a.cache, w.sb, first_entry()) : -1;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int i = warp; i < 2 * G; i += kJoinThreads / 32) {
+      const int g = i % G, which = i / G;
+      const auto s = shared[which];
+      if (!s.on) continue;
+      float m = kLowest, l = 0.f;
+      for (int k = s.c0 + lane; k <= s.c1; k += 32) {
+        const float2 st = __ldcg(&a.part_stats[part_of(k, s.c0, s.behind) + g]);
+        const float to = fmaxf(m, st.x);
+        l = l * (m == to ? 1.f : ex2_approx(m - to)) + st.y * (st.x == to ? 1.f : ex2_approx(st.x - to));
+        m = to;
+      }
+      const float top = warp_max(m);
+      l = warp_sum(l * (m == top ? 1.f : ex2_approx(m - top)));
+      if (lane == 0) s_ref[which][g] = make_float2(top, l == 0.f ? 0.f : 1.f / l);
+    }
+    __syncthreads();
+    for (; more; more = seek(), page = more && first_entry() < w.len
+                                           ? cache_page(a.cache, w.sb, first_entry()) : -1) {
+      const int e = first_entry();
+      const float2 *of_row = a.stats + (size_t)w.sb * a.hq + w.sh * G, *of_part = s_ref[part > 0];
+      const bool whole = w.whole();
       const float* s =
           a.scores + ((size_t)(span.x0 + next) * a.side + at_side) * G * 128 + 4 * lane;
-      const int page = cache_page(a.cache, w.sb, e);
+      next += kJoinThreads / 32;
+      if (page < 0) continue;  // also behind the last entry
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
       for (int g = 0; g < G; ++g) {
@@ -791,7 +763,6 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
         sum.z += ex2_approx(y.z - st.x) * st.y;
         sum.w += ex2_approx(y.w - st.x) * st.y;
       }
-      if (page < 0) continue;
       float* to = a.cache.weight + a.cache.meta(page, e & ((1 << a.cache.page_shift) - 1), w.sh);
       if (e + 4 <= w.len) {
         red_add_v4(to, sum);
@@ -801,8 +772,49 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
         if (e + 2 < w.len) atomicAdd(to + 2, sum.z);
       }
     }
-    x += n;
-    ++part;
+  } else {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
+  if (c1 == 0) return;
+  const int v = tid % V, run = tid / V;
+  for (int g = c - c0 - 1; g < G; g += c1 - c0) {
+    // every run with a reference of its own, so that sums need not wait for the references
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    float m = kLowest, l = 0.f;
+#pragma unroll 8
+    for (int i = c0 + run; i <= c1; i += R) {
+      const size_t at = part_of(i, c0, behind) + g;
+      const float2 st = __ldcg(&a.part_stats[at]);
+      const float4 p = __ldcg(reinterpret_cast<const float4*>(a.parts + at * D) + v);
+      const float to = fmaxf(m, st.x);
+      const float f = m == to ? 1.f : ex2_approx(m - to), e = st.x == to ? 1.f : ex2_approx(st.x - to);
+      m = to;
+      l = l * f + st.y * e;
+      sum.x = sum.x * f + p.x * e, sum.y = sum.y * f + p.y * e;
+      sum.z = sum.z * f + p.z * e, sum.w = sum.w * f + p.w * e;
+    }
+    s_sum[tid] = sum;
+    if (v == 0) s_run[run] = make_float2(m, l);
+    __syncthreads();
+    if (run == 0) {
+      float top = kLowest, all = 0.f;
+#pragma unroll 8
+      for (int j = 0; j < R; ++j) top = fmaxf(top, s_run[j].x);
+      sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+      for (int j = 0; j < R; ++j) {
+        const float2 st = s_run[j];
+        const float e = st.x == top ? 1.f : ex2_approx(st.x - top);
+        const float4 p = s_sum[j * V + v];
+        all += st.y * e;
+        sum.x += p.x * e, sum.y += p.y * e, sum.z += p.z * e, sum.w += p.w * e;
+      }
+      const float inv = all == 0.f ? 0.f : 1.f / all;
+      const uint2 o = make_uint2(pack_bf16(sum.x * inv, sum.y * inv),
+                                 pack_bf16(sum.z * inv, sum.w * inv));
+      reinterpret_cast<uint2*>(a.o + (row0 + g) * D)[v] = all == 0.f ? make_uint2(0, 0) : o;
+    }
+    __syncthreads();
   }
 }
 
@@ -816,7 +828,7 @@ cudaError_t launch_t(const PagedArgs& a, const CUtensorMap& mq, const CUtensorMa
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (a.whole && !WEIGHTS) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.grid * (WEIGHTS ? 1 + kWeightBlocks : 1));
+  cfg.gridDim = dim3(a.grid);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -824,7 +836,7 @@ cudaError_t launch_t(const PagedArgs& a, const CUtensorMap& mq, const CUtensorMa
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_paged_join<D>, a);
+  return cudaLaunchKernelEx(&cfg, k_paged_join<D, WEIGHTS>, a);
 }
 
 template <int D, bool WEIGHTS>

@@ -110,6 +110,8 @@ msa_status check_paged(const msa_cache* c, const msa_table* t, const msa_paged_p
   if (!(std::isfinite(p->softmax_scale * kLog2E) && p->softmax_scale > 0.f))
     return MSA_ERR_INVALID_ARG;
   if (p->hq > 1024 || p->hq / c->hkv > kPagedMaxGroup) return MSA_ERR_UNSUPPORTED;
+  if ((((long long)a->cache.capacity + 127) >> 7) * c->hkv > 0x7fffffffll)  // tiles of a sequence
+    return MSA_ERR_UNSUPPORTED;
   if (!stride_of(p->q_stride, p->hq, c->d, 2, q_stride)) return MSA_ERR_INVALID_ARG;
   if (p->accumulate) {
     if (!c->weight) return MSA_ERR_INVALID_ARG;

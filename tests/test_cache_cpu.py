@@ -165,6 +165,8 @@ def test_bad_numbers(m):
         assert lib.msa_paged_attention(by(ok[0]), by(ok[1]), by(p), P, P, P, 1 << 30, None) == status
     p = m.make_paged_params(4, accumulate=True)
     assert m.msa_paged_attention_workspace_size(_cache(m, weight=0), ok[1], p) == 0
+    many = _cache(m, hkv=1024, page_size=256), _table(m, max_pages=(1 << 22) - 1, stride=1 << 22)
+    assert m.msa_paged_attention_workspace_size(*many, m.make_paged_params(1024)) == 0
     huge = _table(m, num_seqs=(1 << 20) - 1, max_pages=1 << 20, stride=1 << 20)
     assert m.msa_paged_attention_workspace_size(_cache(m), huge, p) == 0
     empty = _table(m, num_seqs=0)
