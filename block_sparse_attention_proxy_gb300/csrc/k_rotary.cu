@@ -11,7 +11,7 @@
 // or 16 neighbours), or 16 elements that only move.  It takes 8 sines and cosines once
 // and goes over several heads of its token with them, four on their way at once.  Bound: HBM, each
 // row read and written once: 32768 tokens of 20 heads of d = 128 in bf16 53 us, 6.3 TB/s; 131072 of
-// 10 in fp32 198 us, 6.8 TB/s (a copy: 6.8); appending 32768 tokens of 16 + 4 + 4 heads 65 us.
+// 10 in fp32 197 us, 6.8 TB/s (a copy: 6.8); appending 32768 tokens of 16 + 4 + 4 heads 65 us.
 #include "cache_common.cuh"
 
 #include <cuda_fp16.h>
@@ -19,7 +19,7 @@
 namespace msa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 64;  // small blocks leave registers free sooner: 256 took 0 to 9 % longer
 constexpr float kPi = 3.14159265358979f;
 
 // Eight elements as fp32.
@@ -303,8 +303,8 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // Threads along a token's heads: as few as give each SM 512 threads, since each of them looks its
-// document up and takes the sines again (24001 tokens of 9 heads: 19.1 us with 4096, 14.2 with
-// 2048, 11.6 with 512; 6000 tokens of 40: 17.2, 11.3, 7.8, and 8.7 with 256).
+// document up and takes the sines again (in blocks of 256, 24001 tokens of 9 heads: 19.1 us with
+// 4096, 14.2 with 2048, 11.6 with 512; 2000 tokens of 40: 17.2, 11.3, 7.8, and 8.7 with 256).
 unsigned grid_of(RotaryArgs& a, int heads) {
   const long long cols = a.d / 16, want = 512ll * sm_count();
   const long long rows = cols * a.T;
