@@ -630,7 +630,8 @@ __global__ void __launch_bounds__(PagedCfg<D, GC>::kThreads, PagedCfg<D, GC>::kC
       for (int g = 0; g < CH; ++g) {
         if (h0 + g >= a.G) continue;
         const float sum = (wSum[g] + wSum[CH + g]) + (wSum[2 * CH + g] + wSum[3 * CH + g]);
-        const float v = o[g] + lo[g];
+        // an infinite value times the lower part of its weight may be NaN
+        const float v = fabsf(o[g]) == INFINITY ? o[g] : o[g] + lo[g];
         if (whole) {
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
           const __nv_bfloat16 h = __float2bfloat16_rn(sum == 0.f ? 0.f : v * inv);

@@ -166,6 +166,27 @@ def test_infinite_and_nan_scores(accumulate):
         assert not gain[:, 1].any()
 
 
+def test_infinite_values():
+    """An infinite element of v makes its column of o infinite, whatever its weight's roundings."""
+    m = _m()
+    lens = [300, 2000, 40]
+    for d, hq in ((64, 4), (128, 16)):
+        cache, table, n = _filled(lens, 64, 2, d, 65)
+        for b, i, h, x, value in ((0, 7, 0, 3, float("inf")), (0, 299, 1, 0, float("-inf")),
+                                  (1, 1500, 0, 63, float("inf")), (1, 3, 0, 63, float("inf")),
+                                  (1, 9, 1, 5, float("inf")), (1, 1999, 1, 5, float("-inf"))):
+            cache.v[int(table[b, i // 64]), i % 64, h, x] = value
+        cache.k[int(table[0, 0]), 7, 0] = 0
+        q = _normal(3, hq, d, seed=66, scale=0.1)
+        q[0, 0] = 0  # all weights equal: their lower parts may be zero
+        o = m.paged_attention(q, cache, table, n)
+        want, limit, _ = attend_exact(q, cache.k, cache.v, table, lens)
+        assert want.isinf().any() and want.isnan().any()
+        assert torch.equal(o.isinf().cpu(), want.isinf()) and torch.equal(o.isnan().cpu(), want.isnan())
+        assert torch.equal(o.double().cpu()[want.isinf()], want[want.isinf()])
+        within(o, want, limit)
+
+
 def test_scores_at_the_lowest_values():
     """Finite scores of -1e30 and below keep their weights."""
     m = _m()
