@@ -188,10 +188,10 @@ msa_status msa_rotary(const msa_rotary_params* p, const int32_t* cu_seqlens, con
                       const void* q, const void* k, void* q_out, void* k_out,
                       msa_stream_t stream) {
   RotaryArgs a;
+  if (p && p->total_tokens == 0) return check_rotary(p, p->num_docs > 0, false, &a);
   if ((cu_seqlens != nullptr) == (positions != nullptr)) return MSA_ERR_INVALID_ARG;
   const msa_status st = check_rotary(p, cu_seqlens != nullptr, positions != nullptr, &a);
   if (st != MSA_OK) return st;
-  if (a.T == 0) return MSA_OK;
   const size_t bytes = p->dtype == MSA_FP32 ? 4 : 2;
   const struct { const void *in, *out; int heads; long long stride; } x[2] = {
       {q, q_out, a.hq, a.qs}, {k, k_out, a.hkv, a.ks}};

@@ -210,6 +210,9 @@ def test_bad_rotations(m):
                dict(hq=2048), dict(hq=3000), dict(total_tokens=1 << 25), dict(d=0, frequencies=[])):
         assert call(**kw) == 2, kw
     assert call(total_tokens=0, q=0, k=0) == 0
+    assert call(total_tokens=0, q=0, k=0, pos=None) == 0  # of an empty tensor
+    assert call(total_tokens=0, pos=None, num_docs=3, cu=P) == 0
+    assert call(total_tokens=0, pos=None, dtype=3) == 1
 
 
 def test_bad_appends(m):

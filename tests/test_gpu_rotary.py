@@ -262,4 +262,7 @@ def test_refusals():
             call()
     empty = m.rotary(q[:0], k[:0], plan, cu_seqlens=torch.zeros(2, dtype=torch.int32, device="cuda"))
     assert empty[0].shape == (0, 2, 64) and empty[1].shape == (0, 1, 64)
+    empty = m.rotary(q[:0].requires_grad_(), k[:0], plan, positions=at[:0])
+    assert empty[0].shape == (0, 2, 64)
+    empty[0].sum().backward()
     assert m.msa_get_device_status() == 0
