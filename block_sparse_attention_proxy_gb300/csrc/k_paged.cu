@@ -61,7 +61,7 @@ struct PagedCfg {
   // each of 4: 57 us with two, 52 with one).
   static constexpr int kPs = GC == 16 && D == 128 ? 1 : 2;
   static constexpr int kCtas = GC <= 16 && 3 * kTile + 2 * kQ + kPs * kP <= 114688 ? 2 : 1;  // per SM
-  static constexpr int kMisc = GC <= 16 ? 1024 : 3072;  // barriers, sums over the warps
+  static constexpr int kMisc = GC <= 16 ? 1024 : 2816;  // barriers, sums over the warps
   static constexpr int kRoom = kCtas == 2 ? 115712 : 232448;
   static constexpr int kRing = (kRoom - 2 * kQ - kPs * kP - kMisc) / kTile;  // K and V tiles in flight
   static constexpr int kSmem = kRing * kTile + 2 * kQ + kPs * kP + kMisc;
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(PagedCfg<D, GC>::kThreads, PagedCfg<D, GC>::kC
     // ------------------------------ loads ----------------------------------------
     const int rows = min(128, 1 << a.cache.page_shift);  // of a box
     const int box = lane / NCH, ch = lane % NCH;         // one box of a tile per lane
-    int s = 0, round = 0, part = 0;
+    int s = 0, lap = 0, part = 0;
     bool ok = true;
     // The page of this lane's box of a tile.  It is looked up a tile ahead, and kept for the values.
     auto page_of = [&](int b, int len, int t) {
@@ -384,13 +384,13 @@ __global__ void __launch_bounds__(PagedCfg<D, GC>::kThreads, PagedCfg<D, GC>::kC
     };
     auto load = [&](const CUtensorMap* tm, int h, int len, int t, int page) {
       const int valid = min(128, len - t * 128), n = (valid + rows - 1) / rows;  // entries, boxes
-      if (round > 0 && !(ok = wait(B_E + s, (round & 1) ^ 1, t))) return;
+      if (lap > 0 && !(ok = wait(B_E + s, (lap & 1) ^ 1, t))) return;
       if (lane == 0) mbar_arrive_expect_tx(bar(B_F + s), n * rows * NCH * 128);
       __syncwarp();
       if (box < n)
         tma_load_4d(smem_u32(sKV + s * C::kTile) + ch * 16384 + box * rows * 128, tm, bar(B_F + s),
                     64 * ch, h, (t * 128 + box * rows) & ((1 << a.cache.page_shift) - 1), page);
-      if (++s == NR) s = 0, ++round;
+      if (++s == NR) s = 0, ++lap;
     };
     struct { int h, len, t, page; } last{0, 0, -1, 0};
     PagedWalk w(a, span, blockIdx.x);
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(PagedCfg<D, GC>::kThreads, PagedCfg<D, GC>::kC
     if (*abort_flag) {
       for (int i = max(0, part - 2); i < part; ++i) drain_bar(bar(B_Q + (i & 1)), (i >> 1) & 1);
       for (int i = 0; i < NR; ++i)
-        if (i < s || round > 0) drain_bar(bar(B_F + i), (i < s ? round : round - 1) & 1);
+        if (i < s || lap > 0) drain_bar(bar(B_F + i), (i < s ? lap : lap - 1) & 1);
     }
   } else if (warp == kProducts) {
     // ------------------------------ products -------------------------------------
@@ -431,13 +431,13 @@ __global__ void __launch_bounds__(PagedCfg<D, GC>::kThreads, PagedCfg<D, GC>::kC
                    p_lo = desc_lo(smem_u32(sP), 16);
     // d = 64 fills half of the 128 rows of V^T: the other half repeats it and is not read
     const uint32_t v_lo = desc_lo(smem_u32(sKV), D == 128 ? 16384 : 0);
-    int s = 0, round = 0, part = 0, u = 0;  // ring position, parts, tiles
+    int s = 0, lap = 0, part = 0, u = 0;  // ring position, parts, tiles
     bool ok = true, first = false, pending = false, new_part = false;
     int valid = 0;
     // O += V^T P^T of tile u - 1, which has `valid` entries; the first of part `part - 1`, or of
     // the one before where a new part's first scores have been issued since
     auto values = [&](int of) {
-      if (!(ok = wait(B_F + s, round & 1, u))) return;
+      if (!(ok = wait(B_F + s, lap & 1, u))) return;
       const int steps = (valid + 15) / 16;
       if (valid < 16 * steps) {  // entries behind the end: P is zero there, V must be finite
         uint8_t* tile = sKV + s * C::kTile;
@@ -461,14 +461,14 @@ __global__ void __launch_bounds__(PagedCfg<D, GC>::kThreads, PagedCfg<D, GC>::kC
                  idO, !first || kk > 0);
       mma_commit(el, bar(B_PV + (up & 1)));
       mma_commit(el, bar(B_E + s));
-      if (++s == NR) s = 0, ++round;
+      if (++s == NR) s = 0, ++lap;
     };
     PagedWalk w(a, span, blockIdx.x);
     while (ok && w.next(a)) {
       if (!(ok = wait(B_Q + (part & 1), (part >> 1) & 1, part))) break;
       new_part = true;
       for (int t = w.t0; ok && t < w.t1; ++t) {
-        if (!(ok = wait(B_F + s, round & 1, u))) break;
+        if (!(ok = wait(B_F + s, lap & 1, u))) break;
         tc_fence_after();
         const uint32_t k = k_lo + s * (C::kTile >> 4), q = q_lo + (part & 1) * (C::kQ >> 4);
 #pragma unroll
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(PagedCfg<D, GC>::kThreads, PagedCfg<D, GC>::kC
         mma_commit(el, bar(B_S + (u & 1)));
         mma_commit(el, bar(B_E + s));
         if (t + 1 == w.t1) mma_commit(el, bar(B_QE + (part & 1)));
-        if (++s == NR) s = 0, ++round;
+        if (++s == NR) s = 0, ++lap;
         if (pending) values(new_part ? part - 1 : part);
         if (!ok) break;
         pending = true;
