@@ -52,8 +52,8 @@ __device__ __forceinline__ void move_warp(const CacheArgs& c, int h, const long 
   // lane l has the places of move i0 + l
   const int mine = i0 + lane;
   const bool there = lane < N * groups && mine < n;
-  const long long f = there ? (on_chip ? from[mine] : __ldcg(from + mine)) : -1;
-  const long long t = there ? (on_chip ? to[mine] : __ldcg(to + mine)) : -1;
+  const long long f = there ? (on_chip ? from[mine] : fetch(from + mine)) : -1;
+  const long long t = there ? (on_chip ? to[mine] : fetch(to + mine)) : -1;
   uint16_t* base = (x < half ? c.k : c.v) + 8 * (x < half ? x : x - half);
   const long long ps = x < half ? c.kp : c.vp, ss = x < half ? c.ks : c.vs,
                   at = h * (x < half ? c.kh : c.vh);
@@ -61,8 +61,8 @@ __device__ __forceinline__ void move_warp(const CacheArgs& c, int h, const long 
   float w = 0.f;
   int p = 0;
   if (f >= 0 && t >= 0) {
-    w = __ldcg(c.weight + c.meta((int)(f >> c.page_shift), (int)f & mask, h));
-    if (c.position) p = __ldcg(c.position + c.meta((int)(f >> c.page_shift), (int)f & mask, h));
+    w = fetch(c.weight + c.meta((int)(f >> c.page_shift), (int)f & mask, h));
+    if (c.position) p = fetch(c.position + c.meta((int)(f >> c.page_shift), (int)f & mask, h));
   }
   long long dst[N];
 #pragma unroll
@@ -71,7 +71,7 @@ __device__ __forceinline__ void move_warp(const CacheArgs& c, int h, const long 
     const long long tj = __shfl_sync(0xffffffffu, t, j * groups + group);
     dst[j] = fj < 0 || tj < 0 ? -1 : (tj >> c.page_shift) * ps + (tj & mask) * ss + at;
     if (dst[j] >= 0)
-      row[j] = __ldcg(reinterpret_cast<const uint4*>(base + (fj >> c.page_shift) * ps +
+      row[j] = fetch(reinterpret_cast<const uint4*>(base + (fj >> c.page_shift) * ps +
                                                      (fj & mask) * ss + at));
   }
 #pragma unroll
@@ -121,7 +121,8 @@ __global__ void __launch_bounds__(kListThreads, 2)
   const int row = blockIdx.x / blocks, rank = blockIdx.x - row * blocks;
   const int b = row / c.hkv, h = row - b * c.hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_for_previous();
+  let_next_start();
   // The first pages that this thread needs do not wait for the length.
   constexpr int kBatch = 4;
   const int* table = c.table + (long long)b * c.table_stride;
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(kListThreads, 2)
   for (int j = 0; j < kBatch; ++j) {
     const int i = 4 * (tid + j * threads);
     early[j] = i < slice && i < c.capacity - rank * slice
-                   ? __ldg(table + ((rank * slice + i) >> c.page_shift))
+                   ? fetch(table + ((rank * slice + i) >> c.page_shift))
                    : -1;
   }
   const int n = cache_len(c, b);
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(kListThreads, 2)
     for (int j = 0; j < kBatch; ++j) {
       const int i = i0 + 4 * j * threads;
       page[j] = -1;
-      if (i < end) page[j] = i0 == begin + 4 * tid ? early[j] : __ldg(table + (i >> c.page_shift));
+      if (i < end) page[j] = i0 == begin + 4 * tid ? early[j] : fetch(table + (i >> c.page_shift));
       if (i < end && (unsigned)page[j] >= (unsigned)c.num_pages) {
         set_status(c.status, MSA_ERR_DEVICE_CHECK);
         page[j] = -1;
@@ -189,8 +190,8 @@ __global__ void __launch_bounds__(kListThreads, 2)
       p[j] = make_int4(INT_MIN, INT_MIN, INT_MIN, INT_MIN);
       if (page[j] < 0) continue;
       const long long m = c.meta(page[j], (i0 + 4 * j * threads) & mask, h);
-      if (KEYS) w[j] = __ldcg(reinterpret_cast<const float4*>(c.weight + m));
-      if (a.recent > 0) p[j] = __ldcg(reinterpret_cast<const int4*>(c.position + m));
+      if (KEYS) w[j] = fetch(reinterpret_cast<const float4*>(c.weight + m));
+      if (a.recent > 0) p[j] = fetch(reinterpret_cast<const int4*>(c.position + m));
     }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
@@ -227,8 +228,8 @@ __global__ void __launch_bounds__(kListThreads, 2)
     if (KEYS) return s_key[i - begin];
     const long long m = place(i);
     if (m < 0) return 0;
-    if (a.recent > 0 && __ldcg(c.position + m) >= limit) return kRecent;
-    return rank_of(__ldcg(c.weight + m));
+    if (a.recent > 0 && fetch(c.position + m) >= limit) return kRecent;
+    return rank_of(fetch(c.weight + m));
   };
   if (KEYS && a.recent > 0) {  // each thread its own entries
     for (int i = 4 * tid; i < end - begin; i += 4 * threads) {
@@ -423,8 +424,8 @@ __global__ void __launch_bounds__(kListThreads, 2)
 // One warp a block, so that a block's registers are free as soon as its moves are done.
 __global__ void __launch_bounds__(32) k_evict_move(const __grid_constant__ EvictArgs a, int chunks) {
   const int row = blockIdx.x / chunks, chunk = blockIdx.x - row * chunks;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int n = __ldcg(a.count + row), i0 = chunk * kAtOnce * (128 / a.cache.d);
+  wait_for_previous();
+  const int n = fetch(a.count + row), i0 = chunk * kAtOnce * (128 / a.cache.d);
   if (i0 >= n) return;
   const long long* from = a.pairs + (size_t)row * 2 * a.most;
   move_warp<kAtOnce>(a.cache, row % a.cache.hkv, from, from + a.most, false,
@@ -436,22 +437,8 @@ cudaError_t list(const EvictArgs& a, int rows, int blocks, int slice, int thread
                  cudaStream_t st) {
   const cudaError_t e = dense_prepare<k_evict_list<KEYS, FUSED>>(0, 0, KEYS ? kMostKeys * 8 + kMostKeys / 4 : 0);
   if (e != cudaSuccess) return e;
-  if (blocks == 1) {
-    k_evict_list<KEYS, FUSED><<<rows, threads, KEYS ? slice * 8 + slice / 4 : 0, st>>>(a, 1, slice);
-    return cudaGetLastError();
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(rows * blocks));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = KEYS ? slice * 8 + slice / 4 : 0;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = blocks;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_evict_list<KEYS, FUSED>, a, blocks, slice);
+  return launch_early(k_evict_list<KEYS, FUSED>, (unsigned)(rows * blocks), threads,
+                      KEYS ? slice * 8 + slice / 4 : 0, st, blocks, a, blocks, slice);
 }
 
 }  // namespace
@@ -484,16 +471,7 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st, int* launches) {
   *launches = fused ? 1 : 2;
   if (e != cudaSuccess || fused) return e;
   const int step = kAtOnce * (128 / c.d), chunks = (a.most + step - 1) / step;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(rows * chunks));
-  cfg.blockDim = dim3(32);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_evict_move, a, chunks);
+  return launch_early(k_evict_move, (unsigned)(rows * chunks), 32, 0, st, 1, a, chunks);
 }
 
 }  // namespace msa

@@ -348,12 +348,15 @@ __global__ void __launch_bounds__(PagedCfg<D, GC>::kThreads, PagedCfg<D, GC>::kC
     *abort_flag = 0;
     fence_barrier_init();
   }
+  wait_for_previous();
+  // The next kernel may start only behind the allocation: it could otherwise hold tensor memory that
+  // this one needs, and wait for its end.
   if (warp == kProducts) {
     tmem_alloc(smem_u32(tslot), C::kCols);
     tmem_relinquish();
+    let_next_start();
   }
   __syncwarp();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   PagedSpan span;
   paged_span(a, blockIdx.x / a.side, scan, C::kThreads, &span);
   // The loading warp has what it needs and starts; the others wait for its barriers.
@@ -681,7 +684,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
   auto part_of = [&](int i, int c0, bool behind) {
     return (((size_t)i * a.side + at_side) * 2 + (i == c0 && behind)) * G;
   };
-  // What follows from the lengths alone is worked out before k_paged's results are waited for.
+  // What follows from the lengths alone is worked out before k_paged's results are waited for: it
+  // lets this kernel start once all before it is complete, and writes no length and no page.
   // The row of this team's first tile, if it begins before that:
   int c0 = 0, c1 = 0;
   bool behind = false;
@@ -728,14 +732,14 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
     auto first_entry = [&] { return (w.t0 + next - done) * 128 + 4 * lane; };
     bool more = seek();
     int page = more && first_entry() < w.len ? cache_page(a.cache, w.sb, first_entry()) : -1;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_previous();
     for (int i = warp; i < 2 * G; i += kJoinThreads / 32) {
       const int g = i % G, which = i / G;
       const auto s = shared[which];
       if (!s.on) continue;
       float m = kLowest, l = 0.f;
       for (int k = s.c0 + lane; k <= s.c1; k += 32) {
-        const float2 st = __ldcg(&a.part_stats[part_of(k, s.c0, s.behind) + g]);
+        const float2 st = fetch(&a.part_stats[part_of(k, s.c0, s.behind) + g]);
         const float to = fmaxf(m, st.x);
         l = l * (m == to ? 1.f : ex2_approx(m - to)) + st.y * (st.x == to ? 1.f : ex2_approx(st.x - to));
         m = to;
@@ -757,8 +761,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
       for (int g = 0; g < G; ++g) {
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(s + g * 128));
-        const float2 st = whole ? __ldcg(of_row + g) : of_part[g];
+        const float4 y = fetch(reinterpret_cast<const float4*>(s + g * 128));
+        const float2 st = whole ? fetch(of_row + g) : of_part[g];
         sum.x += ex2_approx(y.x - st.x) * st.y;
         sum.y += ex2_approx(y.y - st.x) * st.y;
         sum.z += ex2_approx(y.z - st.x) * st.y;
@@ -774,7 +778,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
       }
     }
   } else {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_previous();
   }
   if (c1 == 0) return;
   const int v = tid % V, run = tid / V;
@@ -785,8 +789,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
 #pragma unroll 8
     for (int i = c0 + run; i <= c1; i += R) {
       const size_t at = part_of(i, c0, behind) + g;
-      const float2 st = __ldcg(&a.part_stats[at]);
-      const float4 p = __ldcg(reinterpret_cast<const float4*>(a.parts + at * D) + v);
+      const float2 st = fetch(&a.part_stats[at]);
+      const float4 p = fetch(reinterpret_cast<const float4*>(a.parts + at * D) + v);
       const float to = fmaxf(m, st.x);
       const float f = m == to ? 1.f : ex2_approx(m - to), e = st.x == to ? 1.f : ex2_approx(st.x - to);
       m = to;
@@ -825,19 +829,9 @@ cudaError_t launch_t(const PagedArgs& a, const CUtensorMap& mq, const CUtensorMa
   using C = PagedCfg<D, GC>;
   cudaError_t e = dense_prepare<k_paged<D, GC, WEIGHTS>>(C::kThreads, 0, C::kSmem);
   if (e != cudaSuccess) return e;
-  k_paged<D, GC, WEIGHTS><<<a.grid, C::kThreads, C::kSmem, st>>>(mq, mk, mv, a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (a.whole && !WEIGHTS) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.grid);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_paged_join<D, WEIGHTS>, a);
+  e = launch_early(k_paged<D, GC, WEIGHTS>, a.grid, C::kThreads, C::kSmem, st, 1, mq, mk, mv, a);
+  if (e != cudaSuccess || (a.whole && !WEIGHTS)) return e;
+  return launch_early(k_paged_join<D, WEIGHTS>, a.grid, kJoinThreads, 0, st, 1, a);
 }
 
 template <int D, bool WEIGHTS>

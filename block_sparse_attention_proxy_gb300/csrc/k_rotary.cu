@@ -28,7 +28,7 @@ struct Eight;
 template <>
 struct Eight<__nv_bfloat16> {
   uint4 w;
-  __device__ void load(const __nv_bfloat16* p) { w = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ void load(const __nv_bfloat16* p) { w = fetch(reinterpret_cast<const uint4*>(p)); }
   __device__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = w; }
   __device__ void get(float (&x)[8]) const {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -44,7 +44,7 @@ struct Eight<__nv_bfloat16> {
 template <>
 struct Eight<__half> {
   uint4 w;
-  __device__ void load(const __half* p) { w = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ void load(const __half* p) { w = fetch(reinterpret_cast<const uint4*>(p)); }
   __device__ void store(__half* p) const { *reinterpret_cast<uint4*>(p) = w; }
   __device__ void get(float (&x)[8]) const {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -69,8 +69,8 @@ template <>
 struct Eight<float> {
   float4 w[2];
   __device__ void load(const float* p) {
-    w[0] = __ldg(reinterpret_cast<const float4*>(p));
-    w[1] = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    w[0] = fetch(reinterpret_cast<const float4*>(p));
+    w[1] = fetch(reinterpret_cast<const float4*>(p) + 1);
   }
   __device__ void store(float* p) const {
     reinterpret_cast<float4*>(p)[0] = w[0];
@@ -89,15 +89,15 @@ struct Eight<float> {
 
 // Documents (or sequences) that do not begin at 0, fall, or end behind T.
 __device__ __forceinline__ void check_docs(const RotaryArgs& a) {
-  bool bad = threadIdx.x == 0 && (__ldg(a.cu) != 0 || __ldg(a.cu + a.ndoc) > a.T);
+  bool bad = threadIdx.x == 0 && (fetch(a.cu) != 0 || fetch(a.cu + a.ndoc) > a.T);
   for (int b = threadIdx.x; b < a.ndoc; b += kThreads)
-    bad |= __ldg(a.cu + b + 1) < __ldg(a.cu + b);
+    bad |= fetch(a.cu + b + 1) < fetch(a.cu + b);
   if (bad) set_status(a.status, MSA_ERR_DEVICE_CHECK);
 }
 
 __device__ __forceinline__ long long position_of(const RotaryArgs& a, int t) {
-  return a.position_bytes == 8 ? (long long)__ldg(static_cast<const long long*>(a.positions) + t)
-                               : (long long)__ldg(static_cast<const int*>(a.positions) + t);
+  return a.position_bytes == 8 ? (long long)fetch(static_cast<const long long*>(a.positions) + t)
+                               : (long long)fetch(static_cast<const int*>(a.positions) + t);
 }
 
 // Cosines and sines of 8 pairs from `pair` on at position p.  Results of 16 bits take the hardware's
@@ -173,6 +173,7 @@ __device__ __forceinline__ Place place_of(const RotaryArgs& a) {
 template <typename T, bool INTER>
 __global__ void __launch_bounds__(kThreads)
     k_rotary(const __grid_constant__ RotaryArgs a) {
+  wait_for_previous();
   if (a.cu && blockIdx.x == 0) check_docs(a);
   const Place p = place_of<INTER>(a);
   if (!p.ok) return;
@@ -185,8 +186,8 @@ __global__ void __launch_bounds__(kThreads)
   long long pos;
   if (a.cu) {
     const int b = doc_of_token(a.cu, a.ndoc, p.token);
-    pos = p.token - __ldg(a.cu + b);
-    padding = p.token >= __ldg(a.cu + a.ndoc);
+    pos = p.token - fetch(a.cu + b);
+    padding = p.token >= fetch(a.cu + a.ndoc);
   } else {
     pos = position_of(a, p.token);
   }
@@ -226,6 +227,7 @@ template <bool INTER>
 __global__ void __launch_bounds__(kThreads)
     k_append(const __grid_constant__ RotaryArgs a, const __grid_constant__ CacheArgs cache) {
   using T = __nv_bfloat16;
+  wait_for_previous();
   if (a.cu && blockIdx.x == 0) check_docs(a);
   const Place p = place_of<INTER>(a);
   if (!p.ok) return;
@@ -235,11 +237,11 @@ __global__ void __launch_bounds__(kThreads)
   bool padding = false;
   if (a.cu) {
     seq = doc_of_token(a.cu, a.ndoc, t);
-    entry = t - __ldg(a.cu + seq);
-    padding = t >= __ldg(a.cu + a.ndoc);
+    entry = t - fetch(a.cu + seq);
+    padding = t >= fetch(a.cu + a.ndoc);
   }
   if (!padding) {
-    const int len = __ldg(cache.lens + seq);
+    const int len = fetch(cache.lens + seq);
     const long long e = (long long)len + entry;
     if (len < 0 || entry < 0 || e >= cache.capacity) {
       set_status(a.status, MSA_ERR_DEVICE_CHECK);
@@ -319,23 +321,17 @@ unsigned grid_of(RotaryArgs& a, int heads) {
 
 cudaError_t launch_rotary(RotaryArgs& a, int dtype, bool interleaved, cudaStream_t st) {
   const unsigned grid = grid_of(a, a.hq + a.hkv);
-  auto go = [&](auto kernel) { kernel<<<grid, kThreads, 0, st>>>(a); };
+  auto go = [&](auto kernel) { return launch_early(kernel, grid, kThreads, 0, st, 1, a); };
   if (dtype == MSA_BF16)
-    interleaved ? go(k_rotary<__nv_bfloat16, true>) : go(k_rotary<__nv_bfloat16, false>);
-  else if (dtype == MSA_FP16)
-    interleaved ? go(k_rotary<__half, true>) : go(k_rotary<__half, false>);
-  else
-    interleaved ? go(k_rotary<float, true>) : go(k_rotary<float, false>);
-  return cudaGetLastError();
+    return interleaved ? go(k_rotary<__nv_bfloat16, true>) : go(k_rotary<__nv_bfloat16, false>);
+  if (dtype == MSA_FP16)
+    return interleaved ? go(k_rotary<__half, true>) : go(k_rotary<__half, false>);
+  return interleaved ? go(k_rotary<float, true>) : go(k_rotary<float, false>);
 }
 
 cudaError_t launch_append(RotaryArgs& a, const CacheArgs& c, bool interleaved, cudaStream_t st) {
   const unsigned grid = grid_of(a, a.hq + 2 * a.hkv);
-  if (interleaved)
-    k_append<true><<<grid, kThreads, 0, st>>>(a, c);
-  else
-    k_append<false><<<grid, kThreads, 0, st>>>(a, c);
-  return cudaGetLastError();
+  return launch_early(interleaved ? k_append<true> : k_append<false>, grid, kThreads, 0, st, 1, a, c);
 }
 
 }  // namespace msa

@@ -554,6 +554,66 @@ def test_captured_steps():
     assert _status() == 0
 
 
+@pytest.mark.parametrize("start,hq,hkv,d,page", [
+    ([5, 100, 77], 8, 2, 128, 64),             # rows of one tile: no join
+    ([700, 20, 3001, 129], 8, 8, 64, 16),      # shared rows
+    ([300, 2000], 64, 1, 128, 128),
+])
+def test_each_call_uses_all_that_the_last_one_wrote(start, hq, hkv, d, page):
+    """Calls whose every input comes from the call before: in a row and captured as with the device
+    idle before each."""
+    m = _m()
+    keep, layers, plan = max(start) - 3, 4, m.rotary_plan(d)
+    q0, k0, v0 = (_normal(len(start), h, d, seed=300 + i) for i, h in enumerate((hq, hkv, hkv)))
+    scale = d ** -0.5
+
+    def build():
+        out = []
+        for i in range(layers):
+            cache, table, n = _filled([x + 2 for x in start], page, hkv, d, 310 + 5 * i, spare=0)
+            out.append((cache, table, n - 2))
+        return out
+
+    def run(state, idle):
+        def done(x):
+            if idle:
+                torch.cuda.synchronize()
+            return x
+        q = q0
+        for cache, table, lens in state:
+            k, v = q[:, :hkv] + k0, q[:, -hkv:] + v0
+            q = done(m.cache_append(cache, done(k), done(v), table, lens, plan=plan, q=q))
+            o = done(m.paged_attention(q, cache, table, done(lens + 1), scale, accumulate=True))
+            kept = done(m.cache_evict(cache, table, lens + 1, keep, 4))
+            o2 = done(m.paged_attention(o, cache, table, kept, scale))
+            q, _ = m.rotary(o2, o[:, :hkv], plan, positions=kept)
+            done(q)
+            q = done(m.paged_attention(q, cache, table, kept, scale)) + q
+        return q
+
+    state = build()
+    want = run(state, True)
+    wanted = [x.clone() for c, _, _ in state for x in c]
+    for captured in (False, True):
+        for _ in range(3):
+            state = build()
+            torch.cuda.synchronize()
+            if captured:
+                stream = torch.cuda.Stream()
+                with torch.cuda.stream(stream):
+                    graph = torch.cuda.CUDAGraph()
+                    with torch.cuda.graph(graph, stream=stream):
+                        got = run(state, False)
+                    graph.replay()
+                torch.cuda.synchronize()
+            else:
+                got = run(state, False)
+            assert torch.equal(got, want)
+            for a, b in zip([x for c, _, _ in state for x in c], wanted):
+                assert torch.equal(a, b)
+    assert _status() == 0
+
+
 # ------------------------------ what is refused or flagged -----------------------
 
 
