@@ -29,9 +29,9 @@
 // 2.3e-3 against 1.7e-3).  With weights asked for, the scores go out in fp32 and the join adds
 // 2^(s - m) / l of the group's heads to each entry's weight.
 //
-// Measured: 64 sequences of 4096 entries, 32 heads on 8 of d = 128: 164 us, 6.55 TB/s, 0.97 of a
+// Measured: 64 sequences of 4096 entries, 32 heads on 8 of d = 128: 162 us, 6.6 TB/s, 0.97 of a
 // copy's; one of 131072: 84 us, of which 4 are the join; 23 of 2047, 12 heads of d = 64: 33 us (the
-// bytes take 21), with weights 41; four of 103: 6 us, most of it the way through one tile.
+// bytes take 21), with weights 38; four of 103: 6 us, most of it the way through one tile.
 #include "cache_common.cuh"
 #include "dense_common.cuh"
 

@@ -10,8 +10,8 @@
 // A thread has 16 elements of a row: 8 pairs (two runs of 8 elements half the rotated part apart,
 // or 16 neighbours), or 16 elements that only move.  It takes 8 sines and cosines once
 // and goes over several heads of its token with them, four on their way at once.  Bound: HBM, each
-// row read and written once: 32768 tokens of 20 heads of d = 128 in bf16 53 us, 6.3 TB/s; 131072 of
-// 10 in fp32 197 us, 6.8 TB/s (a copy: 6.8); appending 32768 tokens of 16 + 4 + 4 heads 65 us.
+// row read and written once: 32768 tokens of 20 heads of d = 128 in bf16 52 us, 6.4 TB/s; 131072 of
+// 10 in fp32 196 us, 6.8 TB/s (a copy: 6.8); appending 32768 tokens of 16 + 4 + 4 heads 64 us.
 #include "cache_common.cuh"
 
 #include <cuda_fp16.h>

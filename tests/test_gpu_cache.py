@@ -614,6 +614,55 @@ def test_each_call_uses_all_that_the_last_one_wrote(start, hq, hkv, d, page):
     assert _status() == 0
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_streams_that_part_and_meet(captured):
+    """One cache filled, read on two streams at once, copied, and evicted from where they meet."""
+    m = _m()
+    lens, hq, hkv, d, page = [300, 77, 1500], 8, 2, 128, 64
+    plan, q0 = m.rotary_plan(d), _normal(3, hq, d, seed=400)
+    k0, v0 = (_normal(3, hkv, d, seed=401 + i) for i in range(2))
+
+    def run(cache, table, n, main, side):
+        q = m.cache_append(cache, k0, v0, table, n, plan=plan, q=q0)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            a = m.paged_attention(q, cache, table, n + 1)
+            a = m.rotary(a, None, plan, positions=n)[0]
+        b = m.rotary(q, None, plan, positions=n)[0]
+        b = m.paged_attention(b, cache, table, n + 1)
+        main.wait_stream(side)
+        c = m.paged_attention(a, cache, table, n + 1, accumulate=True)
+        out = torch.empty_like(c)
+        out.copy_(c)
+        out = m.rotary(out, None, plan, positions=n)[0]
+        kept = m.cache_evict(cache, table, n + 1, 64, 8)
+        return a, b, c, out, kept
+
+    def fresh():
+        cache, table, n = _filled([x + 1 for x in lens], page, hkv, d, 403, spare=0)
+        torch.cuda.synchronize()
+        return cache, table, n - 1
+
+    now = torch.cuda.current_stream()
+    state = fresh()
+    want = [*run(*state, now, now), *state[0]]
+    for _ in range(3):
+        main, side, state = torch.cuda.Stream(), torch.cuda.Stream(), fresh()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(main):
+            if captured:
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph, stream=main):
+                    got = run(*state, main, side)
+                graph.replay()
+            else:
+                got = run(*state, main, side)
+        torch.cuda.synchronize()
+        for x, y in zip([*got, *state[0]], want):
+            assert torch.equal(x, y)
+    assert _status() == 0
+
+
 # ------------------------------ what is refused or flagged -----------------------
 
 
