@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads)
   bool padding = false;
   long long pos;
   if (a.cu) {
-    const int b = doc_of_token(a.cu, a.ndoc, p.token);
+    const int b = doc_of_token<false>(a.cu, a.ndoc, p.token);
     pos = p.token - fetch(a.cu + b);
     padding = p.token >= fetch(a.cu + a.ndoc);
   } else {
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kThreads)
   int seq = t, entry = 0, page = -1;
   bool padding = false;
   if (a.cu) {
-    seq = doc_of_token(a.cu, a.ndoc, t);
+    seq = doc_of_token<false>(a.cu, a.ndoc, t);
     entry = t - fetch(a.cu + seq);
     padding = t >= fetch(a.cu + a.ndoc);
   }

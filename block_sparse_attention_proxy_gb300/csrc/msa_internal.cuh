@@ -116,12 +116,16 @@ __device__ __forceinline__ float warp_max(float x) {
   return x;
 }
 
-// Index of the document holding global token t (cu has ndoc+1 entries).
+// Index of the document holding global token t (cu has ndoc+1 entries).  READ_ONLY: nothing writes cu
+// while the kernel is on the GPU; a kernel that may start before the one that writes it takes
+// plain loads.
+template <bool READ_ONLY = true>
 __device__ __forceinline__ int doc_of_token(const int32_t* cu, int ndoc, int t) {
   int lo = 0, hi = ndoc - 1;
   while (lo < hi) {
     int mid = (lo + hi + 1) >> 1;
-    if (__ldg(cu + mid) <= t) lo = mid; else hi = mid - 1;
+    const int begin = READ_ONLY ? __ldg(cu + mid) : cu[mid];
+    if (begin <= t) lo = mid; else hi = mid - 1;
   }
   return lo;
 }

@@ -3,6 +3,7 @@ before any CUDA call."""
 import ctypes
 import math
 import os
+import re
 from fractions import Fraction
 
 import pytest
@@ -275,3 +276,21 @@ def test_struct_layouts(m):
     assert ctypes.sizeof(a.MsaCache) == 4 * 8 + 4 * 4 + 6 * 8
     assert ctypes.sizeof(a.MsaTable) == 2 * 8 + 2 * 4 + 8
     assert ctypes.sizeof(a.MsaPagedParams) == 2 * 4 + 8 + 2 * 4
+
+
+def test_kernels_that_start_early_read_by_plain_loads():
+    """They may be on the GPU before their inputs are written: read-only loads, which may move ahead of
+    the wait for those, are not for them."""
+    import block_sparse_attention_proxy_gb300 as package
+
+    csrc = os.path.join(os.path.dirname(package.__file__), "csrc")
+    early = []
+    for name in sorted(os.listdir(csrc)):
+        with open(os.path.join(csrc, name)) as f:
+            code = re.sub(r"//[^\n]*|/\*.*?\*/", "", f.read(), flags=re.S)
+        if name != "cache_common.cuh" and "launch_early(" not in code:
+            continue
+        early.append(name)
+        for word in ("__ldg", "ld.global.nc", "__restrict__", "doc_of_token(", "doc_of_block("):
+            assert word not in code, f"{name}: {word}"
+    assert early == ["cache_common.cuh", "k_evict.cu", "k_paged.cu", "k_rotary.cu"]

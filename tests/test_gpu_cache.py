@@ -663,6 +663,78 @@ def test_streams_that_part_and_meet(captured):
     assert _status() == 0
 
 
+@pytest.mark.parametrize("writer", ["cumsum", "cumsum of 64 bits", "eviction"])
+def test_documents_that_the_last_call_wrote(writer):
+    """cu_seqlens overwritten in place, by the call just before, for every rotation, its backward and
+    every append: in a row and captured as with the device idle before each.  An eviction
+    of rows within their budget writes their lengths, and lets the next kernel start early."""
+    m = _m()
+    wide = writer == "cumsum of 64 bits"
+    T, seqs, layers, hq, hkv, d, page = 6000, 40, 5, 4, 2, 64, 16
+    plan, g = m.rotary_plan(d), torch.Generator().manual_seed(450)
+    cuts = [torch.cat([torch.tensor([0]), torch.randint(0, T + 1, (seqs - 1,), generator=g).sort()[0],
+                       torch.tensor([T - 7 * i])]).clamp(max=T - 7 * i) for i in range(layers)]
+    cuts = [c.to("cuda", torch.int64 if wide else torch.int32) for c in cuts]
+    counts = [c.diff() for c in cuts]
+    pages = -(-T // page)
+    table = torch.arange(pages * seqs, device="cuda", dtype=torch.int32).view(seqs, pages)
+    lens = torch.zeros(seqs, dtype=torch.int32, device="cuda")
+    q0, k0 = (_normal(T, h, d, seed=451 + i) for i, h in enumerate((hq, hkv)))
+    # the cache whose evictions write documents: a row for each of their ends
+    small = m.paged_cache(1, 256, 1, 64, scores=True)
+    budget = torch.zeros(seqs + 1, T // 256 + 1, dtype=torch.int32, device="cuda")
+
+    def run(cache, idle):
+        def done(x):
+            if idle:
+                torch.cuda.synchronize()
+            return x
+        cu = torch.zeros(seqs + 1, dtype=cuts[0].dtype, device="cuda")
+        out, q, k = [], q0, k0
+        for i in range(layers):
+            def documents():
+                if writer == "eviction":
+                    return done(m.cache_evict(small, budget, cuts[i], T, 0))
+                done(torch.cumsum(counts[i], 0, dtype=cu.dtype, out=cu[1:]))
+                return cu
+            x, y = q.detach().requires_grad_(), k.detach().requires_grad_()
+            fresh = documents()
+            a, b = m.rotary(x, y, plan, cu_seqlens=fresh)
+            done(a)
+            back = torch.autograd.grad((a, b), (x, y), (q0, k0))
+            done(back[0])
+            fresh = documents()
+            r = done(m.cache_append(cache, k, b.detach(), table, lens, cu_seqlens=fresh, plan=plan, q=q))
+            out += [a.detach(), b.detach(), *back, r]
+            done(cu.zero_())
+            q, k = a.detach() + r, b.detach() + back[1]
+        return out
+
+    def empty():
+        c = m.paged_cache(pages * seqs, page, hkv, d, scores=True)
+        torch.cuda.synchronize()
+        return c
+
+    cache = empty()
+    want = [*run(cache, True), *cache]
+    for captured in (False, True):
+        for _ in range(2):
+            cache = empty()
+            if captured:
+                stream = torch.cuda.Stream()
+                with torch.cuda.stream(stream):
+                    graph = torch.cuda.CUDAGraph()
+                    with torch.cuda.graph(graph, stream=stream):
+                        got = run(cache, False)
+                    graph.replay()
+                torch.cuda.synchronize()
+            else:
+                got = run(cache, False)
+            for a, b in zip([*got, *cache], want):
+                assert torch.equal(a, b)
+    assert _status() == 0
+
+
 # ------------------------------ what is refused or flagged -----------------------
 
 
