@@ -454,7 +454,7 @@ int evict_blocks(const CacheArgs& c) {
   return blocks;
 }
 bool evict_on_chip(const CacheArgs& c, int most) {
-  return most <= kMostFused && evict_blocks(c) == 1;
+  return most == 0 || (most <= kMostFused && evict_blocks(c) == 1);
 }
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st, int* launches) {

@@ -302,3 +302,33 @@ def test_kernels_that_start_early_read_by_plain_loads():
         for word in ("__ldg", "ld.global.nc", "__restrict__", "doc_of_token(", "doc_of_block("):
             assert word not in code, f"{name}: {word}"
     assert early == ["cache_common.cuh", "k_evict.cu", "k_paged.cu", "k_rotary.cu"]
+
+
+def _evict(m, cache, table, keep, room, ws):
+    return m.load().msa_cache_evict(ctypes.byref(cache), ctypes.byref(table), keep, 0, 64 * P, room, ws,
+                                    None)
+
+
+@pytest.mark.parametrize("seqs,hkv", [(1, 1), (4, 8), (8, 8), (100, 8)])
+@pytest.mark.parametrize("pages,keep", [(64, 4096), (64, 5000), (512, 32768), (4096, 1 << 30),
+                                        (16, 1024)])
+def test_budgets_that_no_row_can_exceed(m, seqs, hkv, pages, keep):
+    """Nothing can move: no workspace is asked for, and none is missed."""
+    cache, table = _cache(m, hkv=hkv), _table(m, num_seqs=seqs, max_pages=pages, stride=pages)
+    assert m.msa_cache_evict_workspace_size(cache, table, keep) == 256
+    assert _evict(m, cache, table, keep, None, 0) == 4  # there is no device
+
+
+def test_sizes_of_256_say_that_nothing_is_used(m):
+    """Every eviction that uses its workspace asks for more."""
+    cache = _cache(m)
+    for seqs in (1, 30, 32):
+        for pages in (3, 17, 64, 700):
+            table = _table(m, num_seqs=seqs, max_pages=pages, stride=pages)
+            for keep in {1, 64, pages * 64 - 1, pages * 64, pages * 64 + 1, pages * 32}:
+                size = m.msa_cache_evict_workspace_size(cache, table, keep)
+                if size == 256:
+                    assert _evict(m, cache, table, keep, None, 0) == 4
+                else:
+                    assert size > 256 and _evict(m, cache, table, keep, None, 0) == 1
+                    assert _evict(m, cache, table, keep, P, size - 1) == 3

@@ -417,6 +417,27 @@ def test_evict_long_rows_and_wide_tables(lens, keep, recent, spare):
     _evict(lens, keep, recent, 256, 1, 64, spare=spare)
 
 
+@pytest.mark.parametrize("seqs", [1, 4, 8, 9])
+@pytest.mark.parametrize("more", [0, 1, 5000])
+@pytest.mark.parametrize("pages", [64, 300])
+def test_budgets_that_no_row_can_exceed(pages, more, seqs):
+    """Long tables whose every entry fits the budget, through the Python and the C call."""
+    m = _m()
+    cache = m.paged_cache(pages + 1, 64, 8, 64, scores=True)
+    table = torch.arange(pages, device="cuda", dtype=torch.int32).repeat(seqs, 1)
+    n = torch.tensor([pages * 64 - 700 * i for i in range(seqs)], device="cuda").clamp(min=0).int()
+    before = [x.clone() for x in cache]
+    assert torch.equal(m.cache_evict(cache, table, n, pages * 64 + more, 128), n)
+    left = torch.empty_like(n)
+    c, t = m.make_cache(cache), m.make_table(table, n)
+    size = m.msa_cache_evict_workspace_size(c, t, pages * 64 + more)
+    assert size == 256
+    m.msa_cache_evict(c, t, pages * 64 + more, 128, left, n.new_empty(0))
+    assert torch.equal(left, n) and _status() == 0
+    for x, y in zip(cache, before):
+        assert torch.equal(x, y)
+
+
 def test_evict_ties_and_unusual_weights():
     """Equal weights, zeros of both signs, infinities, NaN and negative numbers."""
     def change(cache, table):
