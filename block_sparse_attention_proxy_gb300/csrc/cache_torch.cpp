@@ -276,7 +276,7 @@ std::optional<Tensor> cache_append(const Tensor& ck, const Tensor& cv,
   constexpr const char* who = "cache_append";
   Pages c(who, ck, cv, weight, position, table, lens);
   const Tensor cu = or_none(cu_), positions = or_none(positions_), q = or_none(q_);
-  for (const Tensor* t : {&k, &v, &q}) no_grad(*t, who);
+  for (const Tensor& t : {k, v, q, c.weight}) no_grad(t, who);
   if (k.dim() != 3 || k.size(0) > kMost)
     throw py::value_error("k and v must be [T, Hkv, d] as in the cache, on its device");
   const int64_t T = k.size(0);
@@ -351,6 +351,7 @@ Tensor paged_attention(const Tensor& q, const Tensor& ck, const Tensor& cv,
        "q must be bf16 [sequences, Hq, d], d as in the cache, on its device");
   if (accumulate && !c.weight.defined())
     throw py::value_error("the cache keeps no weights to add to");
+  if (accumulate) no_grad(c.weight, who);
   c10::cuda::CUDAGuard guard(ck.device());
   at::NoGradGuard no_grad;
   c.describe(table, lens);
@@ -377,6 +378,7 @@ Tensor cache_evict(const Tensor& ck, const Tensor& cv, const std::optional<Tenso
   constexpr const char* who = "cache_evict";
   Pages c(who, ck, cv, weight, position, table, lens);
   if (!c.weight.defined()) throw py::value_error("the cache keeps no weights to go by");
+  no_grad(c.weight, who);
   if (keep < 1 || keep > kMost || recent < 0 || recent > keep)
     throw py::value_error("keep >= 1 and 0 <= recent <= keep expected");
   if (recent > 0 && !c.position.defined())

@@ -845,6 +845,37 @@ def test_refusals():
     assert _status() == 0
 
 
+def test_weights_that_require_a_gradient_are_refused():
+    """They are written in place; so is a tangent, which would stay as it was."""
+    import torch.autograd.forward_ad as fw
+
+    m = _m()
+    cache, table, n = _filled([100, 20], 64, 2, 64, 53)
+    q, kv = _normal(2, 4, 64, seed=54), _normal(2, 2, 64, seed=55)
+    before = [x.clone() for x in cache]
+
+    def calls(c):
+        return (lambda: m.paged_attention(q, c, table, n, accumulate=True),
+                lambda: m.cache_append(c, kv, kv, table, n), lambda: m.cache_evict(c, table, n, 10, 2))
+
+    learned = cache._replace(weight=cache.weight.clone().requires_grad_())
+    for call in calls(learned):
+        with pytest.raises(NotImplementedError, match="requires a gradient"):
+            call()
+    with fw.dual_level():
+        dual = cache._replace(weight=fw.make_dual(cache.weight, torch.ones_like(cache.weight)))
+        for call in calls(dual):
+            with pytest.raises(NotImplementedError, match="forward-mode"):
+                call()
+    for x, y in zip(cache, before):
+        assert torch.equal(x, y)
+    assert not m.paged_attention(q, learned, table, n).requires_grad  # does not write them
+    with torch.no_grad():
+        for call in calls(learned):
+            call()
+    assert _status() == 0
+
+
 def test_c_entry_points_give_the_functions_results():
     """With workspaces of the size that is asked for, full of NaN; one byte less is refused."""
     m = _m()
