@@ -204,6 +204,9 @@ msa_status msa_rotary(const msa_rotary_params* p, const int32_t* cu_seqlens, con
                   ((size_t)(a.T - 1) * z.stride + (size_t)z.heads * a.d) * bytes))
         return MSA_ERR_INVALID_ARG;
   }
+  const size_t row = (size_t)a.T * a.d * bytes;
+  if (a.hq > 0 && a.hkv > 0 && overlap(q_out, row * a.hq, k_out, row * a.hkv))
+    return MSA_ERR_INVALID_ARG;
   if (!aligned(cu_seqlens, 4) || (positions && !aligned(positions, p->position_bytes)))
     return MSA_ERR_INVALID_ARG;
   if (status_ptr(&a.status) != cudaSuccess) return MSA_ERR_CUDA;

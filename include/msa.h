@@ -317,9 +317,9 @@ msa_status msa_dense_bwd(const msa_dense_params* params, const int32_t* cu_seqle
  * result is rounded once.
  *
  * q, q_out [T, hq, d], k, k_out [T, hkv, d] (null with hkv = 0), one type; the outputs are
- * contiguous and must not overlap the inputs.  Either cu_seqlens is given (a position is the
- * place in the document; rows behind the last document come out zero) or positions [T],
- * int32 or int64, of any sign.
+ * contiguous and must not overlap the inputs or one another.  Either cu_seqlens is given (a
+ * position is the place in the document; rows behind the last document come out zero) or
+ * positions [T], int32 or int64, of any sign.
  */
 typedef enum msa_dtype { MSA_BF16 = 0, MSA_FP16 = 1, MSA_FP32 = 2 } msa_dtype;
 

@@ -332,3 +332,19 @@ def test_sizes_of_256_say_that_nothing_is_used(m):
                 else:
                     assert size > 256 and _evict(m, cache, table, keep, None, 0) == 1
                     assert _evict(m, cache, table, keep, P, size - 1) == 3
+
+
+def test_rotated_rows_over_each_other_are_refused(m):
+    """q_out [10, 2, 64] and k_out [10, 1, 64] of bf16: 2560 and 1280 bytes."""
+    p = m.make_rotary_params(10, 2, 1, 64, [1] * 16)
+    alone = {hq: m.make_rotary_params(10, hq, 2 - hq, 64, [1] * 16) for hq in (0, 2)}
+
+    def call(qo, ko, p=p):
+        return m.load().msa_rotary(ctypes.byref(p), None, P, P, 8 * P, qo, ko, None)
+
+    far = 64 * P
+    for ko in (far, far + 2544, far - 1264):
+        assert call(far, ko) == 1
+    for ko in (far + 2560, far - 1280):
+        assert call(far, ko) == 4  # there is no device
+    assert call(far, None, alone[2]) == 4 and call(None, far, alone[0]) == 4
