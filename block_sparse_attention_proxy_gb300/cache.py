@@ -128,7 +128,8 @@ def cache_append(cache: PagedCache, k, v, table, lens, cu_seqlens=None, position
     """Stores new tokens behind the `lens` entries of each sequence, which it does not change: one a
     sequence, or those that `cu_seqlens` [sequences + 1] gives it.  With `plan` k is rotated,
     by `positions` [T] or else the entries' numbers, and q, if given, is returned rotated
-    too.  New entries have weight 0.  Inference only."""
+    too.  New entries have weight 0.  k, v and q may be rows of the cache, but none that the call
+    writes.  Inference only."""
     return (_front or _load()).cache_append(*cache, k, v, table, lens, cu_seqlens, positions, plan,
                                             q)
 

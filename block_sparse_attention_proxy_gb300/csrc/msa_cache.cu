@@ -278,6 +278,12 @@ msa_status msa_paged_attention(const msa_cache* cache, const msa_table* table,
   if (a.cache.nseq == 0) return MSA_OK;
   if ((st = check_cache_pointers(a.cache)) != MSA_OK) return st;
   if (!q || !o || !aligned(q, 16) || !aligned(o, 16)) return MSA_ERR_INVALID_ARG;
+  // over itself a row is read by the CTA that writes it, or (shared rows) before the join writes
+  const long long packed = (long long)a.hq * a.cache.d;
+  if ((o != q || qs != packed) &&
+      overlap(o, (size_t)a.cache.nseq * packed * 2, q,
+              ((size_t)(a.cache.nseq - 1) * qs + packed) * 2))
+    return MSA_ERR_INVALID_ARG;
   const PagedWorkspace w = paged_workspace(a, p->accumulate != 0);
   if ((w.total > 0 && !ws) || !aligned(ws, 256)) return MSA_ERR_INVALID_ARG;
   if (ws_bytes < w.total) return MSA_ERR_WORKSPACE;

@@ -386,7 +386,9 @@ typedef struct msa_table {
  * and v copied, weight starts at 0.  With hq > 0 the queries q [T, hq, d] are rotated too, to q_out.
  * rotary->hkv and d are the cache's, dtype is MSA_BF16, inverse 0 and num_docs num_seqs or, without
  * cu_seqlens, 0; its strides are those of q and k, v_stride that of v.  Tokens behind the last
- * sequence enter nowhere, their rows of q_out come out zero.
+ * sequence enter nowhere, their rows of q_out come out zero.  q_out must not overlap q, k, v or the
+ * cache; q, k and v may be rows of the cache, but none that the call writes (which those are,
+ * only the table says: this is not checked).
  */
 msa_status msa_cache_append(const msa_cache* cache, const msa_table* table,
                             const msa_rotary_params* rotary, int64_t v_stride,
@@ -398,7 +400,7 @@ msa_status msa_cache_append(const msa_cache* cache, const msa_table* table,
  * Attention of one new token of each sequence over its entries (its own among them, if it has been
  * appended):
  *   s_j = softmax_scale q . k_j,  j < lens[b],  p = softmax(s),  o = sum_j p_j v_j.
- * q, o [num_seqs, hq, d] bf16, o contiguous; any hq / hkv from 1 to 64, hq <= 1024.  A sequence
+ * q, o [num_seqs, hq, d] bf16, o contiguous, and either q itself or without overlap with it; any hq / hkv from 1 to 64, hq <= 1024.  A sequence
  * without entries gets o = 0.  With `accumulate` the weights that an entry gets from the hq / hkv
  * heads of its KV head are added to cache->weight.  A score of -inf takes no weight; a sequence all
  * of whose scores are -inf gets o = 0.  Sums have a fixed order (the weights too, unless

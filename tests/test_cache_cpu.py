@@ -348,3 +348,23 @@ def test_rotated_rows_over_each_other_are_refused(m):
     for ko in (far + 2560, far - 1280):
         assert call(far, ko) == 4  # there is no device
     assert call(far, None, alone[2]) == 4 and call(None, far, alone[0]) == 4
+
+
+def test_attention_over_its_queries(m):
+    """o over q [3, 4, 64] itself is taken as far as its workspace; over a part of it, or over rows of
+    another stride, it is refused."""
+    cache, table = _cache(m), _table(m)
+
+    def call(q, o, stride=0):
+        p = m.make_paged_params(4, q_stride=stride)
+        return m.load().msa_paged_attention(ctypes.byref(cache), ctypes.byref(table), ctypes.byref(p), q,
+                                            o, P, 0, None)
+
+    size = 3 * 4 * 64 * 2
+    for o in (0, size, -size):
+        assert call(64 * P, 64 * P + o) == 3
+        assert call(64 * P, 64 * P + o, 256) == 3
+    for o in (16, 512, size - 16, 16 - size):
+        assert call(64 * P, 64 * P + o) == 1
+    assert call(64 * P, 64 * P, 512) == 1 and call(64 * P, 64 * P + 2 * 512 * 2 + 496, 512) == 1
+    assert call(64 * P, 64 * P + 2 * 512 * 2 + 512, 512) == 3

@@ -914,6 +914,20 @@ def test_c_entry_points_give_the_functions_results():
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("lens,hq,hkv", [([4000, 0, 300, 129], 8, 2), ([5, 100, 0, 77], 20, 4),
+                                         ([9000], 64, 1)])
+def test_attention_over_its_queries(lens, hq, hkv):
+    """Rows that CTAs share, rows of one CTA, and none: o may be q."""
+    m = _m()
+    cache, table, n = _filled(lens, 32, hkv, 64, 72, spare=0)
+    q, other = _normal(len(lens), hq, 64, seed=73), m.PagedCache(*(x.clone() for x in cache))
+    want = m.paged_attention(q, cache, table, n, 0.2, accumulate=True)
+    c, t, p = m.make_cache(other), m.make_table(table, n), m.make_paged_params(hq, 0.2, accumulate=True)
+    ws = torch.empty(m.msa_paged_attention_workspace_size(c, t, p), dtype=torch.uint8, device="cuda")
+    m.msa_paged_attention(c, t, p, q, q, ws)
+    assert torch.equal(q, want) and torch.equal(other.weight, cache.weight) and _status() == 0
+
+
 def test_inference_mode():
     m = _m()
     with torch.inference_mode():
