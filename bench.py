@@ -25,9 +25,9 @@ it (HostInputStep: the copies overlap the kernels on two copy streams).
 (1k tiny, 32k varlen, 128k, 512k, 1M), each with the dense SDPA comparator and
 the fp64 CPU oracle timed on the host cores (every row for the tiny and varlen
 workloads, a seeded sample of rows for the others).
-With N > 1 (torchrun), every rank runs an independent replica on its own GPU
-(the path has no exchange step); the aggregate counts all ranks' work over the
-slowest rank's time; per_config is measured on rank 0's GPU only.
+One GPU: the selection kernel's cluster-multicast loads are for runs on one GPU alone, so
+N > 1 and more than one rank are refused (the reference arm, which uses no GPU, runs under
+torchrun on rank 0).
 """
 from __future__ import annotations
 
@@ -199,11 +199,7 @@ def dist_setup():
     if world > 1:
         import torch.distributed as dist
 
-        if torch.cuda.is_available():
-            torch.cuda.set_device(local)
-            dist.init_process_group("nccl")
-        else:  # host-only runs of the rank logic (CPU tests)
-            dist.init_process_group("gloo")
+        dist.init_process_group("gloo")  # the rank logic alone: main() refuses to measure
     elif torch.cuda.is_available():
         torch.cuda.set_device(0)
     return world, rank, local
@@ -223,8 +219,7 @@ def max_over_ranks(x: float, world: int) -> float:
         return x
     import torch.distributed as dist
 
-    dev = "cuda" if dist.get_backend() == "nccl" else "cpu"
-    t = torch.tensor([x], dtype=torch.float64, device=dev)
+    t = torch.tensor([x], dtype=torch.float64)
     dist.all_reduce(t, op=dist.ReduceOp.MAX)
     return float(t.item())
 
@@ -782,6 +777,9 @@ def main():
     args = ap.parse_args()
     if args.warmup < 3 and args.impl == "ours":
         print("note: fewer than 3 warm-up steps", file=sys.stderr)
+    if args.impl == "ours" and max(args.gpus, int(os.environ.get("WORLD_SIZE", "1"))) > 1:
+        raise SystemExit("bench.py runs on one GPU: the selection kernel's cluster-multicast loads "
+                         "are not for runs on several")
     if args.impl == "reference":
         run_reference(args)
     elif args.only_select:

@@ -74,3 +74,14 @@ def test_reference_arm_under_torchrun_prints_one_line_from_rank0():
     assert d["config"]["workload"].startswith("tiny")
     assert d["e2e"]["value"] == d["value"] and d["e2e"]["h2d_bytes_per_step"] == 0
     assert d["cpu_baseline"]["value"] == d["value"] and d["cpu_baseline"]["cores"] >= 1
+
+
+def test_more_than_one_gpu_is_refused():
+    """Before anything is set up: no rank meets another, none touches a GPU."""
+    for flags, env in ((["--gpus", "2"], {}), (["--gpus", "4", "--only-select"], {}),
+                       ([], dict(WORLD_SIZE="2", RANK="1", LOCAL_RANK="1")),
+                       (["--only-select"], dict(WORLD_SIZE="2", RANK="0", LOCAL_RANK="0"))):
+        r = subprocess.run([sys.executable, "bench.py", "--steps", "1", "--workload", "tiny", *flags],
+                           cwd=ROOT, capture_output=True, text=True, timeout=300,
+                           env={**os.environ, "CUDA_VISIBLE_DEVICES": "", **env})
+        assert r.returncode != 0 and "one GPU" in r.stderr and "{" not in r.stdout, r.stderr[-500:]
