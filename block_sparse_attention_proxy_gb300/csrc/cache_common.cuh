@@ -25,6 +25,15 @@ __device__ __forceinline__ T fetch(const T* p) {
   return *p;
 }
 
+// A load of a number that the kernels before the previous one wrote, ahead of the wait: the previous
+// one has waited for them before it let this kernel start, but this kernel has not, so the load goes
+// past L1, which might still hold what was there before.
+__device__ __forceinline__ int32_t fetch_ahead(const int32_t* p) {
+  int32_t x;
+  asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
+  return x;
+}
+
 constexpr int kRotaryMaxPairs = 128;     // head dim 256
 constexpr int kCacheMaxSeqs = 1 << 20;
 constexpr int kCacheMaxEntries = 1 << 30;  // of one sequence: max_pages * page_size
@@ -55,15 +64,18 @@ struct CacheArgs {
 };
 
 // Length of sequence b within what the table can name; others are flagged.
+template <bool AHEAD = false>
 __device__ __forceinline__ int cache_len(const CacheArgs& c, int b) {
-  const int n = fetch(c.lens + b);
+  const int n = AHEAD ? fetch_ahead(c.lens + b) : fetch(c.lens + b);
   if (n >= 0 && n <= c.capacity) return n;
   set_status(c.status, MSA_ERR_DEVICE_CHECK);
   return n < 0 ? 0 : c.capacity;
 }
 // Page of entry i of sequence b, or -1 (flagged) where the table names none of the cache's.
+template <bool AHEAD = false>
 __device__ __forceinline__ int cache_page(const CacheArgs& c, int b, int i) {
-  const int page = fetch(c.table + (long long)b * c.table_stride + (i >> c.page_shift));
+  const int32_t* at = c.table + (long long)b * c.table_stride + (i >> c.page_shift);
+  const int page = AHEAD ? fetch_ahead(at) : fetch(at);
   if ((unsigned)page < (unsigned)c.num_pages) return page;
   set_status(c.status, MSA_ERR_DEVICE_CHECK);
   return -1;

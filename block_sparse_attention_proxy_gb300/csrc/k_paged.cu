@@ -75,17 +75,19 @@ struct PagedSpan {
   long long x0, x1;
   int b, off;
 };
+template <bool AHEAD>  // whether before wait_for_previous
 __device__ __forceinline__ int tiles_of(const CacheArgs& c, int b) {
-  return (cache_len(c, b) + 127) >> 7;
+  return (cache_len<AHEAD>(c, b) + 127) >> 7;
 }
 
 // Counts the tiles of all sequences (every thread of the block, n of them) and looks up the tiles
 // of team c.  With `whole` its range begins and ends with rows: at the first row that begins
 // at or behind the cut.  `sm`: n / 32 + 2 numbers.
+template <bool AHEAD>
 __device__ PagedCuts paged_span(const PagedArgs& a, int c, long long* sm, int n, PagedSpan* span) {
   if (a.direct) {  // a row for each team at most: nothing to count
     span->b = c / a.groups;
-    const int tiles = span->b < a.cache.nseq ? tiles_of(a.cache, span->b) : 0;
+    const int tiles = span->b < a.cache.nseq ? tiles_of<AHEAD>(a.cache, span->b) : 0;
     span->off = (c - span->b * a.groups) * tiles;
     span->x0 = (long long)c * ((a.cache.capacity + 127) / 128);
     span->x1 = span->x0 + tiles;
@@ -96,7 +98,7 @@ __device__ PagedCuts paged_span(const PagedArgs& a, int c, long long* sm, int n,
   const int per = (a.cache.nseq + n - 1) / n, first = min(tid * per, a.cache.nseq),
             last = min(first + per, a.cache.nseq);
   long long mine = 0;
-  for (int b = first; b < last; ++b) mine += tiles_of(a.cache, b);
+  for (int b = first; b < last; ++b) mine += tiles_of<AHEAD>(a.cache, b);
   mine *= a.groups;
   long long incl = mine;
 #pragma unroll
@@ -121,7 +123,7 @@ __device__ PagedCuts paged_span(const PagedArgs& a, int c, long long* sm, int n,
       long long left = x[i] - before;
       int b = first;
       for (; b < last - 1; ++b) {
-        const long long t = (long long)tiles_of(a.cache, b) * a.groups;
+        const long long t = (long long)tiles_of<AHEAD>(a.cache, b) * a.groups;
         if (left < t) break;
         left -= t;
       }
@@ -136,7 +138,7 @@ __device__ PagedCuts paged_span(const PagedArgs& a, int c, long long* sm, int n,
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (s_b[i] >= a.cache.nseq) continue;
-      const int tiles = tiles_of(a.cache, s_b[i]), t = s_off[i] % tiles;
+      const int tiles = tiles_of<AHEAD>(a.cache, s_b[i]), t = s_off[i] % tiles;
       if (t == 0) continue;
       x[i] += tiles - t;
       if (i == 0) span->off += tiles - t;
@@ -148,6 +150,7 @@ __device__ PagedCuts paged_span(const PagedArgs& a, int c, long long* sm, int n,
 }
 
 // The rows (sequence, KV head) that a CTA's range of tiles runs through.
+template <bool AHEAD>
 struct PagedWalk {
   int b, h, t;      // next tile; h: group of KV heads
   long long left;   // tiles of the range that are left
@@ -158,7 +161,7 @@ struct PagedWalk {
   int at_side;      // of the CTA
   __device__ __forceinline__ void seek(const PagedArgs& a) {
     while (b < a.cache.nseq) {
-      len = cache_len(a.cache, b);
+      len = cache_len<AHEAD>(a.cache, b);
       tiles = (len + 127) >> 7;
       if (tiles > 0) return;
       ++b;
@@ -358,7 +361,7 @@ __global__ void __launch_bounds__(PagedCfg<D, GC>::kThreads, PagedCfg<D, GC>::kC
   }
   __syncwarp();
   PagedSpan span;
-  paged_span(a, blockIdx.x / a.side, scan, C::kThreads, &span);
+  paged_span<false>(a, blockIdx.x / a.side, scan, C::kThreads, &span);
   // The loading warp has what it needs and starts; the others wait for its barriers.
   tc_fence_before();
   if (warp == kLoads)
@@ -396,7 +399,7 @@ __global__ void __launch_bounds__(PagedCfg<D, GC>::kThreads, PagedCfg<D, GC>::kC
       if (++s == NR) s = 0, ++lap;
     };
     struct { int h, len, t, page; } last{0, 0, -1, 0};
-    PagedWalk w(a, span, blockIdx.x);
+    PagedWalk<false> w(a, span, blockIdx.x);
     while (ok && w.next(a)) {
       int page = page_of(w.sb, w.len, w.t0);
       if (part >= 2 && !(ok = wait(B_QE + (part & 1), ((part >> 1) & 1) ^ 1, part))) break;
@@ -466,7 +469,7 @@ __global__ void __launch_bounds__(PagedCfg<D, GC>::kThreads, PagedCfg<D, GC>::kC
       mma_commit(el, bar(B_E + s));
       if (++s == NR) s = 0, ++lap;
     };
-    PagedWalk w(a, span, blockIdx.x);
+    PagedWalk<false> w(a, span, blockIdx.x);
     while (ok && w.next(a)) {
       if (!(ok = wait(B_Q + (part & 1), (part >> 1) & 1, part))) break;
       new_part = true;
@@ -510,7 +513,7 @@ __global__ void __launch_bounds__(PagedCfg<D, GC>::kThreads, PagedCfg<D, GC>::kC
     bool dead = false;
     int u = 0, part = 0;
     long long x = span.x0;  // tile over all rows
-    PagedWalk w(a, span, blockIdx.x);
+    PagedWalk<false> w(a, span, blockIdx.x);
     while (w.next(a)) {
       // references: of this thread, or (kShared) of the warpgroup
       float own[C::kShared ? 1 : CH], l[CH];
@@ -679,19 +682,20 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
   const int c = blockIdx.x / a.side, at_side = blockIdx.x % a.side, G = a.G;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   PagedSpan span;
-  const PagedCuts cuts = paged_span(a, c, scan, kJoinThreads, &span);
+  const PagedCuts cuts = paged_span<true>(a, c, scan, kJoinThreads, &span);
   // Where team i keeps its part of a row whose first tile is team c0's: see k_paged.
   auto part_of = [&](int i, int c0, bool behind) {
     return (((size_t)i * a.side + at_side) * 2 + (i == c0 && behind)) * G;
   };
   // What follows from the lengths alone is worked out before k_paged's results are waited for: it
-  // lets this kernel start once all before it is complete, and writes no length and no page.
+  // lets this kernel start once all before it is complete, and writes no length and no page (which
+  // fetch_ahead reads here).
   // The row of this team's first tile, if it begins before that:
   int c0 = 0, c1 = 0;
   bool behind = false;
   size_t row0 = 0;
   if (!a.whole && c > 0 && c < cuts.n) {
-    const int tiles = tiles_of(a.cache, span.b), h = span.off / tiles, t = span.off - h * tiles;
+    const int tiles = tiles_of<true>(a.cache, span.b), h = span.off / tiles, t = span.off - h * tiles;
     const long long r0 = span.x0 - t;
     if (t > 0) {
       c0 = cuts.team_of(r0);
@@ -705,7 +709,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
     // the first and the last of the range.
     struct { int c0, c1; bool on, behind; } shared[2] = {};
     {
-      PagedWalk w(a, span, blockIdx.x);
+      PagedWalk<true> w(a, span, blockIdx.x);
       long long x = span.x0;
       for (int parts = 0; w.next(a); ++parts, x += w.t1 - w.t0) {
         if (w.whole()) continue;
@@ -717,7 +721,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
         s.behind = cuts.cut(s.c0) < r0;
       }
     }
-    PagedWalk w(a, span, blockIdx.x);
+    PagedWalk<true> w(a, span, blockIdx.x);
     int next = warp;                 // this warp's tile, counted over the range
     int part = -1, done = 0, n = 0;  // tiles before the part, of the part
     auto seek = [&] {
@@ -731,7 +735,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
     };
     auto first_entry = [&] { return (w.t0 + next - done) * 128 + 4 * lane; };
     bool more = seek();
-    int page = more && first_entry() < w.len ? cache_page(a.cache, w.sb, first_entry()) : -1;
+    int page = more && first_entry() < w.len ? cache_page<true>(a.cache, w.sb, first_entry()) : -1;
     wait_for_previous();
     for (int i = warp; i < 2 * G; i += kJoinThreads / 32) {
       const int g = i % G, which = i / G;

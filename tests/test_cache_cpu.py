@@ -368,3 +368,16 @@ def test_attention_over_its_queries(m):
         assert call(64 * P, 64 * P + o) == 1
     assert call(64 * P, 64 * P, 512) == 1 and call(64 * P, 64 * P + 2 * 512 * 2 + 496, 512) == 1
     assert call(64 * P, 64 * P + 2 * 512 * 2 + 512, 512) == 3
+
+
+def test_the_join_reads_past_l1_before_its_wait():
+    """What it works out ahead of its wait rests on lengths and pages that it has not waited for."""
+    import block_sparse_attention_proxy_gb300 as package
+
+    with open(os.path.join(os.path.dirname(package.__file__), "csrc", "k_paged.cu")) as f:
+        code = re.sub(r"//[^\n]*", "", f.read())
+    join = code[code.index("k_paged_join(const"):]
+    ahead = join[:join.index("wait_for_previous()")]
+    assert "paged_span<true>(" in ahead and "PagedWalk<true> w" in ahead
+    for word in ("fetch(", "<false>", "cache_len(", "cache_page(", "tiles_of(", "PagedWalk w"):
+        assert word not in ahead, word

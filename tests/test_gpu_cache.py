@@ -756,6 +756,51 @@ def test_documents_that_the_last_call_wrote(writer):
     assert _status() == 0
 
 
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("lens,hq,hkv,d,page", [([3000, 200, 0, 1020], 8, 2, 128, 64),
+                                                ([9000], 16, 16, 64, 16), ([100, 900], 64, 1, 64, 256)])
+def test_lengths_and_pages_changed_in_place(lens, hq, hkv, d, page, captured):
+    """One table and one tensor of lengths, rewritten before each of many attentions over rows that
+    CTAs share: as with the device idle before each."""
+    m = _m()
+    steps = 12
+    cache, table0, top = _filled(lens, page, hkv, d, 460, spare=0)
+    q = _normal(len(lens), hq, d, seed=470)
+    weight0 = cache.weight.clone()
+    at = [(top - 83 * i * i).clamp(min=0) for i in range(steps)]
+    order = [torch.cat([torch.roll(r[r >= 0], i), r[r < 0]]) for i in range(steps) for r in table0]
+    order = torch.stack(order).view(steps, *table0.shape).int()
+
+    def run(idle):
+        table, n, out = torch.empty_like(table0), torch.empty_like(top), []
+        for i in range(steps):
+            n.copy_(at[i])
+            table.copy_(order[i])
+            if idle:
+                torch.cuda.synchronize()
+            out.append(m.paged_attention(q, cache, table, n, 0.1, accumulate=i % 2 == 0))
+            if idle:
+                torch.cuda.synchronize()
+        return out
+
+    want, weights = run(True), cache.weight.clone()
+    for _ in range(3):
+        cache.weight.copy_(weight0)
+        torch.cuda.synchronize()
+        if captured:
+            stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+            with torch.cuda.stream(stream):
+                with torch.cuda.graph(graph, stream=stream):
+                    got = run(False)
+                graph.replay()
+        else:
+            got = run(False)
+        torch.cuda.synchronize()
+        for x, y in zip([*got, cache.weight], [*want, weights]):
+            assert torch.equal(x, y)
+    assert _status() == 0
+
+
 # ------------------------------ what is refused or flagged -----------------------
 
 
