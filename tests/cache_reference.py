@@ -114,3 +114,11 @@ def within(got, want, limit, name=""):
     assert torch.equal(fine, got.isfinite()), f"{name}: other places are finite"
     over = ((got - want).abs() - limit)[fine]
     assert not over.numel() or over.max() <= 0, f"{name}: {over.max():.3e} over the limit"
+
+
+def placed(got, want, name=""):
+    """NaN in the same places, and every infinity with its sign."""
+    got, want = (t.detach().double().cpu() for t in (got, want))
+    assert torch.equal(got.isnan(), want.isnan()), f"{name}: NaN in other places"
+    at = want.isinf() | got.isinf()
+    assert torch.equal(got[at], want[at]), f"{name}: other infinities"

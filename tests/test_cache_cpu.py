@@ -381,3 +381,59 @@ def test_the_join_reads_past_l1_before_its_wait():
     assert "paged_span<true>(" in ahead and "PagedWalk<true> w" in ahead
     for word in ("fetch(", "<false>", "cache_len(", "cache_page(", "tiles_of(", "PagedWalk w"):
         assert word not in ahead, word
+
+
+def test_placed_finds_planted_mistakes():
+    from cache_reference import placed
+
+    inf, nan = float("inf"), float("nan")
+    want = torch.tensor([1.0, inf, -inf, nan])
+    placed(want + torch.tensor([0.5, 0, 0, 0]), want)
+    for wrong in ([1.0, -inf, -inf, nan], [1.0, nan, -inf, nan], [1.0, inf, -inf, inf],
+                  [1.0, inf, -inf, 0.0], [inf, inf, -inf, nan], [1.0, 3e38, -inf, nan]):
+        with pytest.raises(AssertionError):
+            placed(torch.tensor(wrong), want)
+
+
+def _half_a_unit(words, doubles):
+    """Whether every whole number lies within half of 2^-64 of a turn of its frequency (and 2^-150
+    for the literal of 2 pi, right to 2^-157 of itself)."""
+    two_pi = Fraction(int("6283185307179586476925286766559005768394338798750"), 10 ** 48)
+    for word, f in zip(words, doubles, strict=True):
+        off = Fraction(word, 2 ** 64) - Fraction(f) / two_pi
+        if abs(off - round(off)) > Fraction(1, 2 ** 65) + Fraction(1, 2 ** 150):
+            return False
+    return True
+
+
+@pytest.mark.parametrize("dims,kw", [(64, {}), (128, {}), (256, dict(base=1e6)), (16, dict(base=0.5)),
+                                     (32, dict(stretch=4.0)),
+                                     (128, dict(stretch=8.0, trained_length=4096)),
+                                     (16, dict(frequencies=[0.0, -1.0, 1e-9, 7.5, 6.25, 1, 2, 3])),
+                                     (16, dict(frequencies=[5e-324, -1e-20, 1e15, -3.7e9, 0.1, 2.0 ** -60,
+                                                            6.283185307179586, -6.283185307179587]))])
+def test_plan_frequencies_to_half_a_unit(m, dims, kw):
+    """Of the doubles that the documented rule gives, in its order of operations."""
+    if "frequencies" in kw:
+        doubles = [float(f) for f in kw["frequencies"]]
+    else:
+        doubles, s = [], kw.get("stretch", 1.0)
+        for i in range(dims // 2):
+            f = kw.get("base", 10000.0) ** (-2 * i / dims)
+            part = 0.0
+            if "trained_length" in kw:
+                turns = kw["trained_length"] * f / (2 * math.pi)
+                part = min(1.0, max(0.0, (turns - 1.0) / (32.0 - 1.0)))
+            doubles.append(f * (part + (1 - part) / s))
+    assert _half_a_unit(m.rotary_plan(dims, **kw).frequencies, doubles)
+
+
+@pytest.mark.parametrize("dims", [64, 128])
+def test_half_a_unit_finds_plans_of_64_bit_floats(m, dims):
+    doubles = [10000.0 ** (-2 * i / dims) for i in range(dims // 2)]
+    rounded = [int(f / (2 * math.pi) % 1 * 2.0 ** 64) for f in doubles]
+    assert not _half_a_unit(rounded, doubles)
+    words = list(m.rotary_plan(dims).frequencies)
+    for i in (0, dims // 4, dims // 2 - 1):
+        for by in (-1, 1):
+            assert not _half_a_unit(words[:i] + [words[i] + by] + words[i + 1:], doubles)

@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from cache_reference import attend_exact, evict_exact, gather, rotary_exact, within
+from cache_reference import attend_exact, evict_exact, gather, placed, rotary_exact, within
 
 pytestmark = pytest.mark.gpu
 
@@ -164,6 +164,29 @@ def test_infinite_and_nan_scores(accumulate):
         gain = (gather(cache.weight.transpose(1, 2), table[1], 300)
                 - gather(before.transpose(1, 2), table[1], 300))
         assert not gain[:, 1].any()
+
+
+@pytest.mark.parametrize("lens", [[300, 200, 90], [3000, 200, 1111]])
+def test_weights_of_infinite_and_nan_scores(lens):
+    """NaN in every entry that a head with such a score has weighed, zero gain where all scores are
+    -inf: whole rows and rows that CTAs share."""
+    m = _m()
+    cache, table, n = _filled(lens, 32, 2, 64, 74)
+    q = _normal(3, 8, 64, seed=75)
+    q[:, :, 0] = 1
+    cache.k[..., 0] = 0
+    for b, i, h, value in ((0, 150, 0, float("inf")), (1, 20, 1, float("nan")), (2, 89, 1, float("-inf"))):
+        cache.k[int(table[b, i // 32]), i % 32, h, 0] = value
+    for i in range(lens[2]):
+        cache.k[int(table[2, i // 32]), i % 32, 0, 0] = float("-inf")
+    cache.weight.zero_()
+    o = m.paged_attention(q, cache, table, n, softmax_scale=0.125, accumulate=True)
+    want, _, weights = attend_exact(q, cache.k, cache.v, table, lens, 0.125)
+    placed(o, want, "o")
+    for b, length in enumerate(lens):
+        gain = gather(cache.weight.transpose(1, 2), table[b], length).T
+        placed(gain, weights[b][0], "weight")
+    assert not gain[0].any() and gain[1].sum() > 3.9 and _status() == 0
 
 
 def test_infinite_values():

@@ -4,7 +4,7 @@ import random
 import pytest
 import torch
 
-from cache_reference import positions_of, rotary_exact, within
+from cache_reference import placed, positions_of, rotary_exact, within
 
 pytestmark = pytest.mark.gpu
 
@@ -266,3 +266,21 @@ def test_refusals():
     assert empty[0].shape == (0, 2, 64)
     empty[0].sum().backward()
     assert m.msa_get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_infinite_and_nan_elements(dtype, interleaved):
+    """Each reaches its pair, with the sign that the angle gives it, and no other."""
+    m = _m()
+    q, r = _rows(60, 3, 64, 40, dtype), random.Random(41)
+    for _ in range(200):
+        value = r.choice([float("inf"), float("-inf"), float("nan")])
+        q[r.randrange(60), r.randrange(3), r.randrange(64)] = value
+    at = [r.randrange(0, 5000) for _ in range(60)]
+    got = m.rotary(q, None, m.rotary_plan(48, interleaved=interleaved),
+                   positions=torch.tensor(at, device="cuda"))[0]
+    want, limit = rotary_exact(q, at, _freq(48), interleaved)
+    assert want.isinf().any() and want.isnan().any()
+    placed(got, want)
+    within(got, want, limit)
