@@ -1,18 +1,20 @@
-"""Rotary positions and a paged key-value cache: what answering with a trained model needs
-beside the attention over packed documents.
+"""Rotary positions and a paged key-value cache: for answering with layers of plain causal
+attention (no block selection, no position bias), one new token of each sequence at a time.
 
     plan = rotary_plan(d)                                           # once
     q, k = rotary(q, k, plan, cu_seqlens=cu_seqlens)                # in training, differentiable
 
     cache = paged_cache(pages, page_size, hkv, d, scores=True)      # once
-    q = cache_append(cache, k, v, table, lens, plan=plan, q=q)      # each step: a token a sequence
-    lens += 1
+    q = cache_append(cache, k, v, table, lens, positions=at, plan=plan, q=q)  # a token a sequence
+    lens, at = lens + 1, at + 1
     o = paged_attention(q, cache, table, lens, accumulate=True)
     lens = cache_evict(cache, table, lens, keep=4096, recent=128)   # where a budget is set
 
 Entry i of a sequence lies in page table[b, i // page_size], slot i % page_size; which pages a
 sequence has is the caller's.  Keys are stored rotated, so the order of the entries carries no
-meaning and eviction may move them.  Nothing is read back to the host: no call waits for the GPU,
+meaning and eviction may move them.  From the first eviction on a sequence has fewer entries than
+its text has tokens: a new token's position is then the caller's to count (`at`); where nothing is ever
+evicted it may be left out.  Nothing is read back to the host: no call waits for the GPU,
 all may be captured in a CUDA graph.  The front end (csrc/cache_torch.cpp) only moves tensors in and
 out of the library; every step runs in its kernels.
 
@@ -128,7 +130,8 @@ def cache_append(cache: PagedCache, k, v, table, lens, cu_seqlens=None, position
     """Stores new tokens behind the `lens` entries of each sequence, which it does not change: one a
     sequence, or those that `cu_seqlens` [sequences + 1] gives it.  With `plan` k is rotated,
     by `positions` [T] or else the entries' numbers, and q, if given, is returned rotated
-    too.  New entries have weight 0.  k, v and q may be rows of the cache, but none that the call
+    too.  After an eviction those numbers are no positions any more: `positions` has to be given.
+    New entries have weight 0.  k, v and q may be rows of the cache, but none that the call
     writes.  Inference only."""
     return (_front or _load()).cache_append(*cache, k, v, table, lens, cu_seqlens, positions, plan,
                                             q)
@@ -147,5 +150,7 @@ def cache_evict(cache: PagedCache, table, lens, keep: int, recent: int) -> torch
     """Cuts sequences down to `keep` entries and returns the new lengths.  For each KV head by
     itself the entries of the newest `recent` positions stay, and of the others those with the largest
     accumulated weights (equal ones: the lower entry).  What stays moves to the first `keep`
-    entries; pages behind them are free."""
+    entries; pages behind them are free.  From then on cache_append needs `positions`.  Weights come
+    from paged_attention alone, one token at a time: those of a prompt that no token has attended to are
+    0, and of such entries the oldest stay, unless the caller fills cache.weight."""
     return (_front or _load()).cache_evict(*cache, table, lens, keep, recent)

@@ -382,7 +382,8 @@ typedef struct msa_table {
  * New entries for the cache.  Token t of sequence b (cu_seqlens [num_seqs + 1]; null: one token
  * a sequence, T = num_seqs) becomes entry lens[b] + (its place among the sequence's new
  * tokens); lens are the lengths before the call and are not written.  Its position is
- * positions[t], or, with positions null, the entry's number; k is rotated by it as by msa_rotary
+ * positions[t], or, with positions null, the entry's number (after msa_cache_evict no longer its
+ * place in the text: give positions); k is rotated by it as by msa_rotary
  * and v copied, weight starts at 0.  With hq > 0 the queries q [T, hq, d] are rotated too, to q_out.
  * rotary->hkv and d are the cache's, dtype is MSA_BF16, inverse 0 and num_docs num_seqs or, without
  * cu_seqlens, 0; its strides are those of q and k, v_stride that of v.  Tokens behind the last

@@ -539,6 +539,46 @@ def test_answering_under_a_budget():
     assert _status() == 0
 
 
+def test_documented_steps_under_a_budget():
+    """The module's own loop, run as it stands there with a smaller budget: each entry that is left has
+    the position of its token, its key turned by that, and the newest ones are among them."""
+    import re
+
+    m = _m()
+    lines = [x.strip() for x in m.cache.__doc__.splitlines() if x.startswith("    ")]
+    step = [x for x in lines if re.match(r"q = cache_append|lens, at|o = paged|lens = cache_evict", x)]
+    assert len(step) == 4
+    step = "\n".join(step).replace("keep=4096", "keep=20").replace("recent=128", "recent=3")
+    plan, hq, hkv, d, steps = m.rotary_plan(64), 4, 2, 64, 50
+    table = torch.arange(8, device="cuda", dtype=torch.int32).view(2, 4)
+    space = dict(cache_append=m.cache_append, paged_attention=m.paged_attention, plan=plan,
+                 cache_evict=m.cache_evict, cache=m.paged_cache(8, 16, hkv, d, scores=True), table=table,
+                 lens=torch.zeros(2, dtype=torch.int32, device="cuda"),
+                 at=torch.zeros(2, dtype=torch.int64, device="cuda"))
+    keys, values = [], []
+    for i in range(steps):
+        space |= dict(q=_normal(2, hq, d, seed=500 + i, scale=0.2), k=_normal(2, hkv, d, seed=600 + i),
+                      v=_normal(2, hkv, d, seed=700 + i))
+        keys.append(m.rotary(space["k"], None, plan, positions=torch.tensor([i, i], device="cuda"))[0])
+        values.append(space["v"])
+        exec(step, space)
+        n = min(i + 1, 20)
+        assert space["lens"].tolist() == [n, n] and space["at"].tolist() == [i + 1, i + 1]
+        for b in range(2):
+            at = gather(space["cache"].position.transpose(1, 2), table[b], n).tolist()
+            for h in range(hkv):
+                own = [x[h] for x in at]
+                assert len(set(own)) == n and set(range(max(0, i - 2), i + 1)) <= set(own) and max(own) == i
+    for b in range(2):
+        k, v, at = (gather(x, table[b], 20) for x in (space["cache"].k, space["cache"].v,
+                                                     space["cache"].position.transpose(1, 2)))
+        for h in range(hkv):
+            for e in range(20):
+                t = int(at[e, h])
+                assert torch.equal(k[e, h], keys[t][b, h]) and torch.equal(v[e, h], values[t][b, h])
+    assert _status() == 0
+
+
 def test_captured_steps():
     """A step captured once and replayed, two graphs with workspaces of their own side by side."""
     m = _m()
