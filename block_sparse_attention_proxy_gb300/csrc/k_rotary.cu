@@ -5,7 +5,7 @@
 // f is in turns a position, as a fraction of 2^64, so p f modulo a turn is one product of whole
 // numbers that drops what lies above 64 bits: exact at any position, where an angle in fp32
 // is off by radians from some 2^24 on.  The turn's upper 32 bits become half turns in [-1, 1)
-// (2^-32 of a turn, below fp32's own step).
+// (see turns()).
 //
 // A thread has 16 elements of a row: 8 pairs (two runs of 8 elements half the rotated part apart,
 // or 16 neighbours), or 16 elements that only move.  It takes 8 sines and cosines once
@@ -100,22 +100,33 @@ __device__ __forceinline__ long long position_of(const RotaryArgs& a, int t) {
                                : (long long)fetch(static_cast<const int*>(a.positions) + t);
 }
 
-// Cosines and sines of 8 pairs from `pair` on at position p.  Results of 16 bits take the hardware's
-// functions, whose error over a turn (2^-21) is far below their rounding: sincospif's
-// instructions for 8 pairs outnumbered those for the rows where a thread has few heads.
+// Cosines and sines of 8 pairs from `pair` on at position p.
+//
+// fp32: the upper 32 bits of a turn do not fit a float; what it drops (2^-25 of half a turn at most, 9.4e-8
+// radians, as much as the functions' own error) comes back by the first term of the angle sum.
+//
+// Results of 16 bits take the hardware's functions of the rounded angle, off by 2^-21.19 at most between
+// -pi and pi: sincospif's instructions for 8 pairs outnumbered those for the rows where a thread has few
+// heads (24001 tokens of 9 heads of d = 64, half of each: 22 us and 11.6).  Against the length of the pair
+// that is far below half a step (2^-8 in bf16, 2^-11 in fp16), against an element that nearly cancels it is
+// not: one below 2^-10 of its pair (fp16; 2^-13 in bf16) may be off by more than its own rounding.
 template <typename T>
 __device__ __forceinline__ void turns(const RotaryArgs& a, int pair, long long p, float (&c)[8],
                                       float (&s)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint64_t turn = a.freq[pair + i] * (uint64_t)p;
-    const float half = (float)(int32_t)(turn >> 32);  // 2^-31 half turns, in [-1, 1)
+    const int32_t whole = (int32_t)(turn >> 32);  // 2^-31 half turns, in [-1, 1)
+    const float half = (float)whole;
     float sn, cs;
     if (sizeof(T) == 2) {
       sn = __sinf(half * (0x1p-31f * kPi));
       cs = __cosf(half * (0x1p-31f * kPi));
     } else {
       sincospif(half * 0x1p-31f, &sn, &cs);
+      const float rest = (float)(whole - (int32_t)half) * (0x1p-31f * kPi), s0 = sn;
+      sn = fmaf(cs, rest, sn);
+      cs = fmaf(-s0, rest, cs);
     }
     c[i] = cs * a.amplitude;
     s[i] = sn * a.amplitude * a.sign;

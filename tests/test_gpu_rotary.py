@@ -1,4 +1,5 @@
 """Rotary positions against their definition in fp64."""
+import math
 import random
 
 import pytest
@@ -284,3 +285,27 @@ def test_infinite_and_nan_elements(dtype, interleaved):
     assert want.isinf().any() and want.isnan().any()
     placed(got, want)
     within(got, want, limit)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_fp32_sines_keep_the_turn(interleaved):
+    """Unit vectors come out as the cosine and the sine of the plan's turns.  sincospif is off by one step
+    at most (2^-24 below 1) and the correction for what a float drops of the turn rounds once (2^-25);
+    the turn itself is cut at 2^-32 (2^-29 radians), the second term of the angle sum is below 2^-47."""
+    m = _m()
+    g = torch.Generator().manual_seed(50)
+    at = torch.cat([torch.arange(64), torch.randint(-2 ** 40, 2 ** 40, (8000,), generator=g)])
+    x = torch.zeros(len(at), 2, 64, device="cuda")
+    pair = slice(0, 64, 2) if interleaved else slice(0, 32)
+    other = slice(1, 64, 2) if interleaved else slice(32, 64)
+    x[:, 0, pair] = 1
+    x[:, 1, other] = 1
+    plan = m.rotary_plan(64, interleaved=interleaved)
+    y = m.rotary(x, None, plan, positions=at.cuda())[0].double().cpu()
+    turn = torch.tensor([[(f * p) % 2 ** 64 / 2 ** 64 for f in plan.frequencies] for p in at.tolist()],
+                        dtype=torch.float64) * (2 * math.pi)
+    limit = torch.full_like(turn, 2.0 ** -24 + 2.0 ** -25 + 2.0 ** -28)
+    within(y[:, 0, pair], turn.cos(), limit)
+    within(y[:, 0, other], turn.sin(), limit)
+    within(y[:, 1, pair], -turn.sin(), limit)
+    within(y[:, 1, other], turn.cos(), limit)
