@@ -10,7 +10,7 @@
 // A thread has 16 elements of a row: 8 pairs (two runs of 8 elements half the rotated part apart,
 // or 16 neighbours), or 16 elements that only move.  It takes 8 sines and cosines once
 // and goes over several heads of its token with them, four on their way at once.  Bound: HBM, each
-// row read and written once: 32768 tokens of 20 heads of d = 128 in bf16 52 us, 6.4 TB/s; 131072 of
+// row read and written once: 32768 tokens of 20 heads of d = 128 in bf16 53 us, 6.3 TB/s; 131072 of
 // 10 in fp32 196 us, 6.8 TB/s (a copy: 6.8); appending 32768 tokens of 16 + 4 + 4 heads 64 us.
 #include "cache_common.cuh"
 
@@ -100,16 +100,12 @@ __device__ __forceinline__ long long position_of(const RotaryArgs& a, int t) {
                                : (long long)fetch(static_cast<const int*>(a.positions) + t);
 }
 
-// Cosines and sines of 8 pairs from `pair` on at position p.
-//
-// fp32: the upper 32 bits of a turn do not fit a float; what it drops (2^-25 of half a turn at most, 9.4e-8
-// radians, as much as the functions' own error) comes back by the first term of the angle sum.
-//
-// Results of 16 bits take the hardware's functions of the rounded angle, off by 2^-21.19 at most between
-// -pi and pi: sincospif's instructions for 8 pairs outnumbered those for the rows where a thread has few
-// heads (24001 tokens of 9 heads of d = 64, half of each: 22 us and 11.6).  Against the length of the pair
-// that is far below half a step (2^-8 in bf16, 2^-11 in fp16), against an element that nearly cancels it is
-// not: one below 2^-10 of its pair (fp16; 2^-13 in bf16) may be off by more than its own rounding.
+// Cosines and sines of 8 pairs from `pair` on at position p.  The upper 32 bits of a turn do not fit a
+// float; what it drops (2^-25 of half a turn at most, 9.4e-8 radians, as much as the functions' own error)
+// comes back by the first term of the angle sum for fp32 results; 16-bit ones are rounded far above it.
+// The hardware's sines, off by 2^-21 of a pair's length, are not taken for those either: an fp16 element
+// below 2^-10 of its pair would be off by more than its rounding, and they save 1 % (32768 tokens of 20
+// heads 52.9 -> 52.4 us, a step of 64 tokens 2.5 -> 2.35).
 template <typename T>
 __device__ __forceinline__ void turns(const RotaryArgs& a, int pair, long long p, float (&c)[8],
                                       float (&s)[8]) {
@@ -119,11 +115,8 @@ __device__ __forceinline__ void turns(const RotaryArgs& a, int pair, long long p
     const int32_t whole = (int32_t)(turn >> 32);  // 2^-31 half turns, in [-1, 1)
     const float half = (float)whole;
     float sn, cs;
-    if (sizeof(T) == 2) {
-      sn = __sinf(half * (0x1p-31f * kPi));
-      cs = __cosf(half * (0x1p-31f * kPi));
-    } else {
-      sincospif(half * 0x1p-31f, &sn, &cs);
+    sincospif(half * 0x1p-31f, &sn, &cs);
+    if (sizeof(T) == 4) {
       const float rest = (float)(whole - (int32_t)half) * (0x1p-31f * kPi), s0 = sn;
       sn = fmaf(cs, rest, sn);
       cs = fmaf(-s0, rest, cs);

@@ -4,9 +4,9 @@ results of kernels that compute in fp32 from 16-bit operands.
 Rotary.  A turn is exact to 2^-32 before it becomes a float in [-1, 1) (2^-25 of half a turn:
 less than 2^-23 radians), sine and cosine are off by at most 2^-23 more, the amplitude's product
 and the two products' sum by 2^-24 each of |a| + |b|: together 2^-21 amplitude (|a| + |b|),
-and the rounding of the result, half a step.  For 16-bit results sine and cosine are the hardware's,
-whose error is given as at most 2^-21.19 between -pi and pi: 2^-21.19 + 2^-23 + 2 * 2^-24 = 1.13 *
-2^-21, within 2^-20.
+and the rounding of the result, half a step.  For 16-bit results 2^-20 is allowed (enough for the
+hardware's sine and cosine, off by 2^-21.19 between -pi and pi); test_sines_of_16_bit_results has
+the kernel's own limit.
 
 Attention.  U = 2^-8, half a bf16 step.  A score is a sum of at most 128 products accumulated in
 fp32, each addition off by at most 2^-23 of A = sum |q||k| scale: 2^-16 A; exponentials, sums

@@ -309,3 +309,23 @@ def test_fp32_sines_keep_the_turn(interleaved):
     within(y[:, 0, other], turn.sin(), limit)
     within(y[:, 1, pair], -turn.sin(), limit)
     within(y[:, 1, other], turn.cos(), limit)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_sines_of_16_bit_results(dtype):
+    """Elements that nearly cancel too.  sincospif is off by 2^-24 at most, the float that holds the turn
+    by 2^-25 of half a turn, the turn itself by 2^-29 radians; the result is rounded once."""
+    m = _m()
+    g = torch.Generator().manual_seed(51)
+    at = torch.randint(-2 ** 40, 2 ** 40, (8000,), generator=g)
+    x = torch.zeros(len(at), 2, 64, device="cuda", dtype=dtype)
+    x[:, 0, :32] = x[:, 1, 32:] = 1
+    plan = m.rotary_plan(64)
+    y = m.rotary(x, None, plan, positions=at.cuda())[0].double().cpu()
+    turn = torch.tensor([[(f * p) % 2 ** 64 / 2 ** 64 for f in plan.frequencies] for p in at.tolist()],
+                        dtype=torch.float64) * (2 * math.pi)
+    c, s, fi = turn.cos(), turn.sin(), torch.finfo(dtype)
+    assert (c.abs() < 2.0 ** -12).sum() > 10 and (s.abs() < 2.0 ** -12).sum() > 10
+    off = 2.0 ** -24 + math.pi * 2.0 ** -25 + 2.0 ** -28
+    for got, want in ((y[:, 0, :32], c), (y[:, 0, 32:], s), (y[:, 1, :32], -s), (y[:, 1, 32:], c)):
+        within(got, want, off + fi.eps / 2 * (want.abs() + off + fi.tiny))
