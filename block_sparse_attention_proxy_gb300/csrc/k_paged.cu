@@ -870,6 +870,11 @@ void paged_shape(PagedArgs* a) {
   // rows together take as long as their bytes, and the join 4 us more.  Measured at 8 heads of
   // d = 128 (shared, whole, in us): 1 sequence of 3 tiles 8.2, 6.7, of 5 7.9, 8.6; 16 sequences of up
   // to 7 tiles 16.9, 12.5, 14 tiles 23.4, 20.0, 26 tiles 34.9, 33.0, 51 tiles 56.7, 59.5.
+  // kWholeTiles is not where full rows stop to gain but where one long row among short ones
+  // starts to lose: the rule sees what the table can name, not the lengths, and then one CTA has the
+  // long row to itself.  16 sequences, one of the table's width and the others of 150 entries: 12 tiles
+  // 12.6, 13.6, 14 tiles 12.6, 15.4, 26 tiles 11.5, 25.6 (all of the width: 24.9, 19.5; 26.7, 21.9; 40.8,
+  // 36.2); 12 heads of d = 64: 12 tiles 11.0, 11.8, 26 tiles 11.8, 21.4 (20.7, 16.0; 33.8, 28.5).
   const long long rows = (long long)c.nseq * c.hkv;
   const double tile = c.d == 128 ? 0.85 : 0.7, share = c.d == 128 ? 0.007 : 0.0035;
   a->whole = row <= kWholeTiles && row * (tile - share * rows) <= 3.5;

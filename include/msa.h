@@ -358,7 +358,7 @@ msa_status msa_rotary(const msa_rotary_params* params, const int32_t* cu_seqlens
  * (rotated), so the order of a sequence's entries carries no meaning.  Sequences may share
  * pages that are only read; pages that a call writes (msa_cache_append, msa_cache_evict, the
  * weights) belong to one sequence.  What the table names behind a sequence's length is not
- * read.  A page out of range, a length below 0 or beyond max_pages * page_size is recorded as
+ * used.  A page out of range, a length below 0 or beyond max_pages * page_size is recorded as
  * MSA_ERR_DEVICE_CHECK, nothing out of the cache is touched, and the call's results are undefined.
  */
 typedef struct msa_cache {
@@ -401,11 +401,14 @@ msa_status msa_cache_append(const msa_cache* cache, const msa_table* table,
  * Attention of one new token of each sequence over its entries (its own among them, if it has been
  * appended):
  *   s_j = softmax_scale q . k_j,  j < lens[b],  p = softmax(s),  o = sum_j p_j v_j.
- * q, o [num_seqs, hq, d] bf16, o contiguous, and either q itself or without overlap with it; any hq / hkv from 1 to 64, hq <= 1024.  A sequence
- * without entries gets o = 0.  With `accumulate` the weights that an entry gets from the hq / hkv
- * heads of its KV head are added to cache->weight.  A score of -inf takes no weight; a sequence all
- * of whose scores are -inf gets o = 0.  Sums have a fixed order (the weights too, unless
- * sequences share pages): results repeat bit for bit.
+ * q, o [num_seqs, hq, d] bf16, o contiguous and either q itself or without overlap with it; any
+ * hq / hkv from 1 to 64, hq <= 1024.  A sequence without entries gets o = 0.  With `accumulate` the
+ * weights that an entry gets from the hq / hkv heads of its KV head are added to cache->weight.  A
+ * score of -inf takes no weight; a sequence all of whose scores are -inf gets o = 0.  Scores,
+ * exponentials and sums are fp32; a probability has 16 bits in its product with v (two bf16
+ * parts).  It is normalised last: o may overflow where 256 |v| summed over the entries exceeds
+ * fp32's range.  Sums have a fixed order (the weights too, unless sequences share pages): results
+ * repeat bit for bit.
  */
 typedef struct msa_paged_params {
   int32_t hq;
