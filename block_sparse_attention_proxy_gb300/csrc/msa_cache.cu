@@ -280,7 +280,7 @@ msa_status msa_paged_attention(const msa_cache* cache, const msa_table* table,
   if (!q || !o || !aligned(q, 16) || !aligned(o, 16)) return MSA_ERR_INVALID_ARG;
   // over itself a row is read by the CTA that writes it, or (shared rows) before the join writes
   const long long packed = (long long)a.hq * a.cache.d;
-  if ((o != q || qs != packed) &&
+  if ((o != q || (a.cache.nseq > 1 && qs != packed)) &&
       overlap(o, (size_t)a.cache.nseq * packed * 2, q,
               ((size_t)(a.cache.nseq - 1) * qs + packed) * 2))
     return MSA_ERR_INVALID_ARG;

@@ -368,6 +368,8 @@ def test_attention_over_its_queries(m):
         assert call(64 * P, 64 * P + o) == 1
     assert call(64 * P, 64 * P, 512) == 1 and call(64 * P, 64 * P + 2 * 512 * 2 + 496, 512) == 1
     assert call(64 * P, 64 * P + 2 * 512 * 2 + 512, 512) == 3
+    table = _table(m, num_seqs=1)  # of one row any stride
+    assert call(64 * P, 64 * P, 512) == 3 and call(64 * P, 64 * P + 16, 512) == 1
 
 
 def test_the_join_reads_past_l1_before_its_wait():
